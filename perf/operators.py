@@ -211,7 +211,8 @@ def _plain_ns(s):
 def _workspace(s, nbytes):
     """The workspace that a program makes once and keeps."""
     if "ws" not in s:
-        s["ws"] = torch.empty(nbytes(), dtype=torch.uint8, device="cuda")
+        from moe_expert_layer_permute_gb300 import binding as moe
+        s["ws"] = moe.Workspace(nbytes())
     return s["ws"]
 
 
