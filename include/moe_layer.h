@@ -64,7 +64,7 @@ extern "C" {
  * types row; the English copy of that table drops the row).  Forward only, like DeepGEMM's kernel:
  * moe_bwd returns MOE_ERR_UNSUPPORTED for it. */
 typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_FP8_BWD = 2, MOE_FP8_FP4 = 3 } moe_precision;
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_I32 = 2 } moe_dtype;
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_I32 = 2, MOE_DT_U8 = 3 } moe_dtype;
 
 /* A view of a caller-owned buffer: `data` is a device pointer for the layer calls. */
 typedef struct {
@@ -199,6 +199,64 @@ const char* moe_strerror(int code);
 int moe_router_fwd(const moe_tensor* logits, moe_tensor* topk_idx, moe_tensor* topk_w, void* stream);
 int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const moe_tensor* dtopk_w,
                    moe_tensor* dlogits, void* stream);
+
+/* ---- training the router: balance loss, z-loss, per-expert counts ----------------------------- */
+/* A router trained on the layer's loss alone tends to send most tokens to few experts.  The usual
+ * remedy adds two losses on the logits l [T, E], one that is least when the picks spread evenly and one
+ * that holds the logits' size, each over a whole batch or over each sequence of it:
+ *   p[t] = softmax(l[t]) over all E experts, lse[t] = log sum_e exp(l[t,e])
+ *   a token counts in segment s if seg_offsets[s] <= t < seg_offsets[s+1] and its mask is not 0
+ *   tokens[s]    = n, the counted tokens
+ *   counts[s,e]  = picks of expert e among the counted tokens' k (ids outside [0, E) are dropped)
+ *   loss[s,0]    = E / (k n^2) * sum_e counts[s,e] * sum_t p[t,e]     (1 for an even spread)
+ *   loss[s,1]    = 1 / n * sum_t lse[t]^2                             (both 0 where n = 0)
+ *
+ * moe_balance_fwd: logits fp32 [T, E], topk_idx int32 [T, k] -> counts int32 [B, E], tokens int32
+ *   [B], loss fp32 [B, 2].  mask: uint8 [T] or NULL (every token counts); seg_offsets: int32 [B+1],
+ *   ascending (tokens before the first or past the last offset count nowhere), or NULL for one
+ *   segment of all tokens (B = 1).  `workspace` is a zeroed moe_scratch handle of at least
+ *   moe_balance_workspace_bytes(T, E, B) bytes, 256-byte aligned; its desc is not read.
+ * moe_balance_bwd: dlogits fp32 [T, E] (overwritten) of sum_s dloss[s] . loss[s], counts taken as
+ *   constants, plus, with topk_w and dtopk_w (both or neither), what moe_router_bwd gives for them, in
+ *   the same pass:
+ *     dlogits[t,e] = dloss[s,0] E / (k n^2) p[t,e] (counts[s,e] - sum_i p[t,i] counts[s,i])
+ *                  + dloss[s,1] 2 / n lse[t] p[t,e]            (both only where token t counts)
+ *                  + w_j (dw_j - sum_i w_i dw_i)               (where e = topk_idx[t,j])
+ *   topk_idx: distinct experts per token; counts and tokens as moe_balance_fwd wrote them.
+ * Rows of tokens that do not count are not read: they may hold anything.  A counted row that is -inf
+ * throughout has p = 0 and adds nothing to the losses; NaN or +inf in a counted row give NaN.  Sums
+ * are taken in an order that depends on the sizes alone, so results repeat bit for bit.  Outputs may
+ * not overlap inputs.  Limits as moe_router_fwd's, and 1 <= B <= 65535 (MOE_ERR_UNSUPPORTED);
+ * T = 0 gives zeros. */
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t B);   /* 0: outside the limits */
+int moe_balance_fwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* mask,
+                    const moe_tensor* seg_offsets, moe_tensor* counts, moe_tensor* tokens, moe_tensor* loss,
+                    moe_scratch* workspace, void* stream);
+int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* topk_w,
+                    const moe_tensor* dtopk_w, const moe_tensor* mask, const moe_tensor* seg_offsets,
+                    const moe_tensor* counts, const moe_tensor* tokens, const moe_tensor* dloss, moe_tensor* dlogits,
+                    void* stream);
+
+/* ---- training the weights: orthogonalised updates ---------------------------------------------- */
+/* The update of the Muon optimiser: each matrix of G [N, R, C] (bf16 or fp32: a momentum, or a
+ * gradient as moe_bwd gives it, every expert a matrix) is moved towards the nearest orthogonal one by
+ * `steps` Newton-Schulz steps:
+ *   X = G / (|G|_F + eps);  per step, with its (a, b, c):  A = X X^T,  X <- a X + (b A + c A A) X
+ * (on G^T where R > C, which gives the same), and O [N, R, C] bf16 receives X.  coeffs: host floats,
+ * (a, b, c) for each step, or NULL for (3.4445, -4.7750, 2.0315) throughout.  O may be G itself (bf16).
+ * The products take fp16 operands with fp32 sums: O is within about 2.5e-3 (2-norm, bf16's own
+ * rounding of 1.7e-3 included) of the exact result for the default coefficients and five steps.
+ * A zero matrix (an expert without tokens) gives zeros; one with a NaN, an infinity or a squared norm
+ * beyond fp32 gives NaN, the others of the batch unharmed.
+ * `workspace`: a zeroed moe_scratch handle of at least moe_orthogonalise_workspace_bytes(N, R, C)
+ * bytes, 256-byte aligned, whose first four bytes (the status word that moe_read_device_status
+ * returns) the caller has set to zero; its desc is not read, moe_set_wait_limit applies.
+ * N <= 65535, R, C <= 32768, N * ceil(R/128) * ceil(C/128) < 2^31, steps <= 16, eps in [1e-20, 1],
+ * coefficients in [-16, 16]: MOE_ERR_UNSUPPORTED outside; N = 0 launches nothing. */
+#define MOE_ORTHOGONALISE_MAX_STEPS 16
+size_t moe_orthogonalise_workspace_bytes(int64_t N, int64_t R, int64_t C);   /* 0: outside the limits */
+int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const float* coeffs, float eps,
+                      moe_scratch* workspace, void* stream);
 
 /* ---- routing without caller-provided scratch ---------------------------------------------- */
 /* The pages have no counterpart to this entry point; it exists for callers that cannot allocate

@@ -16,7 +16,7 @@ from . import build as _build
 
 # ---- C structures ---------------------------------------------------------------------------
 MOE_BF16, MOE_MXFP8, MOE_FP8_BWD, MOE_FP8_FP4 = 0, 1, 2, 3
-MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32 = 0, 1, 2
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8 = 0, 1, 2, 3
 MOE_FLAG_SAVE_GU, MOE_FLAG_REUSE_FWD, MOE_FLAG_REUSE_WEIGHTS, MOE_FLAG_FUSED_COMBINE = 0x1, 0x2, 0x4, 0x8
 (MOE_VIEW_COUNTS, MOE_VIEW_OFFSETS, MOE_VIEW_PERM, MOE_VIEW_INV, MOE_VIEW_PAD_OFFSETS, MOE_VIEW_XPERM,
  MOE_VIEW_HID, MOE_VIEW_GU, MOE_VIEW_YPART, MOE_VIEW_DG, MOE_VIEW_HW, MOE_VIEW_DYPERM) = range(12)
@@ -34,7 +34,8 @@ ERR = {v: k for k, v in ERRORS.items()}
 # every symbol the header declares
 EXPORTS = ("moe_scratch_bytes", "moe_fwd", "moe_bwd", "moe_read_device_status", "moe_strerror",
            "moe_scratch_view", "moe_trace_enable", "moe_trace_reset", "moe_trace_read", "moe_route_static",
-           "moe_router_fwd", "moe_router_bwd", "moe_set_wait_limit")
+           "moe_router_fwd", "moe_router_bwd", "moe_set_wait_limit", "moe_balance_workspace_bytes", "moe_balance_fwd",
+           "moe_balance_bwd", "moe_orthogonalise_workspace_bytes", "moe_orthogonalise")
 
 
 class MoeTensor(ctypes.Structure):
@@ -87,6 +88,17 @@ def _load() -> ctypes.CDLL:
     lib.moe_router_bwd.restype = ctypes.c_int
     lib.moe_set_wait_limit.argtypes = [_P(MoeScratch), ctypes.c_int64, ctypes.c_uint32]
     lib.moe_set_wait_limit.restype = ctypes.c_int
+    lib.moe_balance_workspace_bytes.argtypes = [ctypes.c_int64] * 3
+    lib.moe_balance_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_balance_fwd.argtypes = [_P(MoeTensor)] * 7 + [_P(MoeScratch), ctypes.c_void_p]
+    lib.moe_balance_fwd.restype = ctypes.c_int
+    lib.moe_balance_bwd.argtypes = [_P(MoeTensor)] * 10 + [ctypes.c_void_p]
+    lib.moe_balance_bwd.restype = ctypes.c_int
+    lib.moe_orthogonalise_workspace_bytes.argtypes = [ctypes.c_int64] * 3
+    lib.moe_orthogonalise_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_orthogonalise.argtypes = [_P(MoeTensor)] * 2 + [ctypes.c_int32, _P(ctypes.c_float), ctypes.c_float,
+                                                            _P(MoeScratch), ctypes.c_void_p]
+    lib.moe_orthogonalise.restype = ctypes.c_int
     return lib
 
 
@@ -103,7 +115,8 @@ def strerror(code: int) -> str:
     return LIB.moe_strerror(code).decode()
 
 
-_DT = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.int32: MOE_DT_I32}
+_DT = {torch.bfloat16: MOE_DT_BF16, torch.float32: MOE_DT_F32, torch.int32: MOE_DT_I32, torch.uint8: MOE_DT_U8,
+       torch.bool: MOE_DT_U8}
 
 
 def as_moe_tensor(t: torch.Tensor) -> MoeTensor:
@@ -171,6 +184,22 @@ class Scratch:
         off, nbytes = view_span(self.handle.desc, which)
         raw = self.buffer[off:off + nbytes]
         return raw.view(dtype).view(*shape)
+
+
+class Workspace:
+    """A caller-owned device buffer and its C handle for moe_balance_fwd and moe_orthogonalise (their
+    *_workspace_bytes); moe_read_device_status takes it as it takes a Scratch."""
+
+    def __init__(self, nbytes: int, device="cuda"):
+        if nbytes <= 0:
+            raise MoeError(ERR["MOE_ERR_UNSUPPORTED"], "Workspace")
+        self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.buffer[:256].zero_()        # the status word
+        self.handle = MoeScratch()
+        self.handle.data = self.buffer.data_ptr()
+        self.handle.bytes = nbytes
+
+    set_wait_limit = Scratch.set_wait_limit
 
 
 def _stream_ptr(stream) -> int:
@@ -252,3 +281,52 @@ def moe_router_bwd(topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> None:
     rc = LIB.moe_router_bwd(*[ctypes.byref(a) for a in args], _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_router_bwd")
+
+
+def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
+    return int(LIB.moe_balance_workspace_bytes(T, E, B))
+
+
+def _ref(t):
+    return None if t is None else ctypes.byref(as_moe_tensor(t))
+
+
+def moe_balance_fwd(logits, topk_idx, counts, tokens, loss, workspace: Workspace, mask=None, seg_offsets=None,
+                    stream=None) -> None:
+    """Balance loss, z-loss and per-expert counts of each segment: logits fp32 [T, E], topk_idx int32
+    [T, k], mask bool or uint8 [T] or None, seg_offsets int32 [B+1] or None (B = 1) -> counts int32
+    [B, E], tokens int32 [B], loss fp32 [B, 2]."""
+    rc = LIB.moe_balance_fwd(_ref(logits), _ref(topk_idx), _ref(mask), _ref(seg_offsets), _ref(counts), _ref(tokens),
+                             _ref(loss), ctypes.byref(workspace.handle), _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_balance_fwd")
+
+
+def moe_balance_bwd(logits, topk_idx, topk_w, dtopk_w, counts, tokens, dloss, dlogits, mask=None, seg_offsets=None,
+                    stream=None) -> None:
+    """dlogits fp32 [T, E] of the losses (dloss fp32 [B, 2]) and, unless topk_w and dtopk_w are None,
+    of the top-k weights (what moe_router_bwd gives), in one pass."""
+    rc = LIB.moe_balance_bwd(_ref(logits), _ref(topk_idx), _ref(topk_w), _ref(dtopk_w), _ref(mask), _ref(seg_offsets),
+                             _ref(counts), _ref(tokens), _ref(dloss), _ref(dlogits), _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_balance_bwd")
+
+
+def moe_orthogonalise_workspace_bytes(N: int, R: int, C: int) -> int:
+    return int(LIB.moe_orthogonalise_workspace_bytes(N, R, C))
+
+
+def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None) -> None:
+    """O bf16 [N, R, C] = every matrix of G (bf16 or fp32, [N, R, C]) after `steps` Newton-Schulz steps.
+    coeffs: (a, b, c) for every step, a sequence of `steps` such triples, or None for the defaults."""
+    co = None
+    if coeffs is not None:
+        flat = [float(v) for c in coeffs for v in (c if hasattr(c, "__len__") else (c,))]
+        if len(flat) == 3:
+            flat *= max(steps, 1)
+        if len(flat) != 3 * steps:
+            raise MoeError(ERR["MOE_ERR_SHAPE"], "moe_orthogonalise")
+        co = (ctypes.c_float * len(flat))(*flat)
+    rc = LIB.moe_orthogonalise(_ref(G), _ref(O), steps, co, eps, ctypes.byref(workspace.handle), _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_orthogonalise")

@@ -97,6 +97,26 @@ cudaError_t launch_router_fwd(cudaStream_t st, const float* logits, int T, int E
 cudaError_t launch_router_bwd(cudaStream_t st, const int* topk_idx, const float* topk_w, const float* dtopk_w, int T,
                               int E, int k, float* dlogits);
 
+// balance loss, z-loss and per-expert counts of each segment, and their gradient joined with the
+// top-k weights' (balance.cu); mask, seg_offsets, and topk_w with dtopk_w may be null
+size_t balance_workspace(int64_t T, int64_t E, int64_t B);
+cudaError_t launch_balance_fwd(cudaStream_t st, const float* logits, const int* topk_idx, const uint8_t* mask,
+                               const int* seg_offsets, int T, int E, int k, int B, int* counts, int* tokens, float* loss,
+                               void* workspace);
+cudaError_t launch_balance_bwd(cudaStream_t st, const float* logits, const int* topk_idx, const float* topk_w,
+                               const float* dtopk_w, const uint8_t* mask, const int* seg_offsets, const int* counts,
+                               const int* tokens, const float* dloss, int T, int E, int k, int B, float* dlogits);
+
+// Newton-Schulz orthogonalisation of N matrices [R, C] (orthogonal.cu); coeffs: 3 * steps host floats
+size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C);
+cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int64_t N, int64_t R, int64_t C, void* O,
+                                 int steps, const float* coeffs, float eps, void* workspace, int* status,
+                                 long long wait_limit, bool withhold_loads);
+// 3-D tensor map over a batch of row-major fp16 matrices [rows, cols] of pitch ld (a multiple of 8
+// elements), box {64, box_rows, 1}, 128-byte swizzle; reads outside a matrix are zero (gemm.cu)
+bool tmap_batched_f16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t batch,
+                      uint32_t box_rows);
+
 // grouped GEMMs (persistent, TMA + tcgen05)
 enum class GemmKind : int {
     FwdGateUp = 0,     // [g|u] = X_perm W13[e]^T, epilogue w h = w silu(g) u (MXFP8: h, unweighted)

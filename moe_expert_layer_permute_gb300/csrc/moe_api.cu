@@ -525,6 +525,116 @@ int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const m
     return MOE_OK;
 }
 
+static int check_workspace(const moe_scratch* w, size_t need) {
+    if (!w) return MOE_ERR_NULL;
+    if (!w->data || reinterpret_cast<uintptr_t>(w->data) % 256 != 0 || w->bytes < need) return MOE_ERR_SCRATCH;
+    return MOE_OK;
+}
+
+// mask and segments shared by both directions of the balance loss; B from the per-segment tensor
+static int check_segments(const moe_tensor* mask, const moe_tensor* off, const moe_tensor* per_segment, int64_t T,
+                          int64_t* B) {
+    if (!per_segment) return MOE_ERR_NULL;
+    if (per_segment->ndim != 1 || per_segment->shape[0] < 1) return MOE_ERR_SHAPE;
+    *B = per_segment->shape[0];
+    if (*B > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!off && *B != 1) return MOE_ERR_SHAPE;
+    int rc;
+    if (mask && (rc = check_tensor(mask, MOE_DT_U8, 1, T, 0, 0))) return rc;
+    if (off && (rc = check_tensor(off, MOE_DT_I32, 1, *B + 1, 0, 0))) return rc;
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t B) {
+    if (T < 0 || T >= (int64_t)INT32_MAX / 32 || E < 1 || E > kMaxExperts || B < 1 || B > 65535) return 0;
+    return balance_workspace(T, E, B);
+}
+
+int moe_balance_fwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* mask,
+                    const moe_tensor* seg_offsets, moe_tensor* counts, moe_tensor* tokens, moe_tensor* loss,
+                    moe_scratch* workspace, void* stream) {
+    int64_t T, E, k, B;
+    int rc = router_shape(logits, topk_idx, &T, &E, &k);
+    if (rc) return rc;
+    if ((rc = check_segments(mask, seg_offsets, tokens, T, &B))) return rc;
+    if ((rc = check_tensor(logits, MOE_DT_F32, 2, T, E, 0))) return rc;
+    if ((rc = check_tensor(topk_idx, MOE_DT_I32, 2, T, k, 0))) return rc;
+    if ((rc = check_tensor(counts, MOE_DT_I32, 2, B, E, 0))) return rc;
+    if ((rc = check_tensor(tokens, MOE_DT_I32, 1, B, 0, 0))) return rc;
+    if ((rc = check_tensor(loss, MOE_DT_F32, 2, B, 2, 0))) return rc;
+    if ((rc = check_workspace(workspace, balance_workspace(T, E, B)))) return rc;
+    MOE_TRY_CUDA(launch_balance_fwd(
+        reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const float*>(logits->data),
+        reinterpret_cast<const int*>(topk_idx->data), mask ? reinterpret_cast<const uint8_t*>(mask->data) : nullptr,
+        seg_offsets ? reinterpret_cast<const int*>(seg_offsets->data) : nullptr, (int)T, (int)E, (int)k, (int)B,
+        reinterpret_cast<int*>(counts->data), reinterpret_cast<int*>(tokens->data), reinterpret_cast<float*>(loss->data),
+        workspace->data));
+    return MOE_OK;
+}
+
+int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* topk_w,
+                    const moe_tensor* dtopk_w, const moe_tensor* mask, const moe_tensor* seg_offsets,
+                    const moe_tensor* counts, const moe_tensor* tokens, const moe_tensor* dloss, moe_tensor* dlogits,
+                    void* stream) {
+    int64_t T, E, k, B;
+    int rc = router_shape(logits, topk_idx, &T, &E, &k);
+    if (rc) return rc;
+    if ((rc = check_segments(mask, seg_offsets, tokens, T, &B))) return rc;
+    if ((topk_w == nullptr) != (dtopk_w == nullptr)) return MOE_ERR_NULL;
+    if ((rc = check_tensor(logits, MOE_DT_F32, 2, T, E, 0))) return rc;
+    if ((rc = check_tensor(topk_idx, MOE_DT_I32, 2, T, k, 0))) return rc;
+    if (topk_w && (rc = check_tensor(topk_w, MOE_DT_F32, 2, T, k, 0))) return rc;
+    if (dtopk_w && (rc = check_tensor(dtopk_w, MOE_DT_F32, 2, T, k, 0))) return rc;
+    if ((rc = check_tensor(counts, MOE_DT_I32, 2, B, E, 0))) return rc;
+    if ((rc = check_tensor(tokens, MOE_DT_I32, 1, B, 0, 0))) return rc;
+    if ((rc = check_tensor(dloss, MOE_DT_F32, 2, B, 2, 0))) return rc;
+    if ((rc = check_tensor(dlogits, MOE_DT_F32, 2, T, E, 0))) return rc;
+    MOE_TRY_CUDA(launch_balance_bwd(
+        reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const float*>(logits->data),
+        reinterpret_cast<const int*>(topk_idx->data), topk_w ? reinterpret_cast<const float*>(topk_w->data) : nullptr,
+        dtopk_w ? reinterpret_cast<const float*>(dtopk_w->data) : nullptr,
+        mask ? reinterpret_cast<const uint8_t*>(mask->data) : nullptr,
+        seg_offsets ? reinterpret_cast<const int*>(seg_offsets->data) : nullptr, reinterpret_cast<const int*>(counts->data),
+        reinterpret_cast<const int*>(tokens->data), reinterpret_cast<const float*>(dloss->data), (int)T, (int)E, (int)k,
+        (int)B, reinterpret_cast<float*>(dlogits->data)));
+    return MOE_OK;
+}
+
+static bool ns_supported(int64_t N, int64_t R, int64_t C) {
+    return N >= 0 && N <= 65535 && R >= 1 && R <= 32768 && C >= 1 && C <= 32768 &&
+           N * ((R + 127) / 128) * ((C + 127) / 128) < INT32_MAX;
+}
+
+size_t moe_orthogonalise_workspace_bytes(int64_t N, int64_t R, int64_t C) {
+    return ns_supported(N, R, C) ? orthogonalise_workspace(N, R, C) : 0;
+}
+
+int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const float* coeffs, float eps,
+                      moe_scratch* workspace, void* stream) {
+    if (!G || !O) return MOE_ERR_NULL;
+    if (G->ndim != 3 || steps < 1) return MOE_ERR_SHAPE;
+    const int64_t N = G->shape[0], R = G->shape[1], C = G->shape[2];
+    if (N < 0 || R < 1 || C < 1) return MOE_ERR_SHAPE;
+    if (!ns_supported(N, R, C) || steps > MOE_ORTHOGONALISE_MAX_STEPS || !(eps >= 1e-20f && eps <= 1.f))
+        return MOE_ERR_UNSUPPORTED;
+    const bool f32 = G->dtype == MOE_DT_F32;
+    int rc;
+    if ((rc = check_tensor(G, f32 ? MOE_DT_F32 : MOE_DT_BF16, 3, N, R, C))) return rc;
+    if ((rc = check_tensor(O, MOE_DT_BF16, 3, N, R, C))) return rc;
+    if ((rc = check_workspace(workspace, orthogonalise_workspace(N, R, C)))) return rc;
+    float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
+    for (int i = 0; i < 3 * steps; ++i) {
+        co[i] = coeffs ? coeffs[i] : i % 3 == 0 ? 3.4445f : i % 3 == 1 ? -4.7750f : 2.0315f;
+        if (!(co[i] >= -16.f && co[i] <= 16.f)) return MOE_ERR_UNSUPPORTED;
+    }
+    if (N == 0) return MOE_OK;
+    MOE_TRY_CUDA(launch_orthogonalise(reinterpret_cast<cudaStream_t>(stream), G->data, f32, N, R, C, O->data, steps, co, eps,
+                                      workspace->data, reinterpret_cast<int*>(workspace->data),
+                                      (long long)workspace->state[2],
+                                      (workspace->state[3] & MOE_TEST_WITHHOLD_LOADS) != 0));
+    return MOE_OK;
+}
+
 const char* moe_strerror(int code) {
     switch (code) {
         case MOE_OK: return "ok";
