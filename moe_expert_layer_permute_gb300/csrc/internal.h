@@ -110,12 +110,13 @@ cudaError_t launch_balance_bwd(cudaStream_t st, const float* logits, const int* 
 // Newton-Schulz orthogonalisation of N matrices [R, C] (orthogonal.cu); coeffs: 3 * steps host floats
 size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C);
 cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int64_t N, int64_t R, int64_t C, void* O,
-                                 int steps, const float* coeffs, float eps, void* workspace, int* status,
+                                 int steps, const float* coeffs, float eps, void* workspace, int num_sms, int* status,
                                  long long wait_limit, bool withhold_loads);
-// 3-D tensor map over a batch of row-major fp16 matrices [rows, cols] of pitch ld (a multiple of 8
-// elements), box {64, box_rows, 1}, 128-byte swizzle; reads outside a matrix are zero (gemm.cu)
-bool tmap_batched_f16(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t batch,
-                      uint32_t box_rows);
+// 3-D tensor map over a batch of row-major fp16 or bf16 matrices [rows, cols] of pitch ld (a multiple of 8
+// elements), box {box_cols, box_rows, 1}; box_cols 64 (128-byte swizzle) or 32 (64-byte swizzle).
+// Outside a matrix, reads are zero and stores are dropped (gemm.cu)
+bool tmap_batched(CUtensorMap* m, const void* ptr, bool bf16, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t batch,
+                  uint32_t box_cols, uint32_t box_rows);
 
 // grouped GEMMs (persistent, TMA + tcgen05)
 enum class GemmKind : int {

@@ -628,8 +628,10 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
         if (!(co[i] >= -16.f && co[i] <= 16.f)) return MOE_ERR_UNSUPPORTED;
     }
     if (N == 0) return MOE_OK;
+    const int nsm = num_sms_current();
+    if (nsm <= 0) return MOE_ERR_CUDA;
     MOE_TRY_CUDA(launch_orthogonalise(reinterpret_cast<cudaStream_t>(stream), G->data, f32, N, R, C, O->data, steps, co, eps,
-                                      workspace->data, reinterpret_cast<int*>(workspace->data),
+                                      workspace->data, nsm, reinterpret_cast<int*>(workspace->data),
                                       (long long)workspace->state[2],
                                       (workspace->state[3] & MOE_TEST_WITHHOLD_LOADS) != 0));
     return MOE_OK;

@@ -26,10 +26,9 @@
 namespace moe {
 
 constexpr float kXScale = 256.f, kABScale = 1024.f, kLoScale = 2048.f;
-constexpr int kNsTile = 128;       // output tile
-constexpr int kNsStages = 3;
+constexpr int kNsStages = 6;
 constexpr int kNsThreads = 192;    // TMA, MMA, four epilogue warps
-constexpr int kNsOperand = kNsTile * 128;   // bytes of one operand's K slice: 128 x 64 fp16
+constexpr int kNsSet = 4096;       // bytes of two staging boxes
 constexpr int kNormPart = 32768;   // elements of one partial sum of squares
 constexpr int kNormParts = 512;    // most partial sums of a matrix
 
@@ -120,21 +119,25 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a
 
 // ---- the three products ------------------------------------------------------------------------------
 enum NsMode { NS_GRAM = 0, NS_POLY, NS_APPLY };
+// How the last step stores O: not at all (an inner step), through TMA boxes as it stands or flipped, or
+// by plain stores where its rows are not multiples of 16 bytes
+enum NsOut { NS_O_NONE = 0, NS_O_BOX, NS_O_BOX_FLIP, NS_O_PLAIN, NS_O_PLAIN_FLIP };
 
 struct NsArgs {
-    int m, n, lda, ldx, k_blocks, tiles_n, tiles;   // tiles per matrix
+    int m, n, lda, ldx;
+    int tiles_n, tiles;          // tile columns (APPLY), tiles per matrix
+    int units;                   // tiles of the whole batch
+    int k_blocks;
     int k_wrap;                  // k_blocks, or half of them: APPLY with B's rounding error as a second B
     int batch;                   // N: matrix N + i of the B array is the rounding error of matrix i's B
     float a, b, c;
     const float* inv_s;          // [N] in the first step, null after it
     const __half* A;             // POLY: reads its tile of A
-    __half* out;                 // GRAM: A, POLY: B, APPLY: next X
-    __half* out_lo;              // POLY: B's rounding error (null: not kept)
     const __half* xhi;           // APPLY: this X
     const __half* xlo;           // APPLY: its rounding error (null: exact)
-    __half* xlo_out;             // APPLY: the next X's rounding error (null: not kept)
-    __nv_bfloat16* O;            // APPLY, last step: the result
-    int flip;                    // O is [n, m]
+    int keep_lo;                 // POLY: store B's rounding error; APPLY: the next X's
+    int out_kind;                // NsOut
+    __nv_bfloat16* O;
     int* status;
     long long wait_limit;
     int withhold_loads;
@@ -146,152 +149,371 @@ __device__ __forceinline__ void ns_wait_drain(uint64_t* bar, uint32_t parity) {
         if (clock64() - t0 > kDrainCycles) break;
 }
 
-// One 128 x 128 tile per block.  GRAM and POLY are symmetric: tiles of the lower triangle alone, each
-// stored twice.  Operands: GRAM rows of X by rows of X, POLY rows of A by rows of A (A = A^T), both
-// contiguous along K; APPLY rows of B by columns of X (contiguous along N).
-// K past the edge is zero-filled by the TMA.
+struct NsTile {
+    int mat, i, j;
+};
 template <int MODE>
-__global__ void __launch_bounds__(kNsThreads) ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                                                            const __grid_constant__ CUtensorMap tmB, const NsArgs a) {
+__device__ __forceinline__ NsTile ns_tile(int unit, const NsArgs& a) {
+    NsTile t;
+    t.mat = unit / a.tiles;
+    int left = unit - t.mat * a.tiles;
+    if (MODE == NS_APPLY) {
+        t.i = left / a.tiles_n;
+        t.j = left - t.i * a.tiles_n;
+    } else {
+        t.i = 0;
+        while (left > t.i) left -= ++t.i;   // row i of the lower triangle has i + 1 tiles
+        t.j = left;
+    }
+    return t;
+}
+
+// A warp's output boxes: 32 rows x 64 bytes (32 16-bit values), 64-byte swizzle.
+// the lane's row of 32 values, packed in pairs
+__device__ __forceinline__ void ns_box_row(uint32_t box, int lane, const uint32_t* v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+}
+// the transpose: the lane's value j goes to row j, column lane
+__device__ __forceinline__ void ns_box_col(uint32_t box, int lane, const uint32_t* v) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint16_t h = (uint16_t)(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2), "h"(h)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ uint32_t ns_pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 ns_unpack_half(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+// 32 consecutive fp16 of a row, packed; zeros past the pitch
+__device__ __forceinline__ void ns_row32(uint32_t* d, const __half* row, int col, int ld) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 v = col + 8 * q < ld ? *reinterpret_cast<const uint4*>(row + col + 8 * q) : make_uint4(0, 0, 0, 0);
+        d[4 * q] = v.x; d[4 * q + 1] = v.y; d[4 * q + 2] = v.z; d[4 * q + 3] = v.w;
+    }
+}
+
+// Persistent blocks walk the batch's tiles.  Warp 0 loads, warp 1 issues the MMAs, four warps store (see
+// gemm.cu for the scheme): six stages of 32 KB, two accumulators, waits bounded.
+//   PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each holding 128 rows of the first operand and
+//   half of the second; otherwise one CTA computes 128 x 128.
+// GRAM and POLY are symmetric: tiles of the lower triangle alone, and those below the diagonal are stored
+// twice, as they are and transposed through shared memory.  Operands: GRAM rows of X by rows of X, POLY
+// rows of A by rows of A (A = A^T), both contiguous along K; APPLY rows of B by columns of X (contiguous
+// along N).  The TMA fills K past the edge with zeros and drops stores outside a matrix, so no size needs
+// padding beyond 16-byte rows.
+template <int MODE, bool PAIR>
+__global__ void __launch_bounds__(kNsThreads, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD, const NsArgs a) {
     grid_dep_wait();
+    constexpr int kTile = PAIR ? 256 : 128;      // rows and columns of a unit's tile
+    constexpr int kOperand = 128 * 128;          // bytes of one operand's K slice per CTA: 128 x 64 fp16
+    constexpr bool kBmn = MODE == NS_APPLY;
+    constexpr uint32_t kIdesc = idesc_f16(kTile, kTile, false, kBmn);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = smem + kNsStages * kNsOperand;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + kNsStages * kNsOperand);
+    uint8_t* sB = sA + kNsStages * kOperand;
+    uint8_t* sOut = sB + kNsStages * kOperand;   // per epilogue warp two sets of two boxes
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 4 * 2 * kNsSet);
     uint64_t* empty = full + kNsStages;
-    uint64_t* done = empty + kNsStages;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* tfull = empty + kNsStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int mat = blockIdx.x / a.tiles, tile = blockIdx.x - mat * a.tiles;
-    int ti, tj;
-    if (MODE == NS_APPLY) {
-        ti = tile / a.tiles_n;
-        tj = tile - ti * a.tiles_n;
-    } else {
-        ti = 0;
-        int left = tile;
-        while (left > ti) left -= ++ti;   // row ti of the triangle has ti + 1 tiles
-        tj = left;
-    }
-    const int m0 = ti * kNsTile, n0 = tj * kNsTile;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int stride = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kNsStages; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
-        mbar_init(done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull + b, 1);
+            mbar_init(tempty + b, (PAIR ? 2 : 1) * 4);
+        }
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(tslot, kNsTile);
+    if (warp == 1) {
+        if constexpr (PAIR) tmem_alloc_pair(tslot, 2 * kTile);
+        else tmem_alloc(tslot, 2 * kTile);
+    }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // the peer's barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    constexpr bool kBmn = MODE == NS_APPLY;
-    constexpr uint32_t kIdesc = idesc_f16(kNsTile, kNsTile, false, kBmn);
 
     if (warp == 0) {
         if (lane == 0 && !a.withhold_loads) {
-            int issued = 0;
-            for (int kb = 0; kb < a.k_blocks; ++kb) {
-                const int st = kb % kNsStages;
-                if (!mbar_wait(empty + st, ((kb / kNsStages) & 1) ^ 1u, abort_flag, a.status, a.wait_limit)) break;
-                mbar_arrive_expect_tx(full + st, 2 * kNsOperand);
-                const int k0 = (kb < a.k_wrap ? kb : kb - a.k_wrap) * 64;
-                tma_load_3d(sA + st * kNsOperand, &tmA, full + st, k0, m0, kb < a.k_wrap ? mat : mat + a.batch);
-                if (kBmn) {
-                    tma_load_3d(sB + st * kNsOperand, &tmB, full + st, n0, k0, mat);
-                    tma_load_3d(sB + st * kNsOperand + 64 * 128, &tmB, full + st, n0 + 64, k0, mat);
-                } else {
-                    tma_load_3d(sB + st * kNsOperand, &tmB, full + st, k0, n0, mat);
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int u = unit0; u < a.units && ok; u += stride) {
+                const NsTile t = ns_tile<MODE>(u, a);
+                const int m0 = t.i * kTile + rank * 128, n0 = t.j * kTile + rank * 128;
+                for (int kb = 0; kb < a.k_blocks; ++kb) {
+                    if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, a.status, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dA = sA + stage * kOperand;
+                    uint8_t* dB = sB + stage * kOperand;
+                    const bool second = kb >= a.k_wrap;
+                    const int k0 = (second ? kb - a.k_wrap : kb) * 64;
+                    const int matA = second ? t.mat + a.batch : t.mat;
+                    if constexpr (PAIR) {
+                        // both CTAs' copies land on the leader's barrier, which expects both
+                        const uint32_t lbar = cluster_addr(full + stage, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(full + stage, 4 * kOperand);
+                        tma_load_3d_pair(dA, &tmA, lbar, k0, m0, matA);
+                        if (kBmn) {
+                            tma_load_3d_pair(dB, &tmB, lbar, n0, k0, t.mat);
+                            tma_load_3d_pair(dB + kOperand / 2, &tmB, lbar, n0 + 64, k0, t.mat);
+                        } else {
+                            tma_load_3d_pair(dB, &tmB, lbar, k0, n0, t.mat);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(full + stage, 2 * kOperand);
+                        tma_load_3d(dA, &tmA, full + stage, k0, m0, matA);
+                        if (kBmn) {
+                            tma_load_3d(dB, &tmB, full + stage, n0, k0, t.mat);
+                            tma_load_3d(dB + kOperand / 2, &tmB, full + stage, n0 + 64, k0, t.mat);
+                        } else {
+                            tma_load_3d(dB, &tmB, full + stage, k0, n0, t.mat);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == kNsStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                ++issued;
             }
-            // the block does not exit before its copies have landed (bounded), whoever gave up
+            // this CTA's copies have landed (bounded) before it exits, whoever gave up; a pair's land on
+            // the leader's barriers, and the peer waits for the releases that follow them instead
+            uint64_t* last = rank == 0 ? full : empty;
             for (int s = 0; s < kNsStages; ++s)
-                if (issued > s) ns_wait_drain(full + s, (uint32_t)(((issued - s + kNsStages - 1) / kNsStages - 1) & 1));
+                if (issued > s) ns_wait_drain(last + s, (uint32_t)(((issued - s + kNsStages - 1) / kNsStages - 1) & 1));
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            long long consumed = 0;
             bool ok = true;
-            for (int kb = 0; kb < a.k_blocks; ++kb) {
-                const int st = kb % kNsStages;
-                if (!mbar_wait(full + st, (kb / kNsStages) & 1, abort_flag, a.status, a.wait_limit)) {
+            const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
+            for (int u = unit0; u < a.units && ok; u += stride) {
+                if (!(PAIR ? mbar_wait_cluster(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit)
+                           : mbar_wait(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sa = smem_u32(sA) + st * kNsOperand, sb = smem_u32(sB) + st * kNsOperand;
+                const uint32_t d = tmem + (uint32_t)(acc * kTile);
+                for (int kb = 0; kb < a.k_blocks; ++kb) {
+                    if (!mbar_wait(full + stage, phase, abort_flag, a.status, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = a_base + stage * kOperand, sb = b_base + stage * kOperand;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tmem, sdesc_sw128(sa + ks * 32, 16, 1024),
-                             kBmn ? sdesc_sw128(sb + ks * 2048, 64 * 128, 1024) : sdesc_sw128(sb + ks * 32, 16, 1024),
-                             kIdesc, (kb | ks) != 0);
-                mma_commit(empty + st);
-            }
-            mma_commit(done);
-            if (!ok) ns_wait_drain(done, 0);
-        }
-    } else if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, a.status, a.wait_limit) && !*abort_flag)) {
-        tc_fence_after();
-        const int quarter = warp & 3;
-        const int r = m0 + quarter * 32 + lane;
-        const float is = a.inv_s ? __ldg(a.inv_s + mat) : 1.f;
-        const long long row = (long long)mat * a.m + r;
-#pragma unroll 1
-        for (int c0 = 0; c0 < kNsTile; c0 += 32) {
-            float v[32];
-            __syncwarp();
-            tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + c0, v);
-            const int col = n0 + c0;
-            if (r >= a.m) continue;
-            if (MODE != NS_APPLY) {
-                if (MODE == NS_GRAM) {
-                    const float f = kABScale / (kXScale * kXScale) * is * is;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= f;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = col + j < a.m ? a.b * __half2float(a.A[row * a.lda + col + j]) + a.c / kABScale * v[j] : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (col + j >= a.m) continue;
-                    const __half h = __float2half_rn(v[j]);
-                    a.out[row * a.lda + col + j] = h;
-                    if (ti != tj) a.out[((long long)mat * a.m + col + j) * a.lda + r] = h;
-                    // (kept for a single tile only)
-                    if (MODE == NS_POLY && a.out_lo) a.out_lo[row * a.lda + col + j] = __float2half_rn(v[j] - __half2float(h));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (col + j >= a.n) continue;
-                    const long long at = row * a.ldx + col + j;
-                    float x = __half2float(a.xhi[at]);
-                    if (a.xlo) x += __half2float(a.xlo[at]) * (1.f / kLoScale);
-                    x = is * (a.a * x + v[j] * (1.f / kABScale));
-                    if (a.O) {
-                        const long long o = a.flip ? ((long long)mat * a.n + col + j) * a.m + r : row * a.n + col + j;
-                        a.O[o] = __float2bfloat16_rn(x * (1.f / kXScale));
-                    } else {
-                        const __half h = __float2half_rn(x);
-                        a.out[at] = h;
-                        if (a.xlo_out) a.xlo_out[at] = __float2half_rn((x - __half2float(h)) * kLoScale);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t ad = sdesc_sw128(sa + ks * 32, 16, 1024);
+                        const uint64_t bd = kBmn ? sdesc_sw128(sb + ks * 2048, kOperand / 2, 1024)
+                                                 : sdesc_sw128(sb + ks * 32, 16, 1024);
+                        if constexpr (PAIR) mma_bf16_pair(d, ad, bd, kIdesc, (kb | ks) != 0);
+                        else mma_bf16(d, ad, bd, kIdesc, (kb | ks) != 0);
+                    }
+                    if constexpr (PAIR) mma_commit_pair_mc(empty + stage, 0x3);
+                    else mma_commit(empty + stage);
+                    ++consumed;
+                    if (++stage == kNsStages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
+                if (!ok) break;
+                if constexpr (PAIR) mma_commit_pair_mc(tfull + acc, 0x3);
+                else mma_commit(tfull + acc);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok) {
+                if constexpr (PAIR) mma_commit_pair_mc(drain, 0x1);
+                else mma_commit(drain);
+                ns_wait_drain(drain, 0);
+            } else if (PAIR) {
+                // the releases of the last stages have landed before the CTA may exit
+                for (int s = 0; s < kNsStages; ++s)
+                    if (consumed > s)
+                        ns_wait_drain(empty + s, (uint32_t)(((consumed - s + kNsStages - 1) / kNsStages - 1) & 1));
             }
         }
-        tc_fence_before();
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        uint8_t* boxes = sOut + quarter * 2 * kNsSet;
+        int acc = 0, set = 0;
+        uint32_t acc_phase = 0;
+        for (int u = unit0; u < a.units; u += stride) {
+            const NsTile t = ns_tile<MODE>(u, a);
+            const int row0 = t.i * kTile + rank * 128 + quarter * 32, r = row0 + lane;
+            const int n0 = t.j * kTile;
+            const int n_end = MODE == NS_APPLY ? a.n : a.m;
+            const float is = a.inv_s ? __ldg(a.inv_s + t.mat) : 1.f;
+            const bool live = r < a.m;
+            const __half* arow = a.A + ((long long)t.mat * a.m + r) * a.lda;
+            const __half* hrow = a.xhi + ((long long)t.mat * a.m + r) * a.ldx;
+            const __half* lrow = a.xlo + ((long long)t.mat * a.m + r) * a.ldx;
+            // what the first 32 columns need is requested before the accumulator wait, the next 32 columns'
+            // while these are worked on
+            uint32_t pre[16], pre_lo[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pre[j] = pre_lo[j] = 0;
+            if (MODE == NS_POLY && live) ns_row32(pre, arow, n0, a.lda);
+            if (MODE == NS_APPLY && live) {
+                ns_row32(pre, hrow, n0, a.ldx);
+                if (a.xlo) ns_row32(pre_lo, lrow, n0, a.ldx);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(tfull + acc, acc_phase, abort_flag, a.status, a.wait_limit))) break;
+            tc_fence_after();
+            if (row0 < a.m) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < kTile && n0 + c0 < n_end; c0 += 32) {
+                    const int col = n0 + c0;
+                    float v[32];
+                    tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + c0), v);
+                    uint32_t out[16], low[16];
+                    if constexpr (MODE == NS_GRAM) {
+                        const float f = kABScale / (kXScale * kXScale) * is * is;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f, v[2 * j + 1] * f);
+                    } else if constexpr (MODE == NS_POLY) {
+                        const float fc = a.c / kABScale;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 x = ns_unpack_half(pre[j]);
+                            v[2 * j] = a.b * x.x + fc * v[2 * j];
+                            v[2 * j + 1] = a.b * x.y + fc * v[2 * j + 1];
+                            out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
+                        }
+                        if (a.keep_lo) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float2 h = ns_unpack_half(out[j]);
+                                low[j] = ns_pack_half(v[2 * j] - h.x, v[2 * j + 1] - h.y);
+                            }
+                        }
+                        if (live && c0 + 32 < kTile) ns_row32(pre, arow, col + 32, a.lda);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 x = ns_unpack_half(pre[j]);
+                            const float2 l = ns_unpack_half(pre_lo[j]);   // zeros where X is exact
+                            x.x += l.x * (1.f / kLoScale);
+                            x.y += l.y * (1.f / kLoScale);
+                            v[2 * j] = is * (a.a * x.x + v[2 * j] * (1.f / kABScale));
+                            v[2 * j + 1] = is * (a.a * x.y + v[2 * j + 1] * (1.f / kABScale));
+                        }
+                        if (live && c0 + 32 < kTile) {
+                            ns_row32(pre, hrow, col + 32, a.ldx);
+                            if (a.xlo) ns_row32(pre_lo, lrow, col + 32, a.ldx);
+                        }
+                        if (a.out_kind == NS_O_NONE) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
+                                const float2 h = ns_unpack_half(out[j]);
+                                low[j] = ns_pack_half((v[2 * j] - h.x) * kLoScale, (v[2 * j + 1] - h.y) * kLoScale);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                out[j] = pack_bf16x2(v[2 * j] * (1.f / kXScale), v[2 * j + 1] * (1.f / kXScale));
+                        }
+                    }
+                    if (MODE == NS_APPLY && a.out_kind == NS_O_PLAIN_FLIP) {   // a warp's 32 rows are 64 bytes of O
+                        if (live) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (col + j < a.n)
+                                    reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.n + col + j) * a.m + r] =
+                                        (uint16_t)(j & 1 ? out[j >> 1] >> 16 : out[j >> 1]);
+                        }
+                        continue;
+                    }
+                    uint8_t* box = boxes + set * kNsSet;
+                    const uint32_t sbox = smem_u32(box);
+                    if (lane == 0) bulk_wait_read<1>();   // this set's boxes of two chunks ago have been read
+                    __syncwarp();
+                    if (MODE == NS_APPLY && a.out_kind == NS_O_PLAIN) {
+                        ns_box_row(sbox, lane, out);
+                        __syncwarp();
+                        if (col + lane < a.n) {
+                            const int rows = min(32, a.m - row0);
+                            for (int q = 0; q < rows; ++q)
+                                reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.m + row0 + q) * a.n + col + lane] =
+                                    *reinterpret_cast<const uint16_t*>(box + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4) +
+                                                                       (lane & 7) * 2);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    const bool flip = MODE == NS_APPLY && a.out_kind == NS_O_BOX_FLIP;
+                    // the second box: the transpose of a tile below the diagonal, or the rounding error
+                    const bool twin = MODE != NS_APPLY && t.i != t.j;
+                    const bool with_lo = MODE != NS_GRAM && a.keep_lo;
+                    if (flip) ns_box_col(sbox, lane, out);
+                    else ns_box_row(sbox, lane, out);
+                    if (twin) ns_box_col(sbox + kNsSet / 2, lane, out);
+                    else if (with_lo) ns_box_row(sbox + kNsSet / 2, lane, low);
+                    fence_proxy_async_cta();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (flip) tma_store_3d(&tmC, box, row0, col, t.mat);
+                        else tma_store_3d(&tmC, box, col, row0, t.mat);
+                        if (twin) tma_store_3d(&tmC, box + kNsSet / 2, row0, col, t.mat);
+                        else if (with_lo) tma_store_3d(&tmD, box + kNsSet / 2, col, row0, t.mat);
+                        bulk_commit();
+                    }
+                    set ^= 1;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR && rank == 1) mbar_arrive_cluster(tempty + acc, 0);
+                else mbar_arrive(tempty + acc);
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (lane == 0) bulk_wait_all();   // the stores are complete before the CTA exits
     }
+    __syncwarp();
+    tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // no commit or release from the peer is still in flight
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kNsTile);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * kTile);
+        else tmem_dealloc(tmem, 2 * kTile);
     }
 }
 
@@ -316,7 +538,7 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     L->partial = take((size_t)N * L->parts * 4);
     L->inv_s = take((size_t)N * 4);
     L->A = take((size_t)N * L->m * L->lda * 2);
-    L->b_lo = L->m <= kNsTile;
+    L->b_lo = L->m <= 128;
     L->B = take((size_t)N * (L->b_lo ? 2 : 1) * L->m * L->lda * 2);
     L->x0 = take((size_t)N * L->m * L->ldx * 2);
     L->x1 = take((size_t)N * L->m * L->ldx * 2);
@@ -330,19 +552,51 @@ size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C) {
     return ns_layout(N, R, C, &L) ? L.total : 0;
 }
 
-// 3-D map of a batch of row-major [rows, cols] fp16 matrices with pitch ld; box 64 columns x box_rows.
-// Reads outside a matrix are zero.
-static bool ns_tmap(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t ld, int64_t N, int box_rows) {
-    return tmap_batched_f16(m, ptr, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld, (uint64_t)N, (uint32_t)box_rows);
-}
-
-template <int MODE>
-static cudaError_t ns_gemm(cudaStream_t st, const CUtensorMap& ta, const CUtensorMap& tb, const NsArgs& a, int64_t N) {
-    constexpr size_t smem = 1024 + 2 * kNsStages * kNsOperand + 256;
-    static const cudaError_t err =
-        cudaFuncSetAttribute(ns_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    return launch_pdl(ns_gemm_kernel<MODE>, (unsigned)(N * a.tiles), kNsThreads, smem, st, ta, tb, a);
+template <int MODE, bool PAIR>
+static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                           const CUtensorMap& td, const NsArgs& a) {
+    constexpr size_t smem = 1024 + 2 * kNsStages * 16384 + 8 * kNsSet + 256;
+    auto kern = ns_gemm_kernel<MODE, PAIR>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    static int most = 0;    // resident CTAs
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        most = num_sms;
+        if (attr_err == cudaSuccess && PAIR) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 2;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(num_sms / 2 * 2);
+            cfg.blockDim = dim3(kNsThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int clusters = 0;
+            attr_err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+            most = 2 * std::max(1, std::min(clusters, num_sms / 2));
+        }
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    if (!PAIR) return launch_pdl(kern, std::min(a.units, most), kNsThreads, smem, st, ta, tb, tc, td, a);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * std::min(a.units, most / 2));
+    cfg.blockDim = dim3(kNsThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, td, a);
 }
 
 template <typename T>
@@ -357,7 +611,7 @@ static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, in
 }
 
 cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int64_t N, int64_t R, int64_t C, void* O,
-                                 int steps, const float* coeffs, float eps, void* workspace, int* status,
+                                 int steps, const float* coeffs, float eps, void* workspace, int num_sms, int* status,
                                  long long wait_limit, bool withhold_loads) {
     NsLayout L;
     if (!ns_layout(N, R, C, &L)) return cudaErrorInvalidValue;
@@ -365,47 +619,65 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     cudaError_t err = g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1)
                             : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false);
     if (err != cudaSuccess) return err;
-    CUtensorMap ta, tb, tx[2], txn[2];
+    const bool flip = R > C;
+    const int64_t m = L.m, n = L.n;
+    char* X[2] = {w + L.x0, w + L.x1};
+    // operand maps: K-major boxes of 128 rows, and 64 x 64 for X as APPLY's second operand; "s": stores
+    CUtensorMap a_k, b_k, x_k[2], x_n[2], a_s, b_s, bl_s, x_s[2], lo_s, o_s;
+    bool ok = tmap_batched(&a_k, w + L.A, false, m, m, L.lda, N, 64, 128) &&
+              tmap_batched(&b_k, w + L.B, false, m, m, L.lda, L.b_lo ? 2 * N : N, 64, 128) &&
+              tmap_batched(&a_s, w + L.A, false, m, m, L.lda, N, 32, 32) &&
+              tmap_batched(&b_s, w + L.B, false, m, m, L.lda, N, 32, 32) &&
+              tmap_batched(&bl_s, w + L.B + (L.b_lo ? (size_t)N * m * L.lda * 2 : 0), false, m, m, L.lda, N, 32, 32) &&
+              tmap_batched(&lo_s, w + L.lo, false, n, m, L.ldx, N, 32, 32);
     for (int i = 0; i < 2; ++i)
-        if (!ns_tmap(&tx[i], w + (i ? L.x1 : L.x0), L.n, L.m, L.ldx, N, kNsTile) ||
-            !ns_tmap(&txn[i], w + (i ? L.x1 : L.x0), L.n, L.m, L.ldx, N, 64))
-            return cudaErrorInvalidValue;
-    if (!ns_tmap(&ta, w + L.A, L.m, L.m, L.lda, N, kNsTile) || !ns_tmap(&tb, w + L.B, L.m, L.m, L.lda, L.b_lo ? 2 * N : N, kNsTile))
-        return cudaErrorInvalidValue;
-    const int mt = (int)((L.m + kNsTile - 1) / kNsTile), nt = (int)((L.n + kNsTile - 1) / kNsTile);
+        ok = ok && tmap_batched(&x_k[i], X[i], false, n, m, L.ldx, N, 64, 128) &&
+             tmap_batched(&x_n[i], X[i], false, n, m, L.ldx, N, 64, 64) &&
+             tmap_batched(&x_s[i], X[i], false, n, m, L.ldx, N, 32, 32);
+    const bool o_box = C % 8 == 0;   // O's rows are multiples of 16 bytes
+    if (o_box) ok = ok && tmap_batched(&o_s, O, true, C, R, C, N, 32, 32);
+    if (!ok) return cudaErrorInvalidValue;
     NsArgs a{};
-    a.m = (int)L.m; a.n = (int)L.n; a.lda = (int)L.lda; a.ldx = (int)L.ldx;
+    a.m = (int)m; a.n = (int)n; a.lda = (int)L.lda; a.ldx = (int)L.ldx;
     a.batch = (int)N;
     a.status = status;
     a.wait_limit = wait_limit > 0 ? wait_limit : kWaitTimeoutCycles;
     a.withhold_loads = withhold_loads;
     a.A = reinterpret_cast<__half*>(w + L.A);
+    a.O = static_cast<__nv_bfloat16*>(O);
+    const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
+    const int tile = pair ? 256 : 128;
+    const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);
     for (int s = 0; s < steps; ++s) {
         const int cur = s & 1;
         const bool last = s + 1 == steps;
         a.a = coeffs[3 * s]; a.b = coeffs[3 * s + 1]; a.c = coeffs[3 * s + 2];
         a.inv_s = s == 0 ? reinterpret_cast<float*>(w + L.inv_s) : nullptr;
         a.tiles = mt * (mt + 1) / 2;
-        a.k_blocks = a.k_wrap = (int)((L.n + 63) / 64);
-        a.out = reinterpret_cast<__half*>(w + L.A);
-        if ((err = ns_gemm<NS_GRAM>(st, tx[cur], tx[cur], a, N)) != cudaSuccess) return err;
-        a.inv_s = nullptr;
-        a.k_blocks = a.k_wrap = (int)((L.m + 63) / 64);
-        a.out = reinterpret_cast<__half*>(w + L.B);
-        a.out_lo = L.b_lo ? a.out + (size_t)N * L.m * L.lda : nullptr;
-        if ((err = ns_gemm<NS_POLY>(st, ta, ta, a, N)) != cudaSuccess) return err;
-        a.inv_s = s == 0 ? reinterpret_cast<float*>(w + L.inv_s) : nullptr;
-        a.k_blocks = L.b_lo ? 2 * a.k_wrap : a.k_wrap;
+        a.units = (int)N * a.tiles;
+        a.k_blocks = a.k_wrap = (int)((n + 63) / 64);
+        a.keep_lo = 0;
+        a.out_kind = NS_O_NONE;
+        err = pair ? ns_gemm<NS_GRAM, true>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a)
+                   : ns_gemm<NS_GRAM, false>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a);
+        if (err != cudaSuccess) return err;
+        a.k_blocks = a.k_wrap = (int)((m + 63) / 64);
+        a.keep_lo = L.b_lo;
+        err = pair ? ns_gemm<NS_POLY, true>(st, num_sms, a_k, a_k, b_s, bl_s, a)
+                   : ns_gemm<NS_POLY, false>(st, num_sms, a_k, a_k, b_s, bl_s, a);
+        if (err != cudaSuccess) return err;
+        if (L.b_lo) a.k_blocks = 2 * a.k_wrap;
         a.tiles_n = nt;
         a.tiles = mt * nt;
-        a.xhi = reinterpret_cast<__half*>(w + (cur ? L.x1 : L.x0));
+        a.units = (int)N * a.tiles;
+        a.xhi = reinterpret_cast<__half*>(X[cur]);
         a.xlo = (s == 0 ? g_f32 && !last : !last) ? reinterpret_cast<__half*>(w + L.lo) : nullptr;
-        // the last step reads no rounding error, so the one before it keeps none
-        a.xlo_out = s + 2 < steps ? reinterpret_cast<__half*>(w + L.lo) : nullptr;
-        a.out = reinterpret_cast<__half*>(w + (cur ? L.x0 : L.x1));
-        a.O = last ? static_cast<__nv_bfloat16*>(O) : nullptr;
-        a.flip = R > C;
-        if ((err = ns_gemm<NS_APPLY>(st, tb, txn[cur], a, N)) != cudaSuccess) return err;
+        a.keep_lo = s + 2 < steps;   // the last step reads no rounding error, so the one before it keeps none
+        if (last) a.out_kind = o_box ? (flip ? NS_O_BOX_FLIP : NS_O_BOX) : (flip ? NS_O_PLAIN_FLIP : NS_O_PLAIN);
+        const CUtensorMap& out = last ? (o_box ? o_s : x_s[1 - cur]) : x_s[1 - cur];
+        err = pair ? ns_gemm<NS_APPLY, true>(st, num_sms, b_k, x_n[cur], out, lo_s, a)
+                   : ns_gemm<NS_APPLY, false>(st, num_sms, b_k, x_n[cur], out, lo_s, a);
+        if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
 }
