@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -130,6 +131,32 @@ def as_moe_tensor(t: torch.Tensor) -> MoeTensor:
     return m
 
 
+_TENSOR = struct.Struct("=Qii3q3q")     # the fields of MoeTensor; a fifth of the time of filling one
+
+
+def _arg(t):
+    """A tensor (or None) as the bytes of a moe_tensor."""
+    if t is None:
+        return None
+    shape, stride, n = t.shape, t.stride(), t.dim()
+    ptr = t.data_ptr()                  # 0 for an empty tensor
+    dt = _DT.get(t.dtype, -1)
+    if n == 2:
+        return _TENSOR.pack(ptr, dt, 2, shape[0], shape[1], 0, stride[0], stride[1], 0)
+    if n == 3:
+        return _TENSOR.pack(ptr, dt, 3, *shape, *stride)
+    pad = (0,) * max(0, 3 - n)
+    return _TENSOR.pack(ptr, dt, n, *shape[:3], *pad, *stride[:3], *pad)
+
+
+def _packed(name: str, tensors: int, rest: list):
+    """The entry point as a function of `tensors` moe_tensors given by _arg, then `rest`."""
+    fn = LIB[name]                      # a function object of its own, beside LIB.<name>
+    fn.argtypes = [ctypes.c_char_p] * tensors + rest
+    fn.restype = ctypes.c_int
+    return fn
+
+
 def make_desc(T, H, I, E, k, precision=MOE_BF16, flags=0) -> MoeDesc:
     return MoeDesc(T, H, I, E, k, precision, flags)
 
@@ -198,13 +225,14 @@ class Workspace:
         self.handle = MoeScratch()
         self.handle.data = self.buffer.data_ptr()
         self.handle.bytes = nbytes
+        self.address = ctypes.addressof(self.handle)
 
     set_wait_limit = Scratch.set_wait_limit
 
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -287,8 +315,10 @@ def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
     return int(LIB.moe_balance_workspace_bytes(T, E, B))
 
 
-def _ref(t):
-    return None if t is None else ctypes.byref(as_moe_tensor(t))
+_balance_fwd = _packed("moe_balance_fwd", 7, [ctypes.c_void_p, ctypes.c_void_p])
+_balance_bwd = _packed("moe_balance_bwd", 10, [ctypes.c_void_p])
+_orthogonalise = _packed("moe_orthogonalise", 2, [ctypes.c_int32, _P(ctypes.c_float), ctypes.c_float, ctypes.c_void_p,
+                                                  ctypes.c_void_p])
 
 
 def moe_balance_fwd(logits, topk_idx, counts, tokens, loss, workspace: Workspace, mask=None, seg_offsets=None,
@@ -296,8 +326,8 @@ def moe_balance_fwd(logits, topk_idx, counts, tokens, loss, workspace: Workspace
     """Balance loss, z-loss and per-expert counts of each segment: logits fp32 [T, E], topk_idx int32
     [T, k], mask bool or uint8 [T] or None, seg_offsets int32 [B+1] or None (B = 1) -> counts int32
     [B, E], tokens int32 [B], loss fp32 [B, 2]."""
-    rc = LIB.moe_balance_fwd(_ref(logits), _ref(topk_idx), _ref(mask), _ref(seg_offsets), _ref(counts), _ref(tokens),
-                             _ref(loss), ctypes.byref(workspace.handle), _stream_ptr(stream))
+    rc = _balance_fwd(_arg(logits), _arg(topk_idx), _arg(mask), _arg(seg_offsets), _arg(counts), _arg(tokens), _arg(loss),
+                      workspace.address, _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_fwd")
 
@@ -306,8 +336,8 @@ def moe_balance_bwd(logits, topk_idx, topk_w, dtopk_w, counts, tokens, dloss, dl
                     stream=None) -> None:
     """dlogits fp32 [T, E] of the losses (dloss fp32 [B, 2]) and, unless topk_w and dtopk_w are None,
     of the top-k weights (what moe_router_bwd gives), in one pass."""
-    rc = LIB.moe_balance_bwd(_ref(logits), _ref(topk_idx), _ref(topk_w), _ref(dtopk_w), _ref(mask), _ref(seg_offsets),
-                             _ref(counts), _ref(tokens), _ref(dloss), _ref(dlogits), _stream_ptr(stream))
+    rc = _balance_bwd(_arg(logits), _arg(topk_idx), _arg(topk_w), _arg(dtopk_w), _arg(mask), _arg(seg_offsets), _arg(counts),
+                      _arg(tokens), _arg(dloss), _arg(dlogits), _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_bwd")
 
@@ -321,12 +351,10 @@ def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, e
     coeffs: (a, b, c) for every step, a sequence of `steps` such triples, or None for the defaults."""
     co = None
     if coeffs is not None:
-        flat = [float(v) for c in coeffs for v in (c if hasattr(c, "__len__") else (c,))]
-        if len(flat) == 3:
-            flat *= max(steps, 1)
+        flat = [v for c in coeffs for v in c] if hasattr(coeffs[0], "__len__") else list(coeffs) * max(steps, 1)
         if len(flat) != 3 * steps:
             raise MoeError(ERR["MOE_ERR_SHAPE"], "moe_orthogonalise")
         co = (ctypes.c_float * len(flat))(*flat)
-    rc = LIB.moe_orthogonalise(_ref(G), _ref(O), steps, co, eps, ctypes.byref(workspace.handle), _stream_ptr(stream))
+    rc = _orthogonalise(_arg(G), _arg(O), steps, co, eps, workspace.address, _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_orthogonalise")

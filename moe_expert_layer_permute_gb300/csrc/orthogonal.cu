@@ -49,14 +49,42 @@ __device__ __forceinline__ float ns_block_sum(float v) {   // 256 threads; the s
     return v;
 }
 
-template <typename T>
+// eight consecutive values from a 16-byte boundary
+__device__ __forceinline__ void ns_val8(float* v, const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void ns_val8(float* v, const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack_bf16x2(w[j]);
+        v[2 * j] = f.x; v[2 * j + 1] = f.y;
+    }
+}
+
+// Part blockIdx.x of matrix blockIdx.y's sum of squares; VEC: the matrices are multiples of 8 elements.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const T* G, long long elems, int parts, float* partial) {
     grid_dep_wait();
-    const long long base = (long long)blockIdx.y * elems;
+    const T* g = G + (long long)blockIdx.y * elems;
     float v = 0.f;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < elems; i += (long long)parts * 256) {
-        const float g = ns_val(G, base + i);
-        v += g * g;
+    if constexpr (VEC) {
+#pragma unroll 4
+        for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < elems; i += (long long)parts * 2048) {
+            float x[8];
+            ns_val8(x, g + i);
+            float s = x[0] * x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) s += x[j] * x[j];
+            v += s;
+        }
+    } else {
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < elems; i += (long long)parts * 256) {
+            const float x = ns_val(g, i);
+            v += x * x;
+        }
     }
     v = ns_block_sum(v);
     if (threadIdx.x == 0) partial[(long long)blockIdx.y * parts + blockIdx.x] = v;
@@ -82,38 +110,111 @@ struct NsPrep {
     int flip;        // store G^T
 };
 
-// 32 x 32 tiles through shared memory, so that both the plain and the flipped copy are coalesced
-template <typename T>
-__global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a) {
-    grid_dep_wait();
-    __shared__ float tile[32][33];
-    const int mat = blockIdx.z;
+// The factor of matrix `mat`'s first X from its partial sums; `first` also records inv_s.
+__device__ __forceinline__ float ns_factor(const NsPrep& a, int mat, bool first) {
     float v = 0.f;
     for (int i = threadIdx.x; i < a.parts; i += 256) v += a.partial[(long long)mat * a.parts + i];
     float inv_s;
     const float f = ns_split(sqrtf(ns_block_sum(v)), a.eps, &inv_s) * kXScale;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.inv_s[mat] = inv_s;
+    if (first && threadIdx.x == 0) a.inv_s[mat] = inv_s;
+    return f;
+}
+__device__ __forceinline__ uint32_t ns_pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 ns_unpack_half(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+// eight values of X, and their rounding errors, at a 16-byte boundary
+__device__ __forceinline__ void ns_store8(const NsPrep& a, long long at, const float* x) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = ns_pack_half(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<uint4*>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (!a.lo) return;
+    uint32_t l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = ns_unpack_half(h[j]);
+        l[j] = ns_pack_half((x[2 * j] - f.x) * kLoScale, (x[2 * j + 1] - f.y) * kLoScale);
+    }
+    *reinterpret_cast<uint4*>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Rows of multiples of 8 elements, as they stand: X's pitch is C and the matrix one run of elements.
+constexpr int kPrepPer = 4;   // runs of eight per thread
+template <typename T>
+__global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a) {
+    grid_dep_wait();
+    const int mat = blockIdx.y;
+    const long long elems = (long long)a.R * a.C;
+    const float f = ns_factor(a, mat, blockIdx.x == 0);
+#pragma unroll
+    for (int q = 0; q < kPrepPer; ++q) {
+        const long long i = (((long long)blockIdx.x * kPrepPer + q) * 256 + threadIdx.x) * 8;
+        if (i >= elems) break;
+        float x[8];
+        ns_val8(x, G + mat * elems + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= f;
+        ns_store8(a, mat * elems + i, x);
+    }
+}
+
+// G^T for rows of multiples of 8 elements: 64 x 64 tiles through shared memory, 16 bytes a load and 32 a
+// store (the pitch is a multiple of 16 bytes; what is past R in a row's last 16 is never read).
+template <typename T>
+__global__ void __launch_bounds__(256) ns_prep_flip_kernel(const T* G, const NsPrep a) {
+    grid_dep_wait();
+    __shared__ float tile[64][65];
+    const int mat = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+    const float f = ns_factor(a, mat, blockIdx.x == 0 && blockIdx.y == 0);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = 0.f;
+        if (r0 + r < a.R && c0 + c < a.C) ns_val8(x, G + ((long long)mat * a.R + r0 + r) * a.C + c0 + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[r][c + j] = x[j] * f;
+    }
+    __syncthreads();
+    const int c = threadIdx.x & 63, r = (threadIdx.x >> 6) * 16;
+    if (c0 + c >= a.C) return;
+#pragma unroll
+    for (int q = 0; q < 16; q += 8) {
+        if (r0 + r + q >= a.R) break;
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = tile[r + q + j][c];
+        ns_store8(a, ((long long)mat * a.C + c0 + c) * a.ld + r0 + r + q, x);
+    }
+}
+
+// Any size: 32 x 32 tiles, an element at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) ns_prep_any_kernel(const T* G, const NsPrep a) {
+    grid_dep_wait();
+    __shared__ float tile[32][33];
+    const int mat = blockIdx.z, r0 = blockIdx.y * 32, c0 = blockIdx.x * 32;
+    const float f = ns_factor(a, mat, blockIdx.x == 0 && blockIdx.y == 0);
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const long long rows = a.flip ? a.C : a.R;
-    for (int r0 = blockIdx.y * 32; r0 < a.R; r0 += gridDim.y * 32) {
-        const int c0 = blockIdx.x * 32;
-        __syncthreads();
+    const int rows = a.flip ? a.C : a.R, cols = a.flip ? a.R : a.C;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            const int r = r0 + ty + j, c = c0 + tx;
-            tile[ty + j][tx] = r < a.R && c < a.C ? ns_val(G, ((long long)mat * a.R + r) * a.C + c) * f : 0.f;
-        }
-        __syncthreads();
+    for (int j = 0; j < 32; j += 8) {
+        const int r = r0 + ty + j, c = c0 + tx;
+        tile[ty + j][tx] = r < a.R && c < a.C ? ns_val(G, ((long long)mat * a.R + r) * a.C + c) * f : 0.f;
+    }
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            const int r = a.flip ? c0 + ty + j : r0 + ty + j, c = a.flip ? r0 + tx : c0 + tx;
-            if (r >= rows || c >= (a.flip ? a.R : a.C)) continue;
-            const float x = a.flip ? tile[tx][ty + j] : tile[ty + j][tx];
-            const __half h = __float2half_rn(x);
-            const long long at = ((long long)mat * rows + r) * a.ld + c;
-            a.hi[at] = h;
-            if (a.lo) a.lo[at] = __float2half_rn((x - __half2float(h)) * kLoScale);
-        }
+    for (int j = 0; j < 32; j += 8) {
+        const int r = (a.flip ? c0 : r0) + ty + j, c = (a.flip ? r0 : c0) + tx;
+        if (r >= rows || c >= cols) continue;
+        const float x = a.flip ? tile[tx][ty + j] : tile[ty + j][tx];
+        const __half h = __float2half_rn(x);
+        const long long at = ((long long)mat * rows + r) * a.ld + c;
+        a.hi[at] = h;
+        if (a.lo) a.lo[at] = __float2half_rn((x - __half2float(h)) * kLoScale);
     }
 }
 
@@ -184,11 +285,6 @@ __device__ __forceinline__ void ns_box_col(uint32_t box, int lane, const uint32_
                      : "memory");
     }
 }
-__device__ __forceinline__ uint32_t ns_pack_half(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 ns_unpack_half(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 // 32 consecutive fp16 of a row, packed; zeros past the pitch
 __device__ __forceinline__ void ns_row32(uint32_t* d, const __half* row, int col, int ld) {
 #pragma unroll
@@ -602,12 +698,19 @@ static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, 
 template <typename T>
 static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, int R, int C, float eps, char* w, bool lo) {
     float* partial = reinterpret_cast<float*>(w + L.partial);
-    cudaError_t err = launch_pdl(ns_norm_kernel<T>, dim3((unsigned)L.parts, (unsigned)L.N), 256, 0, st, G, (long long)R * C,
-                                 (int)L.parts, partial);
+    const long long elems = (long long)R * C;
+    const unsigned N = (unsigned)L.N;
+    const dim3 parts((unsigned)L.parts, N);
+    cudaError_t err = elems % 8 == 0
+                          ? launch_pdl(ns_norm_kernel<T, true>, parts, 256, 0, st, G, elems, (int)L.parts, partial)
+                          : launch_pdl(ns_norm_kernel<T, false>, parts, 256, 0, st, G, elems, (int)L.parts, partial);
     if (err != cudaSuccess) return err;
-    NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
-             reinterpret_cast<float*>(w + L.inv_s), (int)L.parts, R, C, (int)L.ldx, eps, R > C};
-    return launch_pdl(ns_prep_kernel<T>, dim3((C + 31) / 32, std::min((R + 31) / 32, 32), (unsigned)L.N), 256, 0, st, G, p);
+    const NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
+                   reinterpret_cast<float*>(w + L.inv_s), (int)L.parts, R, C, (int)L.ldx, eps, R > C};
+    if (C % 8 != 0) return launch_pdl(ns_prep_any_kernel<T>, dim3((C + 31) / 32, (R + 31) / 32, N), 256, 0, st, G, p);
+    if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 63) / 64, N), 256, 0, st, G, p);
+    return launch_pdl(ns_prep_kernel<T>, dim3((unsigned)((elems + 8 * 256 * kPrepPer - 1) / (8 * 256 * kPrepPer)), N), 256, 0, st,
+                      G, p);
 }
 
 cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int64_t N, int64_t R, int64_t C, void* O,
