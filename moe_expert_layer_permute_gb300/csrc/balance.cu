@@ -230,11 +230,7 @@ __global__ void __launch_bounds__(kFinCols * kFinGroups) balance_finish_kernel(c
     if (blocks > 1) cluster_sync();
     if (rank == 0 && threadIdx.x == 0) {
         float total = part;
-        for (int b = 1; b < blocks; ++b) {
-            float v;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(&part, b)) : "memory");
-            total += v;
-        }
+        for (int b = 1; b < blocks; ++b) total += ld_cluster_f32(cluster_addr(&part, b));
         const float inv = n > 0 ? 1.f / (float)n : 0.f;
         tokens[s] = n;
         loss[2 * s] = (float)a.E / (float)a.k * inv * inv * total;

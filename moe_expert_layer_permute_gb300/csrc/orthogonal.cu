@@ -29,7 +29,7 @@ constexpr float kXScale = 256.f, kABScale = 1024.f, kLoScale = 2048.f;
 constexpr int kNsStages = 6;
 constexpr int kNsThreads = 192;    // TMA, MMA, four epilogue warps
 constexpr int kNsSet = 4096;       // bytes of two staging boxes
-constexpr int kNormPart = 32768;   // elements of one partial sum of squares
+constexpr int kNormPart = 8192;    // elements of one partial sum of squares
 constexpr int kNormParts = 512;    // most partial sums of a matrix
 
 // ---- norms and the first X ---------------------------------------------------------------------------
@@ -613,7 +613,291 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     }
 }
 
+// ---- matrices of up to 128 rows: the whole operator in one kernel --------------------------------------
+// The products of a matrix with m <= 128 are too small to be launches of their own (17 of them took
+// 120 us at 128 x 2048).  A cluster of CTAs takes a matrix, each CTA 256 of its columns, from G to O: X in
+// fp32 registers (a thread has a row's 128 columns) and its fp16 copy in shared memory, where the rows of
+// 64 columns that GRAM reads along K are, unchanged, what APPLY reads along N.  Per step:
+//   partial A over the CTA's columns -> the cluster's sum, each CTA adding the rows it owns in the CTAs'
+//   order and sending them to all as fp16 -> A A and B in every CTA -> X of the CTA's columns.
+// B enters as fp16 and its rounding error as in the large kernels.
+constexpr int kSmallCols = 256;
+constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
+constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
+constexpr int kSmallA = 2 * 16384;   // A likewise; the partial A in fp32, later B and its rounding error
+constexpr int kSmallBytes = 1024 + kSmallX + 3 * kSmallA + 256;
+
+struct NsSmall {
+    int R, C, m, n, steps, flip;
+    float eps;
+    float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
+    __nv_bfloat16* O;
+    int* status;
+    long long wait_limit;
+    int withhold;
+};
+
+// 16-byte chunk q (of eight) of row r in a 128-byte-swizzled chunk of 64 fp16 columns
+__device__ __forceinline__ uint32_t ns_sw(int r, int q) { return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4)); }
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __restrict__ G, const NsSmall a) {
+    grid_dep_wait();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sX = smem;
+    uint8_t* sA = sX + kSmallX;
+    uint8_t* sP = sA + kSmallA;                 // fp32 [128][128], then B (fp16) and its rounding error
+    uint64_t* done = reinterpret_cast<uint64_t*>(sP + 2 * kSmallA);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    float* warp_sums = reinterpret_cast<float*>(tslot + 2);   // [8]
+    float* my_sum = warp_sums + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = (int)gridDim.x, rank = S > 1 ? (int)cluster_ctarank() : 0, mat = blockIdx.y;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int i = quarter * 32 + lane;                        // row of X
+    const int col0 = rank * kSmallCols + half * 128;          // first of the thread's 128 columns
+    if (threadIdx.x == 0) {
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(tslot, 512);
+    float x[128];
+    float sq = 0.f;
+    const T* g = G + (long long)mat * a.R * a.C;
+    if (VEC && !a.flip) {
+#pragma unroll
+        for (int j = 0; j < 128; j += 8) {
+            if (i < a.m && col0 + j < a.n) {
+                ns_val8(x + j, g + (long long)i * a.C + col0 + j);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[j + q] = 0.f;
+            }
+        }
+    } else {
+        const long long ri = a.flip ? 1 : a.C, rj = a.flip ? a.C : 1;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) x[j] = i < a.m && col0 + j < a.n ? ns_val(g, i * ri + (col0 + j) * rj) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 128; j += 8) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += x[j + q] * x[j + q];
+        sq += s;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) warp_sums[warp] = sq;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    sq = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sq += warp_sums[w];
+    if (S > 1) {
+        if (threadIdx.x == 0) *my_sum = sq;
+        cluster_sync();
+        sq = 0.f;
+        for (int b = 0; b < S; ++b) sq += ld_cluster_f32(cluster_addr(my_sum, b));
+    }
+    float is;
+    const float f = ns_split(sqrtf(sq), a.eps, &is) * kXScale;
+#pragma unroll
+    for (int j = 0; j < 128; ++j) x[j] *= f;
+
+    const uint32_t bX = smem_u32(sX), bA = smem_u32(sA), bP = smem_u32(sP);
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tA = tmem, tP = tmem + 128, tX = tmem + 256;
+    const int kx = min(4, max(0, (a.n - rank * kSmallCols + 63) / 64));   // chunks of X that hold columns
+    const int km = (a.m + 15) / 16;                                       // MMA steps along m
+    constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdX = idesc_f16(128, 256, false, true);
+    uint32_t phase = 0;
+    // every thread after its product's commit; on a wait that ran out the rest goes through without waiting,
+    // so that the CTAs of a cluster stay in step
+    auto wait_mma = [&] {
+        mbar_wait(done, phase, abort_flag, a.status, a.wait_limit);
+        phase ^= 1u;
+        __syncwarp();
+        tc_fence_after();
+    };
+    auto put_x = [&] {   // X as fp16
+#pragma unroll
+        for (int j = 0; j < 128; j += 8)
+            st_shared_v4(bX + (2 * half + j / 64) * 16384 + ns_sw(i, (j & 63) >> 3),
+                         make_uint4(ns_pack_half(x[j], x[j + 1]), ns_pack_half(x[j + 2], x[j + 3]),
+                                    ns_pack_half(x[j + 4], x[j + 5]), ns_pack_half(x[j + 6], x[j + 7])));
+    };
+    put_x();
+    for (int s = 0; s < a.steps; ++s) {
+        const float ca = a.co[3 * s], cb = a.co[3 * s + 1], cc = a.co[3 * s + 2];
+        const float fa = kABScale / (kXScale * kXScale) * is * is;
+        fence_proxy_async_all();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (threadIdx.x == 0 && !a.withhold) {
+            for (int c = 0; c < kx; ++c)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t d = sdesc_sw128(bX + c * 16384 + ks * 32, 16, 1024);
+                    mma_bf16(tA, d, d, kIdM, (c | ks) != 0);
+                }
+            mma_commit(done);
+        }
+        wait_mma();
+        if (S == 1) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v[32];
+                tmem_ld32(tA + lane_addr + 64 * half + 32 * c, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(bA + half * 16384 + ns_sw(i, 4 * c + q),
+                                 make_uint4(ns_pack_half(v[8 * q] * fa, v[8 * q + 1] * fa),
+                                            ns_pack_half(v[8 * q + 2] * fa, v[8 * q + 3] * fa),
+                                            ns_pack_half(v[8 * q + 4] * fa, v[8 * q + 5] * fa),
+                                            ns_pack_half(v[8 * q + 6] * fa, v[8 * q + 7] * fa)));
+            }
+        } else {
+            // fp32 rows of 512 bytes, their 16-byte pieces rotated by the row against bank conflicts
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v[32];
+                tmem_ld32(tA + lane_addr + 64 * half + 32 * c, v);
+                const bool any = kx > 0;   // a CTA past the last column adds nothing
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int at = 16 * half + 8 * c + q;
+                    st_shared_v4(bP + i * 512 + ((at ^ lane) << 4),
+                                 any ? make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                                  __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]))
+                                     : make_uint4(0, 0, 0, 0));
+                }
+            }
+            cluster_sync();
+            const int rows = 128 / S;
+            for (int e = threadIdx.x; e < rows * 32; e += kSmallThreads) {
+                const int r = rank * rows + (e >> 5), at = e & 31;
+                const uint32_t off = (uint32_t)(r * 512 + ((at ^ (r & 31)) << 4));
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int b = 0; b < S; ++b) {
+                    const float4 v = ld_cluster_f32x4(cluster_addr(sP, b) + off);
+                    sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+                }
+                const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
+                const uint32_t to = (uint32_t)((at >> 4) * 16384) + ns_sw(r, (at & 15) >> 1) + (at & 1) * 8;
+                for (int b = 0; b < S; ++b) st_cluster_v2(cluster_addr(sA, b) + to, h0, h1);
+            }
+            fence_proxy_async_all();
+            cluster_sync();   // A is whole in every CTA, and the partial sums have been read
+        }
+        fence_proxy_async_all();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (threadIdx.x == 0 && !a.withhold) {
+            for (int ks = 0; ks < km; ++ks) {
+                const uint64_t d = sdesc_sw128(bA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
+                mma_bf16(tP, d, d, kIdM, ks != 0);
+            }
+            mma_commit(done);
+        }
+        wait_mma();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float v[32];
+            tmem_ld32(tP + lane_addr + 64 * half + 32 * c, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t to = half * 16384 + ns_sw(i, 4 * c + q);
+                const uint4 h = ld_shared_v4(bA + to);
+                const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 A = ns_unpack_half(w[e]);
+                    const float b0 = cb * A.x + cc / kABScale * v[8 * q + 2 * e], b1 = cb * A.y + cc / kABScale * v[8 * q + 2 * e + 1];
+                    hi[e] = ns_pack_half(b0, b1);
+                    const float2 r = ns_unpack_half(hi[e]);
+                    lo[e] = ns_pack_half(b0 - r.x, b1 - r.y);
+                }
+                st_shared_v4(bP + to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            }
+        }
+        fence_proxy_async_all();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (threadIdx.x == 0 && !a.withhold) {
+            for (int part = 0; part < 2; ++part)
+                for (int ks = 0; ks < km; ++ks)
+                    mma_bf16(tX, sdesc_sw128(bP + part * kSmallA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                             sdesc_sw128(bX + ks * 2048, 16384, 1024), kIdX, (part | ks) != 0);
+            mma_commit(done);
+        }
+        wait_mma();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float v[32];
+            tmem_ld32(tX + lane_addr + 128 * half + 32 * c, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[32 * c + j] = is * (ca * x[32 * c + j] + v[j] * (1.f / kABScale));
+        }
+        is = 1.f;
+        if (s + 1 < a.steps) put_x();
+    }
+    // O as it stands (16 bytes of a row at a time) or flipped (a warp's rows are 64 consecutive bytes of O)
+    if (i < a.m) {
+        if (a.flip) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+                if (col0 + j < a.n)
+                    a.O[((long long)mat * a.n + col0 + j) * a.m + i] = __float2bfloat16_rn(x[j] * (1.f / kXScale));
+        } else {
+            __nv_bfloat16* o = a.O + ((long long)mat * a.m + i) * a.n + col0;
+#pragma unroll
+            for (int j = 0; j < 128; j += 8) {
+                if (VEC) {
+                    if (col0 + j < a.n) {
+                        constexpr float u = 1.f / kXScale;
+                        *reinterpret_cast<uint4*>(o + j) =
+                            make_uint4(pack_bf16x2(x[j] * u, x[j + 1] * u), pack_bf16x2(x[j + 2] * u, x[j + 3] * u),
+                                       pack_bf16x2(x[j + 4] * u, x[j + 5] * u), pack_bf16x2(x[j + 6] * u, x[j + 7] * u));
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (col0 + j + q < a.n) o[j + q] = __float2bfloat16_rn(x[j + q] * (1.f / kXScale));
+                }
+            }
+        }
+    }
+    // an MMA whose wait ran out may still be at work (bounded): it ends before its memory is given up
+    if (*abort_flag && threadIdx.x == 0 && !a.withhold) ns_wait_drain(done, phase ^ 1u);
+    tc_fence_before();
+    __syncthreads();
+    if (S > 1) cluster_sync();   // no CTA's shared memory is read or written any more
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---- launches --------------------------------------------------------------------------------------
+// CTAs of a cluster for a matrix that ns_small_kernel takes, 0 for one that it does not
+static int ns_small_cluster(int64_t m, int64_t n) {
+    if (m > 128) return 0;
+    int S = 1;
+    while (S * kSmallCols < n) S *= 2;
+    return S <= 8 ? S : 0;
+}
+
 struct NsLayout {
     int64_t N, m, n, lda, ldx, parts;
     bool b_lo;
@@ -631,6 +915,10 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
     take(256);   // status word
+    if (ns_small_cluster(L->m, L->n)) {
+        L->total = o;
+        return true;
+    }
     L->partial = take((size_t)N * L->parts * 4);
     L->inv_s = take((size_t)N * 4);
     L->A = take((size_t)N * L->m * L->lda * 2);
@@ -695,6 +983,28 @@ static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, 
     return cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, td, a);
 }
 
+template <typename T, bool VEC>
+static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsSmall& a) {
+    auto kern = ns_small_kernel<T, VEC>;
+    static const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = S;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(S, N);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = kSmallBytes;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, G, a);
+}
+
 template <typename T>
 static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, int R, int C, float eps, char* w, bool lo) {
     float* partial = reinterpret_cast<float*>(w + L.partial);
@@ -718,6 +1028,18 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
                                  long long wait_limit, bool withhold_loads) {
     NsLayout L;
     if (!ns_layout(N, R, C, &L)) return cudaErrorInvalidValue;
+    if (const int S = ns_small_cluster(L.m, L.n)) {
+        NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, steps, R > C, eps};
+        std::copy(coeffs, coeffs + 3 * steps, a.co);
+        a.O = static_cast<__nv_bfloat16*>(O);
+        a.status = status;
+        a.wait_limit = wait_limit > 0 ? wait_limit : kWaitTimeoutCycles;
+        a.withhold = withhold_loads;
+        const auto* gf = static_cast<const float*>(G);
+        const auto* gb = static_cast<const __nv_bfloat16*>(G);
+        if (C % 8 == 0) return g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a) : ns_small<__nv_bfloat16, true>(st, gb, S, (int)N, a);
+        return g_f32 ? ns_small<float, false>(st, gf, S, (int)N, a) : ns_small<__nv_bfloat16, false>(st, gb, S, (int)N, a);
+    }
     char* w = static_cast<char*>(workspace);
     cudaError_t err = g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1)
                             : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false);
