@@ -26,9 +26,11 @@
 namespace moe {
 
 constexpr float kXScale = 256.f, kABScale = 1024.f, kLoScale = 2048.f;
-constexpr int kNsStages = 6;
+constexpr int kNsStages = 5;
 constexpr int kNsThreads = 192;    // TMA, MMA, four epilogue warps
-constexpr int kNsSet = 4096;       // bytes of two staging boxes
+constexpr int kNsSlots = 4;        // pairs of boxes per epilogue warp
+constexpr int kNsBox = 2048;       // a box: 32 rows x 32 16-bit values
+constexpr int kNsSmem = 1024 + kNsStages * 32768 + 4 * kNsSlots * 2 * kNsBox + 512;
 constexpr int kNormPart = 8192;    // elements of one partial sum of squares
 constexpr int kNormParts = 512;    // most partial sums of a matrix
 
@@ -233,9 +235,7 @@ struct NsArgs {
     int batch;                   // N: matrix N + i of the B array is the rounding error of matrix i's B
     float a, b, c;
     const float* inv_s;          // [N] in the first step, null after it
-    const __half* A;             // POLY: reads its tile of A
-    const __half* xhi;           // APPLY: this X
-    const __half* xlo;           // APPLY: its rounding error (null: exact)
+    int xlo;                     // APPLY: X has a rounding error (else it is exact, or the step takes none)
     int keep_lo;                 // POLY: store B's rounding error; APPLY: the next X's
     int out_kind;                // NsOut
     __nv_bfloat16* O;
@@ -285,17 +285,43 @@ __device__ __forceinline__ void ns_box_col(uint32_t box, int lane, const uint32_
                      : "memory");
     }
 }
-// 32 consecutive fp16 of a row, packed; zeros past the pitch
-__device__ __forceinline__ void ns_row32(uint32_t* d, const __half* row, int col, int ld) {
+__device__ __forceinline__ void ns_box_read(uint32_t* v, uint32_t box, int lane) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint4 v = col + 8 * q < ld ? *reinterpret_cast<const uint4*>(row + col + 8 * q) : make_uint4(0, 0, 0, 0);
-        d[4 * q] = v.x; d[4 * q + 1] = v.y; d[4 * q + 2] = v.z; d[4 * q + 3] = v.w;
+        const uint4 w = ld_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+        v[4 * q] = w.x; v[4 * q + 1] = w.y; v[4 * q + 2] = w.z; v[4 * q + 3] = w.w;
     }
 }
 
+// The chunks of 32 columns that an epilogue warp works through, tile after tile.
+template <int MODE, int TILE>
+struct NsChunks {
+    int u, stride, rank, quarter;
+    NsTile t;
+    int row0, n0, c, cols;   // the warp's first row, the tile's first column, the chunk, the columns to cover
+    __device__ __forceinline__ void tile(const NsArgs& a) {
+        t = ns_tile<MODE>(u, a);
+        row0 = t.i * TILE + rank * 128 + quarter * 32;
+        n0 = t.j * TILE;
+        c = 0;
+        cols = row0 < a.m ? min(TILE, (MODE == NS_APPLY ? a.n : a.m) - n0) : 0;
+    }
+    // moves over tiles without a chunk for this warp; false past the last unit
+    __device__ __forceinline__ bool settle(const NsArgs& a) {
+        while (u < a.units && c >= cols) {
+            u += stride;
+            if (u < a.units) tile(a);
+        }
+        return u < a.units;
+    }
+};
+
 // Persistent blocks walk the batch's tiles.  Warp 0 loads, warp 1 issues the MMAs, four warps store (see
-// gemm.cu for the scheme): six stages of 32 KB, two accumulators, waits bounded.
+// gemm.cu for the scheme): five stages of 32 KB, two accumulators, waits bounded.  What an epilogue needs
+// besides its accumulator (POLY: A; APPLY: X and its rounding error) comes by TMA into the warp's ring of
+// four slots, three chunks of 32 columns ahead and across tiles: with loads into registers a chunk ahead
+// APPLY waited on memory (256 x 768 x 2048: 851 us a launch).  The results replace it in place and leave
+// by TMA from there.
 //   PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each holding 128 rows of the first operand and
 //   half of the second; otherwise one CTA computes 128 x 128.
 // GRAM and POLY are symmetric: tiles of the lower triangle alone, and those below the diagonal are stored
@@ -306,6 +332,7 @@ __device__ __forceinline__ void ns_row32(uint32_t* d, const __half* row, int col
 template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(kNsThreads, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmL,
                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD, const NsArgs a) {
     grid_dep_wait();
     constexpr int kTile = PAIR ? 256 : 128;      // rows and columns of a unit's tile
@@ -316,13 +343,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + kNsStages * kOperand;
-    uint8_t* sOut = sB + kNsStages * kOperand;   // per epilogue warp two sets of two boxes
-    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 4 * 2 * kNsSet);
+    uint8_t* sBox = sB + kNsStages * kOperand;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sBox + 4 * kNsSlots * 2 * kNsBox);
     uint64_t* empty = full + kNsStages;
     uint64_t* tfull = empty + kNsStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* slot_full = drain + 1;             // [4][kNsSlots]
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(slot_full + 4 * kNsSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
@@ -338,6 +366,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             mbar_init(tempty + b, (PAIR ? 2 : 1) * 4);
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < 4 * kNsSlots; ++i) mbar_init(slot_full + i, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -464,131 +493,155 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     } else {
         const int quarter = warp & 3;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        uint8_t* boxes = sOut + quarter * 2 * kNsSet;
-        int acc = 0, set = 0;
+        uint8_t* boxes = sBox + quarter * kNsSlots * 2 * kNsBox;
+        uint64_t* box_full = slot_full + quarter * kNsSlots;
+        constexpr bool kLoads = MODE != NS_GRAM;
+        const bool two = MODE == NS_APPLY && a.xlo;
+        using Chunks = NsChunks<MODE, kTile>;
+        Chunks cur{unit0, stride, rank, quarter}, ahead{unit0, stride, rank, quarter};
+        if (unit0 < a.units) {
+            cur.tile(a);
+            ahead.tile(a);
+        }
+        uint32_t loaded = 0, used = 0;   // chunks requested and worked on; slot: mod kNsSlots
+        auto request = [&] {             // the next chunk's boxes (lane 0)
+            if (!ahead.settle(a)) return;
+            uint64_t* bar = box_full + loaded % kNsSlots;
+            uint8_t* dst = boxes + (loaded % kNsSlots) * 2 * kNsBox;
+            mbar_arrive_expect_tx(bar, two ? 2 * kNsBox : kNsBox);
+            tma_load_3d(dst, &tmX, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
+            if (two) tma_load_3d(dst + kNsBox, &tmL, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
+            ahead.c += 32;
+            ++loaded;
+        };
+        if (kLoads && lane == 0 && !a.withhold_loads)
+            for (int i = 0; i < kNsSlots - 1; ++i) request();
+        int acc = 0;
         uint32_t acc_phase = 0;
-        for (int u = unit0; u < a.units; u += stride) {
-            const NsTile t = ns_tile<MODE>(u, a);
-            const int row0 = t.i * kTile + rank * 128 + quarter * 32, r = row0 + lane;
-            const int n0 = t.j * kTile;
-            const int n_end = MODE == NS_APPLY ? a.n : a.m;
+        bool ok = true;
+        for (; cur.u < a.units && ok; cur.u += stride) {
+            cur.tile(a);
+            const NsTile t = cur.t;
+            const int row0 = cur.row0, r = row0 + lane;
             const float is = a.inv_s ? __ldg(a.inv_s + t.mat) : 1.f;
-            const bool live = r < a.m;
-            const __half* arow = a.A + ((long long)t.mat * a.m + r) * a.lda;
-            const __half* hrow = a.xhi + ((long long)t.mat * a.m + r) * a.ldx;
-            const __half* lrow = a.xlo + ((long long)t.mat * a.m + r) * a.ldx;
-            // what the first 32 columns need is requested before the accumulator wait, the next 32 columns'
-            // while these are worked on
-            uint32_t pre[16], pre_lo[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pre[j] = pre_lo[j] = 0;
-            if (MODE == NS_POLY && live) ns_row32(pre, arow, n0, a.lda);
-            if (MODE == NS_APPLY && live) {
-                ns_row32(pre, hrow, n0, a.ldx);
-                if (a.xlo) ns_row32(pre_lo, lrow, n0, a.ldx);
-            }
             if (!__all_sync(0xffffffffu, mbar_wait(tfull + acc, acc_phase, abort_flag, a.status, a.wait_limit))) break;
             tc_fence_after();
-            if (row0 < a.m) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < kTile && n0 + c0 < n_end; c0 += 32) {
-                    const int col = n0 + c0;
-                    float v[32];
-                    tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + c0), v);
-                    uint32_t out[16], low[16];
-                    if constexpr (MODE == NS_GRAM) {
-                        const float f = kABScale / (kXScale * kXScale) * is * is;
+            for (int c0 = 0; c0 < cur.cols; c0 += 32, ++used) {
+                const int col = cur.n0 + c0;
+                uint8_t* box = boxes + (used % kNsSlots) * 2 * kNsBox;
+                const uint32_t sbox = smem_u32(box);
+                float v[32];
+                uint32_t out[16], low[16];
+                tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + c0), v);
+                if (kLoads) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(box_full + used % kNsSlots, (used / kNsSlots) & 1, abort_flag,
+                                                           a.status, a.wait_limit));
+                    if (!ok) break;
+                } else {
+                    if (lane == 0) bulk_wait_read<kNsSlots - 1>();   // the slot's last store has read it
+                    __syncwarp();
+                }
+                if constexpr (MODE == NS_GRAM) {
+                    const float f = kABScale / (kXScale * kXScale) * is * is;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f, v[2 * j + 1] * f);
-                    } else if constexpr (MODE == NS_POLY) {
-                        const float fc = a.c / kABScale;
+                    for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f, v[2 * j + 1] * f);
+                } else if constexpr (MODE == NS_POLY) {
+                    ns_box_read(out, sbox, lane);
+                    const float fc = a.c / kABScale;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 x = ns_unpack_half(out[j]);
+                        v[2 * j] = a.b * x.x + fc * v[2 * j];
+                        v[2 * j + 1] = a.b * x.y + fc * v[2 * j + 1];
+                        out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
+                    }
+                    if (a.keep_lo) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float2 x = ns_unpack_half(pre[j]);
-                            v[2 * j] = a.b * x.x + fc * v[2 * j];
-                            v[2 * j + 1] = a.b * x.y + fc * v[2 * j + 1];
-                            out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
+                            const float2 h = ns_unpack_half(out[j]);
+                            low[j] = ns_pack_half(v[2 * j] - h.x, v[2 * j + 1] - h.y);
                         }
+                    }
+                } else {
+                    ns_box_read(out, sbox, lane);
+                    const float fd = is * (1.f / kABScale), fx = is * a.a;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 x = ns_unpack_half(out[j]);
+                        v[2 * j] = fx * x.x + fd * v[2 * j];
+                        v[2 * j + 1] = fx * x.y + fd * v[2 * j + 1];
+                    }
+                    if (two) {
+                        ns_box_read(low, sbox + kNsBox, lane);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 x = ns_unpack_half(low[j]);
+                            v[2 * j] += fx * (1.f / kLoScale) * x.x;
+                            v[2 * j + 1] += fx * (1.f / kLoScale) * x.y;
+                        }
+                    }
+                    if (a.out_kind == NS_O_NONE) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
                         if (a.keep_lo) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 const float2 h = ns_unpack_half(out[j]);
-                                low[j] = ns_pack_half(v[2 * j] - h.x, v[2 * j + 1] - h.y);
-                            }
-                        }
-                        if (live && c0 + 32 < kTile) ns_row32(pre, arow, col + 32, a.lda);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 x = ns_unpack_half(pre[j]);
-                            const float2 l = ns_unpack_half(pre_lo[j]);   // zeros where X is exact
-                            x.x += l.x * (1.f / kLoScale);
-                            x.y += l.y * (1.f / kLoScale);
-                            v[2 * j] = is * (a.a * x.x + v[2 * j] * (1.f / kABScale));
-                            v[2 * j + 1] = is * (a.a * x.y + v[2 * j + 1] * (1.f / kABScale));
-                        }
-                        if (live && c0 + 32 < kTile) {
-                            ns_row32(pre, hrow, col + 32, a.ldx);
-                            if (a.xlo) ns_row32(pre_lo, lrow, col + 32, a.ldx);
-                        }
-                        if (a.out_kind == NS_O_NONE) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
-                                const float2 h = ns_unpack_half(out[j]);
                                 low[j] = ns_pack_half((v[2 * j] - h.x) * kLoScale, (v[2 * j + 1] - h.y) * kLoScale);
                             }
-                        } else {
+                        }
+                    } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                out[j] = pack_bf16x2(v[2 * j] * (1.f / kXScale), v[2 * j + 1] * (1.f / kXScale));
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            out[j] = pack_bf16x2(v[2 * j] * (1.f / kXScale), v[2 * j + 1] * (1.f / kXScale));
                     }
-                    if (MODE == NS_APPLY && a.out_kind == NS_O_PLAIN_FLIP) {   // a warp's 32 rows are 64 bytes of O
-                        if (live) {
+                }
+                const bool flip = MODE == NS_APPLY && a.out_kind == NS_O_BOX_FLIP;
+                const bool plain = MODE == NS_APPLY && a.out_kind == NS_O_PLAIN;
+                const bool plain_flip = MODE == NS_APPLY && a.out_kind == NS_O_PLAIN_FLIP;
+                // the second box: the transpose of a tile below the diagonal, or the rounding error
+                const bool twin = MODE != NS_APPLY && t.i != t.j;
+                const bool with_lo = MODE != NS_GRAM && a.keep_lo;
+                __syncwarp();   // every lane has read the boxes
+                if (plain_flip) {   // a warp's 32 rows are 64 consecutive bytes of O
+                    if (r < a.m) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (col + j < a.n)
-                                    reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.n + col + j) * a.m + r] =
-                                        (uint16_t)(j & 1 ? out[j >> 1] >> 16 : out[j >> 1]);
-                        }
-                        continue;
+                        for (int j = 0; j < 32; ++j)
+                            if (col + j < a.n)
+                                reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.n + col + j) * a.m + r] =
+                                    (uint16_t)(j & 1 ? out[j >> 1] >> 16 : out[j >> 1]);
                     }
-                    uint8_t* box = boxes + set * kNsSet;
-                    const uint32_t sbox = smem_u32(box);
-                    if (lane == 0) bulk_wait_read<1>();   // this set's boxes of two chunks ago have been read
-                    __syncwarp();
-                    if (MODE == NS_APPLY && a.out_kind == NS_O_PLAIN) {
-                        ns_box_row(sbox, lane, out);
-                        __syncwarp();
-                        if (col + lane < a.n) {
-                            const int rows = min(32, a.m - row0);
-                            for (int q = 0; q < rows; ++q)
-                                reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.m + row0 + q) * a.n + col + lane] =
-                                    *reinterpret_cast<const uint16_t*>(box + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4) +
-                                                                       (lane & 7) * 2);
-                        }
-                        __syncwarp();
-                        continue;
-                    }
-                    const bool flip = MODE == NS_APPLY && a.out_kind == NS_O_BOX_FLIP;
-                    // the second box: the transpose of a tile below the diagonal, or the rounding error
-                    const bool twin = MODE != NS_APPLY && t.i != t.j;
-                    const bool with_lo = MODE != NS_GRAM && a.keep_lo;
+                } else {
                     if (flip) ns_box_col(sbox, lane, out);
                     else ns_box_row(sbox, lane, out);
-                    if (twin) ns_box_col(sbox + kNsSet / 2, lane, out);
-                    else if (with_lo) ns_box_row(sbox + kNsSet / 2, lane, low);
-                    fence_proxy_async_cta();
+                    if (twin) ns_box_col(sbox + kNsBox, lane, out);
+                    else if (with_lo) ns_box_row(sbox + kNsBox, lane, low);
+                }
+                if (plain) {   // 64 consecutive bytes of a row of O at a time
                     __syncwarp();
-                    if (lane == 0) {
+                    if (col + lane < a.n) {
+                        const int rows = min(32, a.m - row0);
+                        for (int q = 0; q < rows; ++q)
+                            reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.m + row0 + q) * a.n + col + lane] =
+                                *reinterpret_cast<const uint16_t*>(box + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4) +
+                                                                   (lane & 7) * 2);
+                    }
+                }
+                fence_proxy_async_cta();
+                __syncwarp();
+                if (lane == 0) {
+                    if (!plain && !plain_flip) {
                         if (flip) tma_store_3d(&tmC, box, row0, col, t.mat);
                         else tma_store_3d(&tmC, box, col, row0, t.mat);
-                        if (twin) tma_store_3d(&tmC, box + kNsSet / 2, row0, col, t.mat);
-                        else if (with_lo) tma_store_3d(&tmD, box + kNsSet / 2, col, row0, t.mat);
-                        bulk_commit();
+                        if (twin) tma_store_3d(&tmC, box + kNsBox, row0, col, t.mat);
+                        else if (with_lo) tma_store_3d(&tmD, box + kNsBox, col, row0, t.mat);
                     }
-                    set ^= 1;
+                    bulk_commit();
+                    if (kLoads && !a.withhold_loads) {
+                        bulk_wait_read<1>();   // the chunk before this one has left its slot, the next to be filled
+                        request();
+                    }
                 }
             }
             tc_fence_before();
@@ -600,7 +653,11 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
-        if (lane == 0) bulk_wait_all();   // the stores are complete before the CTA exits
+        if (lane == 0) {
+            bulk_wait_all();   // the stores are complete before the CTA exits, and (bounded) the loads
+            for (uint32_t i = loaded > kNsSlots ? loaded - kNsSlots : 0; i < loaded; ++i)
+                ns_wait_drain(box_full + i % kNsSlots, (i / kNsSlots) & 1);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -937,9 +994,9 @@ size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C) {
 }
 
 template <int MODE, bool PAIR>
-static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
-                           const CUtensorMap& td, const NsArgs& a) {
-    constexpr size_t smem = 1024 + 2 * kNsStages * 16384 + 8 * kNsSet + 256;
+static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tx,
+                           const CUtensorMap& tl, const CUtensorMap& tc, const CUtensorMap& td, const NsArgs& a) {
+    constexpr size_t smem = kNsSmem;
     auto kern = ns_gemm_kernel<MODE, PAIR>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
@@ -965,7 +1022,7 @@ static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, 
         }
     });
     if (attr_err != cudaSuccess) return attr_err;
-    if (!PAIR) return launch_pdl(kern, std::min(a.units, most), kNsThreads, smem, st, ta, tb, tc, td, a);
+    if (!PAIR) return launch_pdl(kern, std::min(a.units, most), kNsThreads, smem, st, ta, tb, tx, tl, tc, td, a);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -980,7 +1037,7 @@ static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, 
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tc, td, a);
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tx, tl, tc, td, a);
 }
 
 template <typename T, bool VEC>
@@ -1047,7 +1104,8 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     const bool flip = R > C;
     const int64_t m = L.m, n = L.n;
     char* X[2] = {w + L.x0, w + L.x1};
-    // operand maps: K-major boxes of 128 rows, and 64 x 64 for X as APPLY's second operand; "s": stores
+    // operand maps: K-major boxes of 128 rows, and 64 x 64 for X as APPLY's second operand; "s": the
+    // epilogues' boxes
     CUtensorMap a_k, b_k, x_k[2], x_n[2], a_s, b_s, bl_s, x_s[2], lo_s, o_s;
     bool ok = tmap_batched(&a_k, w + L.A, false, m, m, L.lda, N, 64, 128) &&
               tmap_batched(&b_k, w + L.B, false, m, m, L.lda, L.b_lo ? 2 * N : N, 64, 128) &&
@@ -1068,7 +1126,6 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     a.status = status;
     a.wait_limit = wait_limit > 0 ? wait_limit : kWaitTimeoutCycles;
     a.withhold_loads = withhold_loads;
-    a.A = reinterpret_cast<__half*>(w + L.A);
     a.O = static_cast<__nv_bfloat16*>(O);
     const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
     const int tile = pair ? 256 : 128;
@@ -1083,25 +1140,24 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         a.k_blocks = a.k_wrap = (int)((n + 63) / 64);
         a.keep_lo = 0;
         a.out_kind = NS_O_NONE;
-        err = pair ? ns_gemm<NS_GRAM, true>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a)
-                   : ns_gemm<NS_GRAM, false>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a);
+        err = pair ? ns_gemm<NS_GRAM, true>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a_s, a_s, a)
+                   : ns_gemm<NS_GRAM, false>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a_s, a_s, a);
         if (err != cudaSuccess) return err;
         a.k_blocks = a.k_wrap = (int)((m + 63) / 64);
         a.keep_lo = L.b_lo;
-        err = pair ? ns_gemm<NS_POLY, true>(st, num_sms, a_k, a_k, b_s, bl_s, a)
-                   : ns_gemm<NS_POLY, false>(st, num_sms, a_k, a_k, b_s, bl_s, a);
+        err = pair ? ns_gemm<NS_POLY, true>(st, num_sms, a_k, a_k, a_s, a_s, b_s, bl_s, a)
+                   : ns_gemm<NS_POLY, false>(st, num_sms, a_k, a_k, a_s, a_s, b_s, bl_s, a);
         if (err != cudaSuccess) return err;
         if (L.b_lo) a.k_blocks = 2 * a.k_wrap;
         a.tiles_n = nt;
         a.tiles = mt * nt;
         a.units = (int)N * a.tiles;
-        a.xhi = reinterpret_cast<__half*>(X[cur]);
-        a.xlo = (s == 0 ? g_f32 && !last : !last) ? reinterpret_cast<__half*>(w + L.lo) : nullptr;
+        a.xlo = (s == 0 ? g_f32 && !last : !last);
         a.keep_lo = s + 2 < steps;   // the last step reads no rounding error, so the one before it keeps none
         if (last) a.out_kind = o_box ? (flip ? NS_O_BOX_FLIP : NS_O_BOX) : (flip ? NS_O_PLAIN_FLIP : NS_O_PLAIN);
         const CUtensorMap& out = last ? (o_box ? o_s : x_s[1 - cur]) : x_s[1 - cur];
-        err = pair ? ns_gemm<NS_APPLY, true>(st, num_sms, b_k, x_n[cur], out, lo_s, a)
-                   : ns_gemm<NS_APPLY, false>(st, num_sms, b_k, x_n[cur], out, lo_s, a);
+        err = pair ? ns_gemm<NS_APPLY, true>(st, num_sms, b_k, x_n[cur], x_s[cur], lo_s, out, lo_s, a)
+                   : ns_gemm<NS_APPLY, false>(st, num_sms, b_k, x_n[cur], x_s[cur], lo_s, out, lo_s, a);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
