@@ -26,11 +26,12 @@
 namespace moe {
 
 constexpr float kXScale = 256.f, kABScale = 1024.f, kLoScale = 2048.f;
-constexpr int kNsStages = 5;
-constexpr int kNsThreads = 192;    // TMA, MMA, four epilogue warps
-constexpr int kNsSlots = 4;        // pairs of boxes per epilogue warp
+constexpr int kNsStages = 4;
+constexpr int kNsEpi = 8;          // epilogue warps: two for each quarter of the TMEM lanes, on alternate columns
+constexpr int kNsThreads = 64 + 32 * kNsEpi;
+constexpr int kNsSlots = 3;        // pairs of boxes per epilogue warp
 constexpr int kNsBox = 2048;       // a box: 32 rows x 32 16-bit values
-constexpr int kNsSmem = 1024 + kNsStages * 32768 + 4 * kNsSlots * 2 * kNsBox + 512;
+constexpr int kNsSmem = 1024 + kNsStages * 32768 + kNsEpi * kNsSlots * 2 * kNsBox + 512;
 constexpr int kNormPart = 8192;    // elements of one partial sum of squares
 constexpr int kNormParts = 512;    // most partial sums of a matrix
 
@@ -293,17 +294,17 @@ __device__ __forceinline__ void ns_box_read(uint32_t* v, uint32_t box, int lane)
     }
 }
 
-// The chunks of 32 columns that an epilogue warp works through, tile after tile.
+// The chunks of 32 columns that an epilogue warp works through (every second one), tile after tile.
 template <int MODE, int TILE>
 struct NsChunks {
-    int u, stride, rank, quarter;
+    int u, stride, rank, quarter, half;
     NsTile t;
     int row0, n0, c, cols;   // the warp's first row, the tile's first column, the chunk, the columns to cover
     __device__ __forceinline__ void tile(const NsArgs& a) {
         t = ns_tile<MODE>(u, a);
         row0 = t.i * TILE + rank * 128 + quarter * 32;
         n0 = t.j * TILE;
-        c = 0;
+        c = 32 * half;
         cols = row0 < a.m ? min(TILE, (MODE == NS_APPLY ? a.n : a.m) - n0) : 0;
     }
     // moves over tiles without a chunk for this warp; false past the last unit
@@ -316,10 +317,10 @@ struct NsChunks {
     }
 };
 
-// Persistent blocks walk the batch's tiles.  Warp 0 loads, warp 1 issues the MMAs, four warps store (see
-// gemm.cu for the scheme): five stages of 32 KB, two accumulators, waits bounded.  What an epilogue needs
+// Persistent blocks walk the batch's tiles.  Warp 0 loads, warp 1 issues the MMAs, eight warps store (see
+// gemm.cu for the scheme): four stages of 32 KB, two accumulators, waits bounded.  What an epilogue needs
 // besides its accumulator (POLY: A; APPLY: X and its rounding error) comes by TMA into the warp's ring of
-// four slots, three chunks of 32 columns ahead and across tiles: with loads into registers a chunk ahead
+// three slots, two chunks of 32 columns ahead and across tiles: with loads into registers a chunk ahead
 // APPLY waited on memory (256 x 768 x 2048: 851 us a launch).  The results replace it in place and leave
 // by TMA from there.
 //   PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each holding 128 rows of the first operand and
@@ -344,13 +345,13 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     uint8_t* sA = smem;
     uint8_t* sB = sA + kNsStages * kOperand;
     uint8_t* sBox = sB + kNsStages * kOperand;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sBox + 4 * kNsSlots * 2 * kNsBox);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sBox + kNsEpi * kNsSlots * 2 * kNsBox);
     uint64_t* empty = full + kNsStages;
     uint64_t* tfull = empty + kNsStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint64_t* slot_full = drain + 1;             // [4][kNsSlots]
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(slot_full + 4 * kNsSlots);
+    uint64_t* slot_full = drain + 1;             // [kNsEpi][kNsSlots]
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(slot_full + kNsEpi * kNsSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
@@ -363,10 +364,10 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull + b, 1);
-            mbar_init(tempty + b, (PAIR ? 2 : 1) * 4);
+            mbar_init(tempty + b, (PAIR ? 2 : 1) * kNsEpi);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < 4 * kNsSlots; ++i) mbar_init(slot_full + i, 1);
+        for (int i = 0; i < kNsEpi * kNsSlots; ++i) mbar_init(slot_full + i, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -491,14 +492,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             }
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        uint8_t* boxes = sBox + quarter * kNsSlots * 2 * kNsBox;
-        uint64_t* box_full = slot_full + quarter * kNsSlots;
+        uint8_t* boxes = sBox + (warp - 2) * kNsSlots * 2 * kNsBox;
+        uint64_t* box_full = slot_full + (warp - 2) * kNsSlots;
         constexpr bool kLoads = MODE != NS_GRAM;
         const bool two = MODE == NS_APPLY && a.xlo;
         using Chunks = NsChunks<MODE, kTile>;
-        Chunks cur{unit0, stride, rank, quarter}, ahead{unit0, stride, rank, quarter};
+        Chunks cur{unit0, stride, rank, quarter, half}, ahead{unit0, stride, rank, quarter, half};
         if (unit0 < a.units) {
             cur.tile(a);
             ahead.tile(a);
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             mbar_arrive_expect_tx(bar, two ? 2 * kNsBox : kNsBox);
             tma_load_3d(dst, &tmX, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
             if (two) tma_load_3d(dst + kNsBox, &tmL, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
-            ahead.c += 32;
+            ahead.c += 64;
             ++loaded;
         };
         if (kLoads && lane == 0 && !a.withhold_loads)
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(tfull + acc, acc_phase, abort_flag, a.status, a.wait_limit))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < cur.cols; c0 += 32, ++used) {
+            for (int c0 = 32 * half; c0 < cur.cols; c0 += 64, ++used) {
                 const int col = cur.n0 + c0;
                 uint8_t* box = boxes + (used % kNsSlots) * 2 * kNsBox;
                 const uint32_t sbox = smem_u32(box);
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 uint32_t out[16], low[16];
                 tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + c0), v);
                 if (kLoads) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(box_full + used % kNsSlots, (used / kNsSlots) & 1, abort_flag,
+                    ok = __all_sync(0xffffffffu, mbar_wait(box_full + used % kNsSlots, used / kNsSlots & 1, abort_flag,
                                                            a.status, a.wait_limit));
                     if (!ok) break;
                 } else {
