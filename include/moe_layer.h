@@ -251,7 +251,7 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
  * `workspace`: a zeroed moe_scratch handle of at least moe_orthogonalise_workspace_bytes(N, R, C)
  * bytes, 256-byte aligned, whose first four bytes (the status word that moe_read_device_status
  * returns) the caller has set to zero; its desc is not read, moe_set_wait_limit applies.
- * N <= 65535, R, C <= 32768, N * ceil(R/128) * ceil(C/128) < 2^31, steps <= 16, eps in [1e-20, 1],
+ * N <= 65535, R, C <= 32768, N * ceil(R/128) * ceil(C/128) < 2^24, steps <= 16, eps in [1e-20, 1],
  * coefficients in [-16, 16]: MOE_ERR_UNSUPPORTED outside; N = 0 launches nothing. */
 #define MOE_ORTHOGONALISE_MAX_STEPS 16
 size_t moe_orthogonalise_workspace_bytes(int64_t N, int64_t R, int64_t C);   /* 0: outside the limits */

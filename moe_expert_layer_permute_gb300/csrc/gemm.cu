@@ -1050,17 +1050,16 @@ static bool tmap_2d_sw64(CUtensorMap* m, const void* ptr, int esize, uint64_t in
 }
 
 bool tmap_batched(CUtensorMap* m, const void* ptr, bool bf16, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t batch,
-                  uint32_t box_cols, uint32_t box_rows) {
+                  uint32_t box_rows) {
     EncodeTiledFn enc = get_encode();
     if (!enc) return false;
     const cuuint64_t dims[3] = {cols, rows, batch};
     const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
-    const cuuint32_t box[3] = {box_cols, box_rows, 1};
+    const cuuint32_t box[3] = {64, box_rows, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
-               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Two-SM MMAs (256 x 256 per CTA pair, each SM holding half of every B tile) for the BF16 weight

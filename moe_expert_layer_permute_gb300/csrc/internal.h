@@ -113,10 +113,10 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
                                  int steps, const float* coeffs, float eps, void* workspace, int num_sms, int* status,
                                  long long wait_limit, bool withhold_loads);
 // 3-D tensor map over a batch of row-major fp16 or bf16 matrices [rows, cols] of pitch ld (a multiple of 8
-// elements), box {box_cols, box_rows, 1}; box_cols 64 (128-byte swizzle) or 32 (64-byte swizzle).
-// Outside a matrix, reads are zero and stores are dropped (gemm.cu)
+// elements), box {64, box_rows, 1}, 128-byte swizzle; outside a matrix, reads are zero and stores are
+// dropped (gemm.cu)
 bool tmap_batched(CUtensorMap* m, const void* ptr, bool bf16, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t batch,
-                  uint32_t box_cols, uint32_t box_rows);
+                  uint32_t box_rows);
 
 // grouped GEMMs (persistent, TMA + tcgen05)
 enum class GemmKind : int {

@@ -602,7 +602,7 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
 
 static bool ns_supported(int64_t N, int64_t R, int64_t C) {
     return N >= 0 && N <= 65535 && R >= 1 && R <= 32768 && C >= 1 && C <= 32768 &&
-           N * ((R + 127) / 128) * ((C + 127) / 128) < INT32_MAX;
+           N * ((R + 127) / 128) * ((C + 127) / 128) < (1 << 24);
 }
 
 size_t moe_orthogonalise_workspace_bytes(int64_t N, int64_t R, int64_t C) {

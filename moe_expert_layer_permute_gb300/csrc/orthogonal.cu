@@ -28,10 +28,10 @@ namespace moe {
 constexpr float kXScale = 256.f, kABScale = 1024.f, kLoScale = 2048.f;
 constexpr int kNsStages = 4;
 constexpr int kNsEpi = 8;          // epilogue warps: two for each quarter of the TMEM lanes, on alternate columns
-constexpr int kNsThreads = 64 + 32 * kNsEpi;
-constexpr int kNsSlots = 3;        // pairs of boxes per epilogue warp
-constexpr int kNsBox = 2048;       // a box: 32 rows x 32 16-bit values
-constexpr int kNsSmem = 1024 + kNsStages * 32768 + kNsEpi * kNsSlots * 2 * kNsBox + 512;
+constexpr int kNsThreads = 32 * (5 + kNsEpi);   // operand loads, MMA, the epilogue, watcher, box loads, box stores
+constexpr int kNsSlots = 3;        // pairs of boxes between the box loads, the epilogue and the box stores
+constexpr int kNsBox = 16384;      // a box: 128 rows x 64 16-bit values, 128-byte swizzle
+constexpr int kNsSmem = 1024 + kNsStages * 32768 + kNsSlots * 2 * kNsBox + 512;
 constexpr int kNormPart = 8192;    // elements of one partial sum of squares
 constexpr int kNormParts = 512;    // most partial sums of a matrix
 
@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const T* G, long long elem
             v += s;
         }
     } else {
+#pragma unroll 8
         for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < elems; i += (long long)parts * 256) {
             const float x = ns_val(g, i);
             v += x * x;
@@ -108,6 +109,7 @@ struct NsPrep {
     __half* hi;
     __half* lo;      // null where G is exact in fp16 (bf16 G)
     float* inv_s;    // [N]
+    int* done;       // [N], zeroed
     int parts, R, C, ld;
     float eps;
     int flip;        // store G^T
@@ -119,7 +121,10 @@ __device__ __forceinline__ float ns_factor(const NsPrep& a, int mat, bool first)
     for (int i = threadIdx.x; i < a.parts; i += 256) v += a.partial[(long long)mat * a.parts + i];
     float inv_s;
     const float f = ns_split(sqrtf(ns_block_sum(v)), a.eps, &inv_s) * kXScale;
-    if (first && threadIdx.x == 0) a.inv_s[mat] = inv_s;
+    if (first && threadIdx.x == 0) {
+        a.inv_s[mat] = inv_s;
+        a.done[mat] = 0;
+    }
     return f;
 }
 __device__ __forceinline__ uint32_t ns_pack_half(float lo, float hi) {
@@ -221,24 +226,32 @@ __global__ void __launch_bounds__(256) ns_prep_any_kernel(const T* G, const NsPr
     }
 }
 
-// ---- the three products ------------------------------------------------------------------------------
+// ---- the steps -----------------------------------------------------------------------------------------
 enum NsMode { NS_GRAM = 0, NS_POLY, NS_APPLY };
-// How the last step stores O: not at all (an inner step), through TMA boxes as it stands or flipped, or
-// by plain stores where its rows are not multiples of 16 bytes
-enum NsOut { NS_O_NONE = 0, NS_O_BOX, NS_O_BOX_FLIP, NS_O_PLAIN, NS_O_PLAIN_FLIP };
+// How the last step stores O: through TMA boxes as it stands or flipped, or by plain stores where its
+// rows are not multiples of 16 bytes
+enum NsOut { NS_O_BOX = 1, NS_O_BOX_FLIP, NS_O_PLAIN, NS_O_PLAIN_FLIP };
+
+// Maps of A, B, X (two buffers), X's rounding error and O with boxes of 64 columns: 128 rows for operands
+// along K and for the epilogue's boxes, 64 ("_t") for X as APPLY's second operand and for transposed boxes
+struct NsMaps {
+    CUtensorMap a, a_t, b, b_t, x[2], x_t[2], lo, o, o_t;
+};
 
 struct NsArgs {
-    int m, n, lda, ldx;
-    int tiles_n, tiles;          // tile columns (APPLY), tiles per matrix
-    int units;                   // tiles of the whole batch
-    int k_blocks;
-    int k_wrap;                  // k_blocks, or half of them: APPLY with B's rounding error as a second B
-    int batch;                   // N: matrix N + i of the B array is the rounding error of matrix i's B
-    float a, b, c;
-    const float* inv_s;          // [N] in the first step, null after it
-    int xlo;                     // APPLY: X has a rounding error (else it is exact, or the step takes none)
-    int keep_lo;                 // POLY: store B's rounding error; APPLY: the next X's
+    int m, n, N, steps;
+    int mt, nt;                  // tile rows and columns of X
+    int tri, full;               // tiles of A's lower triangle, and of X
+    int h, halves;               // matrices of a half group, half groups in flight (see ns_unit)
+    int per_cycle, cycles, supers;
+    int units;
+    int k_gram, k_poly;          // K slices
+    int b_lo;                    // B keeps its rounding error: matrix N + i of the B array, a second product
+    int first_lo;                // the first X has a rounding error (else it is exact)
     int out_kind;                // NsOut
+    float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
+    const float* inv_s;          // [N]
+    int* done;                   // [N] tiles stored (each CTA of a pair counts its part)
     __nv_bfloat16* O;
     int* status;
     long long wait_limit;
@@ -251,78 +264,124 @@ __device__ __forceinline__ void ns_wait_drain(uint64_t* bar, uint32_t parity) {
         if (clock64() - t0 > kDrainCycles) break;
 }
 
-struct NsTile {
-    int mat, i, j;
+struct NsUnit {
+    int mode, step, mat, i, j;
+    bool valid;
 };
-template <int MODE>
-__device__ __forceinline__ NsTile ns_tile(int unit, const NsArgs& a) {
-    NsTile t;
-    t.mat = unit / a.tiles;
-    int left = unit - t.mat * a.tiles;
-    if (MODE == NS_APPLY) {
-        t.i = left / a.tiles_n;
-        t.j = left - t.i * a.tiles_n;
+// A matrix's phases GRAM, POLY, APPLY of each step follow one another; its phase starts when the one before
+// has stored every tile.  So that the CTAs have other work meanwhile, and that X, A and B stay in L2 from
+// one phase to the next, two half groups of h matrices are in flight, half a step apart: cycle c holds
+//   GRAM(a) APPLY(b, the step before) POLY(a) GRAM(b) APPLY(a) POLY(b)
+// with a, b the halves of group c / steps in step c % steps.  With few matrices there is no second half:
+// GRAM(a) POLY(a) APPLY(a).  CTAs take the units of this list in turn; every unit depends on earlier ones only.
+__device__ __forceinline__ NsUnit ns_unit(int unit, const NsArgs& a) {
+    NsUnit u;
+    int c = unit / a.per_cycle, left = unit - c * a.per_cycle, b = 0;
+    const int t = a.h * a.tri, f = a.h * a.full;
+    if (a.halves == 1) {
+        u.mode = left < t ? NS_GRAM : left < 2 * t ? NS_POLY : NS_APPLY;
+        left -= u.mode * t;
+    } else if (left < t) {
+        u.mode = NS_GRAM;
+    } else if ((left -= t) < f) {
+        u.mode = NS_APPLY;
+        b = 1;
+        --c;
+    } else if ((left -= f) < t) {
+        u.mode = NS_POLY;
+    } else if ((left -= t) < t) {
+        u.mode = NS_GRAM;
+        b = 1;
+    } else if ((left -= t) < f) {
+        u.mode = NS_APPLY;
     } else {
-        t.i = 0;
-        while (left > t.i) left -= ++t.i;   // row i of the lower triangle has i + 1 tiles
-        t.j = left;
+        left -= f;
+        u.mode = NS_POLY;
+        b = 1;
     }
-    return t;
+    const int group = c / a.steps;
+    u.step = c - group * a.steps;
+    const int tiles = u.mode == NS_APPLY ? a.full : a.tri;
+    const int k = left / tiles;
+    left -= k * tiles;
+    u.mat = group * a.halves * a.h + b * a.h + k;
+    u.valid = c >= 0 && group < a.supers && u.mat < a.N;
+    if (u.mode == NS_APPLY) {
+        u.i = left / a.nt;
+        u.j = left - u.i * a.nt;
+    } else {   // row i of the triangle has i + 1 tiles
+        u.i = (int)((sqrtf(8.f * left + 1.f) - 1.f) * 0.5f);
+        while (u.i * (u.i + 1) / 2 > left) --u.i;
+        while ((u.i + 1) * (u.i + 2) / 2 <= left) ++u.i;
+        u.j = left - u.i * (u.i + 1) / 2;
+    }
+    return u;
+}
+// tiles of the matrix that come before the unit's phase
+__device__ __forceinline__ int ns_before(const NsUnit& u, const NsArgs& a) {
+    return u.step * (2 * a.tri + a.full) + u.mode * a.tri;
 }
 
-// A warp's output boxes: 32 rows x 64 bytes (32 16-bit values), 64-byte swizzle.
-// the lane's row of 32 values, packed in pairs
-__device__ __forceinline__ void ns_box_row(uint32_t box, int lane, const uint32_t* v) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-}
-// the transpose: the lane's value j goes to row j, column lane
-__device__ __forceinline__ void ns_box_col(uint32_t box, int lane, const uint32_t* v) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const uint16_t h = (uint16_t)(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2), "h"(h)
-                     : "memory");
-    }
-}
-__device__ __forceinline__ void ns_box_read(uint32_t* v, uint32_t box, int lane) {
+// Chunk `at` (16 bytes) of row r of a box
+__device__ __forceinline__ uint32_t ns_sw(int r, int at) { return (uint32_t)(r * 128 + ((at ^ (r & 7)) << 4)); }
+// the thread's 32 columns of its row (columns 32 half .. of the box), packed in pairs
+__device__ __forceinline__ void ns_box_read(uint32_t* v, uint32_t box, int r, int half) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint4 w = ld_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+        const uint4 w = ld_shared_v4(box + ns_sw(r, 4 * half + q));
         v[4 * q] = w.x; v[4 * q + 1] = w.y; v[4 * q + 2] = w.z; v[4 * q + 3] = w.w;
     }
 }
+__device__ __forceinline__ void ns_box_row(uint32_t box, int r, int half, const uint32_t* v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        st_shared_v4(box + ns_sw(r, 4 * half + q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+}
+// the transpose, as two boxes of 64 rows x 64 columns: value j goes to row 32 half + j, column r mod 64 of
+// box r / 64 (a warp writes 64 consecutive bytes at a time)
+__device__ __forceinline__ void ns_box_col(uint32_t box, int r, int half, const uint32_t* v) {
+    box += (r >> 6) * 8192 + (r & 7) * 2;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint16_t h = (uint16_t)(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + ns_sw(32 * half + j, (r & 63) >> 3)), "h"(h) : "memory");
+    }
+}
 
-// The chunks of 32 columns that an epilogue warp works through (every second one), tile after tile.
-template <int MODE, int TILE>
-struct NsChunks {
-    int u, stride, rank, quarter, half;
-    NsTile t;
-    int row0, n0, c, cols;   // the warp's first row, the tile's first column, the chunk, the columns to cover
-    __device__ __forceinline__ void tile(const NsArgs& a) {
-        t = ns_tile<MODE>(u, a);
-        row0 = t.i * TILE + rank * 128 + quarter * 32;
-        n0 = t.j * TILE;
-        c = 32 * half;
-        cols = row0 < a.m ? min(TILE, (MODE == NS_APPLY ? a.n : a.m) - n0) : 0;
-    }
-    // moves over tiles without a chunk for this warp; false past the last unit
-    __device__ __forceinline__ bool settle(const NsArgs& a) {
-        while (u < a.units && c >= cols) {
-            u += stride;
-            if (u < a.units) tile(a);
-        }
-        return u < a.units;
-    }
+// What the epilogue side does with a unit's chunks of 64 columns.
+struct NsPart {
+    int row0, n0, chunks;      // the CTA's first row, the tile's first column
+    int out_kind;              // NsOut in the last step's APPLY, else 0
+    bool load, load_lo;        // the chunk's A or X comes in, and X's rounding error
+    bool twin, keep_lo;        // out go the transpose as well, or a rounding error
 };
+template <int TILE>
+__device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArgs& a) {
+    NsPart p;
+    p.row0 = u.i * TILE + rank * 128;
+    p.n0 = u.j * TILE;
+    p.chunks = p.row0 < a.m ? (min(TILE, (u.mode == NS_APPLY ? a.n : a.m) - p.n0) + 63) / 64 : 0;
+    p.out_kind = u.mode == NS_APPLY && u.step + 1 == a.steps ? a.out_kind : 0;
+    p.load = u.mode != NS_GRAM;
+    // the last step reads X without its rounding error, so the step before keeps none
+    p.load_lo = u.mode == NS_APPLY && u.step + 1 < a.steps && (u.step > 0 || a.first_lo);
+    p.keep_lo = u.mode == NS_POLY ? a.b_lo : u.mode == NS_APPLY && u.step + 2 < a.steps;
+    p.twin = u.mode != NS_APPLY && u.i != u.j;
+    return p;
+}
 
-// Persistent blocks walk the batch's tiles.  Warp 0 loads, warp 1 issues the MMAs, eight warps store (see
-// gemm.cu for the scheme): four stages of 32 KB, two accumulators, waits bounded.  What an epilogue needs
-// besides its accumulator (POLY: A; APPLY: X and its rounding error) comes by TMA into the warp's ring of
-// three slots, two chunks of 32 columns ahead and across tiles: with loads into registers a chunk ahead
-// APPLY waited on memory (256 x 768 x 2048: 851 us a launch).  The results replace it in place and leave
-// by TMA from there.
+// Every step of every matrix in one launch of persistent CTAs, a warp to each job, all waits bounded:
+//   warp 0      operand K slices by TMA into a ring of four stages of 32 KB
+//   warp 1      MMAs into one of two accumulators
+//   warps 2-9   epilogue: lane quarter w % 4, alternate 32 columns; a chunk is 64 columns of the tile
+//   warp 10     watches the matrices' counters ahead of the others: `ready` units of this CTA have inputs
+//   warp 11     what a chunk needs besides its accumulator (POLY: A; APPLY: X and its rounding error), by
+//               TMA into one of three slots
+//   warp 12     stores the slot, where the epilogue has put the results in their place, frees it, and
+//               counts the tile once its stores are complete
+// The box loads and stores have threads of their own since an epilogue warp that issued them spent more
+// time there than on its arithmetic, and boxes of 128-byte rows since narrower ones kept the TMA busy
+// (12,600 cycles a tile of APPLY at K = 768, against 7,900 for its MMAs).
 //   PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each holding 128 rows of the first operand and
 //   half of the second; otherwise one CTA computes 128 x 128.
 // GRAM and POLY are symmetric: tiles of the lower triangle alone, and those below the diagonal are stored
@@ -330,29 +389,29 @@ struct NsChunks {
 // rows of A by rows of A (A = A^T), both contiguous along K; APPLY rows of B by columns of X (contiguous
 // along N).  The TMA fills K past the edge with zeros and drops stores outside a matrix, so no size needs
 // padding beyond 16-byte rows.
-template <int MODE, bool PAIR>
+template <bool PAIR>
 __global__ void __launch_bounds__(kNsThreads, 1)
-    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmL,
-                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD, const NsArgs a) {
+    ns_steps_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsArgs a) {
     grid_dep_wait();
     constexpr int kTile = PAIR ? 256 : 128;      // rows and columns of a unit's tile
     constexpr int kOperand = 128 * 128;          // bytes of one operand's K slice per CTA: 128 x 64 fp16
-    constexpr bool kBmn = MODE == NS_APPLY;
-    constexpr uint32_t kIdesc = idesc_f16(kTile, kTile, false, kBmn);
+    constexpr int kParts = PAIR ? 2 : 1;         // CTAs that store a part of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + kNsStages * kOperand;
     uint8_t* sBox = sB + kNsStages * kOperand;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sBox + kNsEpi * kNsSlots * 2 * kNsBox);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sBox + kNsSlots * 2 * kNsBox);
     uint64_t* empty = full + kNsStages;
     uint64_t* tfull = empty + kNsStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint64_t* slot_full = drain + 1;             // [kNsEpi][kNsSlots]
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(slot_full + kNsEpi * kNsSlots);
+    uint64_t* box_full = drain + 1;              // a slot's loads have landed,
+    uint64_t* box_done = box_full + kNsSlots;    // its results are written,
+    uint64_t* box_free = box_done + kNsSlots;    // and stored
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(box_free + kNsSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    int* ready = reinterpret_cast<int*>(tslot + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
     const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
@@ -364,11 +423,16 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull + b, 1);
-            mbar_init(tempty + b, (PAIR ? 2 : 1) * kNsEpi);
+            mbar_init(tempty + b, kParts * kNsEpi);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < kNsEpi * kNsSlots; ++i) mbar_init(slot_full + i, 1);
+        for (int i = 0; i < kNsSlots; ++i) {
+            mbar_init(box_full + i, 1);
+            mbar_init(box_done + i, kNsEpi);
+            mbar_init(box_free + i, 1);
+        }
         *abort_flag = 0;
+        *ready = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -380,45 +444,68 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     if (PAIR) cluster_sync();   // the peer's barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    // until this CTA's unit q has its inputs (false: gave up); then this thread's TMA loads may read them
+    auto inputs = [&](int q) {
+        if (ld_acquire_cta_shared(ready) <= q) {
+            const long long t0 = clock64();
+            while (ld_acquire_cta_shared(ready) <= q) {
+                if (*abort_flag) return false;
+                if (clock64() - t0 > a.wait_limit) {
+                    *abort_flag = 1;
+                    set_status(a.status, MOE_DEV_TIMEOUT);
+                    return false;
+                }
+            }
+        }
+        fence_proxy_async_global();
+        return true;
+    };
 
     if (warp == 0) {
         if (lane == 0 && !a.withhold_loads) {
-            int stage = 0;
+            int stage = 0, q = 0;
             uint32_t phase = 0;
             long long issued = 0;
             bool ok = true;
-            for (int u = unit0; u < a.units && ok; u += stride) {
-                const NsTile t = ns_tile<MODE>(u, a);
+            for (int unit = unit0; unit < a.units && ok; unit += stride, ++q) {
+                const NsUnit t = ns_unit(unit, a);
+                if (!t.valid) continue;
+                if (!inputs(q)) break;
                 const int m0 = t.i * kTile + rank * 128, n0 = t.j * kTile + rank * 128;
-                for (int kb = 0; kb < a.k_blocks; ++kb) {
+                const bool apply = t.mode == NS_APPLY;
+                const CUtensorMap* tmA = t.mode == NS_GRAM ? &maps.x[t.step & 1] : apply ? &maps.b : &maps.a;
+                const CUtensorMap* tmB = apply ? &maps.x_t[t.step & 1] : tmA;
+                const int wrap = t.mode == NS_GRAM ? a.k_gram : a.k_poly;
+                const int k_blocks = apply && a.b_lo ? 2 * wrap : wrap;
+                for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, a.status, a.wait_limit)) {
                         ok = false;
                         break;
                     }
                     uint8_t* dA = sA + stage * kOperand;
                     uint8_t* dB = sB + stage * kOperand;
-                    const bool second = kb >= a.k_wrap;
-                    const int k0 = (second ? kb - a.k_wrap : kb) * 64;
-                    const int matA = second ? t.mat + a.batch : t.mat;
+                    const bool second = kb >= wrap;
+                    const int k0 = (second ? kb - wrap : kb) * 64;
+                    const int matA = second ? t.mat + a.N : t.mat;
                     if constexpr (PAIR) {
                         // both CTAs' copies land on the leader's barrier, which expects both
                         const uint32_t lbar = cluster_addr(full + stage, 0);
                         if (rank == 0) mbar_arrive_expect_tx(full + stage, 4 * kOperand);
-                        tma_load_3d_pair(dA, &tmA, lbar, k0, m0, matA);
-                        if (kBmn) {
-                            tma_load_3d_pair(dB, &tmB, lbar, n0, k0, t.mat);
-                            tma_load_3d_pair(dB + kOperand / 2, &tmB, lbar, n0 + 64, k0, t.mat);
+                        tma_load_3d_pair(dA, tmA, lbar, k0, m0, matA);
+                        if (apply) {
+                            tma_load_3d_pair(dB, tmB, lbar, n0, k0, t.mat);
+                            tma_load_3d_pair(dB + kOperand / 2, tmB, lbar, n0 + 64, k0, t.mat);
                         } else {
-                            tma_load_3d_pair(dB, &tmB, lbar, k0, n0, t.mat);
+                            tma_load_3d_pair(dB, tmB, lbar, k0, n0, t.mat);
                         }
                     } else {
                         mbar_arrive_expect_tx(full + stage, 2 * kOperand);
-                        tma_load_3d(dA, &tmA, full + stage, k0, m0, matA);
-                        if (kBmn) {
-                            tma_load_3d(dB, &tmB, full + stage, n0, k0, t.mat);
-                            tma_load_3d(dB + kOperand / 2, &tmB, full + stage, n0 + 64, k0, t.mat);
+                        tma_load_3d(dA, tmA, full + stage, k0, m0, matA);
+                        if (apply) {
+                            tma_load_3d(dB, tmB, full + stage, n0, k0, t.mat);
+                            tma_load_3d(dB + kOperand / 2, tmB, full + stage, n0 + 64, k0, t.mat);
                         } else {
-                            tma_load_3d(dB, &tmB, full + stage, k0, n0, t.mat);
+                            tma_load_3d(dB, tmB, full + stage, k0, n0, t.mat);
                         }
                     }
                     ++issued;
@@ -443,7 +530,11 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             long long consumed = 0;
             bool ok = true;
             const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
-            for (int u = unit0; u < a.units && ok; u += stride) {
+            for (int unit = unit0; unit < a.units && ok; unit += stride) {
+                const NsUnit t = ns_unit(unit, a);
+                if (!t.valid) continue;
+                const bool apply = t.mode == NS_APPLY;
+                const int k_blocks = t.mode == NS_GRAM ? a.k_gram : apply && a.b_lo ? 2 * a.k_poly : a.k_poly;
                 if (!(PAIR ? mbar_wait_cluster(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit)
                            : mbar_wait(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit))) {
                     ok = false;
@@ -451,7 +542,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * kTile);
-                for (int kb = 0; kb < a.k_blocks; ++kb) {
+                const uint32_t idesc = apply ? idesc_f16(kTile, kTile, false, true) : idesc_f16(kTile, kTile, false, false);
+                const uint32_t b_step = apply ? 2048 : 32, b_lbo = apply ? kOperand / 2 : 16;
+                for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(full + stage, phase, abort_flag, a.status, a.wait_limit)) {
                         ok = false;
                         break;
@@ -461,10 +554,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t ad = sdesc_sw128(sa + ks * 32, 16, 1024);
-                        const uint64_t bd = kBmn ? sdesc_sw128(sb + ks * 2048, kOperand / 2, 1024)
-                                                 : sdesc_sw128(sb + ks * 32, 16, 1024);
-                        if constexpr (PAIR) mma_bf16_pair(d, ad, bd, kIdesc, (kb | ks) != 0);
-                        else mma_bf16(d, ad, bd, kIdesc, (kb | ks) != 0);
+                        const uint64_t bd = sdesc_sw128(sb + ks * b_step, b_lbo, 1024);
+                        if constexpr (PAIR) mma_bf16_pair(d, ad, bd, idesc, (kb | ks) != 0);
+                        else mma_bf16(d, ad, bd, idesc, (kb | ks) != 0);
                     }
                     if constexpr (PAIR) mma_commit_pair_mc(empty + stage, 0x3);
                     else mma_commit(empty + stage);
@@ -491,121 +583,191 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         ns_wait_drain(empty + s, (uint32_t)(((consumed - s + kNsStages - 1) / kNsStages - 1) & 1));
             }
         }
+    } else if (warp == 2 + kNsEpi) {
+        if (lane == 0) {
+            int q = 0;
+            bool ok = true;
+            for (int unit = unit0; unit < a.units && ok; unit += stride, ++q) {
+                const NsUnit t = ns_unit(unit, a);
+                const int need = t.valid ? kParts * ns_before(t, a) : 0;
+                if (need > 0 && ld_acquire_gpu(a.done + t.mat) < need) {
+                    const long long t0 = clock64();
+                    while (ld_acquire_gpu(a.done + t.mat) < need) {
+                        ok = !*abort_flag;
+                        if (ok && clock64() - t0 > a.wait_limit) {
+                            *abort_flag = 1;
+                            set_status(a.status, MOE_DEV_TIMEOUT);
+                            ok = false;
+                        }
+                        if (!ok) break;
+                    }
+                }
+                if (ok) st_release_cta_shared(ready, q + 1);
+            }
+        }
+    } else if (warp == 3 + kNsEpi) {
+        if (lane == 0 && !a.withhold_loads) {
+            uint32_t k = 0;   // chunks so far; slot: mod kNsSlots
+            int q = 0;
+            bool ok = true;
+            for (int unit = unit0; unit < a.units && ok; unit += stride, ++q) {
+                const NsUnit t = ns_unit(unit, a);
+                if (!t.valid) continue;
+                const NsPart p = ns_part<kTile>(t, rank, a);
+                if (p.chunks == 0) continue;
+                if (p.load && !inputs(q)) break;
+                const CUtensorMap* tm = t.mode == NS_POLY ? &maps.a : &maps.x[t.step & 1];
+                for (int c = 0; c < p.chunks; ++c, ++k) {
+                    const int slot = k % kNsSlots;
+                    if (!mbar_wait(box_free + slot, (k / kNsSlots & 1) ^ 1u, abort_flag, a.status, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!p.load) {
+                        mbar_arrive(box_full + slot);
+                        continue;
+                    }
+                    uint8_t* dst = sBox + slot * 2 * kNsBox;
+                    mbar_arrive_expect_tx(box_full + slot, p.load_lo ? 2 * kNsBox : kNsBox);
+                    tma_load_3d(dst, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
+                    if (p.load_lo) tma_load_3d(dst + kNsBox, &maps.lo, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
+                }
+            }
+            // every load has landed (bounded) before the CTA exits
+            for (uint32_t i = k > kNsSlots ? k - kNsSlots : 0; i < k; ++i)
+                ns_wait_drain(box_full + i % kNsSlots, i / kNsSlots & 1);
+        }
+    } else if (warp == 4 + kNsEpi) {
+        if (lane == 0) {
+            uint32_t k = 0;
+            bool ok = true;
+            for (int unit = unit0; unit < a.units && ok; unit += stride) {
+                const NsUnit t = ns_unit(unit, a);
+                if (!t.valid) continue;
+                const NsPart p = ns_part<kTile>(t, rank, a);
+                const CUtensorMap* tm = t.mode == NS_GRAM ? &maps.a : t.mode == NS_POLY ? &maps.b
+                                        : p.out_kind      ? &maps.o : &maps.x[1 - (t.step & 1)];
+                const CUtensorMap* tm_t = t.mode == NS_GRAM ? &maps.a_t : t.mode == NS_POLY ? &maps.b_t : &maps.o_t;
+                for (int c = 0; c < p.chunks; ++c, ++k) {
+                    const int slot = k % kNsSlots, col = p.n0 + 64 * c;
+                    uint8_t* box = sBox + slot * 2 * kNsBox;
+                    if (!mbar_wait(box_done + slot, k / kNsSlots & 1, abort_flag, a.status, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    if (p.out_kind < NS_O_BOX_FLIP) tma_store_3d(tm, box, col, p.row0, t.mat);
+                    if (p.twin || p.out_kind == NS_O_BOX_FLIP) {
+                        tma_store_3d(tm_t, box + kNsBox, p.row0, col, t.mat);
+                        if (p.row0 + 64 < a.m) tma_store_3d(tm_t, box + kNsBox + 8192, p.row0 + 64, col, t.mat);
+                    } else if (p.keep_lo) {
+                        if (t.mode == NS_POLY) tma_store_3d(&maps.b, box + kNsBox, col, p.row0, t.mat + a.N);
+                        else tma_store_3d(&maps.lo, box + kNsBox, col, p.row0, t.mat);
+                    }
+                    bulk_commit();
+                    if (c > 0) {   // the slot before this one has been read
+                        bulk_wait_read<1>();
+                        mbar_arrive(box_free + (k - 1) % kNsSlots);
+                    }
+                }
+                if (!ok) break;
+                if (p.chunks > 0) {
+                    bulk_wait_read<0>();
+                    mbar_arrive(box_free + (k - 1) % kNsSlots);
+                }
+                if (!p.out_kind) {
+                    // this CTA's part of the tile is stored, and visible to whoever sees the count
+                    bulk_wait_all();
+                    fence_proxy_async_global();
+                    red_release_gpu_add(a.done + t.mat, 1);
+                }
+            }
+            bulk_wait_all();   // the stores are complete before the CTA exits
+        }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        uint8_t* boxes = sBox + (warp - 2) * kNsSlots * 2 * kNsBox;
-        uint64_t* box_full = slot_full + (warp - 2) * kNsSlots;
-        constexpr bool kLoads = MODE != NS_GRAM;
-        const bool two = MODE == NS_APPLY && a.xlo;
-        using Chunks = NsChunks<MODE, kTile>;
-        Chunks cur{unit0, stride, rank, quarter, half}, ahead{unit0, stride, rank, quarter, half};
-        if (unit0 < a.units) {
-            cur.tile(a);
-            ahead.tile(a);
-        }
-        uint32_t loaded = 0, used = 0;   // chunks requested and worked on; slot: mod kNsSlots
-        auto request = [&] {             // the next chunk's boxes (lane 0)
-            if (!ahead.settle(a)) return;
-            uint64_t* bar = box_full + loaded % kNsSlots;
-            uint8_t* dst = boxes + (loaded % kNsSlots) * 2 * kNsBox;
-            mbar_arrive_expect_tx(bar, two ? 2 * kNsBox : kNsBox);
-            tma_load_3d(dst, &tmX, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
-            if (two) tma_load_3d(dst + kNsBox, &tmL, bar, ahead.n0 + ahead.c, ahead.row0, ahead.t.mat);
-            ahead.c += 64;
-            ++loaded;
-        };
-        if (kLoads && lane == 0 && !a.withhold_loads)
-            for (int i = 0; i < kNsSlots - 1; ++i) request();
+        const int br = quarter * 32 + lane;      // row of the CTA's tile, and of a box
+        uint32_t k = 0;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (; cur.u < a.units && ok; cur.u += stride) {
-            cur.tile(a);
-            const NsTile t = cur.t;
-            const int row0 = cur.row0, r = row0 + lane;
-            const float is = a.inv_s ? __ldg(a.inv_s + t.mat) : 1.f;
+        for (int unit = unit0; unit < a.units && ok; unit += stride) {
+            const NsUnit t = ns_unit(unit, a);
+            if (!t.valid) continue;
+            const NsPart p = ns_part<kTile>(t, rank, a);
+            const float is = t.step == 0 ? __ldg(a.inv_s + t.mat) : 1.f;
+            const float ca = a.co[3 * t.step], cb = a.co[3 * t.step + 1], cc = a.co[3 * t.step + 2];
             if (!__all_sync(0xffffffffu, mbar_wait(tfull + acc, acc_phase, abort_flag, a.status, a.wait_limit))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 32 * half; c0 < cur.cols; c0 += 64, ++used) {
-                const int col = cur.n0 + c0;
-                uint8_t* box = boxes + (used % kNsSlots) * 2 * kNsBox;
-                const uint32_t sbox = smem_u32(box);
+            for (int c = 0; c < p.chunks; ++c, ++k) {
+                const int slot = k % kNsSlots, col = p.n0 + 64 * c + 32 * half;
+                const uint32_t sbox = smem_u32(sBox + slot * 2 * kNsBox);
                 float v[32];
                 uint32_t out[16], low[16];
-                tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + c0), v);
-                if (kLoads) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(box_full + used % kNsSlots, used / kNsSlots & 1, abort_flag,
-                                                           a.status, a.wait_limit));
-                    if (!ok) break;
-                } else {
-                    if (lane == 0) bulk_wait_read<kNsSlots - 1>();   // the slot's last store has read it
-                    __syncwarp();
-                }
-                if constexpr (MODE == NS_GRAM) {
+                float2* v2 = reinterpret_cast<float2*>(v);
+                tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + 64 * c + 32 * half), v);
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(box_full + slot, k / kNsSlots & 1, abort_flag, a.status, a.wait_limit));
+                if (!ok) break;
+                if (t.mode == NS_GRAM) {
                     const float f = kABScale / (kXScale * kXScale) * is * is;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f, v[2 * j + 1] * f);
-                } else if constexpr (MODE == NS_POLY) {
-                    ns_box_read(out, sbox, lane);
-                    const float fc = a.c / kABScale;
+                    const float2 ff = make_float2(f, f);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float2 x = ns_unpack_half(out[j]);
-                        v[2 * j] = a.b * x.x + fc * v[2 * j];
-                        v[2 * j + 1] = a.b * x.y + fc * v[2 * j + 1];
-                        out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
+                        v2[j] = mul2(v2[j], ff);
+                        out[j] = ns_pack_half(v2[j].x, v2[j].y);
                     }
-                    if (a.keep_lo) {
+                } else if (t.mode == NS_POLY) {
+                    ns_box_read(out, sbox, br, half);
+                    const float2 fc = make_float2(cc / kABScale, cc / kABScale), fb = make_float2(cb, cb);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v2[j] = fma2(fb, ns_unpack_half(out[j]), mul2(fc, v2[j]));
+                        out[j] = ns_pack_half(v2[j].x, v2[j].y);
+                    }
+                    if (p.keep_lo) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float2 h = ns_unpack_half(out[j]);
-                            low[j] = ns_pack_half(v[2 * j] - h.x, v[2 * j + 1] - h.y);
+                            low[j] = ns_pack_half(v2[j].x - h.x, v2[j].y - h.y);
                         }
                     }
                 } else {
-                    ns_box_read(out, sbox, lane);
-                    const float fd = is * (1.f / kABScale), fx = is * a.a;
+                    ns_box_read(out, sbox, br, half);
+                    const float fd = is * (1.f / kABScale), fx = is * ca, fl = fx * (1.f / kLoScale);
+                    const float2 fd2 = make_float2(fd, fd), fx2 = make_float2(fx, fx), fl2 = make_float2(fl, fl);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 x = ns_unpack_half(out[j]);
-                        v[2 * j] = fx * x.x + fd * v[2 * j];
-                        v[2 * j + 1] = fx * x.y + fd * v[2 * j + 1];
+                    for (int j = 0; j < 16; ++j) v2[j] = fma2(fx2, ns_unpack_half(out[j]), mul2(fd2, v2[j]));
+                    if (p.load_lo) {
+                        ns_box_read(low, sbox + kNsBox, br, half);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v2[j] = fma2(fl2, ns_unpack_half(low[j]), v2[j]);
                     }
-                    if (two) {
-                        ns_box_read(low, sbox + kNsBox, lane);
+                    if (!p.out_kind) {
+                        const float2 minus = make_float2(-1.f, -1.f), ls = make_float2(kLoScale, kLoScale);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 x = ns_unpack_half(low[j]);
-                            v[2 * j] += fx * (1.f / kLoScale) * x.x;
-                            v[2 * j + 1] += fx * (1.f / kLoScale) * x.y;
-                        }
-                    }
-                    if (a.out_kind == NS_O_NONE) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
-                        if (a.keep_lo) {
+                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v2[j].x, v2[j].y);
+                        if (p.keep_lo) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const float2 h = ns_unpack_half(out[j]);
-                                low[j] = ns_pack_half((v[2 * j] - h.x) * kLoScale, (v[2 * j + 1] - h.y) * kLoScale);
+                                const float2 l = mul2(fma2(ns_unpack_half(out[j]), minus, v2[j]), ls);
+                                low[j] = ns_pack_half(l.x, l.y);
                             }
                         }
                     } else {
+                        const float2 us = make_float2(1.f / kXScale, 1.f / kXScale);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            out[j] = pack_bf16x2(v[2 * j] * (1.f / kXScale), v[2 * j + 1] * (1.f / kXScale));
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 o = mul2(v2[j], us);
+                            out[j] = pack_bf16x2(o.x, o.y);
+                        }
                     }
                 }
-                const bool flip = MODE == NS_APPLY && a.out_kind == NS_O_BOX_FLIP;
-                const bool plain = MODE == NS_APPLY && a.out_kind == NS_O_PLAIN;
-                const bool plain_flip = MODE == NS_APPLY && a.out_kind == NS_O_PLAIN_FLIP;
-                // the second box: the transpose of a tile below the diagonal, or the rounding error
-                const bool twin = MODE != NS_APPLY && t.i != t.j;
-                const bool with_lo = MODE != NS_GRAM && a.keep_lo;
-                __syncwarp();   // every lane has read the boxes
-                if (plain_flip) {   // a warp's 32 rows are 64 consecutive bytes of O
+                // results replace what this thread read; transposes go to the second box, which then holds
+                // nothing that another warp still reads
+                if (p.out_kind == NS_O_PLAIN_FLIP) {   // a warp's 32 rows are 64 consecutive bytes of O
+                    const int r = p.row0 + br;
                     if (r < a.m) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -613,51 +775,38 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                                 reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.n + col + j) * a.m + r] =
                                     (uint16_t)(j & 1 ? out[j >> 1] >> 16 : out[j >> 1]);
                     }
+                } else if (p.out_kind == NS_O_BOX_FLIP) {
+                    ns_box_col(sbox + kNsBox, br, half, out);
                 } else {
-                    if (flip) ns_box_col(sbox, lane, out);
-                    else ns_box_row(sbox, lane, out);
-                    if (twin) ns_box_col(sbox + kNsBox, lane, out);
-                    else if (with_lo) ns_box_row(sbox + kNsBox, lane, low);
+                    ns_box_row(sbox, br, half, out);
+                    if (p.twin) ns_box_col(sbox + kNsBox, br, half, out);
+                    else if (p.keep_lo) ns_box_row(sbox + kNsBox, br, half, low);
                 }
-                if (plain) {   // 64 consecutive bytes of a row of O at a time
+                if (p.out_kind == NS_O_PLAIN) {   // 64 consecutive bytes of a row of O at a time
                     __syncwarp();
-                    if (col + lane < a.n) {
-                        const int rows = min(32, a.m - row0);
-                        for (int q = 0; q < rows; ++q)
-                            reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.m + row0 + q) * a.n + col + lane] =
-                                *reinterpret_cast<const uint16_t*>(box + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4) +
-                                                                   (lane & 7) * 2);
-                    }
+                    const int r0 = p.row0 + 32 * quarter;
+                    if (col + lane < a.n)
+                        for (int q = 0; q < min(32, a.m - r0); ++q) {
+                            uint16_t h;
+                            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h)
+                                         : "r"(sbox + ns_sw(32 * quarter + q, 4 * half + (lane >> 3)) + (lane & 7) * 2)
+                                         : "memory");
+                            reinterpret_cast<uint16_t*>(a.O)[((long long)t.mat * a.m + r0 + q) * a.n + col + lane] = h;
+                        }
                 }
                 fence_proxy_async_cta();
                 __syncwarp();
-                if (lane == 0) {
-                    if (!plain && !plain_flip) {
-                        if (flip) tma_store_3d(&tmC, box, row0, col, t.mat);
-                        else tma_store_3d(&tmC, box, col, row0, t.mat);
-                        if (twin) tma_store_3d(&tmC, box + kNsBox, row0, col, t.mat);
-                        else if (with_lo) tma_store_3d(&tmD, box + kNsBox, col, row0, t.mat);
-                    }
-                    bulk_commit();
-                    if (kLoads && !a.withhold_loads) {
-                        bulk_wait_read<1>();   // the chunk before this one has left its slot, the next to be filled
-                        request();
-                    }
-                }
+                if (lane == 0) mbar_arrive(box_done + slot);
             }
             tc_fence_before();
             __syncwarp();
+            if (!ok) break;
             if (lane == 0) {
                 if (PAIR && rank == 1) mbar_arrive_cluster(tempty + acc, 0);
                 else mbar_arrive(tempty + acc);
             }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
-        }
-        if (lane == 0) {
-            bulk_wait_all();   // the stores are complete before the CTA exits, and (bounded) the loads
-            for (uint32_t i = loaded > kNsSlots ? loaded - kNsSlots : 0; i < loaded; ++i)
-                ns_wait_drain(box_full + i % kNsSlots, (i / kNsSlots) & 1);
         }
     }
     __syncwarp();
@@ -694,9 +843,6 @@ struct NsSmall {
     long long wait_limit;
     int withhold;
 };
-
-// 16-byte chunk q (of eight) of row r in a 128-byte-swizzled chunk of 64 fp16 columns
-__device__ __forceinline__ uint32_t ns_sw(int r, int q) { return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4)); }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __restrict__ G, const NsSmall a) {
@@ -959,7 +1105,7 @@ static int ns_small_cluster(int64_t m, int64_t n) {
 struct NsLayout {
     int64_t N, m, n, lda, ldx, parts;
     bool b_lo;
-    size_t partial, inv_s, A, B, x0, x1, lo, total;
+    size_t partial, inv_s, done, A, B, x0, x1, lo, total;
 };
 
 static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
@@ -979,6 +1125,7 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     }
     L->partial = take((size_t)N * L->parts * 4);
     L->inv_s = take((size_t)N * 4);
+    L->done = take((size_t)N * 4);
     L->A = take((size_t)N * L->m * L->lda * 2);
     L->b_lo = L->m <= 128;
     L->B = take((size_t)N * (L->b_lo ? 2 : 1) * L->m * L->lda * 2);
@@ -994,18 +1141,36 @@ size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C) {
     return ns_layout(N, R, C, &L) ? L.total : 0;
 }
 
-template <int MODE, bool PAIR>
-static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tx,
-                           const CUtensorMap& tl, const CUtensorMap& tc, const CUtensorMap& td, const NsArgs& a) {
-    constexpr size_t smem = kNsSmem;
-    auto kern = ns_gemm_kernel<MODE, PAIR>;
+// The most CTAs that are resident at once, and the launch of that many (or one, or a pair, for each unit):
+// cooperative, since CTAs wait for one another's tiles.
+template <bool PAIR>
+static cudaError_t ns_steps(cudaStream_t st, int most, const NsMaps& maps, const NsArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = PAIR ? 2 : 1;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(PAIR ? 2 * std::min(a.units, most / 2) : std::min(a.units, most));
+    cfg.blockDim = dim3(kNsThreads);
+    cfg.dynamicSmemBytes = kNsSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, ns_steps_kernel<PAIR>, maps, a);
+}
+template <bool PAIR>
+static cudaError_t ns_resident(int num_sms, int* most) {
     static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    static int most = 0;    // resident CTAs
+    static cudaError_t err = cudaSuccess;
+    static int ctas = 0;
     std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        most = num_sms;
-        if (attr_err == cudaSuccess && PAIR) {
+        auto kern = ns_steps_kernel<PAIR>;
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
+        ctas = num_sms;
+        if (err == cudaSuccess && PAIR) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute at[1];
             at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1014,31 +1179,16 @@ static cudaError_t ns_gemm(cudaStream_t st, int num_sms, const CUtensorMap& ta, 
             at[0].val.clusterDim.z = 1;
             cfg.gridDim = dim3(num_sms / 2 * 2);
             cfg.blockDim = dim3(kNsThreads);
-            cfg.dynamicSmemBytes = smem;
+            cfg.dynamicSmemBytes = kNsSmem;
             cfg.attrs = at;
             cfg.numAttrs = 1;
             int clusters = 0;
-            attr_err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-            most = 2 * std::max(1, std::min(clusters, num_sms / 2));
+            err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+            ctas = 2 * std::max(1, std::min(clusters, num_sms / 2));
         }
     });
-    if (attr_err != cudaSuccess) return attr_err;
-    if (!PAIR) return launch_pdl(kern, std::min(a.units, most), kNsThreads, smem, st, ta, tb, tx, tl, tc, td, a);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * std::min(a.units, most / 2));
-    cfg.blockDim = dim3(kNsThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tx, tl, tc, td, a);
+    *most = ctas;
+    return err;
 }
 
 template <typename T, bool VEC>
@@ -1074,7 +1224,7 @@ static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, in
                           : launch_pdl(ns_norm_kernel<T, false>, parts, 256, 0, st, G, elems, (int)L.parts, partial);
     if (err != cudaSuccess) return err;
     const NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
-                   reinterpret_cast<float*>(w + L.inv_s), (int)L.parts, R, C, (int)L.ldx, eps, R > C};
+                   reinterpret_cast<float*>(w + L.inv_s), reinterpret_cast<int*>(w + L.done), (int)L.parts, R, C, (int)L.ldx, eps, R > C};
     if (C % 8 != 0) return launch_pdl(ns_prep_any_kernel<T>, dim3((C + 31) / 32, (R + 31) / 32, N), 256, 0, st, G, p);
     if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 63) / 64, N), 256, 0, st, G, p);
     return launch_pdl(ns_prep_kernel<T>, dim3((unsigned)((elems + 8 * 256 * kPrepPer - 1) / (8 * 256 * kPrepPer)), N), 256, 0, st,
@@ -1104,64 +1254,52 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     if (err != cudaSuccess) return err;
     const bool flip = R > C;
     const int64_t m = L.m, n = L.n;
-    char* X[2] = {w + L.x0, w + L.x1};
-    // operand maps: K-major boxes of 128 rows, and 64 x 64 for X as APPLY's second operand; "s": the
-    // epilogues' boxes
-    CUtensorMap a_k, b_k, x_k[2], x_n[2], a_s, b_s, bl_s, x_s[2], lo_s, o_s;
-    bool ok = tmap_batched(&a_k, w + L.A, false, m, m, L.lda, N, 64, 128) &&
-              tmap_batched(&b_k, w + L.B, false, m, m, L.lda, L.b_lo ? 2 * N : N, 64, 128) &&
-              tmap_batched(&a_s, w + L.A, false, m, m, L.lda, N, 32, 32) &&
-              tmap_batched(&b_s, w + L.B, false, m, m, L.lda, N, 32, 32) &&
-              tmap_batched(&bl_s, w + L.B + (L.b_lo ? (size_t)N * m * L.lda * 2 : 0), false, m, m, L.lda, N, 32, 32) &&
-              tmap_batched(&lo_s, w + L.lo, false, n, m, L.ldx, N, 32, 32);
-    for (int i = 0; i < 2; ++i)
-        ok = ok && tmap_batched(&x_k[i], X[i], false, n, m, L.ldx, N, 64, 128) &&
-             tmap_batched(&x_n[i], X[i], false, n, m, L.ldx, N, 64, 64) &&
-             tmap_batched(&x_s[i], X[i], false, n, m, L.ldx, N, 32, 32);
+    NsMaps t;
+    auto map = [&](CUtensorMap* out, size_t at, int64_t cols, int64_t ld, int64_t batch, int rows) {
+        return tmap_batched(out, w + at, false, cols, m, ld, batch, rows);
+    };
+    bool ok = map(&t.a, L.A, m, L.lda, N, 128) && map(&t.a_t, L.A, m, L.lda, N, 64) &&
+              map(&t.b, L.B, m, L.lda, L.b_lo ? 2 * N : N, 128) && map(&t.b_t, L.B, m, L.lda, N, 64) &&
+              map(&t.x[0], L.x0, n, L.ldx, N, 128) && map(&t.x[1], L.x1, n, L.ldx, N, 128) &&
+              map(&t.x_t[0], L.x0, n, L.ldx, N, 64) && map(&t.x_t[1], L.x1, n, L.ldx, N, 64) &&
+              map(&t.lo, L.lo, n, L.ldx, N, 128);
     const bool o_box = C % 8 == 0;   // O's rows are multiples of 16 bytes
-    if (o_box) ok = ok && tmap_batched(&o_s, O, true, C, R, C, N, 32, 32);
+    t.o = t.o_t = t.a;
+    if (o_box) ok = ok && tmap_batched(&t.o, O, true, C, R, C, N, 128) && tmap_batched(&t.o_t, O, true, C, R, C, N, 64);
     if (!ok) return cudaErrorInvalidValue;
+    const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
+    int most = 0;
+    if ((err = pair ? ns_resident<true>(num_sms, &most) : ns_resident<false>(num_sms, &most)) != cudaSuccess) return err;
+    const int tile = pair ? 256 : 128, ctas = pair ? most / 2 : most;
     NsArgs a{};
-    a.m = (int)m; a.n = (int)n; a.lda = (int)L.lda; a.ldx = (int)L.ldx;
-    a.batch = (int)N;
+    a.m = (int)m; a.n = (int)n; a.N = (int)N;
+    a.steps = steps;
+    a.mt = (int)((m + tile - 1) / tile); a.nt = (int)((n + tile - 1) / tile);
+    a.tri = a.mt * (a.mt + 1) / 2; a.full = a.mt * a.nt;
+    // a wave and a quarter of triangle tiles in a half group, the groups equal: fewer and a phase waits for
+    // the last tiles of the one before, more and X leaves L2 in between (256 x 768 x 2048: 6.8, 6.2, 6.1, 6.2
+    // and 6.3 ms with 6, 9, 12, 20 and 64 matrices in a half)
+    const int64_t most_h = std::max<int64_t>(1, (5 * ctas + 4 * a.tri - 1) / (4 * a.tri));
+    a.supers = (int)((N + 2 * most_h - 1) / (2 * most_h));
+    a.halves = N > 1 ? 2 : 1;
+    a.h = (int)((N + a.halves * a.supers - 1) / (a.halves * a.supers));
+    a.supers = ((int)N + a.halves * a.h - 1) / (a.halves * a.h);
+    a.per_cycle = a.halves * a.h * (2 * a.tri + a.full);
+    a.cycles = a.supers * steps + (a.halves - 1);
+    if ((int64_t)a.cycles * a.per_cycle >= INT32_MAX) return cudaErrorInvalidValue;
+    a.units = a.cycles * a.per_cycle;
+    a.k_gram = (int)((n + 63) / 64); a.k_poly = (int)((m + 63) / 64);
+    a.b_lo = L.b_lo;
+    a.first_lo = g_f32;
+    a.out_kind = o_box ? (flip ? NS_O_BOX_FLIP : NS_O_BOX) : (flip ? NS_O_PLAIN_FLIP : NS_O_PLAIN);
+    std::copy(coeffs, coeffs + 3 * steps, a.co);
+    a.inv_s = reinterpret_cast<float*>(w + L.inv_s);
+    a.done = reinterpret_cast<int*>(w + L.done);
+    a.O = static_cast<__nv_bfloat16*>(O);
     a.status = status;
     a.wait_limit = wait_limit > 0 ? wait_limit : kWaitTimeoutCycles;
     a.withhold_loads = withhold_loads;
-    a.O = static_cast<__nv_bfloat16*>(O);
-    const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
-    const int tile = pair ? 256 : 128;
-    const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);
-    for (int s = 0; s < steps; ++s) {
-        const int cur = s & 1;
-        const bool last = s + 1 == steps;
-        a.a = coeffs[3 * s]; a.b = coeffs[3 * s + 1]; a.c = coeffs[3 * s + 2];
-        a.inv_s = s == 0 ? reinterpret_cast<float*>(w + L.inv_s) : nullptr;
-        a.tiles = mt * (mt + 1) / 2;
-        a.units = (int)N * a.tiles;
-        a.k_blocks = a.k_wrap = (int)((n + 63) / 64);
-        a.keep_lo = 0;
-        a.out_kind = NS_O_NONE;
-        err = pair ? ns_gemm<NS_GRAM, true>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a_s, a_s, a)
-                   : ns_gemm<NS_GRAM, false>(st, num_sms, x_k[cur], x_k[cur], a_s, a_s, a_s, a_s, a);
-        if (err != cudaSuccess) return err;
-        a.k_blocks = a.k_wrap = (int)((m + 63) / 64);
-        a.keep_lo = L.b_lo;
-        err = pair ? ns_gemm<NS_POLY, true>(st, num_sms, a_k, a_k, a_s, a_s, b_s, bl_s, a)
-                   : ns_gemm<NS_POLY, false>(st, num_sms, a_k, a_k, a_s, a_s, b_s, bl_s, a);
-        if (err != cudaSuccess) return err;
-        if (L.b_lo) a.k_blocks = 2 * a.k_wrap;
-        a.tiles_n = nt;
-        a.tiles = mt * nt;
-        a.units = (int)N * a.tiles;
-        a.xlo = (s == 0 ? g_f32 && !last : !last);
-        a.keep_lo = s + 2 < steps;   // the last step reads no rounding error, so the one before it keeps none
-        if (last) a.out_kind = o_box ? (flip ? NS_O_BOX_FLIP : NS_O_BOX) : (flip ? NS_O_PLAIN_FLIP : NS_O_PLAIN);
-        const CUtensorMap& out = last ? (o_box ? o_s : x_s[1 - cur]) : x_s[1 - cur];
-        err = pair ? ns_gemm<NS_APPLY, true>(st, num_sms, b_k, x_n[cur], x_s[cur], lo_s, out, lo_s, a)
-                   : ns_gemm<NS_APPLY, false>(st, num_sms, b_k, x_n[cur], x_s[cur], lo_s, out, lo_s, a);
-        if (err != cudaSuccess) return err;
-    }
-    return cudaSuccess;
+    return pair ? ns_steps<true>(st, most, t, a) : ns_steps<false>(st, most, t, a);
 }
 
 }  // namespace moe
