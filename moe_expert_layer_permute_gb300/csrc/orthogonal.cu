@@ -13,7 +13,7 @@
 // fp32.  Small singular values grow about 3.4-fold a step while X's rounding stays relative to its
 // largest ones, so X also keeps its rounding error as a second fp16 (`lo`, times 2^11 again) for the
 // a X term of every step but the last: without it gradients of low rank came out 1 % off, with it
-// 0.1 %.  A matrix of up to 128 rows keeps B's rounding error too, as a second product of APPLY: with few
+// 0.1 %.  A matrix of up to 64 rows keeps B's rounding error too, as a second product of APPLY: with few
 // singular values B's error does not average out (a single row came out up to 0.5 % off).
 #include <algorithm>
 #include <mutex>
@@ -242,6 +242,8 @@ struct NsArgs {
     int m, n, N, steps;
     int mt, nt;                  // tile rows and columns of X
     int tri, full;               // tiles of A's lower triangle, and of X
+    int tri_parts, full_parts;   // the CTAs that store a part of them (both of a pair, or the first where
+                                 // the second's rows are past the edge)
     int h, halves;               // matrices of a half group, half groups in flight (see ns_unit)
     int per_cycle, cycles, supers;
     int units;
@@ -251,7 +253,7 @@ struct NsArgs {
     int out_kind;                // NsOut
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
     const float* inv_s;          // [N]
-    int* done;                   // [N] tiles stored (each CTA of a pair counts its part)
+    int* done;                   // [N] parts of tiles stored
     __nv_bfloat16* O;
     int* status;
     long long wait_limit;
@@ -317,9 +319,10 @@ __device__ __forceinline__ NsUnit ns_unit(int unit, const NsArgs& a) {
     }
     return u;
 }
-// tiles of the matrix that come before the unit's phase
+// parts of tiles of the matrix that come before the unit's phase; a part is counted only after its
+// accumulator has been stored, which its own inputs precede, so the count never runs ahead of a phase
 __device__ __forceinline__ int ns_before(const NsUnit& u, const NsArgs& a) {
-    return u.step * (2 * a.tri + a.full) + u.mode * a.tri;
+    return u.step * (2 * a.tri_parts + a.full_parts) + u.mode * a.tri_parts;
 }
 
 // Chunk `at` (16 bytes) of row r of a box
@@ -395,7 +398,6 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     grid_dep_wait();
     constexpr int kTile = PAIR ? 256 : 128;      // rows and columns of a unit's tile
     constexpr int kOperand = 128 * 128;          // bytes of one operand's K slice per CTA: 128 x 64 fp16
-    constexpr int kParts = PAIR ? 2 : 1;         // CTAs that store a part of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull + b, 1);
-            mbar_init(tempty + b, kParts * kNsEpi);
+            mbar_init(tempty + b, (PAIR ? 2 : 1) * kNsEpi);
         }
         mbar_init(drain, 1);
         for (int i = 0; i < kNsSlots; ++i) {
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             bool ok = true;
             for (int unit = unit0; unit < a.units && ok; unit += stride, ++q) {
                 const NsUnit t = ns_unit(unit, a);
-                const int need = t.valid ? kParts * ns_before(t, a) : 0;
+                const int need = t.valid ? ns_before(t, a) : 0;
                 if (need > 0 && ld_acquire_gpu(a.done + t.mat) < need) {
                     const long long t0 = clock64();
                     while (ld_acquire_gpu(a.done + t.mat) < need) {
@@ -670,10 +672,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                     }
                 }
                 if (!ok) break;
-                if (p.chunks > 0) {
-                    bulk_wait_read<0>();
-                    mbar_arrive(box_free + (k - 1) % kNsSlots);
-                }
+                if (p.chunks == 0) continue;   // not counted: it would be before its turn
+                bulk_wait_read<0>();
+                mbar_arrive(box_free + (k - 1) % kNsSlots);
                 if (!p.out_kind) {
                     // this CTA's part of the tile is stored, and visible to whoever sees the count
                     bulk_wait_all();
@@ -827,7 +828,6 @@ __global__ void __launch_bounds__(kNsThreads, 1)
 // 64 columns that GRAM reads along K are, unchanged, what APPLY reads along N.  Per step:
 //   partial A over the CTA's columns -> the cluster's sum, each CTA adding the rows it owns in the CTAs'
 //   order and sending them to all as fp16 -> A A and B in every CTA -> X of the CTA's columns.
-// B enters as fp16 and its rounding error as in the large kernels.
 constexpr int kSmallCols = 256;
 constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
 constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
@@ -906,8 +906,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     if (S > 1) {
         if (threadIdx.x == 0) *my_sum = sq;
         cluster_sync();
+        float part[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) part[b] = b < S ? ld_cluster_f32(cluster_addr(my_sum, b)) : 0.f;
         sq = 0.f;
-        for (int b = 0; b < S; ++b) sq += ld_cluster_f32(cluster_addr(my_sum, b));
+#pragma unroll
+        for (int b = 0; b < 8; ++b) sq += part[b];
     }
     float is;
     const float f = ns_split(sqrtf(sq), a.eps, &is) * kXScale;
@@ -919,6 +923,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     const uint32_t tA = tmem, tP = tmem + 128, tX = tmem + 256;
     const int kx = min(4, max(0, (a.n - rank * kSmallCols + 63) / 64));   // chunks of X that hold columns
     const int km = (a.m + 15) / 16;                                       // MMA steps along m
+    const int b_parts = a.m <= 64 ? 2 : 1;                                // B, and its rounding error
     constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdX = idesc_f16(128, 256, false, true);
     uint32_t phase = 0;
     // every thread after its product's commit; on a wait that ran out the rest goes through without waiting,
@@ -940,7 +945,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     for (int s = 0; s < a.steps; ++s) {
         const float ca = a.co[3 * s], cb = a.co[3 * s + 1], cc = a.co[3 * s + 2];
         const float fa = kABScale / (kXScale * kXScale) * is * is;
-        fence_proxy_async_all();
+        fence_proxy_async_cta();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -988,10 +993,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             for (int e = threadIdx.x; e < rows * 32; e += kSmallThreads) {
                 const int r = rank * rows + (e >> 5), at = e & 31;
                 const uint32_t off = (uint32_t)(r * 512 + ((at ^ (r & 31)) << 4));
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int b = 0; b < S; ++b) {
-                    const float4 v = ld_cluster_f32x4(cluster_addr(sP, b) + off);
-                    sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+                float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int b = 0; b < 8; ++b)   // all under way before the first is added
+                    v[b] = b < S ? ld_cluster_f32x4(cluster_addr(sP, b) + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    sum.x += v[b].x; sum.y += v[b].y; sum.z += v[b].z; sum.w += v[b].w;
                 }
                 const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
                 const uint32_t to = (uint32_t)((at >> 4) * 16384) + ns_sw(r, (at & 15) >> 1) + (at & 1) * 8;
@@ -1031,15 +1039,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
                     lo[e] = ns_pack_half(b0 - r.x, b1 - r.y);
                 }
                 st_shared_v4(bP + to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                if (b_parts == 2) st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
         }
-        fence_proxy_async_all();
+        fence_proxy_async_cta();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         if (threadIdx.x == 0 && !a.withhold) {
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < b_parts; ++part)
                 for (int ks = 0; ks < km; ++ks)
                     mma_bf16(tX, sdesc_sw128(bP + part * kSmallA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
                              sdesc_sw128(bX + ks * 2048, 16384, 1024), kIdX, (part | ks) != 0);
@@ -1127,7 +1135,7 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     L->inv_s = take((size_t)N * 4);
     L->done = take((size_t)N * 4);
     L->A = take((size_t)N * L->m * L->lda * 2);
-    L->b_lo = L->m <= 128;
+    L->b_lo = L->m <= 64;
     L->B = take((size_t)N * (L->b_lo ? 2 : 1) * L->m * L->lda * 2);
     L->x0 = take((size_t)N * L->m * L->ldx * 2);
     L->x1 = take((size_t)N * L->m * L->ldx * 2);
@@ -1276,6 +1284,9 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     a.steps = steps;
     a.mt = (int)((m + tile - 1) / tile); a.nt = (int)((n + tile - 1) / tile);
     a.tri = a.mt * (a.mt + 1) / 2; a.full = a.mt * a.nt;
+    const bool one_sided = pair && m - (int64_t)(a.mt - 1) * tile <= 128;   // the last tile row
+    a.tri_parts = (pair ? 2 : 1) * a.tri - (one_sided ? a.mt : 0);
+    a.full_parts = (pair ? 2 : 1) * a.full - (one_sided ? a.nt : 0);
     // a wave and a quarter of triangle tiles in a half group, the groups equal: fewer and a phase waits for
     // the last tiles of the one before, more and X leaves L2 in between (256 x 768 x 2048: 6.8, 6.2, 6.1, 6.2
     // and 6.3 ms with 6, 9, 12, 20 and 64 matrices in a half)
