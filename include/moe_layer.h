@@ -128,7 +128,7 @@ typedef struct {
 #define MOE_ERR_LAYOUT       -4   /* rows not contiguous / innermost stride != 1 */
 #define MOE_ERR_ALIGN        -5   /* a pointer or row pitch is not 16-byte aligned */
 #define MOE_ERR_SCRATCH      -6   /* scratch missing, too small, misaligned or made for another desc */
-#define MOE_ERR_STATE        -7   /* MOE_FLAG_REUSE_FWD without a matching saved forward */
+#define MOE_ERR_STATE        -7   /* MOE_FLAG_REUSE_FWD without a matching saved forward; a used workspace */
 #define MOE_ERR_UNSUPPORTED  -8   /* precision or size outside what this build supports */
 #define MOE_ERR_CUDA         -9   /* a CUDA runtime call or kernel launch failed */
 #define MOE_ERR_DEVICE       -10  /* the device status word holds a MOE_DEV_* code */
@@ -215,7 +215,10 @@ int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const m
  *   [B], loss fp32 [B, 2].  mask: uint8 [T] or NULL (every token counts); seg_offsets: int32 [B+1],
  *   ascending (tokens before the first or past the last offset count nowhere), or NULL for one
  *   segment of all tokens (B = 1).  `workspace` is a zeroed moe_scratch handle of at least
- *   moe_balance_workspace_bytes(T, E, B) bytes, 256-byte aligned; its desc is not read.
+ *   moe_balance_workspace_bytes(T, E, B) bytes, 256-byte aligned, which the caller has set to zero once
+ *   (every call leaves zeros, so calls of any sizes may follow; seg_offsets that descend may not, and the
+ *   buffer has to be zeroed again); its desc is not read.  MOE_ERR_STATE for one that moe_orthogonalise
+ *   has used.
  * moe_balance_bwd: dlogits fp32 [T, E] (overwritten) of sum_s dloss[s] . loss[s], counts taken as
  *   constants, plus, with topk_w and dtopk_w (both or neither), what moe_router_bwd gives for them, in
  *   the same pass:

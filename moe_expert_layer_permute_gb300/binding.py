@@ -215,13 +215,13 @@ class Scratch:
 
 class Workspace:
     """A caller-owned device buffer and its C handle for moe_balance_fwd and moe_orthogonalise (their
-    *_workspace_bytes); moe_read_device_status takes it as it takes a Scratch."""
+    *_workspace_bytes); moe_read_device_status takes it as it takes a Scratch.  One that moe_orthogonalise
+    has used is no longer zero, and moe_balance_fwd refuses it."""
 
     def __init__(self, nbytes: int, device="cuda"):
         if nbytes <= 0:
             raise MoeError(ERR["MOE_ERR_UNSUPPORTED"], "Workspace")
-        self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        self.buffer[:256].zero_()        # the status word
+        self.buffer = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         self.handle = MoeScratch()
         self.handle.data = self.buffer.data_ptr()
         self.handle.bytes = nbytes

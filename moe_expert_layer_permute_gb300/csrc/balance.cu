@@ -9,8 +9,11 @@
 //             + w_j (dw_j - sum_i w_i dw_i) where e is the token's pick j
 // The counts carry no gradient.
 //
-// Both directions read each logit once and are bound by memory at large T * E and by launches below.
-// A warp holds one token's row in registers (E / 32 values a lane), so the softmax takes one pass.
+// Both directions are one launch, read each logit once and are bound by memory at large T * E.  W lanes
+// (the least power of two with 16 values a lane, 32 for more than 512 experts) hold one token's row in
+// registers, so the softmax takes one pass and a warp works on 32 / W tokens at once: with a warp to a token
+// the shuffles of its sums were most of the instructions (16,384 x 128: 9.4 and 8.3 us, against 3.7 of
+// memory time).
 #include <algorithm>
 
 #include "common.cuh"
@@ -18,43 +21,50 @@
 
 namespace moe {
 
-constexpr int kBalWarps = 16;         // forward: warps (tokens in flight) per block
 constexpr int kBalMaxChunks = 304;    // forward: most blocks (two per SM)
 constexpr int kBalMinChunk = 32;      // forward: fewest tokens per block
-constexpr int kFinCols = 128;         // finish: columns per block
-constexpr int kFinGroups = 8;         // finish: slot groups per block
 constexpr int kBwdWarps = 8;
+// forward: warps per block; two blocks an SM hold 32 warps where a warp has one row of up to 512 values at
+// a time, which the memory needs then (131,072 x 512: 76 us with eight)
+template <int W, int V>
+constexpr int bal_warps() { return W == 32 && V == 16 ? 16 : 8; }
+// blocks an SM: at most 64 registers for 16 values a lane, 128 for 32 (the backward of 131,072 x 512: 145 us
+// with the 80 registers that the compiler would take, 102 with 64)
+template <int V>
+constexpr int bal_blocks_sm() { return V == 16 ? 4 : 2; }
 
 __device__ __forceinline__ float bal_warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float bal_warp_max(float v) {
+template <int W>
+__device__ __forceinline__ float bal_group_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Column of a lane's value i: with 16-byte rows (E % 4 == 0) four consecutive columns per load,
-// otherwise every 32nd.
-template <bool VEC>
-__device__ __forceinline__ int bal_col(int lane, int i) {
-    return VEC ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i;
+// Column of lane gl's value i (of W lanes): with 16-byte rows (E % 4 == 0) four consecutive columns per
+// load, otherwise every W-th.
+template <int W, bool VEC>
+__device__ __forceinline__ int bal_col(int gl, int i) {
+    return VEC ? 4 * (gl + W * (i >> 2)) + (i & 3) : gl + W * i;
 }
-// the lane's C values of a row; columns past E read as -inf (p = 0)
-template <int C, bool VEC>
-__device__ __forceinline__ void bal_load(float* x, const float* row, int E, int lane) {
+// the lane's V values of a row; columns past E, and all of a row that is not there, read as -inf (p = 0)
+template <int W, int V, bool VEC>
+__device__ __forceinline__ void bal_load(float* x, const float* row, int E, int gl, bool there) {
     if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < C; i += 4) {
+        for (int i = 0; i < V; i += 4) {
             float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (bal_col<VEC>(lane, i) < E) v = __ldg(reinterpret_cast<const float4*>(row + bal_col<VEC>(lane, i)));
+            if (there && bal_col<W, VEC>(gl, i) < E) v = __ldg(reinterpret_cast<const float4*>(row + bal_col<W, VEC>(gl, i)));
             x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = bal_col<VEC>(lane, i) < E ? __ldg(row + bal_col<VEC>(lane, i)) : -INFINITY;
+        for (int i = 0; i < V; ++i)
+            x[i] = there && bal_col<W, VEC>(gl, i) < E ? __ldg(row + bal_col<W, VEC>(gl, i)) : -INFINITY;
     }
 }
 // Segment bounds, held inside [0, T]; without offsets one segment holds every token.
@@ -71,172 +81,210 @@ __device__ __forceinline__ int bal_segment(const int* off, int B, int T, int t) 
     return lo;
 }
 
-// Block c takes tokens [c chunk, (c+1) chunk) and writes one slot of sums for each segment that it
-// meets.  Going through the tokens in order, each chunk end and each segment end advances the slot
-// by one, so slot c + s belongs to this pair alone and chunks + B slots hold them all: no atomics on
-// floats, and sums in an order that depends on the sizes only.
+// The softmax of a group's row: x becomes exp(x - max).  A row of -inf alone has none: p = 0, lse taken as
+// 0.  All lanes of the warp take part.
+struct BalRow {
+    float inv, lse;   // 1 / sum, log-sum-exp
+    float max;
+};
+template <int W, int V>
+__device__ __forceinline__ BalRow bal_softmax(float* x) {
+    BalRow r;
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bool none = m == -INFINITY;
+    if (__any_sync(0xffffffffu, none)) {   // fmaxf passes over NaN: a row of -inf and NaN is NaN
+        int bad = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) bad |= isnan(x[i]);
+#pragma unroll
+        for (int o = W / 2; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        none = none && !bad;
+    }
+    r.max = m;
+    const float base = none ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = __expf(x[i] - base);   // 0 for -inf
+        sum += x[i];
+    }
+    sum = bal_group_sum<W>(sum);
+    r.inv = none ? 0.f : 1.f / sum;
+    r.lse = none ? 0.f : m + logf(sum);
+    return r;
+}
+
+// Forward.  Block c takes tokens [c chunk, (c+1) chunk), and of each segment that it meets sums p, the
+// picks, lse^2 and the tokens: a piece.  A segment inside one block is finished there.  The pieces of a
+// longer one are joined in `workspace`, where the sums of p are held as 64-bit integers, times 2^32 (p sums
+// to at most T < 2^26), and the counts as integers: integers add up to the same in any order, and the block
+// that comes last finishes the segment and leaves zeros for the next call.  The sums of lse^2, which have
+// no such bound, are kept apart, one for each piece (block c's piece of segment s at c + s, which no other
+// has: going through the tokens each block's end and each segment's end advances it by one), and added in
+// order.  One launch: a second one that added 304 blocks' partial sums took 11 us at 128 experts.
 struct BalArgs {
     const float* logits;
     const int* idx;
     const uint8_t* mask;
     const int* off;
     int T, E, k, B, chunk;
-    float* P;      // [slots, E] sum of p
-    int* C;        // [slots, E] picks
-    float* Z;      // [slots] sum of lse^2
-    int* N;        // [slots] counted tokens
+    unsigned long long* P;   // [B, E] sum of p, 2^32 to one; all five are zero between calls, so that calls of
+                             // other sizes may share the workspace
+    int* C;                  // [B, E] picks
+    int* N;                  // [B] counted tokens
+    int* ticket;             // [B] pieces joined
+    float* Z;                // [chunks + B] a piece's sum of lse^2
+    int* counts;
+    int* tokens;
+    float* loss;
 };
+constexpr float kBalFix = 4294967296.f;   // 2^32
 
-template <int C, bool VEC>
-__global__ void __launch_bounds__(32 * kBalWarps) balance_fwd_kernel(const BalArgs a) {
+// Sum over a block, the same on every thread.
+template <int kWarps>
+__device__ __forceinline__ float bal_block_sum(float v, float* part) {
+    v = bal_warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += part[w];
+    return v;
+}
+
+template <int W, int V, bool VEC>
+__global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8 / bal_warps<W, V>()) balance_fwd_kernel(const BalArgs a) {
     grid_dep_wait();
+    constexpr int kWarps = bal_warps<W, V>();
     extern __shared__ float sm[];
-    float* red = sm;                                            // [kBalWarps][E]
-    int* hist = reinterpret_cast<int*>(red + kBalWarps * a.E);  // [E]
-    __shared__ float zred[kBalWarps];
-    __shared__ int nred[kBalWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* red = sm;                                            // [kWarps][E]
+    int* hist = reinterpret_cast<int*>(red + kWarps * a.E);  // [E]
+    __shared__ float part[kWarps];
+    __shared__ int npart[kWarps];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % W;
     const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    for (int s = bal_segment(a.off, a.B, a.T, t0); s < a.B; ++s) {
-        const int s0 = bal_off(a.off, s, a.T);
-        if (s0 >= t1) break;
-        const int lo = max(s0, t0), hi = min(bal_off(a.off, s + 1, a.T), t1);
-        if (lo >= hi) continue;
-        const long long slot = blockIdx.x + s;
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
-        float acc[C];
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] = 0.f;
-        float z2 = 0.f;
-        int n = 0;
-        for (int t = lo + warp; t < hi; t += kBalWarps) {
-            if (a.mask && !__ldg(a.mask + t)) continue;
-            ++n;
-            float x[C];
-            bal_load<C, VEC>(x, a.logits + (long long)t * a.E, a.E, lane);
-            float m = x[0];
-#pragma unroll
-            for (int i = 1; i < C; ++i) m = fmaxf(m, x[i]);
-            m = bal_warp_max(m);
-            float sum = 0.f;
-            // a row of -inf alone has no softmax: p = 0, and nothing is added to either loss
-            const bool none = m == -INFINITY;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                x[i] = none ? 0.f : __expf(x[i] - m);
-                sum += x[i];
+    // a segment without tokens meets no block: the blocks share these out
+    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
+        if (bal_off(a.off, s, a.T) >= bal_off(a.off, s + 1, a.T)) {
+            for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(long long)s * a.E + e] = 0;
+            if (threadIdx.x == 0) {
+                a.tokens[s] = 0;
+                a.loss[2 * s] = a.loss[2 * s + 1] = 0.f;
             }
-            sum = bal_warp_sum(sum);
-            const float inv = none ? 0.f : 1.f / sum;
-            const float lse = none ? 0.f : m + logf(sum);
-            z2 += lse * lse;
+        }
+    for (int s = bal_segment(a.off, a.B, a.T, t0); s < a.B; ++s) {
+        const int s0 = bal_off(a.off, s, a.T), s1 = bal_off(a.off, s + 1, a.T);
+        if (s0 >= t1) break;
+        const int lo = max(s0, t0), hi = min(s1, t1);
+        if (lo >= hi) continue;
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+        float acc[V], z2 = 0.f;
+        int n = 0;
 #pragma unroll
-            for (int i = 0; i < C; ++i) acc[i] += x[i] * inv;
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        constexpr int G = 32 / W;   // tokens of a warp
+        for (int tw = lo + warp * G; tw < hi; tw += kWarps * G) {
+            const int t = tw + lane / W;
+            const bool counts = t < hi && !(a.mask && !__ldg(a.mask + t));
+            float x[V];
+            bal_load<W, V, VEC>(x, a.logits + (long long)t * a.E, a.E, gl, counts);
+            const BalRow r = bal_softmax<W, V>(x);   // (nothing where the token does not count)
+            n += counts && gl == 0;
+            z2 += gl == 0 ? r.lse * r.lse : 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += x[i] * r.inv;
         }
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (bal_col<VEC>(lane, i) < a.E) red[warp * a.E + bal_col<VEC>(lane, i)] = acc[i];
+        for (int i = 0; i < V; ++i) {   // the warp's tokens together; the first group holds them
+#pragma unroll
+            for (int o = W; o < 32; o *= 2) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            if (lane < W && bal_col<W, VEC>(gl, i) < a.E) red[warp * a.E + bal_col<W, VEC>(gl, i)] = acc[i];
+        }
+        z2 = bal_warp_sum(z2);
+        n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) {
-            zred[warp] = z2;
-            nred[warp] = n;
+            part[warp] = z2;
+            npart[warp] = n;
         }
         __syncthreads();
+        const bool masked = a.mask != nullptr;
         for (long long i = (long long)lo * a.k + threadIdx.x; i < (long long)hi * a.k; i += blockDim.x) {
             const int e = __ldg(a.idx + i);
-            if ((unsigned)e < (unsigned)a.E && (!a.mask || __ldg(a.mask + i / a.k))) atomicAdd(hist + e, 1);
+            if ((unsigned)e < (unsigned)a.E && (!masked || __ldg(a.mask + i / a.k))) atomicAdd(hist + e, 1);
+        }
+        z2 = 0.f;
+        n = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            z2 += part[w];
+            n += npart[w];
         }
         __syncthreads();
+        const bool whole = lo == s0 && hi == s1;
+        unsigned long long* P = a.P + (long long)s * a.E;
+        int* K = a.C + (long long)s * a.E;
+        float dot = 0.f;   // sum_e c[e] sum_t p[t,e]
         for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kBalWarps; ++w) v += red[w * a.E + e];
-            a.P[slot * a.E + e] = v;
-            a.C[slot * a.E + e] = hist[e];
-        }
-        if (threadIdx.x == 0) {
-            float v = 0.f;
-            int c = 0;
-            for (int w = 0; w < kBalWarps; ++w) {
-                v += zred[w];
-                c += nred[w];
+            for (int w = 0; w < kWarps; ++w) v += red[w * a.E + e];
+            if (whole) {
+                a.counts[(long long)s * a.E + e] = hist[e];
+                dot += v * (float)hist[e];
+            } else {
+                atomicAdd(P + e, (unsigned long long)__float2ll_rn(v * kBalFix));
+                if (hist[e]) atomicAdd(K + e, hist[e]);
             }
-            a.Z[slot] = v;
-            a.N[slot] = c;
+        }
+        bool finish = whole;
+        if (!whole) {
+            const int c0 = s0 / a.chunk, c1 = (s1 - 1) / a.chunk;   // the blocks that share the segment
+            if (threadIdx.x == 0) {
+                a.Z[blockIdx.x + s] = z2;
+                atomicAdd(a.N + s, n);
+            }
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) last = atomicAdd(a.ticket + s, 1) == c1 - c0;
+            __syncthreads();
+            finish = last;
+            if (finish) {
+                __threadfence();
+                for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+                    const int c = atomicExch(K + e, 0);
+                    const float v = (float)((double)(long long)atomicExch(P + e, 0ull) * (1.0 / kBalFix));
+                    a.counts[(long long)s * a.E + e] = c;
+                    dot += v * (float)c;
+                }
+                z2 = 0.f;
+                for (int q = c0 + (int)threadIdx.x; q <= c1; q += blockDim.x) {
+                    z2 += __ldcg(a.Z + q + s);
+                    a.Z[q + s] = 0.f;
+                }
+                z2 = bal_block_sum<kWarps>(z2, part);
+                if (threadIdx.x == 0) {
+                    n = atomicExch(a.N + s, 0);
+                    a.ticket[s] = 0;
+                }
+            }
+        }
+        if (finish) {
+            dot = bal_block_sum<kWarps>(dot, part);
+            if (threadIdx.x == 0) {
+                const float inv = n > 0 ? 1.f / (float)n : 0.f;
+                if (isnan(z2)) dot = z2;   // a NaN in a counted row: the integer sums do not show it
+                a.tokens[s] = n;
+                a.loss[2 * s] = (float)a.E / (float)a.k * inv * inv * dot;
+                a.loss[2 * s + 1] = inv * z2;
+            }
         }
         __syncthreads();   // the next segment's sums reuse the arrays
     }
-}
-
-// Segment blockIdx.y: a cluster of ceil(E / 128) blocks, 128 columns each, adds the segment's slots
-// (eight groups of threads take every eighth, then the groups in order) and the first block joins the
-// blocks' parts of sum_e c[e] P[e] through distributed shared memory, in their order.
-__global__ void __launch_bounds__(kFinCols * kFinGroups) balance_finish_kernel(const BalArgs a, int* counts, int* tokens,
-                                                                              float* loss) {
-    grid_dep_wait();
-    __shared__ float sp[kFinGroups][kFinCols];
-    __shared__ int sc[kFinGroups][kFinCols];
-    __shared__ float sz[kFinCols * kFinGroups / 32];
-    __shared__ int sn[kFinCols * kFinGroups / 32];
-    __shared__ float part;
-    const int s = blockIdx.y, rank = blockIdx.x, blocks = gridDim.x;
-    const int col = threadIdx.x % kFinCols, grp = threadIdx.x / kFinCols;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = rank * kFinCols + col;
-    const int lo = bal_off(a.off, s, a.T), hi = bal_off(a.off, s + 1, a.T);
-    const int c0 = lo / a.chunk, c1 = hi > lo ? (hi - 1) / a.chunk : c0 - 1;
-    float p = 0.f, z = 0.f;
-    int c = 0, n = 0;
-    if (e < a.E) {
-#pragma unroll 8
-        for (int q = c0 + grp; q <= c1; q += kFinGroups) {
-            const long long at = (long long)(q + s) * a.E + e;
-            p += a.P[at];
-            c += a.C[at];
-        }
-    }
-    for (int q = c0 + (int)threadIdx.x; q <= c1; q += blockDim.x) {
-        z += a.Z[q + s];
-        n += a.N[q + s];
-    }
-    sp[grp][col] = p;
-    sc[grp][col] = c;
-    z = bal_warp_sum(z);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) {
-        sz[warp] = z;
-        sn[warp] = n;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        z = bal_warp_sum(sz[lane]);
-        n = __reduce_add_sync(0xffffffffu, sn[lane]);
-        float mine = 0.f;
-        for (int j = lane; j < kFinCols; j += 32) {
-            float v = 0.f;
-            int k = 0;
-#pragma unroll
-            for (int g = 0; g < kFinGroups; ++g) {
-                v += sp[g][j];
-                k += sc[g][j];
-            }
-            if (rank * kFinCols + j < a.E) {
-                counts[(long long)s * a.E + rank * kFinCols + j] = k;
-                mine += v * (float)k;
-            }
-        }
-        mine = bal_warp_sum(mine);
-        if (lane == 0) part = mine;
-    }
-    if (blocks > 1) cluster_sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        float total = part;
-        for (int b = 1; b < blocks; ++b) total += ld_cluster_f32(cluster_addr(&part, b));
-        const float inv = n > 0 ? 1.f / (float)n : 0.f;
-        tokens[s] = n;
-        loss[2 * s] = (float)a.E / (float)a.k * inv * inv * total;
-        loss[2 * s + 1] = inv * z;
-    }
-    if (blocks > 1) cluster_sync();   // the first block has read the others' parts before they exit
 }
 
 struct BalBwdArgs {
@@ -249,92 +297,84 @@ struct BalBwdArgs {
     const int* counts;
     const int* tokens;
     const float* dloss;
-    int T, E, k, B, per_warp;
+    int T, E, k, B, rounds;
     float* dlogits;
 };
 
-// One warp takes per_warp consecutive tokens and keeps its columns' share of the segment's counts,
-// db E / (k n^2) c[e], in registers while the segment lasts.
-template <int C, bool VEC>
-__global__ void __launch_bounds__(32 * kBwdWarps) balance_bwd_kernel(const BalBwdArgs a) {
+// Each group of W lanes takes `rounds` tokens, a warp's groups neighbouring ones.
+template <int W, int V, bool VEC>
+__global__ void __launch_bounds__(32 * kBwdWarps, bal_blocks_sm<V>()) balance_bwd_kernel(const BalBwdArgs a) {
     grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const long long first = ((long long)blockIdx.x * kBwdWarps + (threadIdx.x >> 5)) * a.per_warp;
+    constexpr int G = 32 / W;
+    const int lane = threadIdx.x & 31, gl = lane % W;
+    const long long first = ((long long)blockIdx.x * kBwdWarps + (threadIdx.x >> 5)) * a.rounds * G;
     if (first >= a.T) return;
-    const int t1 = (int)min((long long)a.T, first + a.per_warp);
     int s = bal_segment(a.off, a.B, a.T, (int)first);
     int held = -1;
-    float cf[C], scale = 0.f, zc = 0.f;
-    for (int t = (int)first; t < t1; ++t) {
-        while (s < a.B && bal_off(a.off, s + 1, a.T) <= t) ++s;
-        const bool counted = s < a.B && bal_off(a.off, s, a.T) <= t && !(a.mask && !__ldg(a.mask + t));
+    float cf[V], scale = 0.f, zc = 0.f;   // db E / (k n^2) c[e] of the lane's columns, that factor, 2 dz / n
+#pragma unroll
+    for (int i = 0; i < V; ++i) cf[i] = 0.f;
+    for (int q = 0; q < a.rounds; ++q) {
+        const long long tw = first + (long long)q * G;
+        if (tw >= a.T) break;
+        const int t = (int)tw + lane / W;
+        const bool live = t < a.T;
+        const float* row = a.logits + (long long)t * a.E;
         float* out = a.dlogits + (long long)t * a.E;
-        // the pick of this lane, and the top-k weights' gradient at it
-        int pick = -1;
-        float add = 0.f;
-        if (a.w) {
-            float w = 0.f, dw = 0.f;
-            if (lane < a.k) {
-                pick = __ldg(a.idx + (long long)t * a.k + lane);
-                w = __ldg(a.w + (long long)t * a.k + lane);
-                dw = __ldg(a.dw + (long long)t * a.k + lane);
+        if (live)
+            while (s < a.B && bal_off(a.off, s + 1, a.T) <= t) ++s;
+        const bool counts = live && s < a.B && bal_off(a.off, s, a.T) <= t && !(a.mask && !__ldg(a.mask + t));
+        float x[V];
+        bal_load<W, V, VEC>(x, row, a.E, gl, counts);
+        if (counts && held != s) {
+            held = s;
+            const int n = __ldg(a.tokens + s);
+            const float inv = n > 0 ? 1.f / (float)n : 0.f;
+            scale = __ldg(a.dloss + 2 * s) * ((float)a.E / (float)a.k) * inv * inv;
+            zc = __ldg(a.dloss + 2 * s + 1) * 2.f * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = bal_col<W, VEC>(gl, i);
+                cf[i] = e < a.E ? scale * (float)__ldg(a.counts + (long long)s * a.E + e) : 0.f;
             }
-            add = w * (dw - bal_warp_sum(w * dw));
-            if ((unsigned)pick >= (unsigned)a.E) pick = -1;
         }
-        float x[C];
-        if (counted) {
-            const float* row = a.logits + (long long)t * a.E;
-            if (held != s) {
-                held = s;
-                const int n = __ldg(a.tokens + s);
-                const float inv = n > 0 ? 1.f / (float)n : 0.f;
-                scale = __ldg(a.dloss + 2 * s) * ((float)a.E / (float)a.k) * inv * inv;
-                zc = __ldg(a.dloss + 2 * s + 1) * 2.f * inv;
+        const long long pk = (long long)t * a.k;
+        float wdw = 0.f;
+        if (a.w && live)
+            for (int j = gl; j < a.k; j += W) wdw += __ldg(a.w + pk + j) * __ldg(a.dw + pk + j);
+        wdw = bal_group_sum<W>(wdw);
+        __syncwarp();
+        const BalRow r = bal_softmax<W, V>(x);   // x is 0 where the token does not count
+        float dot = 0.f;
 #pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    const int e = bal_col<VEC>(lane, i);
-                    cf[i] = e < a.E ? scale * (float)__ldg(a.counts + (long long)s * a.E + e) : 0.f;
-                }
+        for (int i = 0; i < V; ++i) dot += x[i] * cf[i];
+        dot = bal_group_sum<W>(dot);
+        const float shift = zc * r.lse - dot * r.inv;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = counts ? x[i] * r.inv * (cf[i] + shift) : 0.f;
+            if constexpr (VEC) {
+#pragma unroll
+                for (int i = 0; i < V; i += 4)
+                    if (bal_col<W, VEC>(gl, i) < a.E)
+                        *reinterpret_cast<float4*>(out + bal_col<W, VEC>(gl, i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (bal_col<W, VEC>(gl, i) < a.E) out[bal_col<W, VEC>(gl, i)] = x[i];
             }
-            bal_load<C, VEC>(x, row, a.E, lane);
-            const float at_pick = pick >= 0 ? __ldg(row + pick) : 0.f;
-            float m = x[0];
-#pragma unroll
-            for (int i = 1; i < C; ++i) m = fmaxf(m, x[i]);
-            m = bal_warp_max(m);
-            const bool none = m == -INFINITY;
-            float sum = 0.f, dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                x[i] = none ? 0.f : __expf(x[i] - m);
-                sum += x[i];
-                dot += x[i] * cf[i];
-            }
-            sum = bal_warp_sum(sum);
-            dot = bal_warp_sum(dot);
-            const float inv = none ? 0.f : 1.f / sum;
-            const float shift = none ? 0.f : zc * (m + logf(sum)) - dot * inv;
-#pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = x[i] * inv * (cf[i] + shift);
-            if (pick >= 0 && !none)
-                add += __expf(at_pick - m) * inv * (scale * (float)__ldg(a.counts + (long long)s * a.E + pick) + shift);
-        } else {
-#pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = 0.f;
-        }
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < C; i += 4)
-                if (bal_col<VEC>(lane, i) < a.E)
-                    *reinterpret_cast<float4*>(out + bal_col<VEC>(lane, i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (bal_col<VEC>(lane, i) < a.E) out[bal_col<VEC>(lane, i)] = x[i];
         }
         __syncwarp();   // the row's values are ordered before the picks' that replace them
-        if (pick >= 0) out[pick] = add;
+        if (a.w && live)
+            for (int j = gl; j < a.k; j += W) {
+                const int e = __ldg(a.idx + pk + j);
+                if ((unsigned)e >= (unsigned)a.E) continue;
+                float v = __ldg(a.w + pk + j) * (__ldg(a.dw + pk + j) - wdw);
+                if (counts && r.inv != 0.f)
+                    v += __expf(__ldg(row + e) - r.max) * r.inv *
+                         (scale * (float)__ldg(a.counts + (long long)s * a.E + e) + shift);
+                out[e] = v;
+            }
     }
 }
 
@@ -342,42 +382,42 @@ __global__ void __launch_bounds__(32 * kBwdWarps) balance_bwd_kernel(const BalBw
 static int bal_chunk(int64_t T) {
     return (int)std::max<int64_t>(kBalMinChunk, (T + kBalMaxChunks - 1) / kBalMaxChunks);
 }
-static int64_t bal_slots(int64_t T, int64_t B) { return (T + bal_chunk(T) - 1) / bal_chunk(T) + B; }
+static size_t bal_blocks(int64_t T) { return (size_t)((T + bal_chunk(T) - 1) / bal_chunk(T)); }
 
+// the status word's line, then P, C, N, ticket, Z
 size_t balance_workspace(int64_t T, int64_t E, int64_t B) {
-    return (size_t)256 + (size_t)bal_slots(T, B) * (8 * (size_t)E + 8);   // 256: the status word's line
+    return 256 + (size_t)B * (12 * (size_t)E + 8) + 4 * (bal_blocks(T) + (size_t)B);
 }
 
-template <int C, bool VEC>
+template <int W, int V, bool VEC>
 static cudaError_t fwd_c(cudaStream_t st, const BalArgs& a) {
-    const size_t smem = (size_t)(kBalWarps + 1) * a.E * 4;
-    if constexpr (C == 32) {   // up to 68 KB; the smaller ones stay below 48 KB
-        static const cudaError_t err =
-            cudaFuncSetAttribute(balance_fwd_kernel<C, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kBalWarps + 1) * 32 * C * 4);
-        if (err != cudaSuccess) return err;
-    }
-    return launch_pdl(balance_fwd_kernel<C, VEC>, (a.T + a.chunk - 1) / a.chunk, 32 * kBalWarps, smem, st, a);
+    constexpr int kWarps = bal_warps<W, V>();
+    const size_t smem = (size_t)(kWarps + 1) * a.E * 4;   // at most 36 KB
+    // (with no tokens one block writes the zeros)
+    return launch_pdl(balance_fwd_kernel<W, V, VEC>, (unsigned)std::max<size_t>(1, bal_blocks(a.T)), 32 * kWarps, smem, st, a);
 }
-template <int C, bool VEC>
-static cudaError_t bwd_c(cudaStream_t st, const BalBwdArgs& a) {
-    const int warps = (a.T + a.per_warp - 1) / a.per_warp;
-    return launch_pdl(balance_bwd_kernel<C, VEC>, (warps + kBwdWarps - 1) / kBwdWarps, 32 * kBwdWarps, 0, st, a);
+template <int W, int V, bool VEC>
+static cudaError_t bwd_c(cudaStream_t st, BalBwdArgs a) {
+    // as many warps as the GPU holds at 32 an SM (152 SMs), each with so many rounds of tokens
+    constexpr int G = 32 / W;
+    const int groups = (a.T + G - 1) / G;
+    a.rounds = std::max(1, (groups + 152 * 32 - 1) / (152 * 32));
+    const int warps = (groups + a.rounds - 1) / a.rounds;
+    return launch_pdl(balance_bwd_kernel<W, V, VEC>, (warps + kBwdWarps - 1) / kBwdWarps, 32 * kBwdWarps, 0, st, a);
 }
-// values per lane: four at a time where rows are 16-byte aligned
-#define MOE_BAL_DISPATCH(fn, a)                         \
-    if ((a).E % 4 == 0) {                               \
-        if ((a).E <= 128) return fn<4, true>(st, a);    \
-        if ((a).E <= 256) return fn<8, true>(st, a);    \
-        if ((a).E <= 512) return fn<16, true>(st, a);   \
-        return fn<32, true>(st, a);                     \
-    }                                                   \
-    if ((a).E <= 32) return fn<1, false>(st, a);        \
-    if ((a).E <= 64) return fn<2, false>(st, a);        \
-    if ((a).E <= 128) return fn<4, false>(st, a);       \
-    if ((a).E <= 256) return fn<8, false>(st, a);       \
-    if ((a).E <= 512) return fn<16, false>(st, a);      \
-    return fn<32, false>(st, a);
+// lanes a token and values a lane
+#define MOE_BAL_DISPATCH_VEC(fn, a, VEC)                    \
+    if ((a).E <= 16) return fn<1, 16, VEC>(st, a);          \
+    if ((a).E <= 32) return fn<2, 16, VEC>(st, a);          \
+    if ((a).E <= 64) return fn<4, 16, VEC>(st, a);          \
+    if ((a).E <= 128) return fn<8, 16, VEC>(st, a);         \
+    if ((a).E <= 256) return fn<16, 16, VEC>(st, a);        \
+    if ((a).E <= 512) return fn<32, 16, VEC>(st, a);        \
+    return fn<32, 32, VEC>(st, a);
+// four values at a time where rows are 16-byte aligned
+#define MOE_BAL_DISPATCH(fn, a)                             \
+    if ((a).E % 4 == 0) { MOE_BAL_DISPATCH_VEC(fn, a, true) } \
+    MOE_BAL_DISPATCH_VEC(fn, a, false)
 
 static cudaError_t dispatch_fwd(cudaStream_t st, const BalArgs& a) { MOE_BAL_DISPATCH(fwd_c, a) }
 static cudaError_t dispatch_bwd(cudaStream_t st, const BalBwdArgs& a) { MOE_BAL_DISPATCH(bwd_c, a) }
@@ -386,40 +426,24 @@ cudaError_t launch_balance_fwd(cudaStream_t st, const float* logits, const int* 
                                const int* seg_offsets, int T, int E, int k, int B, int* counts, int* tokens, float* loss,
                                void* workspace) {
     BalArgs a{logits, topk_idx, mask, seg_offsets, T, E, k, B, bal_chunk(T)};
-    const size_t slots = bal_slots(T, B);
     char* w = static_cast<char*>(workspace) + 256;
-    a.P = reinterpret_cast<float*>(w);
-    a.C = reinterpret_cast<int*>(w + slots * E * 4);
-    a.Z = reinterpret_cast<float*>(w + slots * E * 8);
-    a.N = reinterpret_cast<int*>(w + slots * E * 8 + slots * 4);
-    if (T > 0) {
-        const cudaError_t err = dispatch_fwd(st, a);
-        if (err != cudaSuccess) return err;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (E + kFinCols - 1) / kFinCols;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((E + kFinCols - 1) / kFinCols, B);
-    cfg.blockDim = dim3(kFinCols * kFinGroups);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, balance_finish_kernel, a, counts, tokens, loss);
+    const size_t be = (size_t)B * E;
+    a.P = reinterpret_cast<unsigned long long*>(w);
+    a.C = reinterpret_cast<int*>(w + be * 8);
+    a.N = a.C + be;
+    a.ticket = a.N + B;
+    a.Z = reinterpret_cast<float*>(a.ticket + B);
+    a.counts = counts;
+    a.tokens = tokens;
+    a.loss = loss;
+    return dispatch_fwd(st, a);
 }
 
 cudaError_t launch_balance_bwd(cudaStream_t st, const float* logits, const int* topk_idx, const float* topk_w,
                                const float* dtopk_w, const uint8_t* mask, const int* seg_offsets, const int* counts,
                                const int* tokens, const float* dloss, int T, int E, int k, int B, float* dlogits) {
     if (T == 0) return cudaSuccess;
-    // as many warps as the GPU holds at 32 warps an SM (152 SMs), each with a run of tokens
-    const int per_warp = std::max(1, (T + 152 * 32 - 1) / (152 * 32));
-    const BalBwdArgs a{logits, topk_idx, topk_w, dtopk_w, mask, seg_offsets, counts, tokens, dloss, T, E, k, B, per_warp,
-                       dlogits};
+    const BalBwdArgs a{logits, topk_idx, topk_w, dtopk_w, mask, seg_offsets, counts, tokens, dloss, T, E, k, B, 0, dlogits};
     return dispatch_bwd(st, a);
 }
 

@@ -563,6 +563,7 @@ int moe_balance_fwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
     if ((rc = check_tensor(tokens, MOE_DT_I32, 1, B, 0, 0))) return rc;
     if ((rc = check_tensor(loss, MOE_DT_F32, 2, B, 2, 0))) return rc;
     if ((rc = check_workspace(workspace, balance_workspace(T, E, B)))) return rc;
+    if (workspace->state[0] != 0) return MOE_ERR_STATE;   // not zero any more
     MOE_TRY_CUDA(launch_balance_fwd(
         reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const float*>(logits->data),
         reinterpret_cast<const int*>(topk_idx->data), mask ? reinterpret_cast<const uint8_t*>(mask->data) : nullptr,
@@ -628,6 +629,7 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
         if (!(co[i] >= -16.f && co[i] <= 16.f)) return MOE_ERR_UNSUPPORTED;
     }
     if (N == 0) return MOE_OK;
+    workspace->state[0] = 1;   // holds data: moe_balance_fwd refuses it
     const int nsm = num_sms_current();
     if (nsm <= 0) return MOE_ERR_CUDA;
     MOE_TRY_CUDA(launch_orthogonalise(reinterpret_cast<cudaStream_t>(stream), G->data, f32, N, R, C, O->data, steps, co, eps,
@@ -646,7 +648,7 @@ const char* moe_strerror(int code) {
         case MOE_ERR_LAYOUT: return "a tensor is not contiguous row-major";
         case MOE_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case MOE_ERR_SCRATCH: return "scratch missing, misaligned or smaller than moe_scratch_bytes";
-        case MOE_ERR_STATE: return "MOE_FLAG_REUSE_FWD without a matching forward saved in scratch";
+        case MOE_ERR_STATE: return "MOE_FLAG_REUSE_FWD without a matching forward saved in scratch, or a workspace that is no longer zero";
         case MOE_ERR_UNSUPPORTED: return "precision or size not supported";
         case MOE_ERR_CUDA: return "a CUDA call or kernel launch failed";
         case MOE_ERR_DEVICE: return "the device status word reports an error";

@@ -69,7 +69,7 @@ def dev(a):
     return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
-def run(bd, logits, idx, w, dw, dloss, mask=None, offsets=None):
+def run(bd, logits, idx, w, dw, dloss, mask=None, offsets=None, ws=None):
     T, E = logits.shape
     B = dloss.shape[0]
     counts = torch.full((B, E), -7, dtype=torch.int32, device="cuda")
@@ -77,8 +77,9 @@ def run(bd, logits, idx, w, dw, dloss, mask=None, offsets=None):
     loss = torch.full((B, 2), float("nan"), device="cuda")
     dl = torch.full((T, E), float("nan"), device="cuda")
     lg, ix, mk, off = dev(logits), dev(idx), dev(mask), dev(offsets)
-    bd.moe_balance_fwd(lg, ix, counts, tokens, loss, bd.Workspace(bd.moe_balance_workspace_bytes(T, E, B)), mask=mk,
-                       seg_offsets=off)
+    ws = ws or bd.Workspace(bd.moe_balance_workspace_bytes(T, E, B))
+    bd.moe_balance_fwd(lg, ix, counts, tokens, loss, ws, mask=mk, seg_offsets=off)
+    assert not ws.buffer.any()                   # as the next call wants it
     bd.moe_balance_bwd(lg, ix, dev(w), dev(dw), counts, tokens, dev(dloss), dl, mask=mk, seg_offsets=off)
     torch.cuda.synchronize()
     return counts.cpu().numpy(), tokens.cpu().numpy(), loss.cpu().numpy(), dl.cpu().numpy()
@@ -252,3 +253,18 @@ def test_captured_in_a_graph(cuda_lib):
     torch.cuda.synchronize()
     ref = reference(fresh, idx, w, dw, losses(1, 20), None, None)
     check((counts.cpu().numpy(), tokens.cpu().numpy(), loss.cpu().numpy(), dl.cpu().numpy()), ref)
+
+
+def test_one_workspace_for_calls_of_all_sizes(cuda_lib):
+    """A call leaves the workspace as the next one, of whatever sizes, needs it, a row of NaN included."""
+    bd = cuda_lib
+    ws = bd.Workspace(bd.moe_balance_workspace_bytes(20000, 1024, 40))
+    for T, E, k, B, bad in [(20000, 8, 2, 1, False), (300, 1024, 4, 40, False), (9000, 130, 8, 3, True), (20000, 512, 8, 1, False)]:
+        logits, idx, w, dw = make(T, E, k, seed=E)
+        offsets = None if B == 1 else np.linspace(0, T, B + 1).astype(np.int32)
+        d = losses(B, 22)
+        if bad:
+            logits[T // 2] = np.nan
+            assert np.isnan(run(bd, logits, idx, w, dw, d, None, offsets, ws)[2]).any()
+        else:
+            check(run(bd, logits, idx, w, dw, d, None, offsets, ws), reference(logits, idx, w, dw, d, None, offsets))

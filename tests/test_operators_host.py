@@ -58,6 +58,9 @@ def test_balance_refuses_layouts_workspaces_and_halves(bd):  # noqa: F811
     assert _fwd(bd, a, _ws(bd, need - 1)) == E["MOE_ERR_SCRATCH"]
     assert _fwd(bd, a, _ws(bd, need, 64)) == E["MOE_ERR_SCRATCH"]
     assert _fwd(bd, a, None) == E["MOE_ERR_NULL"]
+    used = _ws(bd, need)
+    used.state[0] = 1                     # moe_orthogonalise has left data there
+    assert _fwd(bd, a, used) == E["MOE_ERR_STATE"]
     for name in ("logits", "idx", "counts", "tokens", "loss"):
         f, a = _balance(bd)
         a[name] = None
