@@ -138,15 +138,18 @@ def _arg(t):
     """A tensor (or None) as the bytes of a moe_tensor."""
     if t is None:
         return None
-    shape, stride, n = t.shape, t.stride(), t.dim()
-    ptr = t.data_ptr()                  # 0 for an empty tensor
-    dt = _DT.get(t.dtype, -1)
+    if not t.is_cuda:
+        raise MoeError(ERR["MOE_ERR_NULL"], "a tensor that is not on a CUDA device")
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    ptr, dt = t.data_ptr(), _DT.get(t.dtype, -1)      # 0 for an empty tensor, -1 for no moe_dtype
     if n == 2:
         return _TENSOR.pack(ptr, dt, 2, shape[0], shape[1], 0, stride[0], stride[1], 0)
+    if n == 1:
+        return _TENSOR.pack(ptr, dt, 1, shape[0], 0, 0, stride[0], 0, 0)
     if n == 3:
         return _TENSOR.pack(ptr, dt, 3, *shape, *stride)
-    pad = (0,) * max(0, 3 - n)
-    return _TENSOR.pack(ptr, dt, n, *shape[:3], *pad, *stride[:3], *pad)
+    return _TENSOR.pack(ptr, dt, n, 0, 0, 0, 0, 0, 0)  # refused by its ndim
 
 
 def _packed(name: str, tensors: int, rest: list):
