@@ -906,12 +906,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     if (S > 1) {
         if (threadIdx.x == 0) *my_sum = sq;
         cluster_sync();
-        float part[8];
+        float part[16];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) part[b] = b < S ? ld_cluster_f32(cluster_addr(my_sum, b)) : 0.f;
+        for (int b = 0; b < 16; ++b) part[b] = b < S ? ld_cluster_f32(cluster_addr(my_sum, b)) : 0.f;
         sq = 0.f;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) sq += part[b];
+        for (int b = 0; b < 16; ++b) sq += part[b];
     }
     float is;
     const float f = ns_split(sqrtf(sq), a.eps, &is) * kXScale;
@@ -994,12 +994,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
                 const int r = rank * rows + (e >> 5), at = e & 31;
                 const uint32_t off = (uint32_t)(r * 512 + ((at ^ (r & 31)) << 4));
                 float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int b0 = 0; b0 < S; b0 += 8) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b)   // all under way before the first is added
-                    v[b] = b < S ? ld_cluster_f32x4(cluster_addr(sP, b) + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int b = 0; b < 8; ++b)   // all under way before the first is added
+                        v[b] = b0 + b < S ? ld_cluster_f32x4(cluster_addr(sP, b0 + b) + off) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    sum.x += v[b].x; sum.y += v[b].y; sum.z += v[b].z; sum.w += v[b].w;
+                    for (int b = 0; b < 8; ++b) {
+                        sum.x += v[b].x; sum.y += v[b].y; sum.z += v[b].z; sum.w += v[b].w;
+                    }
                 }
                 const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
                 const uint32_t to = (uint32_t)((at >> 4) * 16384) + ns_sw(r, (at & 15) >> 1) + (at & 1) * 8;
@@ -1102,12 +1105,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 }
 
 // ---- launches --------------------------------------------------------------------------------------
-// CTAs of a cluster for a matrix that ns_small_kernel takes, 0 for one that it does not
-static int ns_small_cluster(int64_t m, int64_t n) {
-    if (m > 128) return 0;
+// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others.  One or two take any number of
+// matrices; of more CTAs the kernel runs about 48 us however few there are, and for over two rounds of the
+// GPU's SMs the large kernels are faster (128 x 2048, 1, 16, 32, 128 matrices: 48, 96, 144, 440 us here and
+// 113, 127, 174, 419 there; 100 x 700, 256 matrices: 552 and 360; 32 x 512, 256 matrices: 149 and 188).
+static int ns_small_cluster(int64_t N, int64_t m, int64_t n) {
+    if (m > 128 || n > 16 * kSmallCols) return 0;
     int S = 1;
     while (S * kSmallCols < n) S *= 2;
-    return S <= 8 ? S : 0;
+    return S <= 2 || N * S <= 304 ? S : 0;
 }
 
 struct NsLayout {
@@ -1127,7 +1133,8 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
     take(256);   // status word
-    if (ns_small_cluster(L->m, L->n)) {
+    const int S = ns_small_cluster(N, L->m, L->n);
+    if (S > 0 && S <= 8) {   // (whether a cluster of 16 is possible only the GPU can tell)
         L->total = o;
         return true;
     }
@@ -1199,11 +1206,10 @@ static cudaError_t ns_resident(int num_sms, int* most) {
     return err;
 }
 
+// `*ran` false: this GPU has no room for such a cluster
 template <typename T, bool VEC>
-static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsSmall& a) {
+static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsSmall& a, bool* ran) {
     auto kern = ns_small_kernel<T, VEC>;
-    static const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
-    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1218,7 +1224,27 @@ static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsS
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, G, a);
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    static bool sixteen = false;
+    std::call_once(once, [&] {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+        if (err != cudaSuccess) return;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+            cudaLaunchConfig_t c16 = cfg;
+            cudaLaunchAttribute a16 = at[0];
+            a16.val.clusterDim.x = 16;
+            c16.gridDim = dim3(16, 1);
+            c16.attrs = &a16;
+            c16.numAttrs = 1;
+            int clusters = 0;
+            sixteen = cudaOccupancyMaxActiveClusters(&clusters, kern, &c16) == cudaSuccess && clusters > 0;
+        }
+        if (!sixteen) cudaGetLastError();   // an answer, not an error of this call
+    });
+    if (err != cudaSuccess) return err;
+    *ran = S <= 8 || sixteen;
+    return *ran ? cudaLaunchKernelEx(&cfg, kern, G, a) : cudaSuccess;
 }
 
 template <typename T>
@@ -1244,7 +1270,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
                                  long long wait_limit, bool withhold_loads) {
     NsLayout L;
     if (!ns_layout(N, R, C, &L)) return cudaErrorInvalidValue;
-    if (const int S = ns_small_cluster(L.m, L.n)) {
+    if (const int S = ns_small_cluster(N, L.m, L.n)) {
         NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, steps, R > C, eps};
         std::copy(coeffs, coeffs + 3 * steps, a.co);
         a.O = static_cast<__nv_bfloat16*>(O);
@@ -1253,8 +1279,12 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         a.withhold = withhold_loads;
         const auto* gf = static_cast<const float*>(G);
         const auto* gb = static_cast<const __nv_bfloat16*>(G);
-        if (C % 8 == 0) return g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a) : ns_small<__nv_bfloat16, true>(st, gb, S, (int)N, a);
-        return g_f32 ? ns_small<float, false>(st, gf, S, (int)N, a) : ns_small<__nv_bfloat16, false>(st, gb, S, (int)N, a);
+        bool ran = false;
+        const cudaError_t err = C % 8 == 0 ? (g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a, &ran)
+                                                    : ns_small<__nv_bfloat16, true>(st, gb, S, (int)N, a, &ran))
+                                           : (g_f32 ? ns_small<float, false>(st, gf, S, (int)N, a, &ran)
+                                                    : ns_small<__nv_bfloat16, false>(st, gb, S, (int)N, a, &ran));
+        if (err != cudaSuccess || ran) return err;
     }
     char* w = static_cast<char*>(workspace);
     cudaError_t err = g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1)
