@@ -109,8 +109,8 @@ struct NsPrep {
     __half* hi;
     __half* lo;      // null where G is exact in fp16 (bf16 G)
     float* inv_s;    // [N]
-    int* done;       // [N], zeroed
-    int parts, R, C, ld;
+    int* done;       // [N][counts], zeroed
+    int counts, parts, R, C, ld;
     float eps;
     int flip;        // store G^T
 };
@@ -121,9 +121,9 @@ __device__ __forceinline__ float ns_factor(const NsPrep& a, int mat, bool first)
     for (int i = threadIdx.x; i < a.parts; i += 256) v += a.partial[(long long)mat * a.parts + i];
     float inv_s;
     const float f = ns_split(sqrtf(ns_block_sum(v)), a.eps, &inv_s) * kXScale;
-    if (first && threadIdx.x == 0) {
-        a.inv_s[mat] = inv_s;
-        a.done[mat] = 0;
+    if (first) {
+        if (threadIdx.x == 0) a.inv_s[mat] = inv_s;
+        for (int i = threadIdx.x; i < a.counts; i += 256) a.done[(long long)mat * a.counts + i] = 0;
     }
     return f;
 }
@@ -242,8 +242,8 @@ struct NsArgs {
     int m, n, N, steps;
     int mt, nt;                  // tile rows and columns of X
     int tri, full;               // tiles of A's lower triangle, and of X
-    int tri_parts, full_parts;   // the CTAs that store a part of them (both of a pair, or the first where
-                                 // the second's rows are past the edge)
+    int parts, last_parts;       // CTAs that store a part of a tile: both of a pair, or in the last tile row
+                                 // the first alone where the second's rows are past the edge
     int h, halves;               // matrices of a half group, half groups in flight (see ns_unit)
     int per_cycle, cycles, supers;
     int units;
@@ -253,7 +253,7 @@ struct NsArgs {
     int out_kind;                // NsOut
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
     const float* inv_s;          // [N]
-    int* done;                   // [N] parts of tiles stored
+    int* done;                   // [N][1 + 2 mt] parts of tiles stored: GRAM's; POLY's and APPLY's by tile row
     __nv_bfloat16* O;
     int* status;
     long long wait_limit;
@@ -270,12 +270,16 @@ struct NsUnit {
     int mode, step, mat, i, j;
     bool valid;
 };
-// A matrix's phases GRAM, POLY, APPLY of each step follow one another; its phase starts when the one before
-// has stored every tile.  So that the CTAs have other work meanwhile, and that X, A and B stay in L2 from
-// one phase to the next, two half groups of h matrices are in flight, half a step apart: cycle c holds
+// A matrix's phases GRAM, POLY, APPLY of each step follow one another: POLY starts when GRAM has stored every
+// tile, APPLY of a tile row when POLY has stored that row of B (POLY goes by columns of the triangle, each of
+// which completes a row, by symmetry), GRAM of a tile when APPLY has stored its two rows of X.  What a phase
+// writes while the one before still runs, that one no longer reads: POLY's tiles that touch a row of A are
+// stored before that row of X, and so of A, can change.
+// So that the CTAs have other work while a phase waits, and that X, A and B stay in L2 from one phase to the
+// next, two half groups of h matrices are in flight, half a step apart: cycle c holds
 //   GRAM(a) APPLY(b, the step before) POLY(a) GRAM(b) APPLY(a) POLY(b)
-// with a, b the halves of group c / steps in step c % steps.  With few matrices there is no second half:
-// GRAM(a) POLY(a) APPLY(a).  CTAs take the units of this list in turn; every unit depends on earlier ones only.
+// with a, b the halves of group c / steps in step c % steps; a single matrix goes GRAM POLY APPLY.  CTAs take
+// the units of this list in turn; every unit depends on earlier ones only.
 __device__ __forceinline__ NsUnit ns_unit(int unit, const NsArgs& a) {
     NsUnit u;
     int c = unit / a.per_cycle, left = unit - c * a.per_cycle, b = 0;
@@ -311,18 +315,48 @@ __device__ __forceinline__ NsUnit ns_unit(int unit, const NsArgs& a) {
     if (u.mode == NS_APPLY) {
         u.i = left / a.nt;
         u.j = left - u.i * a.nt;
-    } else {   // row i of the triangle has i + 1 tiles
+    } else {   // by rows, row i of the triangle having i + 1 tiles; by columns, the same backwards
+        if (u.mode == NS_POLY) left = a.tri - 1 - left;
         u.i = (int)((sqrtf(8.f * left + 1.f) - 1.f) * 0.5f);
         while (u.i * (u.i + 1) / 2 > left) --u.i;
         while ((u.i + 1) * (u.i + 2) / 2 <= left) ++u.i;
         u.j = left - u.i * (u.i + 1) / 2;
+        if (u.mode == NS_POLY) {
+            const int i = u.i;
+            u.i = a.mt - 1 - u.j;
+            u.j = a.mt - 1 - i;
+        }
     }
     return u;
 }
-// parts of tiles of the matrix that come before the unit's phase; a part is counted only after its
-// accumulator has been stored, which its own inputs precede, so the count never runs ahead of a phase
-__device__ __forceinline__ int ns_before(const NsUnit& u, const NsArgs& a) {
-    return u.step * (2 * a.tri_parts + a.full_parts) + u.mode * a.tri_parts;
+// The matrix's counters, and what they hold when a unit's inputs are stored.  A part is counted only after
+// its accumulator has been stored, which its own inputs precede, so no count runs ahead of its phase.
+__device__ __forceinline__ int* ns_count(const NsArgs& a, int mat) { return a.done + (long long)mat * (1 + 2 * a.mt); }
+__device__ __forceinline__ int ns_row_parts(const NsArgs& a, int i) { return i + 1 < a.mt ? a.parts : a.last_parts; }
+__device__ __forceinline__ bool ns_wait_count(const int* count, int need, volatile int* abort_flag, const NsArgs& a) {
+    if (ld_acquire_gpu(count) >= need) return true;
+    const long long t0 = clock64();
+    while (ld_acquire_gpu(count) < need) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > a.wait_limit) {
+            *abort_flag = 1;
+            set_status(a.status, MOE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool ns_wait_unit(const NsUnit& u, volatile int* abort_flag, const NsArgs& a) {
+    const int* c = ns_count(a, u.mat);
+    if (u.mode == NS_GRAM)
+        return u.step == 0 ||
+               (ns_wait_count(c + 1 + a.mt + u.i, u.step * a.nt * ns_row_parts(a, u.i), abort_flag, a) &&
+                (u.i == u.j || ns_wait_count(c + 1 + a.mt + u.j, u.step * a.nt * ns_row_parts(a, u.j), abort_flag, a)));
+    if (u.mode == NS_POLY)   // tile rows of 1, 2, .. mt tiles, the last with last_parts
+        return ns_wait_count(c, (u.step + 1) * (a.tri * a.parts - a.mt * (a.parts - a.last_parts)), abort_flag, a);
+    // the tiles (i, 0..i) and (i+1.., i)
+    const int need = u.i + 1 < a.mt ? a.mt * a.parts - (a.parts - a.last_parts) : a.mt * a.last_parts;
+    return ns_wait_count(c + 1 + u.i, (u.step + 1) * need, abort_flag, a);
 }
 
 // Chunk `at` (16 bytes) of row r of a box
@@ -591,19 +625,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             bool ok = true;
             for (int unit = unit0; unit < a.units && ok; unit += stride, ++q) {
                 const NsUnit t = ns_unit(unit, a);
-                const int need = t.valid ? ns_before(t, a) : 0;
-                if (need > 0 && ld_acquire_gpu(a.done + t.mat) < need) {
-                    const long long t0 = clock64();
-                    while (ld_acquire_gpu(a.done + t.mat) < need) {
-                        ok = !*abort_flag;
-                        if (ok && clock64() - t0 > a.wait_limit) {
-                            *abort_flag = 1;
-                            set_status(a.status, MOE_DEV_TIMEOUT);
-                            ok = false;
-                        }
-                        if (!ok) break;
-                    }
-                }
+                ok = !t.valid || ns_wait_unit(t, abort_flag, a);
                 if (ok) st_release_cta_shared(ready, q + 1);
             }
         }
@@ -679,7 +701,15 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                     // this CTA's part of the tile is stored, and visible to whoever sees the count
                     bulk_wait_all();
                     fence_proxy_async_global();
-                    red_release_gpu_add(a.done + t.mat, 1);
+                    int* count = ns_count(a, t.mat);
+                    if (t.mode == NS_GRAM) {
+                        red_release_gpu_add(count, 1);
+                    } else if (t.mode == NS_POLY) {
+                        red_release_gpu_add(count + 1 + t.i, 1);
+                        if (t.i != t.j) red_release_gpu_add(count + 1 + t.j, 1);
+                    } else {
+                        red_release_gpu_add(count + 1 + a.mt + t.i, 1);
+                    }
                 }
             }
             bulk_wait_all();   // the stores are complete before the CTA exits
@@ -1140,7 +1170,7 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     }
     L->partial = take((size_t)N * L->parts * 4);
     L->inv_s = take((size_t)N * 4);
-    L->done = take((size_t)N * 4);
+    L->done = take((size_t)N * (1 + 2 * ((L->m + 127) / 128)) * 4);   // counters (tile rows of 128, or fewer of 256)
     L->A = take((size_t)N * L->m * L->lda * 2);
     L->b_lo = L->m <= 64;
     L->B = take((size_t)N * (L->b_lo ? 2 : 1) * L->m * L->lda * 2);
@@ -1248,7 +1278,8 @@ static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsS
 }
 
 template <typename T>
-static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, int R, int C, float eps, char* w, bool lo) {
+static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, int R, int C, float eps, char* w, bool lo,
+                              int counts) {
     float* partial = reinterpret_cast<float*>(w + L.partial);
     const long long elems = (long long)R * C;
     const unsigned N = (unsigned)L.N;
@@ -1258,7 +1289,7 @@ static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, in
                           : launch_pdl(ns_norm_kernel<T, false>, parts, 256, 0, st, G, elems, (int)L.parts, partial);
     if (err != cudaSuccess) return err;
     const NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
-                   reinterpret_cast<float*>(w + L.inv_s), reinterpret_cast<int*>(w + L.done), (int)L.parts, R, C, (int)L.ldx, eps, R > C};
+                   reinterpret_cast<float*>(w + L.inv_s), reinterpret_cast<int*>(w + L.done), counts, (int)L.parts, R, C, (int)L.ldx, eps, R > C};
     if (C % 8 != 0) return launch_pdl(ns_prep_any_kernel<T>, dim3((C + 31) / 32, (R + 31) / 32, N), 256, 0, st, G, p);
     if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 63) / 64, N), 256, 0, st, G, p);
     return launch_pdl(ns_prep_kernel<T>, dim3((unsigned)((elems + 8 * 256 * kPrepPer - 1) / (8 * 256 * kPrepPer)), N), 256, 0, st,
@@ -1287,11 +1318,15 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         if (err != cudaSuccess || ran) return err;
     }
     char* w = static_cast<char*>(workspace);
-    cudaError_t err = g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1)
-                            : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false);
-    if (err != cudaSuccess) return err;
     const bool flip = R > C;
     const int64_t m = L.m, n = L.n;
+    const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
+    const int tile = pair ? 256 : 128;
+    const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);
+    cudaError_t err =
+        g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1, 1 + 2 * mt)
+              : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false, 1 + 2 * mt);
+    if (err != cudaSuccess) return err;
     NsMaps t;
     auto map = [&](CUtensorMap* out, size_t at, int64_t cols, int64_t ld, int64_t batch, int rows) {
         return tmap_batched(out, w + at, false, cols, m, ld, batch, rows);
@@ -1305,18 +1340,16 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     t.o = t.o_t = t.a;
     if (o_box) ok = ok && tmap_batched(&t.o, O, true, C, R, C, N, 128) && tmap_batched(&t.o_t, O, true, C, R, C, N, 64);
     if (!ok) return cudaErrorInvalidValue;
-    const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
     int most = 0;
     if ((err = pair ? ns_resident<true>(num_sms, &most) : ns_resident<false>(num_sms, &most)) != cudaSuccess) return err;
-    const int tile = pair ? 256 : 128, ctas = pair ? most / 2 : most;
+    const int ctas = pair ? most / 2 : most;
     NsArgs a{};
     a.m = (int)m; a.n = (int)n; a.N = (int)N;
     a.steps = steps;
-    a.mt = (int)((m + tile - 1) / tile); a.nt = (int)((n + tile - 1) / tile);
+    a.mt = mt; a.nt = nt;
     a.tri = a.mt * (a.mt + 1) / 2; a.full = a.mt * a.nt;
-    const bool one_sided = pair && m - (int64_t)(a.mt - 1) * tile <= 128;   // the last tile row
-    a.tri_parts = (pair ? 2 : 1) * a.tri - (one_sided ? a.mt : 0);
-    a.full_parts = (pair ? 2 : 1) * a.full - (one_sided ? a.nt : 0);
+    a.parts = pair ? 2 : 1;
+    a.last_parts = pair && m - (int64_t)(mt - 1) * tile <= 128 ? 1 : a.parts;
     // a wave and a quarter of triangle tiles in a half group, the groups equal: fewer and a phase waits for
     // the last tiles of the one before, more and X leaves L2 in between (256 x 768 x 2048: 6.8, 6.2, 6.1, 6.2
     // and 6.3 ms with 6, 9, 12, 20 and 64 matrices in a half)
