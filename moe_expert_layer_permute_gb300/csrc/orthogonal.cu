@@ -241,7 +241,7 @@ struct NsMaps {
 struct NsArgs {
     int m, n, N, steps;
     int mt, nt;                  // tile rows and columns of X
-    int tri, full;               // tiles of A's lower triangle, and of X
+    int tri, full;               // tiles of A's upper triangle, and of X
     int parts, last_parts;       // CTAs that store a part of a tile: both of a pair, or in the last tile row
                                  // the first alone where the second's rows are past the edge
     int h, halves;               // matrices of a half group, half groups in flight (see ns_unit)
@@ -271,8 +271,8 @@ struct NsUnit {
     bool valid;
 };
 // A matrix's phases GRAM, POLY, APPLY of each step follow one another: POLY starts when GRAM has stored every
-// tile, APPLY of a tile row when POLY has stored that row of B (POLY goes by columns of the triangle, each of
-// which completes a row, by symmetry), GRAM of a tile when APPLY has stored its two rows of X.  What a phase
+// tile, APPLY of a tile row when POLY has stored that row of B (POLY goes by rows of the triangle, each of
+// which completes one, by symmetry), GRAM of a tile when APPLY has stored its two rows of X.  What a phase
 // writes while the one before still runs, that one no longer reads: POLY's tiles that touch a row of A are
 // stored before that row of X, and so of A, can change.
 // So that the CTAs have other work while a phase waits, and that X, A and B stay in L2 from one phase to the
@@ -315,19 +315,24 @@ __device__ __forceinline__ NsUnit ns_unit(int unit, const NsArgs& a) {
     if (u.mode == NS_APPLY) {
         u.i = left / a.nt;
         u.j = left - u.i * a.nt;
-    } else {   // by rows, row i of the triangle having i + 1 tiles; by columns, the same backwards
+    } else {   // the upper triangle by columns, column j having j + 1 tiles; by rows, the same backwards
         if (u.mode == NS_POLY) left = a.tri - 1 - left;
-        u.i = (int)((sqrtf(8.f * left + 1.f) - 1.f) * 0.5f);
-        while (u.i * (u.i + 1) / 2 > left) --u.i;
-        while ((u.i + 1) * (u.i + 2) / 2 <= left) ++u.i;
-        u.j = left - u.i * (u.i + 1) / 2;
+        int j = (int)((sqrtf(8.f * left + 1.f) - 1.f) * 0.5f);
+        while (j * (j + 1) / 2 > left) --j;
+        while ((j + 1) * (j + 2) / 2 <= left) ++j;
+        u.i = left - j * (j + 1) / 2;
+        u.j = j;
         if (u.mode == NS_POLY) {
-            const int i = u.i;
-            u.i = a.mt - 1 - u.j;
-            u.j = a.mt - 1 - i;
+            u.j = a.mt - 1 - u.i;
+            u.i = a.mt - 1 - j;
         }
     }
     return u;
+}
+// The tile's columns, rounded up to what an MMA takes: a last tile column costs what it holds.
+template <int TILE>
+__device__ __forceinline__ int ns_width(const NsUnit& u, const NsArgs& a) {
+    return min(TILE, ((u.mode == NS_APPLY ? a.n : a.m) - u.j * TILE + 31) & ~31);
 }
 // The matrix's counters, and what they hold when a unit's inputs are stored.  A part is counted only after
 // its accumulator has been stored, which its own inputs precede, so no count runs ahead of its phase.
@@ -352,11 +357,11 @@ __device__ __forceinline__ bool ns_wait_unit(const NsUnit& u, volatile int* abor
         return u.step == 0 ||
                (ns_wait_count(c + 1 + a.mt + u.i, u.step * a.nt * ns_row_parts(a, u.i), abort_flag, a) &&
                 (u.i == u.j || ns_wait_count(c + 1 + a.mt + u.j, u.step * a.nt * ns_row_parts(a, u.j), abort_flag, a)));
-    if (u.mode == NS_POLY)   // tile rows of 1, 2, .. mt tiles, the last with last_parts
-        return ns_wait_count(c, (u.step + 1) * (a.tri * a.parts - a.mt * (a.parts - a.last_parts)), abort_flag, a);
-    // the tiles (i, 0..i) and (i+1.., i)
-    const int need = u.i + 1 < a.mt ? a.mt * a.parts - (a.parts - a.last_parts) : a.mt * a.last_parts;
-    return ns_wait_count(c + 1 + u.i, (u.step + 1) * need, abort_flag, a);
+    // of the triangle only the last diagonal tile is in the last tile row
+    const int less = a.parts - a.last_parts;
+    if (u.mode == NS_POLY) return ns_wait_count(c, (u.step + 1) * (a.tri * a.parts - less), abort_flag, a);
+    // the mt tiles (i, i..) and (..i-1, i)
+    return ns_wait_count(c + 1 + u.i, (u.step + 1) * (a.mt * a.parts - (u.i + 1 < a.mt ? 0 : less)), abort_flag, a);
 }
 
 // Chunk `at` (16 bytes) of row r of a box
@@ -421,7 +426,7 @@ __device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArg
 // (12,600 cycles a tile of APPLY at K = 768, against 7,900 for its MMAs).
 //   PAIR: two CTAs share a 256 x 256 tile (cta_group::2), each holding 128 rows of the first operand and
 //   half of the second; otherwise one CTA computes 128 x 128.
-// GRAM and POLY are symmetric: tiles of the lower triangle alone, and those below the diagonal are stored
+// GRAM and POLY are symmetric: tiles of the upper triangle alone, and those above the diagonal are stored
 // twice, as they are and transposed through shared memory.  Operands: GRAM rows of X by rows of X, POLY
 // rows of A by rows of A (A = A^T), both contiguous along K; APPLY rows of B by columns of X (contiguous
 // along N).  The TMA fills K past the edge with zeros and drops stores outside a matrix, so no size needs
@@ -507,7 +512,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const NsUnit t = ns_unit(unit, a);
                 if (!t.valid) continue;
                 if (!inputs(q)) break;
-                const int m0 = t.i * kTile + rank * 128, n0 = t.j * kTile + rank * 128;
+                const int width = ns_width<kTile>(t, a);
+                const int m0 = t.i * kTile + rank * 128, n0 = t.j * kTile + rank * (width / 2);
                 const bool apply = t.mode == NS_APPLY;
                 const CUtensorMap* tmA = t.mode == NS_GRAM ? &maps.x[t.step & 1] : apply ? &maps.b : &maps.a;
                 const CUtensorMap* tmB = apply ? &maps.x_t[t.step & 1] : tmA;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * kTile);
-                const uint32_t idesc = apply ? idesc_f16(kTile, kTile, false, true) : idesc_f16(kTile, kTile, false, false);
+                const uint32_t idesc = idesc_f16(kTile, ns_width<kTile>(t, a), false, apply);
                 const uint32_t b_step = apply ? 2048 : 32, b_lbo = apply ? kOperand / 2 : 16;
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(full + stage, phase, abort_flag, a.status, a.wait_limit)) {
