@@ -429,21 +429,16 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
     __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&u);
     return __bfloat1622float2(v);
 }
-// a * b + c and a * b on two floats at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-          "l"(*reinterpret_cast<unsigned long long*>(&c)));
-    return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return *reinterpret_cast<float2*>(&r);
+// v[0] += a.lo * b, v[1] += a.hi * b: fp16 operands (a packed pair, b in the low half) and fp32 sums in one
+// instruction each, which conversions to fp32 and fmas take two and a half times as long for
+__device__ __forceinline__ void fma_f16x2(float* v, uint32_t a, uint32_t b) {
+    asm("{\n\t.reg .b16 l, h, c, d;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "mov.b32 {c, d}, %3;\n\t"
+        "fma.rn.f32.f16 %0, l, c, %0;\n\t"
+        "fma.rn.f32.f16 %1, h, c, %1;\n\t}"
+        : "+f"(v[0]), "+f"(v[1])
+        : "r"(a), "r"(b));
 }
 // 1/x by the hardware's approximate reciprocal (rcp.approx, about 1 ulp; subnormals flushed).
 __device__ __forceinline__ float rcp_approx(float x) {

@@ -99,8 +99,9 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const T* G, long long elem
 __device__ __forceinline__ float ns_split(float norm, float eps, float* inv_s) {
     const int ex = (int)((__float_as_uint(norm) >> 23) & 0xffu) - 126;   // -62 .. 64: a root of an fp32 sum
     const bool fine = norm <= 3.4e38f;
-    const float p = norm < 1e-30f ? 1.f : __uint_as_float((uint32_t)(127 - ex) << 23);
-    *inv_s = fine ? 1.f / ((norm + eps) * p) : NAN;
+    const bool none = norm < 1e-30f;
+    const float p = none ? 1.f : __uint_as_float((uint32_t)(127 - ex) << 23);
+    *inv_s = none ? 1.f : fine ? 1.f / ((norm + eps) * p) : NAN;   // (X is 0 then)
     return fine ? p : NAN;
 }
 
@@ -410,6 +411,27 @@ __device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArg
     p.keep_lo = u.mode == NS_POLY ? a.b_lo : u.mode == NS_APPLY && u.step + 2 < a.steps;
     p.twin = u.mode != NS_APPLY && u.i != u.j;
     return p;
+}
+
+// What the epilogue multiplies: the accumulator; the tile of A or X that came with it, by an fp16 pair whose
+// sum is the factor to 22 bits; X's rounding error; and in the first step the whole by the rest of the norm.
+// The scales of X, A, B and O are in there.
+struct NsFactors {
+    float d, is;
+    uint32_t hi, lo, err;
+};
+__device__ __forceinline__ NsFactors ns_factors(const NsUnit& u, const NsPart& p, const NsArgs& a) {
+    const float out = p.out_kind ? 1.f / kXScale : 1.f;
+    NsFactors f;
+    f.is = u.step == 0 ? __ldg(a.inv_s + u.mat) : 1.f;
+    f.d = u.mode == NS_GRAM   ? kABScale / (kXScale * kXScale) * f.is * f.is
+          : u.mode == NS_POLY ? a.co[3 * u.step + 2] / kABScale
+                              : out / kABScale;
+    const float x = u.mode == NS_POLY ? a.co[3 * u.step + 1] : out * a.co[3 * u.step];
+    f.hi = ns_pack_half(x, 0.f);
+    f.lo = ns_pack_half(x - ns_unpack_half(f.hi).x, 0.f);
+    f.err = ns_pack_half(x * (1.f / kLoScale), 0.f);
+    return f;
 }
 
 // Every step of every matrix in one launch of persistent CTAs, a warp to each job, all waits bounded:
@@ -732,8 +754,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             const NsUnit t = ns_unit(unit, a);
             if (!t.valid) continue;
             const NsPart p = ns_part<kTile>(t, rank, a);
-            const float is = t.step == 0 ? __ldg(a.inv_s + t.mat) : 1.f;
-            const float ca = a.co[3 * t.step], cb = a.co[3 * t.step + 1], cc = a.co[3 * t.step + 2];
+            const NsFactors f = ns_factors(t, p, a);
             if (!__all_sync(0xffffffffu, mbar_wait(tfull + acc, acc_phase, abort_flag, a.status, a.wait_limit))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -742,62 +763,45 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const uint32_t sbox = smem_u32(sBox + slot * 2 * kNsBox);
                 float v[32];
                 uint32_t out[16], low[16];
-                float2* v2 = reinterpret_cast<float2*>(v);
                 tmem_ld32(tmem + lane_addr + (uint32_t)(acc * kTile + 64 * c + 32 * half), v);
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(box_full + slot, k / kNsSlots & 1, abort_flag, a.status, a.wait_limit));
                 if (!ok) break;
                 if (t.mode == NS_GRAM) {
-                    const float f = kABScale / (kXScale * kXScale) * is * is;
-                    const float2 ff = make_float2(f, f);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v2[j] = mul2(v2[j], ff);
-                        out[j] = ns_pack_half(v2[j].x, v2[j].y);
-                    }
-                } else if (t.mode == NS_POLY) {
-                    ns_box_read(out, sbox, br, half);
-                    const float2 fc = make_float2(cc / kABScale, cc / kABScale), fb = make_float2(cb, cb);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v2[j] = fma2(fb, ns_unpack_half(out[j]), mul2(fc, v2[j]));
-                        out[j] = ns_pack_half(v2[j].x, v2[j].y);
-                    }
-                    if (p.keep_lo) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 h = ns_unpack_half(out[j]);
-                            low[j] = ns_pack_half(v2[j].x - h.x, v2[j].y - h.y);
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f.d, v[2 * j + 1] * f.d);
                 } else {
                     ns_box_read(out, sbox, br, half);
-                    const float fd = is * (1.f / kABScale), fx = is * ca, fl = fx * (1.f / kLoScale);
-                    const float2 fd2 = make_float2(fd, fd), fx2 = make_float2(fx, fx), fl2 = make_float2(fl, fl);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v2[j] = fma2(fx2, ns_unpack_half(out[j]), mul2(fd2, v2[j]));
+                    for (int j = 0; j < 16; ++j) {
+                        v[2 * j] *= f.d;
+                        v[2 * j + 1] *= f.d;
+                        fma_f16x2(v + 2 * j, out[j], f.hi);
+                        fma_f16x2(v + 2 * j, out[j], f.lo);
+                    }
                     if (p.load_lo) {
                         ns_box_read(low, sbox + kNsBox, br, half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v2[j] = fma2(fl2, ns_unpack_half(low[j]), v2[j]);
+                        for (int j = 0; j < 16; ++j) fma_f16x2(v + 2 * j, low[j], f.err);
                     }
-                    if (!p.out_kind) {
-                        const float2 minus = make_float2(-1.f, -1.f), ls = make_float2(kLoScale, kLoScale);
+                    if (t.step == 0 && t.mode == NS_APPLY) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v2[j].x, v2[j].y);
+                        for (int j = 0; j < 32; ++j) v[j] *= f.is;
+                    }
+                    if (p.out_kind) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
                         if (p.keep_lo) {
+                            const uint32_t minus = ns_pack_half(-1.f, 0.f);
+                            const float scale = t.mode == NS_POLY ? 1.f : kLoScale;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const float2 l = mul2(fma2(ns_unpack_half(out[j]), minus, v2[j]), ls);
-                                low[j] = ns_pack_half(l.x, l.y);
+                                fma_f16x2(v + 2 * j, out[j], minus);
+                                low[j] = ns_pack_half(v[2 * j] * scale, v[2 * j + 1] * scale);
                             }
-                        }
-                    } else {
-                        const float2 us = make_float2(1.f / kXScale, 1.f / kXScale);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 o = mul2(v2[j], us);
-                            out[j] = pack_bf16x2(o.x, o.y);
                         }
                     }
                 }

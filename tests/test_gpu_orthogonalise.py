@@ -98,9 +98,10 @@ def test_steps_and_coefficients(cuda_lib, steps):
 
 @pytest.mark.parametrize("scale", [1e-12, 1e-7, 1.0, 1e10])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_scales(cuda_lib, scale, dtype):
+@pytest.mark.parametrize("R,C", [(70, 90), (140, 150)])
+def test_scales(cuda_lib, scale, dtype, R, C):
     """Down to norms that eps outweighs, and up."""
-    G = gauss(2, 70, 90, dtype, 7, scale)
+    G = gauss(2, R, C, dtype, 7, scale)
     assert max(errors(run(cuda_lib, G), exact(G))) < BAR
     assert max(errors(run(cuda_lib, G, eps=1e-3), exact(G, eps=1e-3))) < BAR
 
