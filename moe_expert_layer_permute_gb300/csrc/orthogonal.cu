@@ -67,28 +67,30 @@ __device__ __forceinline__ void ns_val8(float* v, const __nv_bfloat16* p) {
     }
 }
 
-// Part blockIdx.x of matrix blockIdx.y's sum of squares; VEC: the matrices are multiples of 8 elements.
-template <typename T, bool VEC>
+// Part blockIdx.x of matrix blockIdx.y's sum of squares: runs of eight from the first 16-byte boundary on, and
+// by part 0 the few elements before and after them.
+template <typename T>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const T* G, long long elems, int parts, float* partial) {
     grid_dep_wait();
     const T* g = G + (long long)blockIdx.y * elems;
+    const long long head = min(elems, (long long)((16 - reinterpret_cast<uintptr_t>(g) % 16) % 16 / sizeof(T)));
+    const long long runs = (elems - head) / 8;
     float v = 0.f;
-    if constexpr (VEC) {
 #pragma unroll 4
-        for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < elems; i += (long long)parts * 2048) {
-            float x[8];
-            ns_val8(x, g + i);
-            float s = x[0] * x[0];
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < runs; i += (long long)parts * 256) {
+        float x[8];
+        ns_val8(x, g + head + 8 * i);
+        float s = x[0] * x[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) s += x[j] * x[j];
-            v += s;
-        }
-    } else {
-#pragma unroll 8
-        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < elems; i += (long long)parts * 256) {
-            const float x = ns_val(g, i);
-            v += x * x;
-        }
+        for (int j = 1; j < 8; ++j) s += x[j] * x[j];
+        v += s;
+    }
+    if (blockIdx.x == 0) {
+        const long long tail = head + 8 * runs;
+        float x = 0.f;
+        if (threadIdx.x < head) x = ns_val(g, threadIdx.x);
+        else if (threadIdx.x >= 32 && tail + threadIdx.x - 32 < elems) x = ns_val(g, tail + threadIdx.x - 32);
+        v += x * x;
     }
     v = ns_block_sum(v);
     if (threadIdx.x == 0) partial[(long long)blockIdx.y * parts + blockIdx.x] = v;
@@ -156,47 +158,64 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a
     grid_dep_wait();
     const int mat = blockIdx.y;
     const long long elems = (long long)a.R * a.C;
+    const long long i0 = ((long long)blockIdx.x * kPrepPer * 256 + threadIdx.x) * 8;
+    float x[kPrepPer][8];
+#pragma unroll
+    for (int q = 0; q < kPrepPer; ++q)
+        if (i0 + q * 2048 < elems) ns_val8(x[q], G + mat * elems + i0 + q * 2048);
     const float f = ns_factor(a, mat, blockIdx.x == 0);
 #pragma unroll
     for (int q = 0; q < kPrepPer; ++q) {
-        const long long i = (((long long)blockIdx.x * kPrepPer + q) * 256 + threadIdx.x) * 8;
-        if (i >= elems) break;
-        float x[8];
-        ns_val8(x, G + mat * elems + i);
+        if (i0 + q * 2048 >= elems) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= f;
-        ns_store8(a, mat * elems + i, x);
+        for (int j = 0; j < 8; ++j) x[q][j] *= f;
+        ns_store8(a, mat * elems + i0 + q * 2048, x[q]);
     }
 }
 
 // G^T for rows of multiples of 8 elements: 64 x 64 tiles through shared memory, 16 bytes a load and 32 a
-// store (the pitch is a multiple of 16 bytes; what is past R in a row's last 16 is never read).
+// store (the pitch is a multiple of 16 bytes; what is past R in a row's last 16 is never read).  A block goes
+// down kFlipPer tiles, the next one's loads under way while one is stored.
+constexpr int kFlipPer = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) ns_prep_flip_kernel(const T* G, const NsPrep a) {
     grid_dep_wait();
     __shared__ float tile[64][65];
-    const int mat = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+    const int mat = blockIdx.z, c0 = blockIdx.x * 64;
+    const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;   // loads: rows lr, lr + 32, columns lc ..
+    const int c = threadIdx.x >> 2, r = (threadIdx.x & 3) * 16;    // stores: rows r .. of column c, whole lines
+    float x[2][8];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (r0 + q * 32 + lr < a.R && c0 + lc < a.C) {
+                ns_val8(x[q], G + ((long long)mat * a.R + r0 + q * 32 + lr) * a.C + c0 + lc);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[q][j] = 0.f;
+            }
+        }
+    };
+    const int first = blockIdx.y * 64 * kFlipPer, end = min(a.R, first + 64 * kFlipPer);
+    load(first);
     const float f = ns_factor(a, mat, blockIdx.x == 0 && blockIdx.y == 0);
+    for (int r0 = first; r0 < end; r0 += 64) {
+        __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
-        float x[8];
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        if (r0 + r < a.R && c0 + c < a.C) ns_val8(x, G + ((long long)mat * a.R + r0 + r) * a.C + c0 + c);
+            for (int j = 0; j < 8; ++j) tile[q * 32 + lr][lc + j] = x[q][j] * f;
+        __syncthreads();
+        if (r0 + 64 < end) load(r0 + 64);
+        if (c0 + c >= a.C) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) tile[r][c + j] = x[j] * f;
-    }
-    __syncthreads();
-    const int c = threadIdx.x & 63, r = (threadIdx.x >> 6) * 16;
-    if (c0 + c >= a.C) return;
+        for (int q = 0; q < 16; q += 8) {
+            if (r0 + r + q >= a.R) break;
+            float v[8];
 #pragma unroll
-    for (int q = 0; q < 16; q += 8) {
-        if (r0 + r + q >= a.R) break;
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = tile[r + q + j][c];
-        ns_store8(a, ((long long)mat * a.C + c0 + c) * a.ld + r0 + r + q, x);
+            for (int j = 0; j < 8; ++j) v[j] = tile[r + q + j][c];
+            ns_store8(a, ((long long)mat * a.C + c0 + c) * a.ld + r0 + r + q, v);
+        }
     }
 }
 
@@ -1294,14 +1313,13 @@ static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, in
     const long long elems = (long long)R * C;
     const unsigned N = (unsigned)L.N;
     const dim3 parts((unsigned)L.parts, N);
-    cudaError_t err = elems % 8 == 0
-                          ? launch_pdl(ns_norm_kernel<T, true>, parts, 256, 0, st, G, elems, (int)L.parts, partial)
-                          : launch_pdl(ns_norm_kernel<T, false>, parts, 256, 0, st, G, elems, (int)L.parts, partial);
+    cudaError_t err = launch_pdl(ns_norm_kernel<T>, parts, 256, 0, st, G, elems, (int)L.parts, partial);
     if (err != cudaSuccess) return err;
     const NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
                    reinterpret_cast<float*>(w + L.inv_s), reinterpret_cast<int*>(w + L.done), counts, (int)L.parts, R, C, (int)L.ldx, eps, R > C};
     if (C % 8 != 0) return launch_pdl(ns_prep_any_kernel<T>, dim3((C + 31) / 32, (R + 31) / 32, N), 256, 0, st, G, p);
-    if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 63) / 64, N), 256, 0, st, G, p);
+    if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 64 * kFlipPer - 1) / (64 * kFlipPer), N),
+                                 256, 0, st, G, p);
     return launch_pdl(ns_prep_kernel<T>, dim3((unsigned)((elems + 8 * 256 * kPrepPer - 1) / (8 * 256 * kPrepPer)), N), 256, 0, st,
                       G, p);
 }
