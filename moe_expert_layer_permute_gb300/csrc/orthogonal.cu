@@ -887,6 +887,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
 // 64 columns that GRAM reads along K are, unchanged, what APPLY reads along N.  Per step:
 //   partial A over the CTA's columns -> the cluster's sum, each CTA adding the rows it owns in the CTAs'
 //   order and sending them to all as fp16 -> A A and B in every CTA -> X of the CTA's columns.
+// Where m leaves room, up to eight blocks of 256 columns lie one below the other in the CTA's 128 rows: A is
+// the sum of the diagonal blocks of their product, and with A and B laid out block-diagonally the rest goes
+// as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 86 here).
 constexpr int kSmallCols = 256;
 constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
 constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
@@ -894,7 +897,7 @@ constexpr int kSmallA = 2 * 16384;   // A likewise; the partial A in fp32, later
 constexpr int kSmallBytes = 1024 + kSmallX + 3 * kSmallA + 256;
 
 struct NsSmall {
-    int R, C, m, n, steps, flip;
+    int R, C, m, n, mp, steps, flip;   // mp: rows of a block, 128 / mp blocks of columns one below the other
     float eps;
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
     __nv_bfloat16* O;
@@ -919,14 +922,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = (int)gridDim.x, rank = S > 1 ? (int)cluster_ctarank() : 0, mat = blockIdx.y;
     const int quarter = warp & 3, half = warp >> 2;
-    const int i = quarter * 32 + lane;                        // row of X
-    const int col0 = rank * kSmallCols + half * 128;          // first of the thread's 128 columns
+    const int row = quarter * 32 + lane;                      // the thread's row in shared memory,
+    const int mp = a.mp, blocks = 128 / mp;
+    const int i = row & (mp - 1);                             // of X,
+    const int col0 = (rank * blocks + row / mp) * kSmallCols + half * 128;   // and the first of its 128 columns
     if (threadIdx.x == 0) {
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, 512);
+    if (blocks > 1)   // A is zero outside its diagonal blocks
+        for (int e = threadIdx.x; e < kSmallA / 16; e += kSmallThreads) st_shared_v4(smem_u32(sA) + 16 * e, make_uint4(0, 0, 0, 0));
     float x[128];
     float sq = 0.f;
     const T* g = G + (long long)mat * a.R * a.C;
@@ -980,8 +987,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     const uint32_t bX = smem_u32(sX), bA = smem_u32(sA), bP = smem_u32(sP);
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t tA = tmem, tP = tmem + 128, tX = tmem + 256;
-    const int kx = min(4, max(0, (a.n - rank * kSmallCols + 63) / 64));   // chunks of X that hold columns
-    const int km = (a.m + 15) / 16;                                       // MMA steps along m
+    const int kx = min(4, max(0, (a.n - rank * blocks * kSmallCols + 63) / 64));   // chunks of X that hold columns
+    const int km = blocks > 1 ? 8 : (a.m + 15) / 16;                      // MMA steps along the rows
     const int b_parts = a.m <= 64 ? 2 : 1;                                // B, and its rounding error
     constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdX = idesc_f16(128, 256, false, true);
     uint32_t phase = 0;
@@ -996,7 +1003,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     auto put_x = [&] {   // X as fp16
 #pragma unroll
         for (int j = 0; j < 128; j += 8)
-            st_shared_v4(bX + (2 * half + j / 64) * 16384 + ns_sw(i, (j & 63) >> 3),
+            st_shared_v4(bX + (2 * half + j / 64) * 16384 + ns_sw(row, (j & 63) >> 3),
                          make_uint4(ns_pack_half(x[j], x[j + 1]), ns_pack_half(x[j + 2], x[j + 3]),
                                     ns_pack_half(x[j + 4], x[j + 5]), ns_pack_half(x[j + 6], x[j + 7])));
     };
@@ -1018,57 +1025,73 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             mma_commit(done);
         }
         wait_mma();
-        if (S == 1) {
+        if (S == 1 && blocks == 1) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float v[32];
                 tmem_ld32(tA + lane_addr + 64 * half + 32 * c, v);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    st_shared_v4(bA + half * 16384 + ns_sw(i, 4 * c + q),
+                    st_shared_v4(bA + half * 16384 + ns_sw(row, 4 * c + q),
                                  make_uint4(ns_pack_half(v[8 * q] * fa, v[8 * q + 1] * fa),
                                             ns_pack_half(v[8 * q + 2] * fa, v[8 * q + 3] * fa),
                                             ns_pack_half(v[8 * q + 4] * fa, v[8 * q + 5] * fa),
                                             ns_pack_half(v[8 * q + 6] * fa, v[8 * q + 7] * fa)));
             }
         } else {
-            // fp32 rows of 512 bytes, their 16-byte pieces rotated by the row against bank conflicts
+            // the row's columns of its diagonal block in fp32: rows of 512 bytes, their 16-byte pieces rotated
+            // by the row against bank conflicts
+            const bool any = kx > 0;   // a CTA past the last column adds nothing
+            auto put = [&](int at, float v0, float v1, float v2, float v3) {
+                st_shared_v4(bP + row * 512 + ((at ^ lane) << 4),
+                             any ? make_uint4(__float_as_uint(v0), __float_as_uint(v1), __float_as_uint(v2), __float_as_uint(v3))
+                                 : make_uint4(0, 0, 0, 0));
+            };
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                const int cb = 64 * half + 32 * c;
+                if (cb / max(mp, 32) != quarter * 32 / max(mp, 32)) continue;   // the same for the whole warp
                 float v[32];
-                tmem_ld32(tA + lane_addr + 64 * half + 32 * c, v);
-                const bool any = kx > 0;   // a CTA past the last column adds nothing
+                tmem_ld32(tA + lane_addr + cb, v);
+                if (mp >= 32) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int at = 16 * half + 8 * c + q;
-                    st_shared_v4(bP + i * 512 + ((at ^ lane) << 4),
-                                 any ? make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                                  __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]))
-                                     : make_uint4(0, 0, 0, 0));
+                    for (int q = 0; q < 8; ++q) put((cb & (mp - 1)) / 4 + q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else {   // blocks of 16: lanes 0-15 the first half, the others the second
+                    const bool second = lane >= 16;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        put(q, second ? v[16 + 4 * q] : v[4 * q], second ? v[17 + 4 * q] : v[4 * q + 1],
+                            second ? v[18 + 4 * q] : v[4 * q + 2], second ? v[19 + 4 * q] : v[4 * q + 3]);
                 }
             }
-            cluster_sync();
-            const int rows = 128 / S;
-            for (int e = threadIdx.x; e < rows * 32; e += kSmallThreads) {
-                const int r = rank * rows + (e >> 5), at = e & 31;
-                const uint32_t off = (uint32_t)(r * 512 + ((at ^ (r & 31)) << 4));
-                float4 v[8], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (S > 1) cluster_sync();
+            else __syncthreads();
+            const int rows = mp / S, per_row = mp / 4;
+            for (int e = threadIdx.x; e < rows * per_row; e += kSmallThreads) {
+                const int r = rank * rows + e / per_row, at = e & (per_row - 1);
+                float4 v[4], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-                for (int b0 = 0; b0 < S; b0 += 8) {
+                for (int t0 = 0; t0 < S * blocks; t0 += 4) {   // CTA by CTA, block by block
 #pragma unroll
-                    for (int b = 0; b < 8; ++b)   // all under way before the first is added
-                        v[b] = b0 + b < S ? ld_cluster_f32x4(cluster_addr(sP, b0 + b) + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int t = 0; t < 4; ++t) {   // all under way before the first is added
+                        const int b = (t0 + t) / blocks, br = ((t0 + t) & (blocks - 1)) * mp + r;
+                        v[t] = b < S ? ld_cluster_f32x4(cluster_addr(sP, b) + (uint32_t)(br * 512 + ((at ^ (br & 31)) << 4)))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
 #pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        sum.x += v[b].x; sum.y += v[b].y; sum.z += v[b].z; sum.w += v[b].w;
+                    for (int t = 0; t < 4; ++t) {
+                        sum.x += v[t].x; sum.y += v[t].y; sum.z += v[t].z; sum.w += v[t].w;
                     }
                 }
                 const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
-                const uint32_t to = (uint32_t)((at >> 4) * 16384) + ns_sw(r, (at & 15) >> 1) + (at & 1) * 8;
-                for (int b = 0; b < S; ++b) st_cluster_v2(cluster_addr(sA, b) + to, h0, h1);
+                for (int q = 0; q < blocks; ++q) {
+                    const int col = q * mp + 4 * at;
+                    const uint32_t to = (uint32_t)((col >> 6) * 16384) + ns_sw(q * mp + r, (col & 63) >> 3) + (at & 1) * 8;
+                    for (int b = 0; b < S; ++b) st_cluster_v2(cluster_addr(sA, b) + to, h0, h1);
+                }
             }
             fence_proxy_async_all();
-            cluster_sync();   // A is whole in every CTA, and the partial sums have been read
+            if (S > 1) cluster_sync();   // A is whole in every CTA, and the partial sums have been read
         }
         fence_proxy_async_all();
         tc_fence_before();
@@ -1088,7 +1111,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             tmem_ld32(tP + lane_addr + 64 * half + 32 * c, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint32_t to = half * 16384 + ns_sw(i, 4 * c + q);
+                const uint32_t to = half * 16384 + ns_sw(row, 4 * c + q);
                 const uint4 h = ld_shared_v4(bA + to);
                 const uint32_t w[4] = {h.x, h.y, h.z, h.w};
                 uint32_t hi[4], lo[4];
@@ -1164,14 +1187,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 }
 
 // ---- launches --------------------------------------------------------------------------------------
-// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others.  One or two take any number of
-// matrices; of more CTAs the kernel runs about 48 us however few there are, and for over two rounds of the
-// GPU's SMs the large kernels are faster (128 x 2048, 1, 16, 32, 128 matrices: 48, 96, 144, 440 us here and
-// 113, 127, 174, 419 there; 100 x 700, 256 matrices: 552 and 360; 32 x 512, 256 matrices: 149 and 188).
-static int ns_small_cluster(int64_t N, int64_t m, int64_t n) {
-    if (m > 128 || n > 16 * kSmallCols) return 0;
+// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  One or two
+// CTAs take any number of matrices; of more the kernel runs about 48 us however few there are, and for over
+// two rounds of the GPU's SMs the large kernels are faster (128 x 2048, 1, 16, 32, 128 matrices: 48, 96, 144,
+// 440 us here and 113, 127, 174, 419 there; 100 x 700, 256 matrices: 552 and 360; 32 x 512, 256 matrices: 149
+// and 188).
+static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
+    *mp = 128;
+    while (*mp / 2 >= m && *mp > 16 && (128 / *mp) * kSmallCols < n) *mp /= 2;
+    const int cols = 128 / *mp * kSmallCols;
+    if (m > 128 || n > 16 * cols) return 0;
     int S = 1;
-    while (S * kSmallCols < n) S *= 2;
+    while (S * cols < n) S *= 2;
     return S <= 2 || N * S <= 304 ? S : 0;
 }
 
@@ -1192,7 +1219,8 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
     take(256);   // status word
-    const int S = ns_small_cluster(N, L->m, L->n);
+    int mp;
+    const int S = ns_small_cluster(N, L->m, L->n, &mp);
     if (S > 0 && S <= 8) {   // (whether a cluster of 16 is possible only the GPU can tell)
         L->total = o;
         return true;
@@ -1329,8 +1357,9 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
                                  long long wait_limit, bool withhold_loads) {
     NsLayout L;
     if (!ns_layout(N, R, C, &L)) return cudaErrorInvalidValue;
-    if (const int S = ns_small_cluster(N, L.m, L.n)) {
-        NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, steps, R > C, eps};
+    int mp;
+    if (const int S = ns_small_cluster(N, L.m, L.n, &mp)) {
+        NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, mp, steps, R > C, eps};
         std::copy(coeffs, coeffs + 3 * steps, a.co);
         a.O = static_cast<__nv_bfloat16*>(O);
         a.status = status;

@@ -51,7 +51,8 @@ SHAPES = [(1, 1, 1), (2, 1, 5), (2, 3, 1), (3, 2, 200), (1, 16, 16), (2, 24, 40)
           (1, 128, 128), (1, 128, 2048), (3, 129, 127), (2, 127, 1000), (2, 130, 257), (1, 192, 640), (1, 640, 192),
           (2, 256, 256), (1, 257, 255), (1, 384, 385), (5, 256, 128), (1, 777, 300), (1, 1030, 520), (40, 8, 70),
           (1, 60, 1500), (2, 2048, 100), (1, 1025, 128), (2, 100, 2100), (1, 2056, 24), (70, 260, 300),
-          (330, 150, 140), (1, 128, 4096), (2, 3000, 65), (1, 4104, 30), (90, 100, 600)]
+          (330, 150, 140), (1, 128, 4096), (2, 3000, 65), (1, 4104, 30), (90, 100, 600), (2, 16, 2048), (2, 10, 2049),
+          (3, 7, 20000), (2, 32, 1000), (1, 32, 16000), (1, 33, 1030), (2, 64, 512), (2, 5000, 61), (1, 17, 257), (1, 1, 32768)]
 
 
 @pytest.mark.parametrize("N,R,C", SHAPES)
