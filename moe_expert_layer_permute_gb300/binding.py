@@ -2,14 +2,15 @@
 
 Argument marshalling only: torch tensors become `moe_tensor` views (device pointer, dtype,
 shape, strides), the current torch CUDA stream becomes the `stream` argument, and every step of
-the layer runs in the CUDA library.  The library is loaded on import; if it has not been built,
-importing this module raises (there is no fallback).
+the layer runs in the CUDA library.  The balance loss and the orthogonalisation marshal in C++
+(`csrc/marshal.cpp`), since their smallest calls take a few microseconds.  The libraries are loaded
+on import; if they have not been built, importing this module raises (there is no fallback).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -61,6 +62,8 @@ def _load() -> ctypes.CDLL:
     path = _build.LIB
     if not os.path.exists(path):
         raise RuntimeError(f"CUDA library not built ({path}); run moe_expert_layer_permute_gb300.build.build()")
+    if not os.path.exists(_build.MARSHAL):
+        raise RuntimeError(f"marshalling not built ({_build.MARSHAL}); run moe_expert_layer_permute_gb300.build.build()")
     lib = ctypes.CDLL(path)
     lib.moe_scratch_bytes.argtypes = [_P(MoeDesc)]
     lib.moe_scratch_bytes.restype = ctypes.c_size_t
@@ -106,6 +109,17 @@ def _load() -> ctypes.CDLL:
 LIB = _load()
 
 
+def _load_marshal():
+    """The compiled marshalling (`csrc/marshal.cpp`), linked against the library loaded above."""
+    spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_MARSHAL = _load_marshal()
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -129,35 +143,6 @@ def as_moe_tensor(t: torch.Tensor) -> MoeTensor:
         m.shape[i] = t.shape[i]
         m.stride[i] = t.stride(i)
     return m
-
-
-_TENSOR = struct.Struct("=Qii3q3q")     # the fields of MoeTensor; a fifth of the time of filling one
-
-
-def _arg(t):
-    """A tensor (or None) as the bytes of a moe_tensor."""
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise MoeError(ERR["MOE_ERR_NULL"], "a tensor that is not on a CUDA device")
-    shape, stride = t.shape, t.stride()
-    n = len(shape)
-    ptr, dt = t.data_ptr(), _DT.get(t.dtype, -1)      # 0 for an empty tensor, -1 for no moe_dtype
-    if n == 2:
-        return _TENSOR.pack(ptr, dt, 2, shape[0], shape[1], 0, stride[0], stride[1], 0)
-    if n == 1:
-        return _TENSOR.pack(ptr, dt, 1, shape[0], 0, 0, stride[0], 0, 0)
-    if n == 3:
-        return _TENSOR.pack(ptr, dt, 3, *shape, *stride)
-    return _TENSOR.pack(ptr, dt, n, 0, 0, 0, 0, 0, 0)  # refused by its ndim
-
-
-def _packed(name: str, tensors: int, rest: list):
-    """The entry point as a function of `tensors` moe_tensors given by _arg, then `rest`."""
-    fn = LIB[name]                      # a function object of its own, beside LIB.<name>
-    fn.argtypes = [ctypes.c_char_p] * tensors + rest
-    fn.restype = ctypes.c_int
-    return fn
 
 
 def make_desc(T, H, I, E, k, precision=MOE_BF16, flags=0) -> MoeDesc:
@@ -235,7 +220,7 @@ class Workspace:
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -318,19 +303,13 @@ def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
     return int(LIB.moe_balance_workspace_bytes(T, E, B))
 
 
-_balance_fwd = _packed("moe_balance_fwd", 7, [ctypes.c_void_p, ctypes.c_void_p])
-_balance_bwd = _packed("moe_balance_bwd", 10, [ctypes.c_void_p])
-_orthogonalise = _packed("moe_orthogonalise", 2, [ctypes.c_int32, _P(ctypes.c_float), ctypes.c_float, ctypes.c_void_p,
-                                                  ctypes.c_void_p])
-
-
 def moe_balance_fwd(logits, topk_idx, counts, tokens, loss, workspace: Workspace, mask=None, seg_offsets=None,
                     stream=None) -> None:
     """Balance loss, z-loss and per-expert counts of each segment: logits fp32 [T, E], topk_idx int32
     [T, k], mask bool or uint8 [T] or None, seg_offsets int32 [B+1] or None (B = 1) -> counts int32
     [B, E], tokens int32 [B], loss fp32 [B, 2]."""
-    rc = _balance_fwd(_arg(logits), _arg(topk_idx), _arg(mask), _arg(seg_offsets), _arg(counts), _arg(tokens), _arg(loss),
-                      workspace.address, _stream_ptr(stream))
+    rc = _MARSHAL.balance_fwd(logits, topk_idx, mask, seg_offsets, counts, tokens, loss, workspace.address,
+                              None if stream is None else _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_fwd")
 
@@ -339,8 +318,8 @@ def moe_balance_bwd(logits, topk_idx, topk_w, dtopk_w, counts, tokens, dloss, dl
                     stream=None) -> None:
     """dlogits fp32 [T, E] of the losses (dloss fp32 [B, 2]) and, unless topk_w and dtopk_w are None,
     of the top-k weights (what moe_router_bwd gives), in one pass."""
-    rc = _balance_bwd(_arg(logits), _arg(topk_idx), _arg(topk_w), _arg(dtopk_w), _arg(mask), _arg(seg_offsets), _arg(counts),
-                      _arg(tokens), _arg(dloss), _arg(dlogits), _stream_ptr(stream))
+    rc = _MARSHAL.balance_bwd(logits, topk_idx, topk_w, dtopk_w, mask, seg_offsets, counts, tokens, dloss, dlogits,
+                              None if stream is None else _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_bwd")
 
@@ -352,12 +331,9 @@ def moe_orthogonalise_workspace_bytes(N: int, R: int, C: int) -> int:
 def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None) -> None:
     """O bf16 [N, R, C] = every matrix of G (bf16 or fp32, [N, R, C]) after `steps` Newton-Schulz steps.
     coeffs: (a, b, c) for every step, a sequence of `steps` such triples, or None for the defaults."""
-    co = None
+    co = ()
     if coeffs is not None:
-        flat = [v for c in coeffs for v in c] if hasattr(coeffs[0], "__len__") else list(coeffs) * max(steps, 1)
-        if len(flat) != 3 * steps:
-            raise MoeError(ERR["MOE_ERR_SHAPE"], "moe_orthogonalise")
-        co = (ctypes.c_float * len(flat))(*flat)
-    rc = _orthogonalise(_arg(G), _arg(O), steps, co, eps, workspace.address, _stream_ptr(stream))
+        co = [v for c in coeffs for v in c] if hasattr(coeffs[0], "__len__") else tuple(coeffs) * max(steps, 1)
+    rc = _MARSHAL.orthogonalise(G, O, workspace.address, None if stream is None else _stream_ptr(stream), steps, eps, *co)
     if rc:
         raise MoeError(rc, "moe_orthogonalise")

@@ -120,14 +120,43 @@ def test_orthogonalise_refusals(bd):  # noqa: F811
         assert bd.moe_orthogonalise_workspace_bytes(*bad) == 0, bad
 
 
+class _Holder:
+    def __init__(self, bd):
+        self.handle = bd.MoeScratch()
+        self.handle.data, self.handle.bytes = 1 << 40, 1 << 40
+        self.address = ctypes.addressof(self.handle)
+
+
 def test_orthogonalise_coefficient_lists(bd):  # noqa: F811
     """The binding takes one triple or one for each step, nothing else."""
     import torch
     G = torch.zeros(1, 4, 4)
+    for bad in ([(1, 1, 1)] * 4, (1.0, 2.0), [(1, 1)] * 5):
+        with pytest.raises(bd.MoeError, match="SHAPE"):
+            bd.moe_orthogonalise(G, G, _Holder(bd), steps=5, coeffs=bad, stream=0)
+    with pytest.raises(bd.MoeError, match="UNSUPPORTED"):
+        bd.moe_orthogonalise(G, G, _Holder(bd), steps=17, coeffs=(1, 1, 1), stream=0)
+
+
+def test_tensors_off_the_gpu_and_other_things_are_refused(bd):  # noqa: F811
+    import torch
+    ws = _Holder(bd)
+    G, O = torch.zeros(1, 4, 4), torch.zeros(1, 4, 4, dtype=torch.bfloat16)
+    with pytest.raises(bd.MoeError, match="NULL"):
+        bd.moe_orthogonalise(G, O, ws, stream=0)
+    with pytest.raises(bd.MoeError, match="DTYPE"):
+        bd.moe_orthogonalise(G.double(), O, ws, stream=0)
     with pytest.raises(bd.MoeError, match="SHAPE"):
-        bd.moe_orthogonalise(G, G, _Holder(bd), steps=5, coeffs=[(1, 1, 1)] * 4)
-
-
-class _Holder:
-    def __init__(self, bd):
-        self.handle = bd.MoeScratch()
+        bd.moe_orthogonalise(G[0], O[0], ws, stream=0)
+    with pytest.raises(bd.MoeError, match="SHAPE"):
+        bd.moe_orthogonalise(G[None], O[None], ws, stream=0)
+    with pytest.raises(TypeError):
+        bd.moe_orthogonalise([1.0], O, ws, stream=0)
+    logits, idx = torch.zeros(6, 4), torch.zeros(6, 2, dtype=torch.int32)
+    counts, tokens, loss = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2)
+    with pytest.raises(bd.MoeError, match="NULL"):
+        bd.moe_balance_fwd(logits, idx, counts, tokens, loss, ws, stream=0)
+    with pytest.raises(bd.MoeError, match="NULL"):
+        bd.moe_balance_bwd(logits, idx, None, None, counts, tokens, loss, torch.zeros(6, 4), stream=0)
+    with pytest.raises(bd.MoeError, match="DTYPE"):
+        bd.moe_balance_fwd(logits.half(), idx, counts, tokens, loss, ws, stream=0)
