@@ -22,7 +22,6 @@
 namespace moe {
 
 constexpr int kBalMaxChunks = 304;    // forward: most blocks (two per SM)
-constexpr int kBalMinChunk = 32;      // forward: fewest tokens per block
 constexpr int kBwdWarps = 8;
 // forward: warps per block; two blocks an SM hold 32 warps where a warp has one row of up to 512 values at
 // a time, which the memory needs then (131,072 x 512: 76 us with eight)
@@ -184,6 +183,13 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
         const int lo = max(s0, t0), hi = min(s1, t1);
         if (lo >= hi) continue;
         for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+        // the thread's first two picks are under way while the tokens' rows are summed
+        const long long p0 = (long long)lo * a.k + threadIdx.x, pe = (long long)hi * a.k;
+        auto pick = [&](long long i) {
+            const int e = i < pe ? __ldg(a.idx + i) : -1;
+            return (unsigned)e < (unsigned)a.E && (!a.mask || __ldg(a.mask + (unsigned)i / (unsigned)a.k)) ? e : -1;
+        };
+        const int pick0 = pick(p0), pick1 = pick(p0 + 32 * kWarps);
         float acc[V], z2 = 0.f;
         int n = 0;
 #pragma unroll
@@ -213,10 +219,11 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
             npart[warp] = n;
         }
         __syncthreads();
-        const bool masked = a.mask != nullptr;
-        for (long long i = (long long)lo * a.k + threadIdx.x; i < (long long)hi * a.k; i += blockDim.x) {
-            const int e = __ldg(a.idx + i);
-            if ((unsigned)e < (unsigned)a.E && (!masked || __ldg(a.mask + i / a.k))) atomicAdd(hist + e, 1);
+        if (pick0 >= 0) atomicAdd(hist + pick0, 1);
+        if (pick1 >= 0) atomicAdd(hist + pick1, 1);
+        for (long long i = p0 + 64 * kWarps; i < pe; i += 32 * kWarps) {
+            const int e = pick(i);
+            if (e >= 0) atomicAdd(hist + e, 1);
         }
         z2 = 0.f;
         n = 0;
@@ -248,9 +255,11 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
                 a.Z[blockIdx.x + s] = z2;
                 atomicAdd(a.N + s, n);
             }
-            __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0) last = atomicAdd(a.ticket + s, 1) == c1 - c0;
+            if (threadIdx.x == 0) {
+                __threadfence();   // the block's sums, which the barrier orders before it, before its ticket
+                last = atomicAdd(a.ticket + s, 1) == c1 - c0;
+            }
             __syncthreads();
             finish = last;
             if (finish) {
@@ -379,14 +388,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bal_blocks_sm<V>()) balance_bw
 }
 
 // ---- launches --------------------------------------------------------------------------------------
-static int bal_chunk(int64_t T) {
-    return (int)std::max<int64_t>(kBalMinChunk, (T + kBalMaxChunks - 1) / kBalMaxChunks);
+// Tokens of a block: two rounds of its warps at least (a join of two blocks costs more: 64 x 128 took 5.5 us
+// in two blocks)
+static int bal_chunk(int64_t T, int64_t E) {
+    const int64_t least = E <= 16 ? 512 : E <= 32 ? 256 : E <= 64 ? 128 : 64;
+    return (int)std::max<int64_t>(least, (T + kBalMaxChunks - 1) / kBalMaxChunks);
 }
-static size_t bal_blocks(int64_t T) { return (size_t)((T + bal_chunk(T) - 1) / bal_chunk(T)); }
+static size_t bal_blocks(int64_t T, int64_t E) { return (size_t)((T + bal_chunk(T, E) - 1) / bal_chunk(T, E)); }
 
 // the status word's line, then P, C, N, ticket, Z
 size_t balance_workspace(int64_t T, int64_t E, int64_t B) {
-    return 256 + (size_t)B * (12 * (size_t)E + 8) + 4 * (bal_blocks(T) + (size_t)B);
+    return 256 + (size_t)B * (12 * (size_t)E + 8) + 4 * (bal_blocks(T, E) + (size_t)B);
 }
 
 template <int W, int V, bool VEC>
@@ -394,7 +406,7 @@ static cudaError_t fwd_c(cudaStream_t st, const BalArgs& a) {
     constexpr int kWarps = bal_warps<W, V>();
     const size_t smem = (size_t)(kWarps + 1) * a.E * 4;   // at most 36 KB
     // (with no tokens one block writes the zeros)
-    return launch_pdl(balance_fwd_kernel<W, V, VEC>, (unsigned)std::max<size_t>(1, bal_blocks(a.T)), 32 * kWarps, smem, st, a);
+    return launch_pdl(balance_fwd_kernel<W, V, VEC>, (unsigned)std::max<size_t>(1, bal_blocks(a.T, a.E)), 32 * kWarps, smem, st, a);
 }
 template <int W, int V, bool VEC>
 static cudaError_t bwd_c(cudaStream_t st, BalBwdArgs a) {
@@ -425,7 +437,7 @@ static cudaError_t dispatch_bwd(cudaStream_t st, const BalBwdArgs& a) { MOE_BAL_
 cudaError_t launch_balance_fwd(cudaStream_t st, const float* logits, const int* topk_idx, const uint8_t* mask,
                                const int* seg_offsets, int T, int E, int k, int B, int* counts, int* tokens, float* loss,
                                void* workspace) {
-    BalArgs a{logits, topk_idx, mask, seg_offsets, T, E, k, B, bal_chunk(T)};
+    BalArgs a{logits, topk_idx, mask, seg_offsets, T, E, k, B, bal_chunk(T, E)};
     char* w = static_cast<char*>(workspace) + 256;
     const size_t be = (size_t)B * E;
     a.P = reinterpret_cast<unsigned long long*>(w);
