@@ -99,7 +99,7 @@ def losses(B, seed):
 
 SHAPES = [(1, 1, 1, 1), (1, 8, 2, 1), (2, 33, 1, 3), (7, 5, 3, 2), (33, 127, 8, 4), (64, 128, 8, 1), (300, 130, 8, 7),
           (1000, 1024, 32, 3), (777, 1023, 1, 65), (4096, 256, 6, 1), (2500, 512, 8, 900), (12345, 64, 4, 2),
-          (40000, 8, 2, 5)]
+          (40000, 8, 2, 5), (20000, 512, 4, 3), (16500, 1024, 8, 2), (40001, 132, 6, 40), (70000, 68, 2, 1)]
 
 
 @pytest.mark.parametrize("T,E,k,B", SHAPES)
