@@ -80,6 +80,10 @@ __device__ __forceinline__ int bal_segment(const int* off, int B, int T, int t) 
     return lo;
 }
 
+// e^x as a power of two, results below the least normal flushed to 0, which a softmax can do without
+// (131,072 x 512: the forward 52.9 us with __expf, 50.1 so)
+__device__ __forceinline__ float bal_exp(float x) { return exp2_approx(x * 1.442695041f); }
+
 // The softmax of a group's row: x becomes exp(x - max).  A row of -inf alone has none: p = 0, lse taken as
 // 0.  All lanes of the warp take part.
 struct BalRow {
@@ -108,7 +112,7 @@ __device__ __forceinline__ BalRow bal_softmax(float* x) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        x[i] = __expf(x[i] - base);   // 0 for -inf
+        x[i] = bal_exp(x[i] - base);   // 0 for -inf
         sum += x[i];
     }
     sum = bal_group_sum<W>(sum);
@@ -358,10 +362,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bal_blocks_sm<V>()) balance_bw
 #pragma unroll
         for (int i = 0; i < V; ++i) dot += x[i] * cf[i];
         dot = bal_group_sum<W>(dot);
-        const float shift = zc * r.lse - dot * r.inv;
+        const float shift = (zc * r.lse - dot * r.inv) * r.inv;
         if (live) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = counts ? x[i] * r.inv * (cf[i] + shift) : 0.f;
+            for (int i = 0; i < V; ++i) x[i] = counts ? x[i] * (r.inv * cf[i] + shift) : 0.f;
             if constexpr (VEC) {
 #pragma unroll
                 for (int i = 0; i < V; i += 4)
@@ -380,8 +384,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, bal_blocks_sm<V>()) balance_bw
                 if ((unsigned)e >= (unsigned)a.E) continue;
                 float v = __ldg(a.w + pk + j) * (__ldg(a.dw + pk + j) - wdw);
                 if (counts && r.inv != 0.f)
-                    v += __expf(__ldg(row + e) - r.max) * r.inv *
-                         (scale * (float)__ldg(a.counts + (long long)s * a.E + e) + shift);
+                    v += bal_exp(__ldg(row + e) - r.max) *
+                         (r.inv * scale * (float)__ldg(a.counts + (long long)s * a.E + e) + shift);
                 out[e] = v;
             }
     }

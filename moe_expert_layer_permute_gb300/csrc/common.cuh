@@ -446,6 +446,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 2^x by the hardware's approximate power (ex2.approx; results below the least normal flushed to 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // sigmoid(z) = 1 / (1 + e^-z); 1 + e^-z is at least 1, and e^-z = inf gives 0
 __device__ __forceinline__ float sigmoidf_fast(float z) { return rcp_approx(1.0f + __expf(-z)); }
 
