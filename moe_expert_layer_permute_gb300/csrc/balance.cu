@@ -147,17 +147,20 @@ struct BalArgs {
 };
 constexpr float kBalFix = 4294967296.f;   // 2^32
 
-// Sum over a block, the same on every thread.
+// Two sums over a block, whole on thread 0.
 template <int kWarps>
-__device__ __forceinline__ float bal_block_sum(float v, float* part) {
-    v = bal_warp_sum(v);
+__device__ __forceinline__ float2 bal_block_sum2(float a, float b, float2* part) {
+    a = bal_warp_sum(a);
+    b = bal_warp_sum(b);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[w];
-    return v;
+    float2 sum = make_float2(0.f, 0.f);
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kWarps; ++w) {
+            sum.x += part[w].x;
+            sum.y += part[w].y;
+        }
+    return sum;
 }
 
 template <int W, int V, bool VEC>
@@ -168,6 +171,7 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
     float* red = sm;                                            // [kWarps][E]
     int* hist = reinterpret_cast<int*>(red + kWarps * a.E);  // [E]
     __shared__ float part[kWarps];
+    __shared__ float2 part2[kWarps];
     __shared__ int npart[kWarps];
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % W;
@@ -268,27 +272,31 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
             finish = last;
             if (finish) {
                 __threadfence();
-                for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-                    const int c = atomicExch(K + e, 0);
-                    const float v = (float)((double)(long long)atomicExch(P + e, 0ull) * (1.0 / kBalFix));
-                    a.counts[(long long)s * a.E + e] = c;
-                    dot += v * (float)c;
+                // requests first, so that their latencies overlap
+                if (threadIdx.x == 0) {
+                    n = atomicExch(a.N + s, 0);
+                    a.ticket[s] = 0;
                 }
                 z2 = 0.f;
                 for (int q = c0 + (int)threadIdx.x; q <= c1; q += blockDim.x) {
                     z2 += __ldcg(a.Z + q + s);
                     a.Z[q + s] = 0.f;
                 }
-                z2 = bal_block_sum<kWarps>(z2, part);
-                if (threadIdx.x == 0) {
-                    n = atomicExch(a.N + s, 0);
-                    a.ticket[s] = 0;
+                for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+                    const int c = atomicExch(K + e, 0);
+                    const float v = (float)((double)(long long)atomicExch(P + e, 0ull) * (1.0 / kBalFix));
+                    a.counts[(long long)s * a.E + e] = c;
+                    dot += v * (float)c;
                 }
             }
+        } else if (threadIdx.x != 0) {
+            z2 = 0.f;   // every thread has the block's sum
         }
         if (finish) {
-            dot = bal_block_sum<kWarps>(dot, part);
+            const float2 sums = bal_block_sum2<kWarps>(dot, z2, part2);
             if (threadIdx.x == 0) {
+                dot = sums.x;
+                z2 = sums.y;
                 const float inv = n > 0 ? 1.f / (float)n : 0.f;
                 if (isnan(z2)) dot = z2;   // a NaN in a counted row: the integer sums do not show it
                 a.tokens[s] = n;
