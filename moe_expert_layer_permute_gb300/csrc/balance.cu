@@ -70,8 +70,18 @@ __device__ __forceinline__ void bal_load(float* x, const float* row, int E, int 
 __device__ __forceinline__ int bal_off(const int* off, int s, int T) {
     return off ? min(max(__ldg(off + s), 0), T) : (s == 0 ? 0 : T);
 }
-// the first segment that ends after token t (B if none does)
+// The first segment that ends after token t (B if none does), by the whole warp: up to 128 ends are looked at
+// at once, since a search among them is a chain of loads.
 __device__ __forceinline__ int bal_segment(const int* off, int B, int T, int t) {
+    if (!off) return 0;   // one segment of all tokens
+    if (B <= 128) {
+        const int lane = threadIdx.x & 31;
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s += __popc(__ballot_sync(0xffffffffu, 32 * i + lane < B && bal_off(off, 32 * i + lane + 1, T) <= t));
+        return s;
+    }
     int lo = 0, hi = B;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -176,15 +186,6 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % W;
     const int t0 = blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    // a segment without tokens meets no block: the blocks share these out
-    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
-        if (bal_off(a.off, s, a.T) >= bal_off(a.off, s + 1, a.T)) {
-            for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(long long)s * a.E + e] = 0;
-            if (threadIdx.x == 0) {
-                a.tokens[s] = 0;
-                a.loss[2 * s] = a.loss[2 * s + 1] = 0.f;
-            }
-        }
     for (int s = bal_segment(a.off, a.B, a.T, t0); s < a.B; ++s) {
         const int s0 = bal_off(a.off, s, a.T), s1 = bal_off(a.off, s + 1, a.T);
         if (s0 >= t1) break;
@@ -306,6 +307,15 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
         }
         __syncthreads();   // the next segment's sums reuse the arrays
     }
+    // a segment without tokens meets no block: the blocks share these out
+    for (int s = blockIdx.x; s < a.B; s += gridDim.x)
+        if (bal_off(a.off, s, a.T) >= bal_off(a.off, s + 1, a.T)) {
+            for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(long long)s * a.E + e] = 0;
+            if (threadIdx.x == 0) {
+                a.tokens[s] = 0;
+                a.loss[2 * s] = a.loss[2 * s + 1] = 0.f;
+            }
+        }
 }
 
 struct BalBwdArgs {
