@@ -354,6 +354,13 @@ template <int TILE>
 __device__ __forceinline__ int ns_width(const NsUnit& u, const NsArgs& a) {
     return min(TILE, ((u.mode == NS_APPLY ? a.n : a.m) - u.j * TILE + 31) & ~31);
 }
+// A pair's whole tile on the diagonal of A or B: its operands are the same rows, and one copy serves as both
+// (256 x 768 x 2048: 1.1% less time; one CTA's tiles, whose phases wait for those off the diagonal, gain
+// nothing: 3 x 1001 x 777 158.1 -> 159.8 us).
+template <bool PAIR>
+__device__ __forceinline__ bool ns_same(const NsUnit& u, int width) {
+    return PAIR && u.mode != NS_APPLY && u.i == u.j && width == 256;
+}
 // The matrix's counters, and what they hold when a unit's inputs are stored.  A part is counted only after
 // its accumulator has been stored, which its own inputs precede, so no count runs ahead of its phase.
 __device__ __forceinline__ int* ns_count(const NsArgs& a, int mat) { return a.done + (long long)mat * (1 + 2 * a.mt); }
@@ -559,6 +566,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const CUtensorMap* tmA = t.mode == NS_GRAM ? &maps.x[t.step & 1] : apply ? &maps.b : &maps.a;
                 const CUtensorMap* tmB = apply ? &maps.x_t[t.step & 1] : tmA;
                 const int wrap = t.mode == NS_GRAM ? a.k_gram : a.k_poly;
+                const bool same = ns_same<PAIR>(t, width);
+                const uint32_t bytes = (PAIR ? 2 : 1) * (same ? kOperand : 2 * kOperand);
                 const int k_blocks = apply && a.b_lo ? 2 * wrap : wrap;
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, a.status, a.wait_limit)) {
@@ -573,21 +582,21 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                     if constexpr (PAIR) {
                         // both CTAs' copies land on the leader's barrier, which expects both
                         const uint32_t lbar = cluster_addr(full + stage, 0);
-                        if (rank == 0) mbar_arrive_expect_tx(full + stage, 4 * kOperand);
+                        if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
                         tma_load_3d_pair(dA, tmA, lbar, k0, m0, matA);
                         if (apply) {
                             tma_load_3d_pair(dB, tmB, lbar, n0, k0, t.mat);
                             tma_load_3d_pair(dB + kOperand / 2, tmB, lbar, n0 + 64, k0, t.mat);
-                        } else {
+                        } else if (!same) {
                             tma_load_3d_pair(dB, tmB, lbar, k0, n0, t.mat);
                         }
                     } else {
-                        mbar_arrive_expect_tx(full + stage, 2 * kOperand);
+                        mbar_arrive_expect_tx(full + stage, bytes);
                         tma_load_3d(dA, tmA, full + stage, k0, m0, matA);
                         if (apply) {
                             tma_load_3d(dB, tmB, full + stage, n0, k0, t.mat);
                             tma_load_3d(dB + kOperand / 2, tmB, full + stage, n0 + 64, k0, t.mat);
-                        } else {
+                        } else if (!same) {
                             tma_load_3d(dB, tmB, full + stage, k0, n0, t.mat);
                         }
                     }
@@ -625,7 +634,9 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * kTile);
-                const uint32_t idesc = idesc_f16(kTile, ns_width<kTile>(t, a), false, apply);
+                const int width = ns_width<kTile>(t, a);
+                const uint32_t idesc = idesc_f16(kTile, width, false, apply);
+                const uint32_t other = ns_same<PAIR>(t, width) ? a_base : b_base;
                 const uint32_t b_step = apply ? 2048 : 32, b_lbo = apply ? kOperand / 2 : 16;
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(full + stage, phase, abort_flag, a.status, a.wait_limit)) {
@@ -633,7 +644,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = a_base + stage * kOperand, sb = b_base + stage * kOperand;
+                    const uint32_t sa = a_base + stage * kOperand, sb = other + stage * kOperand;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t ad = sdesc_sw128(sa + ks * 32, 16, 1024);
