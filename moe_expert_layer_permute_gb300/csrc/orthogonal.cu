@@ -135,27 +135,29 @@ __device__ __forceinline__ uint32_t ns_pack_half(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 ns_unpack_half(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+// a pair of values of X, and of their rounding errors
+__device__ __forceinline__ uint32_t ns_split_pair(float x, float y, uint32_t* lo) {
+    const uint32_t h = ns_pack_half(x, y);
+    const float2 f = ns_unpack_half(h);
+    *lo = ns_pack_half((x - f.x) * kLoScale, (y - f.y) * kLoScale);
+    return h;
+}
 // eight values of X, and their rounding errors, at a 16-byte boundary
 __device__ __forceinline__ void ns_store8(const NsPrep& a, long long at, const float* x) {
-    uint32_t h[4];
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = ns_pack_half(x[2 * j], x[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) h[j] = ns_split_pair(x[2 * j], x[2 * j + 1], l + j);
     *reinterpret_cast<uint4*>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    if (!a.lo) return;
-    uint32_t l[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 f = ns_unpack_half(h[j]);
-        l[j] = ns_pack_half((x[2 * j] - f.x) * kLoScale, (x[2 * j + 1] - f.y) * kLoScale);
-    }
-    *reinterpret_cast<uint4*>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    if (a.lo) *reinterpret_cast<uint4*>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
 }
+
+// The three kernels below request their part of G before they wait for the norms' kernel: it wrote none of
+// G, and waited itself for what did.
 
 // Rows of multiples of 8 elements, as they stand: X's pitch is C and the matrix one run of elements.
 constexpr int kPrepPer = 4;   // runs of eight per thread
 template <typename T>
 __global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a) {
-    grid_dep_wait();
     const int mat = blockIdx.y;
     const long long elems = (long long)a.R * a.C;
     const long long i0 = ((long long)blockIdx.x * kPrepPer * 256 + threadIdx.x) * 8;
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a
 #pragma unroll
     for (int q = 0; q < kPrepPer; ++q)
         if (i0 + q * 2048 < elems) ns_val8(x[q], G + mat * elems + i0 + q * 2048);
+    grid_dep_wait();
     const float f = ns_factor(a, mat, blockIdx.x == 0);
 #pragma unroll
     for (int q = 0; q < kPrepPer; ++q) {
@@ -173,76 +176,91 @@ __global__ void __launch_bounds__(256) ns_prep_kernel(const T* G, const NsPrep a
     }
 }
 
-// G^T for rows of multiples of 8 elements: 64 x 64 tiles through shared memory, 16 bytes a load and 32 a
-// store (the pitch is a multiple of 16 bytes; what is past R in a row's last 16 is never read).  A block goes
-// down kFlipPer tiles, the next one's loads under way while one is stored.
-constexpr int kFlipPer = 4;
+// Other rows as they stand: runs of eight of X's rows, whose pitch is a multiple of eight; a row's last run
+// is filled up with zeros.
 template <typename T>
-__global__ void __launch_bounds__(256) ns_prep_flip_kernel(const T* G, const NsPrep a) {
+__global__ void __launch_bounds__(256) ns_prep_rows_kernel(const T* G, const NsPrep a) {
+    const int mat = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;   // R ld / 8 < 2^31
+    const int row = i / (a.ld / 8), c = (i - row * (a.ld / 8)) * 8;
+    const T* g = G + ((long long)mat * a.R + row) * a.C + c;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = row < a.R && c + j < a.C ? ns_val(g, j) : 0.f;
     grid_dep_wait();
-    __shared__ float tile[64][65];
+    const float f = ns_factor(a, mat, blockIdx.x == 0);
+    if (row >= a.R) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= f;
+    ns_store8(a, ((long long)mat * a.R + row) * a.ld + c, x);
+}
+
+// G^T by tiles of 64 x 64 through shared memory, which holds fp16 pairs of two rows of G in the order that
+// keeps both its writes and its reads free of bank conflicts (32 x 2048 x 768, bf16: 40 us, 5 TB/s; with single
+// fp32 values there 46).  VEC: rows of multiples of 8 elements, loaded 16 bytes at a time.  Stores are 32
+// bytes (the pitch is a multiple of 16 bytes; what is past R in a row's last 16 is never read).  A block goes
+// down `per` tiles, the next one's loads under way while one is stored.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) ns_prep_flip_kernel(const T* G, const NsPrep a, int per) {
+    constexpr bool kLo = sizeof(T) == 4;
+    __shared__ uint32_t tile[kLo ? 2 : 1][32][65];
     const int mat = blockIdx.z, c0 = blockIdx.x * 64;
-    const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;   // loads: rows lr, lr + 32, columns lc ..
-    const int c = threadIdx.x >> 2, r = (threadIdx.x & 3) * 16;    // stores: rows r .. of column c, whole lines
+    // loads: VEC: rows 2 lp, 2 lp + 1, columns lc ..; else rows 2 (lp + 8 q) .., columns lc, lc + 32
+    const int lp = threadIdx.x >> (VEC ? 3 : 5), lc = VEC ? (threadIdx.x & 7) * 8 : threadIdx.x & 31;
+    const int c = threadIdx.x >> 2, rp = (threadIdx.x & 3) * 8;    // stores: row pairs rp .. of column c
     float x[2][8];
     auto load = [&](int r0) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (r0 + q * 32 + lr < a.R && c0 + lc < a.C) {
-                ns_val8(x[q], G + ((long long)mat * a.R + r0 + q * 32 + lr) * a.C + c0 + lc);
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (VEC) {
+                const int r = r0 + 2 * lp + h;
+                if (r < a.R && c0 + lc < a.C) {
+                    ns_val8(x[h], G + ((long long)mat * a.R + r) * a.C + c0 + lc);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[h][j] = 0.f;
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[q][j] = 0.f;
+                for (int j = 0; j < 8; ++j) {
+                    const int r = r0 + 2 * (lp + 8 * (j >> 1)) + h, col = c0 + lc + 32 * (j & 1);
+                    x[h][j] = r < a.R && col < a.C ? ns_val(G, ((long long)mat * a.R + r) * a.C + col) : 0.f;
+                }
             }
         }
     };
-    const int first = blockIdx.y * 64 * kFlipPer, end = min(a.R, first + 64 * kFlipPer);
+    const int first = blockIdx.y * 64 * per, end = min(a.R, first + 64 * per);
     load(first);
+    grid_dep_wait();
     const float f = ns_factor(a, mat, blockIdx.x == 0 && blockIdx.y == 0);
     for (int r0 = first; r0 < end; r0 += 64) {
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) tile[q * 32 + lr][lc + j] = x[q][j] * f;
+        for (int j = 0; j < 8; ++j) {
+            uint32_t lo;
+            if constexpr (VEC) {   // columns 32 apart are in one bank: one half goes the other way round
+                const bool far = lc >= 32;
+                const int col = lc + (far ? j ^ 4 : j);
+                tile[0][lp][col] = ns_split_pair((far ? x[0][j ^ 4] : x[0][j]) * f, (far ? x[1][j ^ 4] : x[1][j]) * f, &lo);
+                if constexpr (kLo) tile[1][lp][col] = lo;
+            } else {
+                tile[0][lp + 8 * (j >> 1)][lc + 32 * (j & 1)] = ns_split_pair(x[0][j] * f, x[1][j] * f, &lo);
+                if constexpr (kLo) tile[1][lp + 8 * (j >> 1)][lc + 32 * (j & 1)] = lo;
+            }
+        }
         __syncthreads();
         if (r0 + 64 < end) load(r0 + 64);
         if (c0 + c >= a.C) continue;
+        const long long at = ((long long)mat * a.C + c0 + c) * a.ld + r0 + 2 * rp;
 #pragma unroll
-        for (int q = 0; q < 16; q += 8) {
-            if (r0 + r + q >= a.R) break;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = tile[r + q + j][c];
-            ns_store8(a, ((long long)mat * a.C + c0 + c) * a.ld + r0 + r + q, v);
+        for (int q = 0; q < 8; q += 4) {
+            if (r0 + 2 * (rp + q) >= a.R) break;
+            auto run = [&](int t) {
+                return make_uint4(tile[t][rp + q][c], tile[t][rp + q + 1][c], tile[t][rp + q + 2][c], tile[t][rp + q + 3][c]);
+            };
+            *reinterpret_cast<uint4*>(a.hi + at + 2 * q) = run(0);
+            if constexpr (kLo)
+                if (a.lo) *reinterpret_cast<uint4*>(a.lo + at + 2 * q) = run(1);
         }
-    }
-}
-
-// Any size: 32 x 32 tiles, an element at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) ns_prep_any_kernel(const T* G, const NsPrep a) {
-    grid_dep_wait();
-    __shared__ float tile[32][33];
-    const int mat = blockIdx.z, r0 = blockIdx.y * 32, c0 = blockIdx.x * 32;
-    const float f = ns_factor(a, mat, blockIdx.x == 0 && blockIdx.y == 0);
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int rows = a.flip ? a.C : a.R, cols = a.flip ? a.R : a.C;
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        const int r = r0 + ty + j, c = c0 + tx;
-        tile[ty + j][tx] = r < a.R && c < a.C ? ns_val(G, ((long long)mat * a.R + r) * a.C + c) * f : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-        const int r = (a.flip ? c0 : r0) + ty + j, c = (a.flip ? r0 : c0) + tx;
-        if (r >= rows || c >= cols) continue;
-        const float x = a.flip ? tile[tx][ty + j] : tile[ty + j][tx];
-        const __half h = __float2half_rn(x);
-        const long long at = ((long long)mat * rows + r) * a.ld + c;
-        a.hi[at] = h;
-        if (a.lo) a.lo[at] = __float2half_rn((x - __half2float(h)) * kLoScale);
     }
 }
 
@@ -1347,7 +1365,7 @@ static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsS
 
 template <typename T>
 static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, int R, int C, float eps, char* w, bool lo,
-                              int counts) {
+                              int counts, int num_sms) {
     float* partial = reinterpret_cast<float*>(w + L.partial);
     const long long elems = (long long)R * C;
     const unsigned N = (unsigned)L.N;
@@ -1356,11 +1374,16 @@ static cudaError_t ns_first_x(cudaStream_t st, const NsLayout& L, const T* G, in
     if (err != cudaSuccess) return err;
     const NsPrep p{partial, reinterpret_cast<__half*>(w + L.x0), lo ? reinterpret_cast<__half*>(w + L.lo) : nullptr,
                    reinterpret_cast<float*>(w + L.inv_s), reinterpret_cast<int*>(w + L.done), counts, (int)L.parts, R, C, (int)L.ldx, eps, R > C};
-    if (C % 8 != 0) return launch_pdl(ns_prep_any_kernel<T>, dim3((C + 31) / 32, (R + 31) / 32, N), 256, 0, st, G, p);
-    if (R > C) return launch_pdl(ns_prep_flip_kernel<T>, dim3((C + 63) / 64, (R + 64 * kFlipPer - 1) / (64 * kFlipPer), N),
-                                 256, 0, st, G, p);
-    return launch_pdl(ns_prep_kernel<T>, dim3((unsigned)((elems + 8 * 256 * kPrepPer - 1) / (8 * 256 * kPrepPer)), N), 256, 0, st,
-                      G, p);
+    const auto blocks = [](int64_t items, int64_t per) { return (unsigned)((items + per - 1) / per); };
+    if (R > C) {
+        // one tile a block until there are several for each block that an SM holds
+        const int per = (int64_t)N * blocks(C, 64) * blocks(R, 64) > 16 * num_sms ? 4 : 1;
+        const dim3 grid(blocks(C, 64), blocks(R, 64 * per), N);
+        return C % 8 != 0 ? launch_pdl(ns_prep_flip_kernel<T, false>, grid, 256, 0, st, G, p, per)
+                          : launch_pdl(ns_prep_flip_kernel<T, true>, grid, 256, 0, st, G, p, per);
+    }
+    if (C % 8 != 0) return launch_pdl(ns_prep_rows_kernel<T>, dim3(blocks(R * L.ldx, 8 * 256), N), 256, 0, st, G, p);
+    return launch_pdl(ns_prep_kernel<T>, dim3(blocks(elems, 8 * 256 * kPrepPer), N), 256, 0, st, G, p);
 }
 
 cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int64_t N, int64_t R, int64_t C, void* O,
@@ -1392,8 +1415,8 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     const int tile = pair ? 256 : 128;
     const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);
     cudaError_t err =
-        g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1, 1 + 2 * mt)
-              : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false, 1 + 2 * mt);
+        g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1, 1 + 2 * mt, num_sms)
+              : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false, 1 + 2 * mt, num_sms);
     if (err != cudaSuccess) return err;
     NsMaps t;
     auto map = [&](CUtensorMap* out, size_t at, int64_t cols, int64_t ld, int64_t batch, int rows) {
