@@ -439,7 +439,7 @@ __device__ __forceinline__ void ns_box_col(uint32_t box, int r, int half, const 
 struct NsPart {
     int row0, n0, chunks;      // the CTA's first row, the tile's first column
     int out_kind;              // NsOut in the last step's APPLY, else 0
-    bool load, load_lo;        // the chunk's A or X comes in, and X's rounding error
+    bool load;                 // POLY: the chunk of A comes in; APPLY: X's rounding error
     bool twin, keep_lo;        // out go the transpose as well, or a rounding error
 };
 template <int TILE>
@@ -449,32 +449,30 @@ __device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArg
     p.n0 = u.j * TILE;
     p.chunks = p.row0 < a.m ? (min(TILE, (u.mode == NS_APPLY ? a.n : a.m) - p.n0) + 63) / 64 : 0;
     p.out_kind = u.mode == NS_APPLY && u.step + 1 == a.steps ? a.out_kind : 0;
-    p.load = u.mode != NS_GRAM;
     // the last step reads X without its rounding error, so the step before keeps none
-    p.load_lo = u.mode == NS_APPLY && u.step + 1 < a.steps && (u.step > 0 || a.first_lo);
+    p.load = u.mode == NS_POLY || (u.mode == NS_APPLY && u.step + 1 < a.steps && (u.step > 0 || a.first_lo));
     p.keep_lo = u.mode == NS_POLY ? a.b_lo : u.mode == NS_APPLY && u.step + 2 < a.steps;
     p.twin = u.mode != NS_APPLY && u.i != u.j;
     return p;
 }
 
-// What the epilogue multiplies: the accumulator; the tile of A or X that came with it, by an fp16 pair whose
-// sum is the factor to 22 bits; X's rounding error; and in the first step the whole by the rest of the norm.
-// The scales of X, A, B and O are in there.
+// What the epilogue multiplies: the accumulator; in POLY the tile of A that came with it, by an fp16 pair whose
+// sum is b to 22 bits, and a goes to B's diagonal; in APPLY X's rounding error; and in the first step the whole
+// by the rest of the norm.  The scales of X, A, B and O are in there.
 struct NsFactors {
-    float d, is;
-    uint32_t hi, lo, err;
+    float d, is, diag;
+    uint32_t hi, lo;
 };
 __device__ __forceinline__ NsFactors ns_factors(const NsUnit& u, const NsPart& p, const NsArgs& a) {
-    const float out = p.out_kind ? 1.f / kXScale : 1.f;
     NsFactors f;
     f.is = u.step == 0 ? __ldg(a.inv_s + u.mat) : 1.f;
     f.d = u.mode == NS_GRAM   ? kABScale / (kXScale * kXScale) * f.is * f.is
           : u.mode == NS_POLY ? a.co[3 * u.step + 2] / kABScale
-                              : out / kABScale;
-    const float x = u.mode == NS_POLY ? a.co[3 * u.step + 1] : out * a.co[3 * u.step];
+                              : (p.out_kind ? 1.f / kXScale : 1.f) / kABScale;
+    f.diag = a.co[3 * u.step] * kABScale;
+    const float x = u.mode == NS_POLY ? a.co[3 * u.step + 1] : a.co[3 * u.step] / kLoScale;
     f.hi = ns_pack_half(x, 0.f);
     f.lo = ns_pack_half(x - ns_unpack_half(f.hi).x, 0.f);
-    f.err = ns_pack_half(x * (1.f / kLoScale), 0.f);
     return f;
 }
 
@@ -716,7 +714,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const NsPart p = ns_part<kTile>(t, rank, a);
                 if (p.chunks == 0) continue;
                 if (p.load && !inputs(q)) break;
-                const CUtensorMap* tm = t.mode == NS_POLY ? &maps.a : &maps.x[t.step & 1];
+                const CUtensorMap* tm = t.mode == NS_POLY ? &maps.a : &maps.lo;
+                const int second = t.mode == NS_POLY ? 0 : kNsBox;   // the rounding error's place in the slot
                 for (int c = 0; c < p.chunks; ++c, ++k) {
                     const int slot = k % kNsSlots;
                     if (!mbar_wait(box_free + slot, (k / kNsSlots & 1) ^ 1u, abort_flag, a.status, a.wait_limit)) {
@@ -727,10 +726,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         mbar_arrive(box_full + slot);
                         continue;
                     }
-                    uint8_t* dst = sBox + slot * 2 * kNsBox;
-                    mbar_arrive_expect_tx(box_full + slot, p.load_lo ? 2 * kNsBox : kNsBox);
-                    tma_load_3d(dst, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
-                    if (p.load_lo) tma_load_3d(dst + kNsBox, &maps.lo, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
+                    mbar_arrive_expect_tx(box_full + slot, kNsBox);
+                    tma_load_3d(sBox + slot * 2 * kNsBox + second, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
                 }
             }
             // every load has landed (bounded) before the CTA exits
@@ -819,18 +816,24 @@ __global__ void __launch_bounds__(kNsThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f.d, v[2 * j + 1] * f.d);
                 } else {
-                    ns_box_read(out, sbox, br, half);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[2 * j] *= f.d;
-                        v[2 * j + 1] *= f.d;
-                        fma_f16x2(v + 2 * j, out[j], f.hi);
-                        fma_f16x2(v + 2 * j, out[j], f.lo);
-                    }
-                    if (p.load_lo) {
+                    for (int j = 0; j < 32; ++j) v[j] *= f.d;
+                    if (t.mode == NS_POLY) {
+                        ns_box_read(out, sbox, br, half);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            fma_f16x2(v + 2 * j, out[j], f.hi);
+                            fma_f16x2(v + 2 * j, out[j], f.lo);
+                        }
+                        if (p.row0 + 32 * quarter == col) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j == lane) v[j] += f.diag;
+                        }
+                    } else if (p.load) {
                         ns_box_read(low, sbox + kNsBox, br, half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) fma_f16x2(v + 2 * j, low[j], f.err);
+                        for (int j = 0; j < 16; ++j) fma_f16x2(v + 2 * j, low[j], f.hi);
                     }
                     if (t.step == 0 && t.mode == NS_APPLY) {
 #pragma unroll
