@@ -1032,17 +1032,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         __syncwarp();
         tc_fence_after();
     };
-    auto put_x = [&] {   // X as fp16
+    // X as fp16.  The last step takes a X from it too: with B and a of opposite signs by then, (a + B) of one X
+    // errs less than a of the exact and B of the rounded (16 x 27: 1.73e-3 against 1.84e-3 before the rounding
+    // to bf16; dropped from the step before it would cost matrices of low rank 2.3e-3 against 1.2e-3).
+    auto put_x = [&](bool last) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 8)
-            st_shared_v4(bX + (2 * half + j / 64) * 16384 + ns_sw(row, (j & 63) >> 3),
-                         make_uint4(ns_pack_half(x[j], x[j + 1]), ns_pack_half(x[j + 2], x[j + 3]),
-                                    ns_pack_half(x[j + 4], x[j + 5]), ns_pack_half(x[j + 6], x[j + 7])));
+        for (int j = 0; j < 128; j += 8) {
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) h[q] = ns_pack_half(x[j + 2 * q], x[j + 2 * q + 1]);
+            st_shared_v4(bX + (2 * half + j / 64) * 16384 + ns_sw(row, (j & 63) >> 3), make_uint4(h[0], h[1], h[2], h[3]));
+            if (last) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 r = ns_unpack_half(h[q]);
+                    x[j + 2 * q] = r.x;
+                    x[j + 2 * q + 1] = r.y;
+                }
+            }
+        }
     };
-    put_x();
+    put_x(false);
     for (int s = 0; s < a.steps; ++s) {
         const float ca = a.co[3 * s], cb = a.co[3 * s + 1], cc = a.co[3 * s + 2];
-        const float fa = kABScale / (kXScale * kXScale) * is * is;
+        const float fa = kABScale / (kXScale * kXScale) * is * is, fx = is * ca, fv = is * (1.f / kABScale);
         fence_proxy_async_cta();
         tc_fence_before();
         __syncthreads();
@@ -1146,17 +1159,25 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
                 const uint32_t to = half * 16384 + ns_sw(row, 4 * c + q);
                 const uint4 h = ld_shared_v4(bA + to);
                 const uint32_t w[4] = {h.x, h.y, h.z, h.w};
-                uint32_t hi[4], lo[4];
+                float b[8];
+                uint32_t hi[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 A = ns_unpack_half(w[e]);
-                    const float b0 = cb * A.x + cc / kABScale * v[8 * q + 2 * e], b1 = cb * A.y + cc / kABScale * v[8 * q + 2 * e + 1];
-                    hi[e] = ns_pack_half(b0, b1);
-                    const float2 r = ns_unpack_half(hi[e]);
-                    lo[e] = ns_pack_half(b0 - r.x, b1 - r.y);
+                    b[2 * e] = cb * A.x + cc / kABScale * v[8 * q + 2 * e];
+                    b[2 * e + 1] = cb * A.y + cc / kABScale * v[8 * q + 2 * e + 1];
+                    hi[e] = ns_pack_half(b[2 * e], b[2 * e + 1]);
                 }
                 st_shared_v4(bP + to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                if (b_parts == 2) st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                if (b_parts == 2) {
+                    uint32_t lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 r = ns_unpack_half(hi[e]);
+                        lo[e] = ns_pack_half(b[2 * e] - r.x, b[2 * e + 1] - r.y);
+                    }
+                    st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                }
             }
         }
         fence_proxy_async_cta();
@@ -1176,10 +1197,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             float v[32];
             tmem_ld32(tX + lane_addr + 128 * half + 32 * c, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[32 * c + j] = is * (ca * x[32 * c + j] + v[j] * (1.f / kABScale));
+            for (int j = 0; j < 32; ++j) x[32 * c + j] = fx * x[32 * c + j] + fv * v[j];
         }
         is = 1.f;
-        if (s + 1 < a.steps) put_x();
+        if (s + 1 < a.steps) put_x(s + 2 == a.steps);
     }
     // O as it stands (16 bytes of a row at a time) or flipped (a warp's rows are 64 consecutive bytes of O)
     if (i < a.m) {
