@@ -938,6 +938,76 @@ struct NsSmall {
     int withhold;
 };
 
+// A CTA's part of G comes in, and O goes out, through shared memory where G^T is kept or rows are no multiples
+// of 16 bytes (16 x 128 x 255, bf16: 27 us, by single elements of each row 61; with rows of 16-byte pieces, which
+// threads take from G themselves, 16 x 128 x 256 is 24.8 us, and 25.9 this way).  A part is a run of all
+// the CTA's columns, which are G's rows (flip), or for each row of each block of columns one of up to 256
+// elements, `pitch` bytes apart in shared memory: an odd number of words, so that threads of consecutive rows
+// meet no bank conflicts.  Copies are of words of W bytes, aligned on both sides: the data lies as far past a word in
+// shared memory as it does in global memory, words that it begins within come whole and go by elements.
+struct NsSlab {
+    int m, n, log_mp, flip, cta0;   // cta0: the CTA's first column of X
+    // move(first element, offset in shared memory, elements) for this thread's (flip) or warp's runs
+    template <typename F>
+    __device__ __forceinline__ void each(int pitch, F move) const {
+        if (flip) {
+            move(cta0 * m, 0, max(0, min((128 >> log_mp) * kSmallCols, n - cta0)) * m);
+            return;
+        }
+        // (128 n < 2^31; four rows at a time: one after the other took 300 cycles each in their addresses alone)
+#pragma unroll 4
+        for (int k = 0; k < 128 / (kSmallThreads / 32); ++k) {
+            const int r = (threadIdx.x >> 5) + k * (kSmallThreads / 32);
+            const int i = r & ((1 << log_mp) - 1), c = cta0 + (r >> log_mp) * kSmallCols;
+            if (i < m && c < n) move(i * n + c, r * pitch, min(kSmallCols, n - c));
+        }
+    }
+};
+template <int W, int STEP, int UNROLL>
+__device__ __forceinline__ void ns_stage_in(uint32_t to, const void* from, int bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(from) & ~uintptr_t(W - 1);
+    const int end = (int)(reinterpret_cast<uintptr_t>(from) - at) + bytes;
+#pragma unroll UNROLL
+    for (int w = W * (threadIdx.x & (STEP - 1)); w < end; w += W * STEP) {
+        if constexpr (W == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + w), "l"(at + w), "r"(min(W, end - w)) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + w), "l"(at + w), "r"(min(W, end - w)) : "memory");
+    }
+}
+__device__ __forceinline__ uint16_t ns_lds16(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ns_lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+// a run of bf16: the whole words, then (flip's first and last thread, or a row's lanes) what is before and after
+template <int W, int STEP>
+__device__ __forceinline__ void ns_stage_out(void* to, uint32_t from, int bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(to) & ~uintptr_t(W - 1);
+    const int begin = (int)(reinterpret_cast<uintptr_t>(to) - at), end = begin + bytes;
+    const int lo = (begin + W - 1) & ~(W - 1), hi = end & ~(W - 1), t = threadIdx.x & (STEP - 1);
+    if constexpr (W == 16) {
+#pragma unroll 4
+        for (int w = lo + W * t; w < hi; w += W * STEP) *reinterpret_cast<uint4*>(at + w) = ld_shared_v4(from + w);
+    } else {   // up to 129 words
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (lo + W * (t + k * STEP) < hi) v[k] = ns_lds32(from + lo + W * (t + k * STEP));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (lo + W * (t + k * STEP) < hi) *reinterpret_cast<uint32_t*>(at + lo + W * (t + k * STEP)) = v[k];
+    }
+    const int head = begin + 2 * t, tail = max(hi, lo) + 2 * t;   // (a run within one word: lo > hi, all of it is head)
+    if (head < min(lo, end)) *reinterpret_cast<uint16_t*>(at + head) = ns_lds16(from + head);
+    if (tail < end) *reinterpret_cast<uint16_t*>(at + tail) = ns_lds16(from + tail);
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __restrict__ G, const NsSmall a) {
     grid_dep_wait();
@@ -964,25 +1034,46 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, 512);
-    if (blocks > 1)   // A is zero outside its diagonal blocks
+    auto zero_a = [&] {   // A is zero outside its diagonal blocks
         for (int e = threadIdx.x; e < kSmallA / 16; e += kSmallThreads) st_shared_v4(smem_u32(sA) + 16 * e, make_uint4(0, 0, 0, 0));
+    };
+    if (VEC && blocks > 1) zero_a();
     float x[128];
     float sq = 0.f;
     const T* g = G + (long long)mat * a.R * a.C;
-    if (VEC && !a.flip) {
+    const int log_mp = 31 - __clz(mp), block = row >> log_mp, left = i < a.m ? a.n - col0 : 0;   // columns that hold X
+    if constexpr (VEC) {
 #pragma unroll
         for (int j = 0; j < 128; j += 8) {
             if (i < a.m && col0 + j < a.n) {
-                ns_val8(x + j, g + (long long)i * a.C + col0 + j);
+                ns_val8(x + j, g + (long long)i * a.n + col0 + j);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) x[j + q] = 0.f;
             }
         }
     } else {
-        const long long ri = a.flip ? 1 : a.C, rj = a.flip ? a.C : 1;
+        constexpr int kBytes = (int)sizeof(T), kPitch = kSmallCols * kBytes + 4;
+        const uint32_t stage = smem_u32(smem);
+        const NsSlab slab{a.m, a.n, log_mp, a.flip, rank * blocks * kSmallCols};
+        slab.each(kPitch, [&](int e, int at, int count) {
+            if (a.flip) ns_stage_in<16, kSmallThreads, 4>(stage, g + e, count * kBytes);
+            else ns_stage_in<4, 32, kPitch / 128>(stage + at, g + e, count * kBytes);
+        });
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        // the thread's elements: every m-th of the CTA's run, or consecutive ones of its row's
+        const uint32_t past = (uint32_t)reinterpret_cast<uintptr_t>(g + (a.flip ? slab.cta0 * a.m : i * a.n + slab.cta0));
+        const uint32_t from = a.flip ? stage + (past & 15) + (uint32_t)(((block * kSmallCols + half * 128) * a.m + i) * kBytes)
+                                     : stage + (past & 3) + (uint32_t)(row * kPitch + half * 128 * kBytes);
+        const uint32_t step = a.flip ? a.m * kBytes : kBytes;
 #pragma unroll
-        for (int j = 0; j < 128; ++j) x[j] = i < a.m && col0 + j < a.n ? ns_val(g, i * ri + (col0 + j) * rj) : 0.f;
+        for (int j = 0; j < 128; ++j) {   // (what is read past X is within the buffer, and dropped)
+            float v;
+            if constexpr (kBytes == 4) v = __uint_as_float(ns_lds32(from + j * step));
+            else v = __uint_as_float((uint32_t)ns_lds16(from + j * step) << 16);
+            x[j] = j < left ? v : 0.f;
+        }
     }
 #pragma unroll
     for (int j = 0; j < 128; j += 8) {
@@ -998,6 +1089,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
+    if (!VEC && blocks > 1) zero_a();
     sq = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) sq += warp_sums[w];
@@ -1202,31 +1294,35 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         is = 1.f;
         if (s + 1 < a.steps) put_x(s + 2 == a.steps);
     }
-    // O as it stands (16 bytes of a row at a time) or flipped (a warp's rows are 64 consecutive bytes of O)
-    if (i < a.m) {
-        if (a.flip) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-                if (col0 + j < a.n)
-                    a.O[((long long)mat * a.n + col0 + j) * a.m + i] = __float2bfloat16_rn(x[j] * (1.f / kXScale));
-        } else {
+    constexpr float u = 1.f / kXScale;
+    if constexpr (VEC) {
+        if (i < a.m) {
             __nv_bfloat16* o = a.O + ((long long)mat * a.m + i) * a.n + col0;
 #pragma unroll
-            for (int j = 0; j < 128; j += 8) {
-                if (VEC) {
-                    if (col0 + j < a.n) {
-                        constexpr float u = 1.f / kXScale;
-                        *reinterpret_cast<uint4*>(o + j) =
-                            make_uint4(pack_bf16x2(x[j] * u, x[j + 1] * u), pack_bf16x2(x[j + 2] * u, x[j + 3] * u),
-                                       pack_bf16x2(x[j + 4] * u, x[j + 5] * u), pack_bf16x2(x[j + 6] * u, x[j + 7] * u));
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (col0 + j + q < a.n) o[j + q] = __float2bfloat16_rn(x[j + q] * (1.f / kXScale));
-                }
-            }
+            for (int j = 0; j < 128; j += 8)
+                if (col0 + j < a.n)
+                    *reinterpret_cast<uint4*>(o + j) =
+                        make_uint4(pack_bf16x2(x[j] * u, x[j + 1] * u), pack_bf16x2(x[j + 2] * u, x[j + 3] * u),
+                                   pack_bf16x2(x[j + 4] * u, x[j + 5] * u), pack_bf16x2(x[j + 6] * u, x[j + 7] * u));
         }
+    } else {
+        constexpr int kPitch = kSmallCols * 2 + 4;
+        const uint32_t stage = smem_u32(smem);
+        const NsSlab slab{a.m, a.n, log_mp, a.flip, rank * blocks * kSmallCols};
+        __nv_bfloat16* o = a.O + (long long)mat * a.m * a.n;
+        const uint32_t past = (uint32_t)reinterpret_cast<uintptr_t>(o + (a.flip ? slab.cta0 * a.m : i * a.n + slab.cta0));
+        const uint32_t to = a.flip ? stage + (past & 15) + (uint32_t)(((block * kSmallCols + half * 128) * a.m + i) * 2)
+                                   : stage + (past & 3) + (uint32_t)(row * kPitch + half * 256);
+        const uint32_t step = a.flip ? a.m * 2 : 2;
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+            asm volatile("{\n.reg .pred p;\nsetp.lt.s32 p, %2, %3;\n@p st.shared.b16 [%0], %1;\n}" ::"r"(to + j * step),
+                         "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x[j] * u))), "r"(j), "r"(left) : "memory");
+        __syncthreads();
+        slab.each(kPitch, [&](int e, int at, int count) {
+            if (a.flip) ns_stage_out<16, kSmallThreads>(o + e, stage, 2 * count);
+            else ns_stage_out<4, 32>(o + e, stage + at, 2 * count);
+        });
     }
     // an MMA whose wait ran out may still be at work (bounded): it ends before its memory is given up
     if (*abort_flag && threadIdx.x == 0 && !a.withhold) ns_wait_drain(done, phase ^ 1u);
@@ -1426,7 +1522,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         const auto* gf = static_cast<const float*>(G);
         const auto* gb = static_cast<const __nv_bfloat16*>(G);
         bool ran = false;
-        const cudaError_t err = C % 8 == 0 ? (g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a, &ran)
+        const cudaError_t err = C % 8 == 0 && R <= C ? (g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a, &ran)
                                                     : ns_small<__nv_bfloat16, true>(st, gb, S, (int)N, a, &ran))
                                            : (g_f32 ? ns_small<float, false>(st, gf, S, (int)N, a, &ran)
                                                     : ns_small<__nv_bfloat16, false>(st, gb, S, (int)N, a, &ran));

@@ -187,3 +187,20 @@ def test_waits_are_bounded(cuda_lib, N, R, C):
     bd.moe_orthogonalise(G, O, ws)
     assert bd.moe_read_device_status(ws) == 0
     assert max(errors(O, exact(G))) < BAR
+
+
+@pytest.mark.parametrize("N,R,C", [(5, 7, 513), (3, 513, 7), (4, 33, 255), (9, 255, 33), (3, 127, 771), (7, 1, 3), (7, 3, 1),
+                                   (2, 5, 2), (11, 31, 33), (2, 1021, 61), (3, 65, 2047), (3, 2047, 65), (2, 131, 263)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_off_16_bytes_between_guards(cuda_lib, N, R, C, dtype):
+    """Matrices and rows that begin anywhere: nothing beside O is written, and O may be G itself."""
+    G, n = gauss(N, R, C, dtype, seed=R + 3 * C), N * R * C
+    ref = exact(G)
+    buf = torch.full((n + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert max(errors(run(cuda_lib, G, O=buf[8:8 + n].view(N, R, C)), ref)) < BAR
+    assert bool((buf[:8] == 7).all()) and bool((buf[8 + n:] == 7).all())
+    if dtype is torch.bfloat16:
+        buf[8:8 + n] = G.flatten()
+        inside = buf[8:8 + n].view(N, R, C)
+        assert max(errors(run(cuda_lib, inside, O=inside), ref)) < BAR
+        assert bool((buf[:8] == 7).all()) and bool((buf[8 + n:] == 7).all())
