@@ -14,7 +14,10 @@
 // largest ones, so X also keeps its rounding error as a second fp16 (`lo`, times 2^11 again) for the
 // a X term of every step but the last: without it gradients of low rank came out 1 % off, with it
 // 0.1 %.  A matrix of up to 64 rows keeps B's rounding error too, as a second product of APPLY: with few
-// singular values B's error does not average out (a single row came out up to 0.5 % off).
+// singular values B's error does not average out.  In the large kernel the rest of a X goes through the
+// products, as a on B's diagonal: the epilogue then needs no X (256 x 768 x 2048: 1 % less time), and the
+// error moves between kinds of matrices (before the rounding to bf16, 200 x 600: gaussian 1.80 -> 1.56e-3,
+// rank 25 0.8 -> 1.7e-3).
 #include <algorithm>
 #include <mutex>
 
@@ -912,6 +915,126 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     }
 }
 
+// ---- matrices of up to 8 rows: fp32 throughout ------------------------------------------------------------
+// With so few singular values the rounding errors of fp16 operands do not average out (1 x 3 and 5 x 2 came out
+// up to 0.53 % off), and the work is small: a CTA takes a matrix, keeps the product M of the steps' a I + B,
+// 8 x 8, and forms X = M G / (|G| + eps) a column at a time, once a step for A = X X^T and once for O (a
+// recursion of A alone would need no more than the first of these passes, but it loses what is below A's
+// rounding, and with it that A has no negative eigenvalue).  Over 1024 columns a cluster of up to eight CTAs
+// takes the matrix, each some of its columns and all the sums.  Latency of the passes and of six block sums binds it
+// (40 x 8 x 70: 13.8 us, 8 x 32768: 45 us; on the tensor cores, by the kernel below, 20.7 and 86).
+constexpr int kTinyRows = 8;
+constexpr int kTinyThreads = 512;
+struct NsTiny {
+    int m, n, flip, steps, ctas;
+    float eps;
+    float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
+};
+// element (i, k), i <= k, of a symmetric 8 x 8 matrix among its 36
+__device__ __forceinline__ constexpr int ns_tri(int i, int k) { return i * (2 * kTinyRows - 1 - i) / 2 + k; }
+
+template <typename T>
+__global__ void __launch_bounds__(kTinyThreads) ns_tiny_kernel(const T* G, __nv_bfloat16* O, const NsTiny a) {
+    grid_dep_wait();
+    constexpr int K = kTinyRows, kTri = K * (K + 1) / 2, kWarps = kTinyThreads / 32;
+    __shared__ float part[kWarps][kTri], sums[2][kTri], sA[K][K], sC[K][K], sM[K][K];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ti = threadIdx.x >> 3, tk = threadIdx.x & 7;
+    const int S = a.ctas, j0 = (int)(blockIdx.x % S) * kTinyThreads + threadIdx.x;
+    const long long base = (long long)(blockIdx.x / S) * a.m * a.n;
+    const int si = a.flip ? 1 : a.n, sj = a.flip ? a.m : 1;
+    float M[K][K];
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) M[i][k] = i == k ? 1.f : 0.f;
+    if (threadIdx.x < K * K) sM[ti][tk] = ti == tk ? 1.f : 0.f;
+    float f = 1.f;   // 1 / (|G| + eps), which the first pass finds
+    auto column = [&](int j, float* x) {
+        float g[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) g[i] = ns_val(G, base + (long long)min(i, a.m - 1) * si + (long long)j * sj);
+#pragma unroll
+        for (int i = 0; i < K; ++i) g[i] = i < a.m ? g[i] * f : 0.f;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            x[i] = M[i][0] * g[0];
+#pragma unroll
+            for (int k = 1; k < K; ++k) x[i] += M[i][k] * g[k];
+        }
+    };
+    for (int s = 0; s < a.steps; ++s) {
+        float sum[kTri], x[K];
+#pragma unroll
+        for (int e = 0; e < kTri; ++e) sum[e] = 0.f;
+        for (int j = j0; j < a.n; j += S * kTinyThreads) {
+            column(j, x);
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+#pragma unroll
+                for (int k = i; k < K; ++k) sum[ns_tri(i, k)] += x[i] * x[k];
+        }
+#pragma unroll
+        for (int e = 0; e < kTri; ++e) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+            if (lane == 0) part[warp][e] = sum[e];
+        }
+        __syncthreads();
+        float* mine = sums[s & 1];   // (read by the others until they have passed the next step's barrier)
+        if (threadIdx.x < kTri) {
+            float v = 0.f;
+            for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+            mine[threadIdx.x] = v;
+        }
+        if (S > 1) cluster_sync();
+        else __syncthreads();
+        auto total = [&](int e) {
+            float v = S > 1 ? 0.f : mine[e];
+            if (S > 1)
+                for (int c = 0; c < S; ++c) v += ld_cluster_f32(cluster_addr(mine + e, c));
+            return v;
+        };
+        if (threadIdx.x < K * K) sA[ti][tk] = total(ns_tri(min(ti, tk), max(ti, tk)));
+        __syncthreads();
+        if (s == 0) {
+            float sq = 0.f;
+#pragma unroll
+            for (int i = 0; i < K; ++i) sq += sA[i][i];
+            const float norm = sqrtf(sq);
+            f = norm <= 3.4e38f ? 1.f / (norm + a.eps) : NAN;
+            __syncthreads();
+            if (threadIdx.x < K * K) sA[ti][tk] = sA[ti][tk] * f * f;
+        }
+        __syncthreads();
+        if (threadIdx.x < K * K) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < K; ++q) v += sA[ti][q] * sA[q][tk];
+            sC[ti][tk] = (ti == tk ? a.co[3 * s] : 0.f) + a.co[3 * s + 1] * sA[ti][tk] + a.co[3 * s + 2] * v;
+        }
+        __syncthreads();
+        float v = 0.f;
+        if (threadIdx.x < K * K)
+#pragma unroll
+            for (int q = 0; q < K; ++q) v += sC[ti][q] * sM[q][tk];
+        __syncthreads();
+        if (threadIdx.x < K * K) sM[ti][tk] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+            for (int k = 0; k < K; ++k) M[i][k] = sM[i][k];
+    }
+    for (int j = j0; j < a.n; j += S * kTinyThreads) {   // O may be G: a column is read before it is written
+        float x[K];
+        column(j, x);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (i < a.m) O[base + (long long)i * si + (long long)j * sj] = __float2bfloat16_rn(x[i]);
+    }
+    if (S > 1) cluster_sync();   // no CTA's sums are read any more
+}
+
 // ---- matrices of up to 128 rows: the whole operator in one kernel --------------------------------------
 // The products of a matrix with m <= 128 are too small to be launches of their own (17 of them took
 // 120 us at 128 x 2048).  A cluster of CTAs takes a matrix, each CTA 256 of its columns, from G to O: X in
@@ -1368,6 +1491,10 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
     take(256);   // status word
+    if (L->m <= kTinyRows) {
+        L->total = o;
+        return true;
+    }
     int mp;
     const int S = ns_small_cluster(N, L->m, L->n, &mp);
     if (S > 0 && S <= 8) {   // (whether a cluster of 16 is possible only the GPU can tell)
@@ -1442,6 +1569,29 @@ static cudaError_t ns_resident(int num_sms, int* most) {
     return err;
 }
 
+template <typename T>
+static cudaError_t ns_tiny(cudaStream_t st, const T* G, __nv_bfloat16* O, const NsLayout& L, bool flip, int steps,
+                           const float* coeffs, float eps) {
+    int S = 1;
+    while (S < 8 && S * 2 * kTinyThreads < L.n) S *= 2;
+    NsTiny a{(int)L.m, (int)L.n, flip, steps, S, eps};
+    std::copy(coeffs, coeffs + 3 * steps, a.co);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(L.N * S));
+    cfg.blockDim = dim3(kTinyThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, ns_tiny_kernel<T>, G, O, a);
+}
+
 // `*ran` false: this GPU has no room for such a cluster
 template <typename T, bool VEC>
 static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsSmall& a, bool* ran) {
@@ -1511,6 +1661,10 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
                                  long long wait_limit, bool withhold_loads) {
     NsLayout L;
     if (!ns_layout(N, R, C, &L)) return cudaErrorInvalidValue;
+    if (L.m <= kTinyRows) {
+        return g_f32 ? ns_tiny(st, static_cast<const float*>(G), static_cast<__nv_bfloat16*>(O), L, R > C, steps, coeffs, eps)
+                     : ns_tiny(st, static_cast<const __nv_bfloat16*>(G), static_cast<__nv_bfloat16*>(O), L, R > C, steps, coeffs, eps);
+    }
     int mp;
     if (const int S = ns_small_cluster(N, L.m, L.n, &mp)) {
         NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, mp, steps, R > C, eps};
