@@ -484,7 +484,7 @@ __device__ __forceinline__ NsFactors ns_factors(const NsUnit& u, const NsPart& p
 //   warp 1      MMAs into one of two accumulators
 //   warps 2-9   epilogue: lane quarter w % 4, alternate 32 columns; a chunk is 64 columns of the tile
 //   warp 10     watches the matrices' counters ahead of the others: `ready` units of this CTA have inputs
-//   warp 11     what a chunk needs besides its accumulator (POLY: A; APPLY: X and its rounding error), by
+//   warp 11     what a chunk needs besides its accumulator (POLY: A; APPLY: X's rounding error), by
 //               TMA into one of three slots
 //   warp 12     stores the slot, where the epilogue has put the results in their place, frees it, and
 //               counts the tile once its stores are complete
@@ -1459,11 +1459,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 }
 
 // ---- launches --------------------------------------------------------------------------------------
-// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  One or two
-// CTAs take any number of matrices; of more the kernel runs about 48 us however few there are, and for over
-// two rounds of the GPU's SMs the large kernels are faster (128 x 2048, 1, 16, 32, 128 matrices: 48, 96, 144,
-// 440 us here and 113, 127, 174, 419 there; 100 x 700, 256 matrices: 552 and 360; 32 x 512, 256 matrices: 149
-// and 188).
+// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  Up to 64 rows
+// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 684 us
+// here, 1014 there; 64 x 2000, 300: 408 and 759); so do one or two CTAs, and four whose columns are filled
+// (100 x 1000, 200: 286 and 356; 128 x 1024, 256: 384 and 400).  Of more CTAs the kernel runs about 50 us a round
+// of the GPU however few the matrices are, and the large kernel is even with it at 512 CTAs if filled, and at
+// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 159, 263, 471 us here and 217, 267, 430 there;
+// 128 x 4096, 32 and 64: 279, 562 and 329, 504; 70 x 600, 128: 177 and 149).
 static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
     *mp = 128;
     while (*mp / 2 >= m && *mp > 16 && (128 / *mp) * kSmallCols < n) *mp /= 2;
@@ -1471,7 +1473,8 @@ static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
     if (m > 128 || n > 16 * cols) return 0;
     int S = 1;
     while (S * cols < n) S *= 2;
-    return S <= 2 || N * S <= 304 ? S : 0;
+    const bool filled = 4 * n > 3 * S * cols;
+    return *mp < 128 || S <= 2 || (S == 4 && filled) || N * S <= (filled ? 512 : 304) ? S : 0;
 }
 
 struct NsLayout {

@@ -204,3 +204,11 @@ def test_rows_off_16_bytes_between_guards(cuda_lib, N, R, C, dtype):
         inside = buf[8:8 + n].view(N, R, C)
         assert max(errors(run(cuda_lib, inside, O=inside), ref)) < BAR
         assert bool((buf[:8] == 7).all()) and bool((buf[8 + n:] == 7).all())
+
+
+@pytest.mark.parametrize("N,R,C", [(160, 40, 600), (90, 1100, 64), (2, 50, 9000), (1, 16500, 20), (140, 100, 900), (24, 128, 4000),
+                                   (3, 8, 1025), (2, 9000, 8), (2, 9, 1000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_short_and_long_matrices(cuda_lib, N, R, C, dtype):
+    G = gauss(N, R, C, dtype, seed=N + R + C)
+    assert max(errors(run(cuda_lib, G), exact(G))) < BAR
