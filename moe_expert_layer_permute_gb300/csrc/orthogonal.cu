@@ -1052,7 +1052,7 @@ constexpr int kSmallA = 2 * 16384;   // A likewise; the partial A in fp32, later
 constexpr int kSmallBytes = 1024 + kSmallX + 3 * kSmallA + 256;
 
 struct NsSmall {
-    int R, C, m, n, mp, steps, flip;   // mp: rows of a block, 128 / mp blocks of columns one below the other
+    int R, C, m, n, mp, log_mp, log_ctas, steps, flip;   // mp: rows of a block, 128 / mp blocks one below the other
     float eps;
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
     __nv_bfloat16* O;
@@ -1148,9 +1148,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     const int S = (int)gridDim.x, rank = S > 1 ? (int)cluster_ctarank() : 0, mat = blockIdx.y;
     const int quarter = warp & 3, half = warp >> 2;
     const int row = quarter * 32 + lane;                      // the thread's row in shared memory,
-    const int mp = a.mp, blocks = 128 / mp;
+    const int mp = a.mp, blocks = 128 >> a.log_mp;
     const int i = row & (mp - 1);                             // of X,
-    const int col0 = (rank * blocks + row / mp) * kSmallCols + half * 128;   // and the first of its 128 columns
+    const int col0 = (rank * blocks + (row >> a.log_mp)) * kSmallCols + half * 128;   // and the first of its 128 columns
     if (threadIdx.x == 0) {
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -1164,7 +1164,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     float x[128];
     float sq = 0.f;
     const T* g = G + (long long)mat * a.R * a.C;
-    const int log_mp = 31 - __clz(mp), block = row >> log_mp, left = i < a.m ? a.n - col0 : 0;   // columns that hold X
+    const int block = row >> a.log_mp, left = i < a.m ? a.n - col0 : 0;   // columns that hold X
     if constexpr (VEC) {
 #pragma unroll
         for (int j = 0; j < 128; j += 8) {
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     } else {
         constexpr int kBytes = (int)sizeof(T), kPitch = kSmallCols * kBytes + 4;
         const uint32_t stage = smem_u32(smem);
-        const NsSlab slab{a.m, a.n, log_mp, a.flip, rank * blocks * kSmallCols};
+        const NsSlab slab{a.m, a.n, a.log_mp, a.flip, rank * blocks * kSmallCols};
         slab.each(kPitch, [&](int e, int at, int count) {
             if (a.flip) ns_stage_in<16, kSmallThreads, 4>(stage, g + e, count * kBytes);
             else ns_stage_in<4, 32, kPitch / 128>(stage + at, g + e, count * kBytes);
@@ -1310,7 +1310,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int cb = 64 * half + 32 * c;
-                if (cb / max(mp, 32) != quarter * 32 / max(mp, 32)) continue;   // the same for the whole warp
+                if (cb >> max(a.log_mp, 5) != quarter * 32 >> max(a.log_mp, 5)) continue;   // the same for the whole warp
                 float v[32];
                 tmem_ld32(tA + lane_addr + cb, v);
                 if (mp >= 32) {
@@ -1326,15 +1326,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             }
             if (S > 1) cluster_sync();
             else __syncthreads();
-            const int rows = mp / S, per_row = mp / 4;
-            for (int e = threadIdx.x; e < rows * per_row; e += kSmallThreads) {
-                const int r = rank * rows + e / per_row, at = e & (per_row - 1);
+            const int log_rows = a.log_mp - a.log_ctas, log_blocks = 7 - a.log_mp, log_pieces = a.log_mp - 2;   // a row's 16-byte pieces
+            for (int e = threadIdx.x; e < 1 << (log_rows + log_pieces); e += kSmallThreads) {
+                const int r = (rank << log_rows) + (e >> log_pieces), at = e & ((1 << log_pieces) - 1);
                 float4 v[4], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
                 for (int t0 = 0; t0 < S * blocks; t0 += 4) {   // CTA by CTA, block by block
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {   // all under way before the first is added
-                        const int b = (t0 + t) / blocks, br = ((t0 + t) & (blocks - 1)) * mp + r;
+                        const int b = (t0 + t) >> log_blocks, br = (((t0 + t) & (blocks - 1)) << a.log_mp) + r;
                         v[t] = b < S ? ld_cluster_f32x4(cluster_addr(sP, b) + (uint32_t)(br * 512 + ((at ^ (br & 31)) << 4)))
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
@@ -1345,8 +1345,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
                 }
                 const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
                 for (int q = 0; q < blocks; ++q) {
-                    const int col = q * mp + 4 * at;
-                    const uint32_t to = (uint32_t)((col >> 6) * 16384) + ns_sw(q * mp + r, (col & 63) >> 3) + (at & 1) * 8;
+                    const int col = (q << a.log_mp) + 4 * at;
+                    const uint32_t to = (uint32_t)((col >> 6) * 16384) + ns_sw((q << a.log_mp) + r, (col & 63) >> 3) + (at & 1) * 8;
                     for (int b = 0; b < S; ++b) st_cluster_v2(cluster_addr(sA, b) + to, h0, h1);
                 }
             }
@@ -1431,7 +1431,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     } else {
         constexpr int kPitch = kSmallCols * 2 + 4;
         const uint32_t stage = smem_u32(smem);
-        const NsSlab slab{a.m, a.n, log_mp, a.flip, rank * blocks * kSmallCols};
+        const NsSlab slab{a.m, a.n, a.log_mp, a.flip, rank * blocks * kSmallCols};
         __nv_bfloat16* o = a.O + (long long)mat * a.m * a.n;
         const uint32_t past = (uint32_t)reinterpret_cast<uintptr_t>(o + (a.flip ? slab.cta0 * a.m : i * a.n + slab.cta0));
         const uint32_t to = a.flip ? stage + (past & 15) + (uint32_t)(((block * kSmallCols + half * 128) * a.m + i) * 2)
@@ -1476,6 +1476,8 @@ static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
     const bool filled = 4 * n > 3 * S * cols;
     return *mp < 128 || S <= 2 || (S == 4 && filled) || N * S <= (filled ? 512 : 304) ? S : 0;
 }
+
+static int ns_log2(int v) { return v < 2 ? 0 : 1 + ns_log2(v / 2); }
 
 struct NsLayout {
     int64_t N, m, n, lda, ldx, parts;
@@ -1670,7 +1672,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     }
     int mp;
     if (const int S = ns_small_cluster(N, L.m, L.n, &mp)) {
-        NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, mp, steps, R > C, eps};
+        NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, mp, ns_log2(mp), ns_log2(S), steps, R > C, eps};
         std::copy(coeffs, coeffs + 3 * steps, a.co);
         a.O = static_cast<__nv_bfloat16*>(O);
         a.status = status;
