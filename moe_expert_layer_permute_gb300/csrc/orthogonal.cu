@@ -1044,7 +1044,7 @@ __global__ void __launch_bounds__(kTinyThreads) ns_tiny_kernel(const T* G, __nv_
 //   order and sending them to all as fp16 -> A A and B in every CTA -> X of the CTA's columns.
 // Where m leaves room, up to eight blocks of 256 columns lie one below the other in the CTA's 128 rows: A is
 // the sum of the diagonal blocks of their product, and with A and B laid out block-diagonally the rest goes
-// as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 86 here).
+// as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 76 here).
 constexpr int kSmallCols = 256;
 constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
 constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
@@ -1460,12 +1460,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 
 // ---- launches --------------------------------------------------------------------------------------
 // CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  Up to 64 rows
-// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 684 us
-// here, 1014 there; 64 x 2000, 300: 408 and 759); so do one or two CTAs, and four whose columns are filled
-// (100 x 1000, 200: 286 and 356; 128 x 1024, 256: 384 and 400).  Of more CTAs the kernel runs about 50 us a round
-// of the GPU however few the matrices are, and the large kernel is even with it at 512 CTAs if filled, and at
-// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 159, 263, 471 us here and 217, 267, 430 there;
-// 128 x 4096, 32 and 64: 279, 562 and 329, 504; 70 x 600, 128: 177 and 149).
+// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 636 us
+// here, 1014 there; 64 x 2000, 300: 383 and 759); so do one or two CTAs, and four whose columns are filled
+// (100 x 1000, 200: 260 and 356; 128 x 1024, 256: 346 and 400).  Of more CTAs the kernel runs about 48 us a round
+// of the GPU however few the matrices are, and the large kernel is even with it beyond 512 CTAs if filled, and at
+// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 150, 249, 443 us here and 217, 267, 430 there;
+// 128 x 4096, 32 and 64: 263, 530 and 329, 504; 70 x 600, 128: 161 and 149).
 static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
     *mp = 128;
     while (*mp / 2 >= m && *mp > 16 && (128 / *mp) * kSmallCols < n) *mp /= 2;
