@@ -248,7 +248,8 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
  * (on G^T where R > C, which gives the same), and O [N, R, C] bf16 receives X.  coeffs: host floats,
  * (a, b, c) for each step, or NULL for (3.4445, -4.7750, 2.0315) throughout.  O may be G itself (bf16).
  * The products take fp16 operands with fp32 sums: O is within about 2.5e-3 (2-norm, bf16's own
- * rounding of 1.7e-3 included) of the exact result for the default coefficients and five steps.
+ * rounding of 1.7e-3 included) of the exact result for the default coefficients and five steps; with up
+ * to 8 rows or columns, whose few errors would not average out, they are fp32 throughout.
  * A zero matrix (an expert without tokens) gives zeros; one with a NaN, an infinity or a squared norm
  * beyond fp32 gives NaN, the others of the batch unharmed.
  * `workspace`: a zeroed moe_scratch handle of at least moe_orthogonalise_workspace_bytes(N, R, C)
