@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "slab.h"
 
 #include <cuda_fp16.h>
 
@@ -1046,8 +1047,6 @@ __global__ void __launch_bounds__(kTinyThreads) ns_tiny_kernel(const T* G, __nv_
 // Where m leaves room, up to eight blocks of 256 columns lie one below the other in the CTA's 128 rows: A is
 // the sum of the diagonal blocks of their product, and with A and B laid out block-diagonally the rest goes
 // as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 76 here).
-constexpr int kSmallCols = 256;
-constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
 constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
 constexpr int kSmallA = 2 * 16384;   // A likewise; the partial A in fp32, later B and its rounding error
 constexpr int kSmallBytes = 1024 + kSmallX + 3 * kSmallA + 256;
@@ -1062,42 +1061,15 @@ struct NsSmall {
     int withhold;
 };
 
-// A CTA's part of G comes in, and O goes out, through shared memory where G^T is kept or rows are no multiples
-// of 16 bytes (16 x 128 x 255, bf16: 27 us, by single elements of each row 61; with rows of 16-byte pieces, which
-// threads take from G themselves, 16 x 128 x 256 is 24.8 us, and 25.9 this way).  A part is a run of all
-// the CTA's columns, which are G's rows (flip), or for each row of each block of columns one of up to 256
-// elements, `pitch` bytes apart in shared memory: an odd number of words, so that threads of consecutive rows
-// meet no bank conflicts.  Copies are of words of W bytes, aligned on both sides: the data lies as far past a word in
-// shared memory as it does in global memory, words that it begins within come whole and go by elements.
-struct NsSlab {
-    int m, n, log_mp, flip, cta0;   // cta0: the CTA's first column of X
-    // move(first element, offset in shared memory, elements) for this thread's (flip) or warp's runs
-    template <typename F>
-    __device__ __forceinline__ void each(int pitch, F move) const {
-        if (flip) {
-            move(cta0 * m, 0, max(0, min((128 >> log_mp) * kSmallCols, n - cta0)) * m);
-            return;
-        }
-        // (128 n < 2^31; four rows at a time: one after the other took 300 cycles each in their addresses alone)
-#pragma unroll 4
-        for (int k = 0; k < 128 / (kSmallThreads / 32); ++k) {
-            const int r = (threadIdx.x >> 5) + k * (kSmallThreads / 32);
-            const int i = r & ((1 << log_mp) - 1), c = cta0 + (r >> log_mp) * kSmallCols;
-            if (i < m && c < n) move(i * n + c, r * pitch, min(kSmallCols, n - c));
-        }
-    }
-};
 template <int W, int STEP, int UNROLL>
 __device__ __forceinline__ void ns_stage_in(uint32_t to, const void* from, int bytes) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(from) & ~uintptr_t(W - 1);
-    const int end = (int)(reinterpret_cast<uintptr_t>(from) - at) + bytes;
-#pragma unroll UNROLL
-    for (int w = W * (threadIdx.x & (STEP - 1)); w < end; w += W * STEP) {
+    const NsWords<W> words(reinterpret_cast<uintptr_t>(from), bytes);
+    words.template each<STEP, UNROLL>(threadIdx.x & (STEP - 1), [&](int w, int held) {
         if constexpr (W == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + w), "l"(at + w), "r"(min(W, end - w)) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + w), "l"(words.at + w), "r"(held) : "memory");
         else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + w), "l"(at + w), "r"(min(W, end - w)) : "memory");
-    }
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + w), "l"(words.at + w), "r"(held) : "memory");
+    });
 }
 __device__ __forceinline__ uint16_t ns_lds16(uint32_t at) {
     uint16_t v;
@@ -1180,9 +1152,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         constexpr int kBytes = (int)sizeof(T), kPitch = kSmallCols * kBytes + 4;
         const uint32_t stage = smem_u32(smem);
         const NsSlab slab{a.m, a.n, a.log_mp, a.flip, rank * blocks * kSmallCols};
-        slab.each(kPitch, [&](int e, int at, int count) {
-            if (a.flip) ns_stage_in<16, kSmallThreads, 4>(stage, g + e, count * kBytes);
-            else ns_stage_in<4, 32, kPitch / 128>(stage + at, g + e, count * kBytes);
+        slab.each(kPitch, warp, [&](const NsRun& run) {
+            if (a.flip) ns_stage_in<16, kSmallThreads, 4>(stage, g + run.first, run.count * kBytes);
+            else ns_stage_in<4, 32, kPitch / 128>(stage + run.at, g + run.first, run.count * kBytes);
         });
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
@@ -1490,9 +1462,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             asm volatile("{\n.reg .pred p;\nsetp.lt.s32 p, %2, %3;\n@p st.shared.b16 [%0], %1;\n}" ::"r"(to + j * step),
                          "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x[j] * u))), "r"(j), "r"(left) : "memory");
         __syncthreads();
-        slab.each(kPitch, [&](int e, int at, int count) {
-            if (a.flip) ns_stage_out<16, kSmallThreads>(o + e, stage, 2 * count);
-            else ns_stage_out<4, 32>(o + e, stage + at, 2 * count);
+        slab.each(kPitch, warp, [&](const NsRun& run) {
+            if (a.flip) ns_stage_out<16, kSmallThreads>(o + run.first, stage, 2 * run.count);
+            else ns_stage_out<4, 32>(o + run.first, stage + run.at, 2 * run.count);
         });
     }
     // an MMA whose wait ran out may still be at work (bounded): it ends before its memory is given up
@@ -1507,24 +1479,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 }
 
 // ---- launches --------------------------------------------------------------------------------------
-// CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  Up to 64 rows
-// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 636 us
-// here, 1014 there; 64 x 2000, 300: 383 and 759); so do one or two CTAs, and four whose columns are filled
-// (100 x 1000, 200: 260 and 356; 128 x 1024, 256: 346 and 400).  Of more CTAs the kernel runs about 48 us a round
-// of the GPU however few the matrices are, and the large kernel is even with it beyond 512 CTAs if filled, and at
-// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 150, 249, 443 us here and 217, 267, 430 there;
-// 128 x 4096, 32 and 64: 263, 530 and 329, 504; 70 x 600, 128: 161 and 149).
-static int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
-    *mp = 128;
-    while (*mp / 2 >= m && *mp > 16 && (128 / *mp) * kSmallCols < n) *mp /= 2;
-    const int cols = 128 / *mp * kSmallCols;
-    if (m > 128 || n > 16 * cols) return 0;
-    int S = 1;
-    while (S * cols < n) S *= 2;
-    const bool filled = 4 * n > 3 * S * cols;
-    return *mp < 128 || S <= 2 || (S == 4 && filled) || N * S <= (filled ? 512 : 304) ? S : 0;
-}
-
 static int ns_log2(int v) { return v < 2 ? 0 : 1 + ns_log2(v / 2); }
 
 struct NsLayout {
