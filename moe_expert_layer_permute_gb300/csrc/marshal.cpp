@@ -101,12 +101,14 @@ PyObject* orthogonalise(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
     }
     const long steps = PyLong_AsLong(args[4]);
+    if (PyErr_Occurred()) return nullptr;
     const double eps = PyFloat_AsDouble(args[5]);
+    if (PyErr_Occurred()) return nullptr;
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
     const Py_ssize_t given = n - 6;
-    if (!PyErr_Occurred() && given != 0 && (steps < 1 || given != 3 * steps || steps > MOE_ORTHOGONALISE_MAX_STEPS))
+    if (given != 0 && (steps < 1 || given != 3 * steps || steps > MOE_ORTHOGONALISE_MAX_STEPS))
         return PyLong_FromLong(steps < 1 || given != 3 * steps ? MOE_ERR_SHAPE : MOE_ERR_UNSUPPORTED);
-    for (Py_ssize_t i = 0; i < given; ++i) co[i] = (float)PyFloat_AsDouble(args[6 + i]);
+    for (Py_ssize_t i = 0; i < given; ++i) co[i] = (float)PyFloat_AsDouble(args[6 + i]);   // given <= the array's size
     if (PyErr_Occurred() || !read(&a, args, 4, 2, 4, true)) return nullptr;
     int rc;
     Py_BEGIN_ALLOW_THREADS;

@@ -1,0 +1,16 @@
+"""What the binding of the balance loss and the orthogonalisation does with arguments of wrong kinds (no GPU)."""
+import pytest
+import torch
+
+from test_abi_host import bd  # noqa: F401  (the library fixture)
+from test_operators_host import _Holder
+
+
+@pytest.mark.parametrize("kw", [{"steps": 4000, "coeffs": (1.0, 1.0, 1.0), "eps": "x"}, {"steps": 17.5, "coeffs": [(1, 1, 1)] * 400},
+                                {"steps": 2 ** 70, "coeffs": [(1, 1, 1)] * 400}, {"steps": 5, "coeffs": [("x", 1, 1)] * 5},
+                                {"steps": 16, "coeffs": [(1, 1, 1)] * 16, "eps": None}])
+def test_coefficients_beside_arguments_of_other_kinds(bd, kw):  # noqa: F811
+    """More coefficients than any call takes, and steps or eps that are no numbers: an exception, nothing else."""
+    G = torch.zeros(1, 4, 4)
+    with pytest.raises((TypeError, OverflowError)):
+        bd.moe_orthogonalise(G, G, _Holder(bd), stream=0, **kw)
