@@ -112,7 +112,7 @@ PyObject* orthogonalise(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (PyErr_Occurred() || !read(&a, args, 4, 2, 4, true)) return nullptr;
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = moe_orthogonalise(a.t[0], a.t[1], (int32_t)std::min<long>(steps, INT32_MAX), given ? co : nullptr, (float)eps,
+    rc = moe_orthogonalise(a.t[0], a.t[1], (int32_t)std::clamp<long>(steps, INT32_MIN, INT32_MAX), given ? co : nullptr, (float)eps,
                            a.workspace, a.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);

@@ -14,3 +14,11 @@ def test_coefficients_beside_arguments_of_other_kinds(bd, kw):  # noqa: F811
     G = torch.zeros(1, 4, 4)
     with pytest.raises((TypeError, OverflowError)):
         bd.moe_orthogonalise(G, G, _Holder(bd), stream=0, **kw)
+
+
+@pytest.mark.parametrize("steps,code", [(-2 ** 32 + 5, "SHAPE"), (-2 ** 62, "SHAPE"), (0, "SHAPE"), (2 ** 32 + 5, "UNSUPPORTED")])
+def test_step_counts_beyond_32_bits(bd, steps, code):  # noqa: F811
+    """Refused as what they are, and not taken modulo 2^32."""
+    G, O = torch.zeros(1, 4, 4), torch.zeros(1, 4, 4, dtype=torch.bfloat16)
+    with pytest.raises(bd.MoeError, match=code):
+        bd.moe_orthogonalise(G, O, _Holder(bd), stream=0, steps=steps)
