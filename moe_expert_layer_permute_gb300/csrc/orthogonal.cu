@@ -1212,8 +1212,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     const int b_parts = a.m <= 64 ? 2 : 1;                                // B, and its rounding error
     constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdX = idesc_f16(128, 256, false, true);
     uint32_t phase = 0;
-    // every thread after its product's commit; on a wait that ran out the rest goes through without waiting,
-    // so that the CTAs of a cluster stay in step
+    // Every thread after its product's commit; on a wait that ran out the rest goes through without waiting, so that
+    // the CTAs of a cluster stay in step, and without products: the one whose wait ran out is the only one that can
+    // still be at work, and its commit ends `done`'s phase `open`.
+    int open = -1;
+    auto issues = [&] { return threadIdx.x == 0 && !a.withhold && !*abort_flag; };
+    auto commit = [&] {
+        mma_commit(done);
+        open = (int)phase;
+    };
     auto wait_mma = [&] {
         mbar_wait(done, phase, abort_flag, a.status, a.wait_limit);
         phase ^= 1u;
@@ -1248,14 +1255,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (threadIdx.x == 0 && !a.withhold) {
+        if (issues()) {
             for (int c = 0; c < kx; ++c)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t d = sdesc_sw128(bX + c * 16384 + ks * 32, 16, 1024);
                     mma_bf16(tA, d, d, kIdM, (c | ks) != 0);
                 }
-            mma_commit(done);
+            commit();
         }
         wait_mma();
         if (S == 1 && blocks == 1) {
@@ -1377,12 +1384,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (threadIdx.x == 0 && !a.withhold) {
+        if (issues()) {
             for (int ks = 0; ks < km; ++ks) {
                 const uint64_t d = sdesc_sw128(bA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
                 mma_bf16(tP, d, d, kIdM, ks != 0);
             }
-            mma_commit(done);
+            commit();
         }
         wait_mma();
 #pragma unroll
@@ -1419,12 +1426,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (threadIdx.x == 0 && !a.withhold) {
+        if (issues()) {
             for (int part = 0; part < b_parts; ++part)
                 for (int ks = 0; ks < km; ++ks)
                     mma_bf16(tX, sdesc_sw128(bP + part * kSmallA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
                              sdesc_sw128(bX + ks * 2048, 16384, 1024), kIdX, (part | ks) != 0);
-            mma_commit(done);
+            commit();
         }
         wait_mma();
 #pragma unroll
@@ -1468,7 +1475,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         });
     }
     // an MMA whose wait ran out may still be at work (bounded): it ends before its memory is given up
-    if (*abort_flag && threadIdx.x == 0 && !a.withhold) ns_wait_drain(done, phase ^ 1u);
+    if (*abort_flag && open >= 0) ns_wait_drain(done, (uint32_t)open);
     tc_fence_before();
     __syncthreads();
     if (S > 1) cluster_sync();   // no CTA's shared memory is read or written any more
