@@ -247,9 +247,14 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
  *   X = G / (|G|_F + eps);  per step, with its (a, b, c):  A = X X^T,  X <- a X + (b A + c A A) X
  * (on G^T where R > C, which gives the same), and O [N, R, C] bf16 receives X.  coeffs: host floats,
  * (a, b, c) for each step, or NULL for (3.4445, -4.7750, 2.0315) throughout.  O may be G itself (bf16).
- * The products take fp16 operands with fp32 sums: O is within about 2.5e-3 (2-norm, bf16's own
- * rounding of 1.7e-3 included) of the exact result for the default coefficients and five steps; with up
- * to 8 rows or columns, whose few errors would not average out, they are fp32 throughout.
+ * The products take fp16 operands with fp32 sums.  With the default coefficients and five steps O is within
+ * about 2.5e-3 (2-norm, bf16's own rounding of 1.7e-3 included) of the exact result where the singular
+ * vectors of G are spread over many rows and columns, and up to 128 rows or columns also where a few lines of
+ * some 200 values or more along the longer edge hold all of G (a router's gradient when a batch meets few
+ * experts).  Where fewer values hold a singular vector (a few entries, a small block, a diagonal; past 128
+ * rows and columns a few lines) the errors of the products do not average out: 2 to 5e-3 as a rule, up to about
+ * 1e-2, beside the rounding of O, which for a single value is up to 3.9e-3.  With up to 8 rows or columns the
+ * products are fp32 throughout.
  * A zero matrix (an expert without tokens) gives zeros; one with a NaN, an infinity or a squared norm
  * beyond fp32 gives NaN, the others of the batch unharmed.
  * `workspace`: a zeroed moe_scratch handle of at least moe_orthogonalise_workspace_bytes(N, R, C)

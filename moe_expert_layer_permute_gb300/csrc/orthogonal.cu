@@ -13,8 +13,14 @@
 // fp32.  Small singular values grow about 3.4-fold a step while X's rounding stays relative to its
 // largest ones, so X also keeps its rounding error as a second fp16 (`lo`, times 2^11 again) for the
 // a X term of every step but the last: without it gradients of low rank came out 1 % off, with it
-// 0.1 %.  A matrix of up to 64 rows keeps B's rounding error too, as a second product of APPLY: with few
-// singular values B's error does not average out.  In the large kernel the rest of a X goes through the
+// 0.1 %.  What A's and B's roundings do depends on G: the error of a singular value is their errors' mean over
+// the entries that its vectors weigh, next to nothing where those are many, and the steps amplify it (the
+// slope of the polynomial reaches 1.8).  A matrix of up to 128 rows keeps the rounding errors of A and B, as second
+// products of POLY (A by twice its error, which along a singular vector is what both orders give) and of APPLY: 4 of
+// 128 rows of 1024 values alone came out up to 6.8e-3 off without, 1.2e-3 with them (before the rounding to bf16),
+// dense ones 1.5e-3 and 0.9e-3.  More rows would take 1.7 times the arithmetic (768 x 2048) and go without: 4 of
+// 300 rows come out up to 6.3e-3 off, and a few entries, in any size, up to 1e-2, since X's own rounding in
+// GRAM counts there.  In the large kernel the rest of a X goes through the
 // products, as a on B's diagonal: the epilogue then needs no X (256 x 768 x 2048: 1 % less time), and the
 // error moves between kinds of matrices (before the rounding to bf16, 200 x 600: gaussian 1.80 -> 1.56e-3,
 // rank 25 0.8 -> 1.7e-3).
@@ -145,6 +151,14 @@ __device__ __forceinline__ uint32_t ns_split_pair(float x, float y, uint32_t* lo
     const uint32_t h = ns_pack_half(x, y);
     const float2 f = ns_unpack_half(h);
     *lo = ns_pack_half((x - f.x) * kLoScale, (y - f.y) * kLoScale);
+    return h;
+}
+// a pair of values of A, and twice their rounding errors (see ns_small_kernel)
+__device__ __forceinline__ uint32_t ns_split_a(float x, float y, uint32_t* twice) {
+    const uint32_t h = ns_pack_half(x, y);
+    float v[2] = {2.f * x, 2.f * y};
+    fma_f16x2(v, h, 0xc000u);   // -2
+    *twice = ns_pack_half(v[0], v[1]);
     return h;
 }
 // eight values of X, and their rounding errors, at a 16-byte boundary
@@ -291,7 +305,7 @@ struct NsArgs {
     int per_cycle, cycles, supers;
     int units;
     int k_gram, k_poly;          // K slices
-    int b_lo;                    // B keeps its rounding error: matrix N + i of the B array, a second product
+    int ab_lo;                   // A and B keep their rounding errors: matrix N + i of their arrays, second products
     int first_lo;                // the first X has a rounding error (else it is exact)
     int out_kind;                // NsOut
     float co[3 * MOE_ORTHOGONALISE_MAX_STEPS];
@@ -444,7 +458,7 @@ __device__ __forceinline__ void ns_box_col(uint32_t box, int r, int half, const 
 struct NsPart {
     int row0, n0, chunks;      // the CTA's first row, the tile's first column
     int out_kind;              // NsOut in the last step's APPLY, else 0
-    bool load;                 // POLY: the chunk of A comes in; APPLY: X's rounding error
+    bool load;                 // POLY: the chunk of A comes in, and of its rounding error; APPLY: X's rounding error
     bool twin, keep_lo;        // out go the transpose as well, or a rounding error
 };
 template <int TILE>
@@ -456,7 +470,7 @@ __device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArg
     p.out_kind = u.mode == NS_APPLY && u.step + 1 == a.steps ? a.out_kind : 0;
     // the last step reads X without its rounding error, so the step before keeps none
     p.load = u.mode == NS_POLY || (u.mode == NS_APPLY && u.step + 1 < a.steps && (u.step > 0 || a.first_lo));
-    p.keep_lo = u.mode == NS_POLY ? a.b_lo : u.mode == NS_APPLY && u.step + 2 < a.steps;
+    p.keep_lo = u.mode == NS_APPLY ? u.step + 2 < a.steps : a.ab_lo;
     p.twin = u.mode != NS_APPLY && u.i != u.j;
     return p;
 }
@@ -466,7 +480,7 @@ __device__ __forceinline__ NsPart ns_part(const NsUnit& u, int rank, const NsArg
 // by the rest of the norm.  The scales of X, A, B and O are in there.
 struct NsFactors {
     float d, is, diag;
-    uint32_t hi, lo;
+    uint32_t hi, lo, half;
 };
 __device__ __forceinline__ NsFactors ns_factors(const NsUnit& u, const NsPart& p, const NsArgs& a) {
     NsFactors f;
@@ -478,6 +492,7 @@ __device__ __forceinline__ NsFactors ns_factors(const NsUnit& u, const NsPart& p
     const float x = u.mode == NS_POLY ? a.co[3 * u.step + 1] : a.co[3 * u.step] / kLoScale;
     f.hi = ns_pack_half(x, 0.f);
     f.lo = ns_pack_half(x - ns_unpack_half(f.hi).x, 0.f);
+    f.half = ns_pack_half(0.5f * x, 0.f);   // (A's rounding error is held twice)
     return f;
 }
 
@@ -589,7 +604,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const int wrap = t.mode == NS_GRAM ? a.k_gram : a.k_poly;
                 const bool same = ns_same<PAIR>(t, width);
                 const uint32_t bytes = (PAIR ? 2 : 1) * (same ? kOperand : 2 * kOperand);
-                const int k_blocks = apply && a.b_lo ? 2 * wrap : wrap;
+                const int k_blocks = t.mode != NS_GRAM && a.ab_lo ? 2 * wrap : wrap;   // A A, A by its error; B X, its error by X
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, a.status, a.wait_limit)) {
                         ok = false;
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                     uint8_t* dB = sB + stage * kOperand;
                     const bool second = kb >= wrap;
                     const int k0 = (second ? kb - wrap : kb) * 64;
-                    const int matA = second ? t.mat + a.N : t.mat;
+                    const int matA = second && apply ? t.mat + a.N : t.mat, matB = second && !apply ? t.mat + a.N : t.mat;
                     if constexpr (PAIR) {
                         // both CTAs' copies land on the leader's barrier, which expects both
                         const uint32_t lbar = cluster_addr(full + stage, 0);
@@ -609,7 +624,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                             tma_load_3d_pair(dB, tmB, lbar, n0, k0, t.mat);
                             tma_load_3d_pair(dB + kOperand / 2, tmB, lbar, n0 + 64, k0, t.mat);
                         } else if (!same) {
-                            tma_load_3d_pair(dB, tmB, lbar, k0, n0, t.mat);
+                            tma_load_3d_pair(dB, tmB, lbar, k0, n0, matB);
                         }
                     } else {
                         mbar_arrive_expect_tx(full + stage, bytes);
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                             tma_load_3d(dB, tmB, full + stage, n0, k0, t.mat);
                             tma_load_3d(dB + kOperand / 2, tmB, full + stage, n0 + 64, k0, t.mat);
                         } else if (!same) {
-                            tma_load_3d(dB, tmB, full + stage, k0, n0, t.mat);
+                            tma_load_3d(dB, tmB, full + stage, k0, n0, matB);
                         }
                     }
                     ++issued;
@@ -647,7 +662,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 const NsUnit t = ns_unit(unit, a);
                 if (!t.valid) continue;
                 const bool apply = t.mode == NS_APPLY;
-                const int k_blocks = t.mode == NS_GRAM ? a.k_gram : apply && a.b_lo ? 2 * a.k_poly : a.k_poly;
+                const int k_blocks = t.mode == NS_GRAM ? a.k_gram : a.ab_lo ? 2 * a.k_poly : a.k_poly;
                 if (!(PAIR ? mbar_wait_cluster(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit)
                            : mbar_wait(tempty + acc, acc_phase ^ 1u, abort_flag, a.status, a.wait_limit))) {
                     ok = false;
@@ -720,7 +735,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 if (p.chunks == 0) continue;
                 if (p.load && !inputs(q)) break;
                 const CUtensorMap* tm = t.mode == NS_POLY ? &maps.a : &maps.lo;
-                const int second = t.mode == NS_POLY ? 0 : kNsBox;   // the rounding error's place in the slot
+                const bool poly = t.mode == NS_POLY, both = poly && a.ab_lo;   // A, and its rounding error (twice)
+                const int second = poly ? 0 : kNsBox;   // the rounding error's place in the slot
                 for (int c = 0; c < p.chunks; ++c, ++k) {
                     const int slot = k % kNsSlots;
                     if (!mbar_wait(box_free + slot, (k / kNsSlots & 1) ^ 1u, abort_flag, a.status, a.wait_limit)) {
@@ -731,8 +747,10 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         mbar_arrive(box_full + slot);
                         continue;
                     }
-                    mbar_arrive_expect_tx(box_full + slot, kNsBox);
-                    tma_load_3d(sBox + slot * 2 * kNsBox + second, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
+                    uint8_t* box = sBox + slot * 2 * kNsBox;
+                    mbar_arrive_expect_tx(box_full + slot, both ? 2 * kNsBox : kNsBox);
+                    tma_load_3d(box + second, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat);
+                    if (both) tma_load_3d(box + kNsBox, tm, box_full + slot, p.n0 + 64 * c, p.row0, t.mat + a.N);
                 }
             }
             // every load has landed (bounded) before the CTA exits
@@ -762,8 +780,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         tma_store_3d(tm_t, box + kNsBox, p.row0, col, t.mat);
                         if (p.row0 + 64 < a.m) tma_store_3d(tm_t, box + kNsBox + 8192, p.row0 + 64, col, t.mat);
                     } else if (p.keep_lo) {
-                        if (t.mode == NS_POLY) tma_store_3d(&maps.b, box + kNsBox, col, p.row0, t.mat + a.N);
-                        else tma_store_3d(&maps.lo, box + kNsBox, col, p.row0, t.mat);
+                        if (t.mode == NS_APPLY) tma_store_3d(&maps.lo, box + kNsBox, col, p.row0, t.mat);
+                        else tma_store_3d(tm, box + kNsBox, col, p.row0, t.mat + a.N);
                     }
                     bulk_commit();
                     if (c > 0) {   // the slot before this one has been read
@@ -817,7 +835,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(box_full + slot, k / kNsSlots & 1, abort_flag, a.status, a.wait_limit));
                 if (!ok) break;
-                if (t.mode == NS_GRAM) {
+                if (t.mode == NS_GRAM && !p.keep_lo) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j] * f.d, v[2 * j + 1] * f.d);
                 } else {
@@ -829,6 +847,11 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         for (int j = 0; j < 16; ++j) {
                             fma_f16x2(v + 2 * j, out[j], f.hi);
                             fma_f16x2(v + 2 * j, out[j], f.lo);
+                        }
+                        if (p.keep_lo) {
+                            ns_box_read(low, sbox + kNsBox, br, half);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) fma_f16x2(v + 2 * j, low[j], f.half);
                         }
                         if (p.row0 + 32 * quarter == col) {
 #pragma unroll
@@ -852,7 +875,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                         for (int j = 0; j < 16; ++j) out[j] = ns_pack_half(v[2 * j], v[2 * j + 1]);
                         if (p.keep_lo) {
                             const uint32_t minus = ns_pack_half(-1.f, 0.f);
-                            const float scale = t.mode == NS_POLY ? 1.f : kLoScale;
+                            const float scale = t.mode == NS_GRAM ? 2.f : t.mode == NS_POLY ? 1.f : kLoScale;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 fma_f16x2(v + 2 * j, out[j], minus);
@@ -1047,9 +1070,13 @@ __global__ void __launch_bounds__(kTinyThreads) ns_tiny_kernel(const T* G, __nv_
 // Where m leaves room, up to eight blocks of 256 columns lie one below the other in the CTA's 128 rows: A is
 // the sum of the diagonal blocks of their product, and with A and B laid out block-diagonally the rest goes
 // as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 76 here).
+// A's rounding error lies below A in each chunk of columns, so that A A and A by its error are one MMA of 256 columns
+// (of 128 each, with operands that differ, an MMA takes 112 cycles, and 16 of them 300 more than these eight).  The
+// errors of A and B cost 16 x 128 x 256 24.6 -> 31.8 us and 1 x 128 x 2048 47.9 -> 55.9.
 constexpr int kSmallX = 4 * 16384;   // X: four chunks of 128 rows x 64 columns (128-byte swizzle)
-constexpr int kSmallA = 2 * 16384;   // A likewise; the partial A in fp32, later B and its rounding error
-constexpr int kSmallBytes = 1024 + kSmallX + 3 * kSmallA + 256;
+// A, and later B, with its rounding error: for each 64 columns the 128 rows of A and then those of its error
+constexpr int kSmallA = 4 * 16384, kSmallLo = 16384, kSmallChunk = 2 * 16384;
+constexpr int kSmallBytes = 1024 + kSmallX + 2 * kSmallA + 256;   // X, A, and the partial A in fp32, later B
 
 struct NsSmall {
     int R, C, m, n, mp, log_mp, log_ctas, steps, flip;   // mp: rows of a block, 128 / mp blocks one below the other
@@ -1112,11 +1139,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     uint8_t* sX = smem;
     uint8_t* sA = sX + kSmallX;
     uint8_t* sP = sA + kSmallA;                 // fp32 [128][128], then B (fp16) and its rounding error
-    uint64_t* done = reinterpret_cast<uint64_t*>(sP + 2 * kSmallA);
+    uint64_t* done = reinterpret_cast<uint64_t*>(sP + kSmallA);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
     float* warp_sums = reinterpret_cast<float*>(tslot + 2);   // [8]
     float* my_sum = warp_sums + 8;
+    volatile int* open = reinterpret_cast<volatile int*>(warp_sums + 9);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = (int)gridDim.x, rank = S > 1 ? (int)cluster_ctarank() : 0, mat = blockIdx.y;
     const int quarter = warp & 3, half = warp >> 2;
@@ -1127,6 +1155,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     if (threadIdx.x == 0) {
         mbar_init(done, 1);
         *abort_flag = 0;
+        *open = -1;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tslot, 512);
@@ -1206,20 +1235,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
 
     const uint32_t bX = smem_u32(sX), bA = smem_u32(sA), bP = smem_u32(sP);
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tA = tmem, tP = tmem + 128, tX = tmem + 256;
+    const uint32_t tA = tmem, tX = tmem + 256;   // (A A too goes to tX)
     const int kx = min(4, max(0, (a.n - rank * blocks * kSmallCols + 63) / 64));   // chunks of X that hold columns
     const int km = blocks > 1 ? 8 : (a.m + 15) / 16;                      // MMA steps along the rows
-    const int b_parts = a.m <= 64 ? 2 : 1;                                // B, and its rounding error
-    constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdX = idesc_f16(128, 256, false, true);
+    constexpr uint32_t kIdM = idesc_f16(128, 128, false, false), kIdP = idesc_f16(128, 256, false, false), kIdX = idesc_f16(128, 256, false, true);
     uint32_t phase = 0;
     // Every thread after its product's commit; on a wait that ran out the rest goes through without waiting, so that
     // the CTAs of a cluster stay in step, and without products: the one whose wait ran out is the only one that can
     // still be at work, and its commit ends `done`'s phase `open`.
-    int open = -1;
     auto issues = [&] { return threadIdx.x == 0 && !a.withhold && !*abort_flag; };
     auto commit = [&] {
         mma_commit(done);
-        open = (int)phase;
+        *open = (int)phase;
     };
     auto wait_mma = [&] {
         mbar_wait(done, phase, abort_flag, a.status, a.wait_limit);
@@ -1249,7 +1276,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
     };
     put_x(false);
     for (int s = 0; s < a.steps; ++s) {
-        const float ca = a.co[3 * s], cb = a.co[3 * s + 1], cc = a.co[3 * s + 2];
+        const float ca = a.co[3 * s], cb = a.co[3 * s + 1], fp = a.co[3 * s + 2] / kABScale;
+        const uint32_t b_hi = ns_pack_half(cb, 0.f), b_lo = ns_pack_half(cb - ns_unpack_half(b_hi).x, 0.f),
+                       b_half = ns_pack_half(0.5f * cb, 0.f);   // b to 22 bits, and half of it
         const float fa = kABScale / (kXScale * kXScale) * is * is, fx = is * ca, fv = is * (1.f / kABScale);
         fence_proxy_async_cta();
         tc_fence_before();
@@ -1271,12 +1300,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
                 float v[32];
                 tmem_ld32(tA + lane_addr + 64 * half + 32 * c, v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st_shared_v4(bA + half * 16384 + ns_sw(row, 4 * c + q),
-                                 make_uint4(ns_pack_half(v[8 * q] * fa, v[8 * q + 1] * fa),
-                                            ns_pack_half(v[8 * q + 2] * fa, v[8 * q + 3] * fa),
-                                            ns_pack_half(v[8 * q + 4] * fa, v[8 * q + 5] * fa),
-                                            ns_pack_half(v[8 * q + 6] * fa, v[8 * q + 7] * fa)));
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t to = bA + half * kSmallChunk + ns_sw(row, 4 * c + q);
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = ns_split_a(v[8 * q + 2 * e] * fa, v[8 * q + 2 * e + 1] * fa, l + e);
+                    st_shared_v4(to, make_uint4(h[0], h[1], h[2], h[3]));
+                    st_shared_v4(to + kSmallLo, make_uint4(l[0], l[1], l[2], l[3]));
+                }
             }
         } else {
             // the row's columns of its diagonal block in fp32: rows of 512 bytes, their 16-byte pieces rotated
@@ -1315,22 +1346,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             const int r0 = (rank << (a.log_mp - a.log_ctas)) + ((int)threadIdx.x >> log_pieces);
             const int pieces = 1 << (a.log_mp - a.log_ctas + log_pieces);
             const int mine = (int)threadIdx.x < pieces ? max(1, pieces / kSmallThreads) : 0;
+            const uint32_t lanes = pieces < 32 ? (1u << pieces) - 1 : 0xffffffffu;   // those with pieces, in the first warp
             auto exchange = [&](auto alone) {   // (with one CTA: plain shared memory)
                 constexpr bool kAlone = decltype(alone)::value;
                 auto give = [&](int j, const float4& sum) {
                     if (j >= mine) return;
-                    const uint32_t h0 = ns_pack_half(sum.x * fa, sum.y * fa), h1 = ns_pack_half(sum.z * fa, sum.w * fa);
+                    // neighbouring lanes trade: the even one stores eight values of A, the odd one their rounding errors
+                    uint32_t l0, l1;
+                    const uint32_t h0 = ns_split_a(sum.x * fa, sum.y * fa, &l0), h1 = ns_split_a(sum.z * fa, sum.w * fa, &l1);
+                    const bool odd = at & 1;
+                    const uint32_t t0 = __shfl_xor_sync(lanes, odd ? h0 : l0, 1), t1 = __shfl_xor_sync(lanes, odd ? h1 : l1, 1);
+                    const uint4 out = odd ? make_uint4(t0, t1, l0, l1) : make_uint4(h0, h1, t0, t1);
                     const int r = r0 + j * down;
                     for (int q = 0; q < blocks; ++q) {
                         const int col = (q << a.log_mp) + 4 * at;
-                        const uint32_t to = (uint32_t)((col >> 6) * 16384) + ns_sw((q << a.log_mp) + r, (col & 63) >> 3) + (at & 1) * 8;
+                        const uint32_t to = (uint32_t)((col >> 6) * kSmallChunk) + ns_sw((q << a.log_mp) + r, (col & 63) >> 3) + (odd ? kSmallLo : 0);
                         if constexpr (kAlone) {
-                            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(bA + to), "r"(h0), "r"(h1) : "memory");
+                            st_shared_v4(bA + to, out);
                         } else {
 #pragma unroll 1
                             for (int b = 0; b < S; b += 2) {
-                                st_cluster_v2(cluster_addr(sA, b) + to, h0, h1);
-                                st_cluster_v2(cluster_addr(sA, b + 1) + to, h0, h1);
+                                st_cluster_v4(cluster_addr(sA, b) + to, out);
+                                st_cluster_v4(cluster_addr(sA, b + 1) + to, out);
                             }
                         }
                     }
@@ -1385,41 +1422,40 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         __syncthreads();
         tc_fence_after();
         if (issues()) {
-            for (int ks = 0; ks < km; ++ks) {
-                const uint64_t d = sdesc_sw128(bA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
-                mma_bf16(tP, d, d, kIdM, ks != 0);
-            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)   // A A, and A by twice its rounding error in the 128 columns that follow
+                if (ks < km) {
+                    const uint64_t d = sdesc_sw128(bA + (ks >> 2) * kSmallChunk + (ks & 3) * 32, 16, 1024);
+                    mma_bf16(tX, d, d, kIdP, ks != 0);
+                }
             commit();
         }
         wait_mma();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            float v[32];
-            tmem_ld32(tP + lane_addr + 64 * half + 32 * c, v);
+            float v[32], w[32];
+            tmem_ld32(tX + lane_addr + 64 * half + 32 * c, v);
+            tmem_ld32(tX + lane_addr + 128 + 64 * half + 32 * c, w);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint32_t to = half * 16384 + ns_sw(row, 4 * c + q);
-                const uint4 h = ld_shared_v4(bA + to);
-                const uint32_t w[4] = {h.x, h.y, h.z, h.w};
-                float b[8];
-                uint32_t hi[4];
+                const uint32_t to = half * kSmallChunk + ns_sw(row, 4 * c + q);
+                const uint4 h = ld_shared_v4(bA + to), r = ld_shared_v4(bA + kSmallLo + to);
+                const uint32_t wh[4] = {h.x, h.y, h.z, h.w}, wl[4] = {r.x, r.y, r.z, r.w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 A = ns_unpack_half(w[e]);
-                    b[2 * e] = cb * A.x + cc / kABScale * v[8 * q + 2 * e];
-                    b[2 * e + 1] = cb * A.y + cc / kABScale * v[8 * q + 2 * e + 1];
-                    hi[e] = ns_pack_half(b[2 * e], b[2 * e + 1]);
+                    float* b = v + 8 * q + 2 * e;
+                    b[0] = fp * (b[0] + w[8 * q + 2 * e]);
+                    b[1] = fp * (b[1] + w[8 * q + 2 * e + 1]);
+                    fma_f16x2(b, wh[e], b_hi);
+                    fma_f16x2(b, wh[e], b_lo);
+                    fma_f16x2(b, wl[e], b_half);
+                    hi[e] = ns_pack_half(b[0], b[1]);
+                    fma_f16x2(b, hi[e], 0xbc00u);   // -1
+                    lo[e] = ns_pack_half(b[0], b[1]);
                 }
                 st_shared_v4(bP + to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                if (b_parts == 2) {
-                    uint32_t lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 r = ns_unpack_half(hi[e]);
-                        lo[e] = ns_pack_half(b[2 * e] - r.x, b[2 * e + 1] - r.y);
-                    }
-                    st_shared_v4(bP + kSmallA + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                }
+                st_shared_v4(bP + kSmallLo + to, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
         }
         fence_proxy_async_cta();
@@ -1427,10 +1463,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         __syncthreads();
         tc_fence_after();
         if (issues()) {
-            for (int part = 0; part < b_parts; ++part)
-                for (int ks = 0; ks < km; ++ks)
-                    mma_bf16(tX, sdesc_sw128(bP + part * kSmallA + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
-                             sdesc_sw128(bX + ks * 2048, 16384, 1024), kIdX, (part | ks) != 0);
+#pragma unroll
+            for (int ks = 0; ks < 16; ++ks)   // B, then its rounding error, by X
+                if ((ks & 7) < km)
+                    mma_bf16(tX, sdesc_sw128(bP + ((ks & 7) >> 2) * kSmallChunk + (ks >> 3) * kSmallLo + (ks & 3) * 32, 16, 1024),
+                             sdesc_sw128(bX + (ks & 7) * 2048, 16384, 1024), kIdX, ks != 0);
             commit();
         }
         wait_mma();
@@ -1475,7 +1512,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
         });
     }
     // an MMA whose wait ran out may still be at work (bounded): it ends before its memory is given up
-    if (*abort_flag && open >= 0) ns_wait_drain(done, (uint32_t)open);
+    if (*abort_flag && threadIdx.x == 0 && *open >= 0) ns_wait_drain(done, (uint32_t)*open);
     tc_fence_before();
     __syncthreads();
     if (S > 1) cluster_sync();   // no CTA's shared memory is read or written any more
@@ -1490,7 +1527,7 @@ static int ns_log2(int v) { return v < 2 ? 0 : 1 + ns_log2(v / 2); }
 
 struct NsLayout {
     int64_t N, m, n, lda, ldx, parts;
-    bool b_lo;
+    bool ab_lo;
     size_t partial, inv_s, done, A, B, x0, x1, lo, total;
 };
 
@@ -1518,9 +1555,9 @@ static bool ns_layout(int64_t N, int64_t R, int64_t C, NsLayout* L) {
     L->partial = take((size_t)N * L->parts * 4);
     L->inv_s = take((size_t)N * 4);
     L->done = take((size_t)N * (1 + 2 * ((L->m + 127) / 128)) * 4);   // counters (tile rows of 128, or fewer of 256)
-    L->A = take((size_t)N * L->m * L->lda * 2);
-    L->b_lo = L->m <= 64;
-    L->B = take((size_t)N * (L->b_lo ? 2 : 1) * L->m * L->lda * 2);
+    L->ab_lo = L->m <= 128;
+    L->A = take((size_t)N * (L->ab_lo ? 2 : 1) * L->m * L->lda * 2);
+    L->B = take((size_t)N * (L->ab_lo ? 2 : 1) * L->m * L->lda * 2);
     L->x0 = take((size_t)N * L->m * L->ldx * 2);
     L->x1 = take((size_t)N * L->m * L->ldx * 2);
     L->lo = take((size_t)N * L->m * L->ldx * 2);
@@ -1710,8 +1747,9 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     auto map = [&](CUtensorMap* out, size_t at, int64_t cols, int64_t ld, int64_t batch, int rows) {
         return tmap_batched(out, w + at, false, cols, m, ld, batch, rows);
     };
-    bool ok = map(&t.a, L.A, m, L.lda, N, 128) && map(&t.a_t, L.A, m, L.lda, N, 64) &&
-              map(&t.b, L.B, m, L.lda, L.b_lo ? 2 * N : N, 128) && map(&t.b_t, L.B, m, L.lda, N, 64) &&
+    const int64_t nab = L.ab_lo ? 2 * N : N;
+    bool ok = map(&t.a, L.A, m, L.lda, nab, 128) && map(&t.a_t, L.A, m, L.lda, N, 64) &&
+              map(&t.b, L.B, m, L.lda, nab, 128) && map(&t.b_t, L.B, m, L.lda, N, 64) &&
               map(&t.x[0], L.x0, n, L.ldx, N, 128) && map(&t.x[1], L.x1, n, L.ldx, N, 128) &&
               map(&t.x_t[0], L.x0, n, L.ldx, N, 64) && map(&t.x_t[1], L.x1, n, L.ldx, N, 64) &&
               map(&t.lo, L.lo, n, L.ldx, N, 128);
@@ -1742,7 +1780,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     if ((int64_t)a.cycles * a.per_cycle >= INT32_MAX) return cudaErrorInvalidValue;
     a.units = a.cycles * a.per_cycle;
     a.k_gram = (int)((n + 63) / 64); a.k_poly = (int)((m + 63) / 64);
-    a.b_lo = L.b_lo;
+    a.ab_lo = L.ab_lo;
     a.first_lo = g_f32;
     a.out_kind = o_box ? (flip ? NS_O_BOX_FLIP : NS_O_BOX) : (flip ? NS_O_PLAIN_FLIP : NS_O_PLAIN);
     std::copy(coeffs, coeffs + 3 * steps, a.co);

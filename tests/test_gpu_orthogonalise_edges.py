@@ -36,3 +36,71 @@ def test_a_wait_limit_below_a_products_time(cuda_lib, N, R, C):
         bd.moe_orthogonalise(G, O, ws)
         assert bd.moe_read_device_status(ws) == 0
         assert max(errors(O, ref)) < BAR
+
+
+# The accuracy that the header states.  The kernels' roundings carried through the formulas on the host give O before
+# its own rounding within 2e-3 where singular vectors are spread over many entries and, up to 128 rows, where lines
+# along the longer edge hold them: 2.6e-3 with bf16's 1.7e-3, and 3e-3 leaves room for rows whose own rounding is
+# worse than that.  Where few entries (past 128 rows, few lines) hold a singular vector they give up to 1e-2, and bf16
+# rounds a single value by up to 3.9e-3.
+SPREAD, HELD_BY_FEW = 3e-3, 1.5e-2
+
+
+def lines(N, m, n, k, dtype, seed):
+    """k non-zero lines of n values among m: the gradient of a router that met k experts."""
+    g = torch.Generator().manual_seed(seed)
+    G = torch.zeros(N, m, n)
+    for i in range(N):
+        G[i, torch.randperm(m, generator=g)[:k]] = torch.randn(k, n, generator=g)
+    return (1e-3 * G).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("m,n", [(128, 1024), (40, 200), (16, 200), (100, 300)])
+@pytest.mark.parametrize("k", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tall", [False, True])
+def test_few_lines_up_to_128_rows(cuda_lib, m, n, k, dtype, tall):
+    G = lines(24, m, n, k, dtype, m + n + k)
+    if tall:
+        G = G.transpose(1, 2).contiguous()
+    assert max(errors(run(cuda_lib, G), exact(G))) < SPREAD
+
+
+@pytest.mark.parametrize("N,m,n", [(40, 100, 1100), (2, 100, 5000), (2, 50, 9000), (2, 128, 4500)])
+@pytest.mark.parametrize("k", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("tall", [False, True])
+def test_few_lines_of_matrices_that_no_cluster_takes(cuda_lib, N, m, n, k, tall):
+    """Long or many, so that the kernel of tiles has them."""
+    G = lines(N, m, n, k, torch.float32, m + n + k)
+    if tall:
+        G = G.transpose(1, 2).contiguous()
+    assert max(errors(run(cuda_lib, G), exact(G))) < SPREAD
+
+
+@pytest.mark.parametrize("N,R,C", [(4, 40, 200), (4, 100, 300), (4, 300, 100), (2, 256, 400), (2, 600, 200), (90, 300, 520)])
+@pytest.mark.parametrize("rank", [0, 8, 64])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_spread_matrices(cuda_lib, N, R, C, rank, dtype):
+    g = torch.Generator().manual_seed(R + C + rank)
+    G = torch.randn(N, R, C, generator=g) if rank == 0 else torch.randn(N, R, rank, generator=g) @ torch.randn(N, rank, C, generator=g)
+    G = G.to(dtype).cuda()
+    assert max(errors(run(cuda_lib, G), exact(G))) < SPREAD
+
+
+@pytest.mark.parametrize("R,C", [(16, 20), (100, 120), (128, 300), (150, 170), (256, 400), (400, 256), (300, 900)])
+@pytest.mark.parametrize("kind", ["entry", "block 2", "block 3", "block 4", "diagonal", "lines 4", "columns 2"])
+def test_matrices_held_by_few_values(cuda_lib, R, C, kind):
+    g = torch.Generator().manual_seed(R + C)
+    N, what, k = 16, kind.split()[0], int((kind + " 1").split()[1])
+    G = torch.zeros(N, R, C)
+    if what == "diagonal":
+        i = torch.arange(min(R, C))
+        G[:, i, i] = torch.randn(N, len(i), generator=g)
+    elif what == "lines":
+        G = lines(N, R, C, k, torch.float32, R).cpu()
+    elif what == "columns":
+        G = lines(N, C, R, k, torch.float32, C).cpu().transpose(1, 2).contiguous()
+    else:
+        G[:, 3:3 + k, 5:5 + k] = torch.randn(N, k, k, generator=g)
+    G = G.cuda()
+    assert max(errors(run(cuda_lib, G), exact(G))) < HELD_BY_FEW
