@@ -255,6 +255,12 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
  * rows and columns a few lines) the errors of the products do not average out: 2 to 5e-3 as a rule, up to about
  * 1e-2, beside the rounding of O, which for a single value is up to 3.9e-3.  With up to 8 rows or columns the
  * products are fp32 throughout.
+ * What the numbers have room for: (1) an entry of X carries an absolute error of up to about 1e-9 too, so that
+ * matrices whose norm is a millionth of eps or less lose digits and end as zeros (not with up to 8 rows or
+ * columns).  (2) |G|_F^2 is an fp32 sum: entries under 1e-18 count in it with few digits or not at all, which shows
+ * where eps is as small.  (3) With coefficients of one's own, X's singular values s have to stay under 7.9 after
+ * every step but the last, and |b s^2 + c s^4| and |a + b s^2 + c s^4| under 63: A and B are held in fp16, times
+ * 1024, and beyond it the result can be infinite or NaN (not with up to 8 rows or columns).
  * A zero matrix (an expert without tokens) gives zeros; one with a NaN, an infinity or a squared norm
  * beyond fp32 gives NaN, the others of the batch unharmed.
  * `workspace`: a zeroed moe_scratch handle of at least moe_orthogonalise_workspace_bytes(N, R, C)

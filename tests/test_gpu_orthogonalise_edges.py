@@ -104,3 +104,40 @@ def test_matrices_held_by_few_values(cuda_lib, R, C, kind):
         G[:, 3:3 + k, 5:5 + k] = torch.randn(N, k, k, generator=g)
     G = G.cuda()
     assert max(errors(run(cuda_lib, G), exact(G))) < HELD_BY_FEW
+
+
+@pytest.mark.parametrize("N,R,C", [(2, 100, 300), (2, 300, 90), (2, 300, 520), (2, 6, 700)])
+@pytest.mark.parametrize("ratio", [1e-5, 1e-7, 1e-9, 1e-11, 1e-13])
+@pytest.mark.parametrize("eps", [1e-7, 1.0])
+def test_norms_far_below_eps(cuda_lib, N, R, C, ratio, eps):
+    """The absolute error that the header states, 1e-9 an entry, beside the relative one."""
+    G = gauss(N, R, C, torch.float32, 31, ratio * eps / (R * C) ** 0.5)
+    ref = exact(G, eps=eps)
+    O = run(cuda_lib, G, eps=eps).double().cpu()
+    for o, r in zip(O, ref):
+        assert float((o - r).norm()) <= BAR * float(r.norm()) + 1e-9 * (R * C) ** 0.5
+
+
+@pytest.mark.parametrize("N,R,C", [(2, 100, 300), (2, 300, 520), (2, 6, 700)])
+def test_entries_whose_squares_leave_fp32(cuda_lib, N, R, C):
+    G = gauss(N, R, C, torch.float32, 32, 1e-17)
+    assert max(errors(run(cuda_lib, G, eps=1e-20), exact(G, eps=1e-20))) < BAR
+    if min(R, C) > 8:
+        assert not run(cuda_lib, gauss(N, R, C, torch.float32, 32, 1e-26), eps=1e-20).any()
+
+
+@pytest.mark.parametrize("N,R,C", [(2, 100, 300), (2, 300, 200), (2, 6, 40)])
+def test_growth_between_steps(cuda_lib, N, R, C):
+    """Singular values up to 7.9 between steps, and 63 for the polynomial of one; with up to 8 rows beyond that too."""
+    g = torch.Generator().manual_seed(33)
+    G = (torch.randn(N, R, 1, generator=g) @ torch.randn(N, 1, C, generator=g)).cuda()       # one singular value: 1
+    for co in ([(7.5, 0, 0)] * 2, [(1, 6, 0), (0.5, 1.2, 0)], [(-7, 0, 0), (16, -1.5, 0.02)]):
+        assert max(errors(run(cuda_lib, G, steps=2, coeffs=co), exact(G, 2, co))) < BAR
+    far = [(9, 0, 0)] * 2                        # 81 in A's one entry where one entry is all there is
+    G[:, 1:] = 0
+    G[:, :, 1:] = 0
+    O = run(cuda_lib, G, steps=2, coeffs=far)
+    if min(R, C) <= 8:
+        assert max(errors(O, exact(G, 2, far))) < BAR
+    else:
+        assert not O.isfinite().all()
