@@ -228,7 +228,8 @@ int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const m
  *   topk_idx: distinct experts per token; counts and tokens as moe_balance_fwd wrote them.
  * Rows of tokens that do not count are not read: they may hold anything.  A counted row that is -inf
  * throughout has p = 0 and adds nothing to the losses; NaN or +inf in a counted row give NaN.  Sums
- * are taken in an order that depends on the sizes alone, so results repeat bit for bit.  Outputs may
+ * are taken in an order that depends on the sizes and offsets alone, so results repeat bit for bit; sums of p over
+ * several hundred tokens carry an absolute error too, in loss[s,0] up to 1e-16 E T / n.  Outputs may
  * not overlap inputs.  Limits as moe_router_fwd's, and 1 <= B <= 65535 (MOE_ERR_UNSUPPORTED);
  * T = 0 gives zeros. */
 size_t moe_balance_workspace_bytes(int64_t T, int64_t E, int64_t B);   /* 0: outside the limits */

@@ -133,8 +133,9 @@ __device__ __forceinline__ BalRow bal_softmax(float* x) {
 
 // Forward.  Block c takes tokens [c chunk, (c+1) chunk), and of each segment that it meets sums p, the
 // picks, lse^2 and the tokens: a piece.  A segment inside one block is finished there.  The pieces of a
-// longer one are joined in `workspace`, where the sums of p are held as 64-bit integers, times 2^32 (p sums
-// to at most T < 2^26), and the counts as integers: integers add up to the same in any order, and the block
+// longer one are joined in `workspace`, where the sums of p are held as 64-bit integers, times the power of two
+// that leaves their sum, at most T, below 2^62 (one that did for every T, 2^32, took the digits of picks with p
+// under 1e-9), and the counts as integers: integers add up to the same in any order, and the block
 // that comes last finishes the segment and leaves zeros for the next call.  The sums of lse^2, which have
 // no such bound, are kept apart, one for each piece (block c's piece of segment s at c + s, which no other
 // has: going through the tokens each block's end and each segment's end advances it by one), and added in
@@ -145,8 +146,9 @@ struct BalArgs {
     const uint8_t* mask;
     const int* off;
     int T, E, k, B, chunk;
-    unsigned long long* P;   // [B, E] sum of p, 2^32 to one; all five are zero between calls, so that calls of
-                             // other sizes may share the workspace
+    float fix, unfix;        // P's one, a power of two, and its inverse
+    unsigned long long* P;   // [B, E] sum of p; all five are zero between calls, so that calls of other sizes may share
+                             // the workspace
     int* C;                  // [B, E] picks
     int* N;                  // [B] counted tokens
     int* ticket;             // [B] pieces joined
@@ -155,7 +157,6 @@ struct BalArgs {
     int* tokens;
     float* loss;
 };
-constexpr float kBalFix = 4294967296.f;   // 2^32
 
 // Two sums over a block, whole on thread 0.
 template <int kWarps>
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
                 a.counts[(long long)s * a.E + e] = hist[e];
                 dot += v * (float)hist[e];
             } else {
-                atomicAdd(P + e, (unsigned long long)__float2ll_rn(v * kBalFix));
+                atomicAdd(P + e, (unsigned long long)__float2ll_rn(v * a.fix));
                 if (hist[e]) atomicAdd(K + e, hist[e]);
             }
         }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(32 * bal_warps<W, V>(), bal_blocks_sm<V>() * 8
                 }
                 for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
                     const int c = atomicExch(K + e, 0);
-                    const float v = (float)((double)(long long)atomicExch(P + e, 0ull) * (1.0 / kBalFix));
+                    const float v = __ll2float_rn((long long)atomicExch(P + e, 0ull)) * a.unfix;
                     a.counts[(long long)s * a.E + e] = c;
                     dot += v * (float)c;
                 }
@@ -459,7 +460,9 @@ static cudaError_t dispatch_bwd(cudaStream_t st, const BalBwdArgs& a) { MOE_BAL_
 cudaError_t launch_balance_fwd(cudaStream_t st, const float* logits, const int* topk_idx, const uint8_t* mask,
                                const int* seg_offsets, int T, int E, int k, int B, int* counts, int* tokens, float* loss,
                                void* workspace) {
-    BalArgs a{logits, topk_idx, mask, seg_offsets, T, E, k, B, bal_chunk(T, E)};
+    BalArgs a{logits, topk_idx, mask, seg_offsets, T, E, k, B, bal_chunk(T, E), (float)(1ull << 62)};
+    for (int64_t most = 1; most < T; most *= 2) a.fix *= 0.5f;
+    a.unfix = 1.f / a.fix;
     char* w = static_cast<char*>(workspace) + 256;
     const size_t be = (size_t)B * E;
     a.P = reinterpret_cast<unsigned long long*>(w);
