@@ -25,11 +25,11 @@
 // error moves between kinds of matrices (before the rounding to bf16, 200 x 600: gaussian 1.80 -> 1.56e-3,
 // rank 25 0.8 -> 1.7e-3).
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "slab.h"
 
 #include <cuda_fp16.h>
@@ -1591,14 +1591,12 @@ static cudaError_t ns_steps(cudaStream_t st, int most, const NsMaps& maps, const
     return cudaLaunchKernelEx(&cfg, ns_steps_kernel<PAIR>, maps, a);
 }
 template <bool PAIR>
-static cudaError_t ns_resident(int num_sms, int* most) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int ctas = 0;
-    std::call_once(once, [&] {
+static cudaError_t ns_resident(int device, int num_sms, int* most) {
+    static PerDevice<int> held;
+    return held.get(device, most, [&](int* ctas) {
         auto kern = ns_steps_kernel<PAIR>;
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
-        ctas = num_sms;
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem);
+        *ctas = num_sms;
         if (err == cudaSuccess && PAIR) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute at[1];
@@ -1613,11 +1611,10 @@ static cudaError_t ns_resident(int num_sms, int* most) {
             cfg.numAttrs = 1;
             int clusters = 0;
             err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-            ctas = 2 * std::max(1, std::min(clusters, num_sms / 2));
+            *ctas = 2 * std::max(1, std::min(clusters, num_sms / 2));
         }
+        return err;
     });
-    *most = ctas;
-    return err;
 }
 
 template <typename T>
@@ -1645,7 +1642,7 @@ static cudaError_t ns_tiny(cudaStream_t st, const T* G, __nv_bfloat16* O, const 
 
 // `*ran` false: this GPU has no room for such a cluster
 template <typename T, bool VEC>
-static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsSmall& a, bool* ran) {
+static cudaError_t ns_small(cudaStream_t st, int device, const T* G, int S, int N, const NsSmall& a, bool* ran) {
     auto kern = ns_small_kernel<T, VEC>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
@@ -1661,12 +1658,12 @@ static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsS
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static bool sixteen = false;
-    std::call_once(once, [&] {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
-        if (err != cudaSuccess) return;
+    static PerDevice<bool> held;
+    bool sixteen = false;
+    const cudaError_t err = held.get(device, &sixteen, [&](bool* fits) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+        if (e != cudaSuccess) return e;
+        *fits = false;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
             cudaLaunchConfig_t c16 = cfg;
             cudaLaunchAttribute a16 = at[0];
@@ -1675,9 +1672,10 @@ static cudaError_t ns_small(cudaStream_t st, const T* G, int S, int N, const NsS
             c16.attrs = &a16;
             c16.numAttrs = 1;
             int clusters = 0;
-            sixteen = cudaOccupancyMaxActiveClusters(&clusters, kern, &c16) == cudaSuccess && clusters > 0;
+            *fits = cudaOccupancyMaxActiveClusters(&clusters, kern, &c16) == cudaSuccess && clusters > 0;
         }
-        if (!sixteen) cudaGetLastError();   // an answer, not an error of this call
+        if (!*fits) cudaGetLastError();   // an answer, not an error of this call
+        return cudaSuccess;
     });
     if (err != cudaSuccess) return err;
     *ran = S <= 8 || sixteen;
@@ -1716,6 +1714,9 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         return g_f32 ? ns_tiny(st, static_cast<const float*>(G), static_cast<__nv_bfloat16*>(O), L, R > C, steps, coeffs, eps)
                      : ns_tiny(st, static_cast<const __nv_bfloat16*>(G), static_cast<__nv_bfloat16*>(O), L, R > C, steps, coeffs, eps);
     }
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return err;
     int mp;
     if (const int S = ns_small_cluster(N, L.m, L.n, &mp)) {
         NsSmall a{(int)R, (int)C, (int)L.m, (int)L.n, mp, ns_log2(mp), ns_log2(S), steps, R > C, eps};
@@ -1727,10 +1728,10 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
         const auto* gf = static_cast<const float*>(G);
         const auto* gb = static_cast<const __nv_bfloat16*>(G);
         bool ran = false;
-        const cudaError_t err = C % 8 == 0 && R <= C ? (g_f32 ? ns_small<float, true>(st, gf, S, (int)N, a, &ran)
-                                                    : ns_small<__nv_bfloat16, true>(st, gb, S, (int)N, a, &ran))
-                                           : (g_f32 ? ns_small<float, false>(st, gf, S, (int)N, a, &ran)
-                                                    : ns_small<__nv_bfloat16, false>(st, gb, S, (int)N, a, &ran));
+        err = C % 8 == 0 && R <= C ? (g_f32 ? ns_small<float, true>(st, device, gf, S, (int)N, a, &ran)
+                                                    : ns_small<__nv_bfloat16, true>(st, device, gb, S, (int)N, a, &ran))
+                                           : (g_f32 ? ns_small<float, false>(st, device, gf, S, (int)N, a, &ran)
+                                                    : ns_small<__nv_bfloat16, false>(st, device, gb, S, (int)N, a, &ran));
         if (err != cudaSuccess || ran) return err;
     }
     char* w = static_cast<char*>(workspace);
@@ -1739,7 +1740,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
     const int tile = pair ? 256 : 128;
     const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);
-    cudaError_t err =
+    err =
         g_f32 ? ns_first_x(st, L, static_cast<const float*>(G), (int)R, (int)C, eps, w, steps > 1, 1 + 2 * mt, num_sms)
               : ns_first_x(st, L, static_cast<const __nv_bfloat16*>(G), (int)R, (int)C, eps, w, false, 1 + 2 * mt, num_sms);
     if (err != cudaSuccess) return err;
@@ -1758,7 +1759,7 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     if (o_box) ok = ok && tmap_batched(&t.o, O, true, C, R, C, N, 128) && tmap_batched(&t.o_t, O, true, C, R, C, N, 64);
     if (!ok) return cudaErrorInvalidValue;
     int most = 0;
-    if ((err = pair ? ns_resident<true>(num_sms, &most) : ns_resident<false>(num_sms, &most)) != cudaSuccess) return err;
+    if ((err = pair ? ns_resident<true>(device, num_sms, &most) : ns_resident<false>(device, num_sms, &most)) != cudaSuccess) return err;
     const int ctas = pair ? most / 2 : most;
     NsArgs a{};
     a.m = (int)m; a.n = (int)n; a.N = (int)N;
