@@ -3,8 +3,9 @@
 Argument marshalling only: torch tensors become `moe_tensor` views (device pointer, dtype,
 shape, strides), the current torch CUDA stream becomes the `stream` argument, and every step of
 the layer runs in the CUDA library.  The balance loss and the orthogonalisation marshal in C++
-(`csrc/marshal.cpp`), since their smallest calls take a few microseconds.  The libraries are loaded
-on import; if they have not been built, importing this module raises (there is no fallback).
+(`csrc/marshal.cpp`), since their smallest calls take a few microseconds.  The library is loaded on
+import, the compiled marshalling by the first call that wants it; if they have not been built, that raises
+(there is no fallback).
 """
 from __future__ import annotations
 
@@ -62,8 +63,6 @@ def _load() -> ctypes.CDLL:
     path = _build.LIB
     if not os.path.exists(path):
         raise RuntimeError(f"CUDA library not built ({path}); run moe_expert_layer_permute_gb300.build.build()")
-    if not os.path.exists(_build.MARSHAL):
-        raise RuntimeError(f"marshalling not built ({_build.MARSHAL}); run moe_expert_layer_permute_gb300.build.build()")
     lib = ctypes.CDLL(path)
     lib.moe_scratch_bytes.argtypes = [_P(MoeDesc)]
     lib.moe_scratch_bytes.restype = ctypes.c_size_t
@@ -109,15 +108,20 @@ def _load() -> ctypes.CDLL:
 LIB = _load()
 
 
-def _load_marshal():
+_MARSHAL = None
+
+
+def _marshal():
     """The compiled marshalling (`csrc/marshal.cpp`), linked against the library loaded above."""
-    spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    return module
-
-
-_MARSHAL = _load_marshal()
+    global _MARSHAL
+    if _MARSHAL is None:
+        if not os.path.exists(_build.MARSHAL):
+            raise RuntimeError(f"marshalling not built ({_build.MARSHAL}); run moe_expert_layer_permute_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_marshal", _build.MARSHAL)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _MARSHAL = module
+    return _MARSHAL
 
 
 class MoeError(RuntimeError):
@@ -308,7 +312,7 @@ def moe_balance_fwd(logits, topk_idx, counts, tokens, loss, workspace: Workspace
     """Balance loss, z-loss and per-expert counts of each segment: logits fp32 [T, E], topk_idx int32
     [T, k], mask bool or uint8 [T] or None, seg_offsets int32 [B+1] or None (B = 1) -> counts int32
     [B, E], tokens int32 [B], loss fp32 [B, 2]."""
-    rc = _MARSHAL.balance_fwd(logits, topk_idx, mask, seg_offsets, counts, tokens, loss, workspace.address,
+    rc = (_MARSHAL or _marshal()).balance_fwd(logits, topk_idx, mask, seg_offsets, counts, tokens, loss, workspace.address,
                               None if stream is None else _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_fwd")
@@ -318,7 +322,7 @@ def moe_balance_bwd(logits, topk_idx, topk_w, dtopk_w, counts, tokens, dloss, dl
                     stream=None) -> None:
     """dlogits fp32 [T, E] of the losses (dloss fp32 [B, 2]) and, unless topk_w and dtopk_w are None,
     of the top-k weights (what moe_router_bwd gives), in one pass."""
-    rc = _MARSHAL.balance_bwd(logits, topk_idx, topk_w, dtopk_w, mask, seg_offsets, counts, tokens, dloss, dlogits,
+    rc = (_MARSHAL or _marshal()).balance_bwd(logits, topk_idx, topk_w, dtopk_w, mask, seg_offsets, counts, tokens, dloss, dlogits,
                               None if stream is None else _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_balance_bwd")
@@ -334,6 +338,6 @@ def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, e
     co = ()
     if coeffs is not None:
         co = [v for c in coeffs for v in c] if hasattr(coeffs[0], "__len__") else tuple(coeffs) * max(steps, 1)
-    rc = _MARSHAL.orthogonalise(G, O, workspace.address, None if stream is None else _stream_ptr(stream), steps, eps, *co)
+    rc = (_MARSHAL or _marshal()).orthogonalise(G, O, workspace.address, None if stream is None else _stream_ptr(stream), steps, eps, *co)
     if rc:
         raise MoeError(rc, "moe_orthogonalise")
