@@ -332,12 +332,26 @@ def moe_orthogonalise_workspace_bytes(N: int, R: int, C: int) -> int:
     return int(LIB.moe_orthogonalise_workspace_bytes(N, R, C))
 
 
+def _triples(coeffs, steps: int) -> list:
+    """The numbers of one triple for every step, or of a triple for each; a sequence, an array or a tensor."""
+    def plain(v):
+        return v.tolist() if hasattr(v, "tolist") else v
+    rows = plain(coeffs)
+    if len(rows) == 3 and isinstance(rows[0], (int, float)):
+        return list(rows) * max(steps, 1)
+    rows = [plain(c) for c in rows]
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [rows] * max(steps, 1)
+    if not rows or any(len(c) != 3 for c in rows):   # (their number the call checks)
+        raise MoeError(ERR["MOE_ERR_SHAPE"], "moe_orthogonalise")
+    return [v for c in rows for v in c]
+
+
 def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None) -> None:
     """O bf16 [N, R, C] = every matrix of G (bf16 or fp32, [N, R, C]) after `steps` Newton-Schulz steps.
-    coeffs: (a, b, c) for every step, a sequence of `steps` such triples, or None for the defaults."""
-    co = ()
-    if coeffs is not None:
-        co = [v for c in coeffs for v in c] if hasattr(coeffs[0], "__len__") else tuple(coeffs) * max(steps, 1)
+    coeffs: (a, b, c) for every step, a sequence of `steps` such triples (numbers, arrays or tensors), or None for the
+    defaults."""
+    co = () if coeffs is None else _triples(coeffs, steps)
     rc = (_MARSHAL or _marshal()).orthogonalise(G, O, workspace.address, None if stream is None else _stream_ptr(stream), steps, eps, *co)
     if rc:
         raise MoeError(rc, "moe_orthogonalise")
