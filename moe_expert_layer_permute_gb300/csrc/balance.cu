@@ -21,7 +21,8 @@
 
 namespace moe {
 
-constexpr int kBalMaxChunks = 304;    // forward: most blocks (two per SM)
+constexpr int kBalSms = 152;
+constexpr int kBalMaxChunks = 2 * kBalSms;   // forward: most blocks
 constexpr int kBwdWarps = 8;
 // forward: warps per block; two blocks an SM hold 32 warps where a warp has one row of up to 512 values at
 // a time, which the memory needs then (131,072 x 512: 76 us with eight)
@@ -140,6 +141,11 @@ __device__ __forceinline__ BalRow bal_softmax(float* x) {
 // no such bound, are kept apart, one for each piece (block c's piece of segment s at c + s, which no other
 // has: going through the tokens each block's end and each segment's end advances it by one), and added in
 // order.  One launch: a second one that added 304 blocks' partial sums took 11 us at 128 experts.
+//
+// A block takes the segments that it meets one after the other, with four barriers and a sum over its warps each, so
+// many short ones cost more than their tokens (131,072 x 128: 18 us with 1 segment, 27 with 1024, 69 with 8192, 590
+// with 65,535; the backward 29, 31, 35, 46), and both directions pass empty segments one by one (65,533 of them in
+// one place: 8 and 10 ms).
 struct BalArgs {
     const float* logits;
     const int* idx;
@@ -433,10 +439,10 @@ static cudaError_t fwd_c(cudaStream_t st, const BalArgs& a) {
 }
 template <int W, int V, bool VEC>
 static cudaError_t bwd_c(cudaStream_t st, BalBwdArgs a) {
-    // as many warps as the GPU holds at 32 an SM (152 SMs), each with so many rounds of tokens
+    // as many warps as the GPU holds at 32 an SM, each with so many rounds of tokens
     constexpr int G = 32 / W;
     const int groups = (a.T + G - 1) / G;
-    a.rounds = std::max(1, (groups + 152 * 32 - 1) / (152 * 32));
+    a.rounds = std::max(1, (groups + kBalSms * 32 - 1) / (kBalSms * 32));
     const int warps = (groups + a.rounds - 1) / a.rounds;
     return launch_pdl(balance_bwd_kernel<W, V, VEC>, (warps + kBwdWarps - 1) / kBwdWarps, 32 * kBwdWarps, 0, st, a);
 }

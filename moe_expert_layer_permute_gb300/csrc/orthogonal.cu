@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(kTinyThreads) ns_tiny_kernel(const T* G, __nv_
 //   order and sending them to all as fp16 -> A A and B in every CTA -> X of the CTA's columns.
 // Where m leaves room, up to eight blocks of 256 columns lie one below the other in the CTA's 128 rows: A is
 // the sum of the diagonal blocks of their product, and with A and B laid out block-diagonally the rest goes
-// as before, with as many CTAs less (96 matrices of 20 x 1210: 471 us with the large kernels, 76 here).
+// as before, with as many CTAs less (96 matrices of 20 x 1210: 80 us; 100 take 202 with the large kernels).
 // A's rounding error lies below A in each chunk of columns, so that A A and A by its error are one MMA of 256 columns
 // (of 128 each, with operands that differ, an MMA takes 112 cycles, and 16 of them 300 more than these eight).  The
 // errors of A and B cost 16 x 128 x 256 24.6 -> 31.8 us and 1 x 128 x 2048 47.9 -> 55.9.
@@ -1339,8 +1339,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ns_small_kernel(const T* __r
             else __syncthreads();
             // Pieces of 16 bytes of the rows that this CTA adds: the thread's j-th is in row r0 + j * down, and its
             // terms come CTA by CTA and block by block, eight loads under way at a time, of as many pieces as they
-            // belong to (one piece after the other: 16 x 128 x 512 44.3 us against 41.8, 300 x 64 x 2000 382 against 367;
-            // of eight or more terms each the network between SMs is the limit, 100 x 4095 56.6 against 57.5).
+            // belong to (16 x 128 x 512: 51 us, 300 x 64 x 2000: 422; one piece after the other they took 2.5 and 15 more; of eight
+            // or more terms each the network between SMs is the limit, 100 x 4095, 68 us, took 1 less).
             const int log_pieces = a.log_mp - 2, log_blocks = 7 - a.log_mp, log_terms = a.log_ctas + log_blocks;
             const int at = threadIdx.x & ((1 << log_pieces) - 1), down = kSmallThreads >> log_pieces, terms = 1 << log_terms;
             const int r0 = (rank << (a.log_mp - a.log_ctas)) + ((int)threadIdx.x >> log_pieces);
@@ -1737,6 +1737,11 @@ cudaError_t launch_orthogonalise(cudaStream_t st, const void* G, bool g_f32, int
     char* w = static_cast<char*>(workspace);
     const bool flip = R > C;
     const int64_t m = L.m, n = L.n;
+    // Pairs take in half as much for the same product, but a tile of theirs is four of one CTA's, and few of them leave
+    // SMs idle.  Even at about half a tile of X for each SM, sooner for a few large matrices, later for several small
+    // ones (us by pairs and by single CTAs; tiles of a pair in X): 1 x 2048 x 2048 (64) 253 and 274, 76 x 200 x 200 (76) 123
+    // and 131, 150 x 200 x 200 (150) 179 and 245, 40 x 300 x 400 (160) 158 and 168, 6 x 1024 x 1024 (96) 209 and 213;
+    // 3 x 777 x 1001 (48) 195 and 157, 5 x 777 x 1001 (80) 194 and 180, 9 x 600 x 600 (81) 188 and 168.
     const bool pair = m > 128 && N * ((m + 255) / 256) * ((n + 255) / 256) >= num_sms / 2;
     const int tile = pair ? 256 : 128;
     const int mt = (int)((m + tile - 1) / tile), nt = (int)((n + tile - 1) / tile);

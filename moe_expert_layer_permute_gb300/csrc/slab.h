@@ -16,12 +16,12 @@ constexpr int kSmallCols = 256;      // columns of one block of X
 constexpr int kSmallThreads = 256;   // eight warps: TMEM lane quarter w % 4, column half w / 4
 
 // CTAs of a cluster for matrices that ns_small_kernel takes, 0 for others, and the rows of a block.  Up to 64 rows
-// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 636 us
-// here, 1014 there; 64 x 2000, 300: 383 and 759); so do one or two CTAs, and four whose columns are filled
-// (100 x 1000, 200: 260 and 356; 128 x 1024, 256: 346 and 400).  Of more CTAs the kernel runs about 48 us a round
+// it takes any number of matrices, since the large kernel's tiles have 128 (200 matrices of 40 x 4096: 692 us
+// here, 1052 there; 64 x 2000, 300: 421 and 815); so do one or two CTAs, and four whose columns are filled
+// (100 x 1000, 200: 316 and 378; 128 x 1024, 256: 434 and 472).  Of more CTAs the kernel runs about 57 us a round
 // of the GPU however few the matrices are, and the large kernel is even with it beyond 512 CTAs if filled, and at
-// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 150, 249, 443 us here and 217, 267, 430 there;
-// 128 x 4096, 32 and 64: 263, 530 and 329, 504; 70 x 600, 128: 161 and 149).
+// two rounds of the SMs if not (128 x 2048, 40, 64, 128 matrices: 176, 290, 528 us here and 231, 284, 455 there;
+// 128 x 4096, 32 and 64: 334, 666 and 361, 559; 70 x 600, 76 and 128: 142, 193 and 127, 163).
 inline int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
     *mp = 128;
     while (*mp / 2 >= m && *mp > 16 && (128 / *mp) * kSmallCols < n) *mp /= 2;
@@ -34,8 +34,8 @@ inline int ns_small_cluster(int64_t N, int64_t m, int64_t n, int* mp) {
 }
 
 // A CTA's part of G comes in, and O goes out, through shared memory where G^T is kept or rows are no multiples
-// of 16 bytes (16 x 128 x 255, bf16: 27 us, by single elements of each row 61; with rows of 16-byte pieces, which
-// threads take from G themselves, 16 x 128 x 256 is 24.8 us, and 25.9 this way).  A part is a run of all
+// of 16 bytes (16 x 128 x 255, bf16: 34 us; by single elements of each row it was 34 us more; 16 x 128 x 256, 32 us with
+// rows of 16-byte pieces, which threads take from G themselves, was 1 us more this way).  A part is a run of all
 // the CTA's columns, which are G's rows (flip), or for each row of each block of columns one of up to 256
 // elements, `pitch` bytes apart in shared memory: an odd number of words, so that threads of consecutive rows
 // meet no bank conflicts.  Copies are of words of W bytes, aligned on both sides: the data lies as far past a word in
