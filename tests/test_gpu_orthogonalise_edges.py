@@ -141,3 +141,11 @@ def test_growth_between_steps(cuda_lib, N, R, C):
         assert max(errors(O, exact(G, 2, far))) < BAR
     else:
         assert not O.isfinite().all()
+
+
+@pytest.mark.parametrize("N,R,C", [(1, 16, 32768), (2, 12, 20001), (3, 20, 9000), (2, 9000, 40), (1, 9, 16500)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_clusters_whose_ctas_add_few_rows(cuda_lib, N, R, C, dtype):
+    """Short, long matrices: down to one row of A, and four threads, for each CTA of sixteen."""
+    G = gauss(N, R, C, dtype, seed=R * C % 1000)
+    assert max(errors(run(cuda_lib, G), exact(G))) < BAR
