@@ -361,7 +361,7 @@ def _own_select(s):
         out.update(idx=s["idx"], w=s["w"])
     if case["dir"] == "fwd":
         return out
-    moe.moe_router_select_bwd(s["logits"], s["idx"], s["w"], s["dw"], s["dlogits"], s["rule"], mask=s["mask"])
+    moe.moe_router_select_bwd(s["logits"], s["idx"], s["w"], s["dw"], s["dlogits"], s["rule"])
     out["dlogits"] = s["dlogits"]
     if s["bias"] is not None and case["dir"] == "train":
         moe.moe_router_bias_step(s["counts"], s["bias"], BIAS_RATE)
