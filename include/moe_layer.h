@@ -105,6 +105,10 @@ typedef struct {
  * then not bitwise reproducible: the fp32 additions follow the tiles' timing, so runs may differ in
  * the last bit of an element; without the flag the combine sums in a fixed order. */
 #define MOE_FLAG_FUSED_COMBINE 0x8u
+/* moe_fwd and moe_bwd: an id of -1 in topk_idx stands for no pick (moe_router_select_fwd writes it for padded tokens and
+ * where too few experts are left).  Its slot is dropped as every id outside [0, E) is, but it is not recorded as
+ * MOE_DEV_BAD_EXPERT. */
+#define MOE_FLAG_NO_PICK 0x10u
 
 /* Host-side handle of a caller-owned device scratch buffer of at least moe_scratch_bytes(desc)
  * bytes.  `epoch` is the caller's: a counter it advances whenever x, W13 or W2 may have changed in
@@ -199,6 +203,50 @@ const char* moe_strerror(int code);
 int moe_router_fwd(const moe_tensor* logits, moe_tensor* topk_idx, moe_tensor* topk_w, void* stream);
 int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const moe_tensor* dtopk_w,
                    moe_tensor* dlogits, void* stream);
+
+/* ---- routing by scores: a bias for the choice, groups of experts -------------------------------------- */
+/* The router of layers that are balanced by a bias instead of (or beside) a loss, and whose experts stand in groups:
+ *   s[t] = softmax(l[t]) over all E experts, or sigmoid(l[t]) of each
+ *   c[t,e] = s[t,e] + bias[e]   (without a bias: s); an expert whose logit or bias is -inf is excluded
+ *   groups of E / groups consecutive experts: a group's value is the sum of its group_rank largest c (of those that are
+ *   not excluded, if they are fewer; without any the group is excluded); the topk_groups largest groups stay
+ *   topk_idx[t]: the k largest c of the groups that stay, in descending order
+ *   topk_w[t,j] = scale s[t, topk_idx[t,j]], divided by the sum of the k picks' s if `renormalise` is not 0
+ * c and the groups' values are compared in 64 bits; without a bias experts are compared by their logits, whose order is
+ * that of their scores.  Equal ones go to the lower index (-0.0 equal to +0.0), NaN ranks above every number.  Where
+ * fewer than k experts are left, the other picks are -1 with weight 0.  The bias carries no gradient.
+ *
+ * moe_router_select_fwd: logits fp32 or bf16 [T, E] -> topk_idx int32 [T, k], topk_w fp32 [T, k] (overwritten).
+ *   bias: fp32 [E] or NULL.  mask: uint8 [T] or NULL; a token whose mask is 0 (padding) is not read: it gets picks
+ *   of -1 and weights of 0.  A layer that is to take such picks wants MOE_FLAG_NO_PICK, else it records them.
+ * moe_router_select_bwd: dlogits [T, E], fp32 or bf16 (overwritten; with `accumulate`, fp32 only, added to, so that the
+ *   balance loss's gradient, from moe_balance_bwd without topk_w, may stand there already) of
+ *   sum_j dtopk_w[t,j] topk_w[t,j].  With D = sum_i w_i dw_i, at the picks:
+ *     sigmoid   w_j (dw_j - D / scale) (1 - s_j), without the D if not renormalised; softmax, renormalised: without (1 - s_j)
+ *     softmax, not renormalised: w_j dw_j - s_j D, and -s_e D at every other expert
+ *   topk_idx, topk_w as moe_router_select_fwd wrote them (distinct experts per token; ids outside [0, E) have no
+ *   gradient, and the logits of a token without any pick are not read).
+ * moe_router_bias_step: counts int32 [B, E] (moe_balance_fwd's, or the layer's MOE_VIEW_COUNTS as one row) ->
+ *   bias[e] += rate sign(mean - n[e]), n[e] the sum of column e and mean that of n, compared as whole numbers.
+ * Limits as moe_router_fwd's, and groups <= 32, a divisor of E; group_rank 1 or 2; k <= topk_groups E / groups;
+ * scale in (0, 1e6]; rate in [0, 1e6].  Outputs may not overlap inputs.  Scores are fp32 with an error of some 2^-22; a
+ * sigmoid's weights keep their digits however small the scores are.  Results repeat bit for bit.  Tokens whose sums lie within
+ * fp32's error of each other cost more (a router whose experts are all equal, with a bias: all of them). */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+    int32_t score;         /* moe_score */
+    int32_t groups;        /* 1: none */
+    int32_t topk_groups;
+    int32_t group_rank;
+    int32_t renormalise;
+    float   scale;
+} moe_router_rule;
+int moe_router_select_fwd(const moe_tensor* logits, const moe_tensor* bias, const moe_tensor* mask, moe_tensor* topk_idx,
+                          moe_tensor* topk_w, const moe_router_rule* rule, void* stream);
+int moe_router_select_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* topk_w,
+                          const moe_tensor* dtopk_w, moe_tensor* dlogits, const moe_router_rule* rule, int32_t accumulate,
+                          void* stream);
+int moe_router_bias_step(const moe_tensor* counts, moe_tensor* bias, float rate, void* stream);
 
 /* ---- training the router: balance loss, z-loss, per-expert counts ----------------------------- */
 /* A router trained on the layer's loss alone tends to send most tokens to few experts.  The usual

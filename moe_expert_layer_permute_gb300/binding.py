@@ -21,6 +21,7 @@ from . import build as _build
 MOE_BF16, MOE_MXFP8, MOE_FP8_BWD, MOE_FP8_FP4 = 0, 1, 2, 3
 MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8 = 0, 1, 2, 3
 MOE_FLAG_SAVE_GU, MOE_FLAG_REUSE_FWD, MOE_FLAG_REUSE_WEIGHTS, MOE_FLAG_FUSED_COMBINE = 0x1, 0x2, 0x4, 0x8
+MOE_FLAG_NO_PICK = 0x10
 (MOE_VIEW_COUNTS, MOE_VIEW_OFFSETS, MOE_VIEW_PERM, MOE_VIEW_INV, MOE_VIEW_PAD_OFFSETS, MOE_VIEW_XPERM,
  MOE_VIEW_HID, MOE_VIEW_GU, MOE_VIEW_YPART, MOE_VIEW_DG, MOE_VIEW_HW, MOE_VIEW_DYPERM) = range(12)
 MOE_DEV_OK, MOE_DEV_BAD_EXPERT, MOE_DEV_TIMEOUT = 0, 1, 2
@@ -38,7 +39,8 @@ ERR = {v: k for k, v in ERRORS.items()}
 EXPORTS = ("moe_scratch_bytes", "moe_fwd", "moe_bwd", "moe_read_device_status", "moe_strerror",
            "moe_scratch_view", "moe_trace_enable", "moe_trace_reset", "moe_trace_read", "moe_route_static",
            "moe_router_fwd", "moe_router_bwd", "moe_set_wait_limit", "moe_balance_workspace_bytes", "moe_balance_fwd",
-           "moe_balance_bwd", "moe_orthogonalise_workspace_bytes", "moe_orthogonalise")
+           "moe_balance_bwd", "moe_orthogonalise_workspace_bytes", "moe_orthogonalise", "moe_router_select_fwd",
+           "moe_router_select_bwd", "moe_router_bias_step")
 
 
 class MoeTensor(ctypes.Structure):
@@ -54,6 +56,11 @@ class MoeDesc(ctypes.Structure):
 class MoeScratch(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("bytes", ctypes.c_uint64), ("desc", MoeDesc),
                 ("epoch", ctypes.c_uint64), ("state", ctypes.c_uint64 * 4)]
+
+
+class MoeRouterRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_rank", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _P = ctypes.POINTER
@@ -102,6 +109,12 @@ def _load() -> ctypes.CDLL:
     lib.moe_orthogonalise.argtypes = [_P(MoeTensor)] * 2 + [ctypes.c_int32, _P(ctypes.c_float), ctypes.c_float,
                                                             _P(MoeScratch), ctypes.c_void_p]
     lib.moe_orthogonalise.restype = ctypes.c_int
+    lib.moe_router_select_fwd.argtypes = [_P(MoeTensor)] * 5 + [_P(MoeRouterRule), ctypes.c_void_p]
+    lib.moe_router_select_fwd.restype = ctypes.c_int
+    lib.moe_router_select_bwd.argtypes = [_P(MoeTensor)] * 5 + [_P(MoeRouterRule), ctypes.c_int32, ctypes.c_void_p]
+    lib.moe_router_select_bwd.restype = ctypes.c_int
+    lib.moe_router_bias_step.argtypes = [_P(MoeTensor)] * 2 + [ctypes.c_float, ctypes.c_void_p]
+    lib.moe_router_bias_step.restype = ctypes.c_int
     return lib
 
 
@@ -301,6 +314,44 @@ def moe_router_bwd(topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> None:
     rc = LIB.moe_router_bwd(*[ctypes.byref(a) for a in args], _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_router_bwd")
+
+
+class RouterRule:
+    """How moe_router_select_fwd chooses and weighs: score "softmax" or "sigmoid", groups of consecutive experts of which
+    topk_groups stay (by the sum of their group_rank largest), weights renormalised over the picks or not, their scale."""
+
+    SCORES = {"softmax": 0, "sigmoid": 1}
+
+    def __init__(self, score="softmax", groups=1, topk_groups=1, group_rank=1, renormalise=True, scale=1.0):
+        if score not in self.SCORES:
+            raise MoeError(ERR["MOE_ERR_UNSUPPORTED"], "RouterRule")
+        self.handle = MoeRouterRule(self.SCORES[score], groups, topk_groups, group_rank, 1 if renormalise else 0, scale)
+        self.address = ctypes.addressof(self.handle)
+
+
+def moe_router_select_fwd(logits, topk_idx, topk_w, rule: RouterRule, bias=None, mask=None, stream=None) -> None:
+    """Routing by scores: logits fp32 or bf16 [T, E], bias fp32 [E] or None, mask bool or uint8 [T] or None -> topk_idx
+    int32 [T, k] (-1 where there is no pick), topk_w fp32 [T, k]."""
+    rc = (_MARSHAL or _marshal()).select_fwd(logits, bias, mask, topk_idx, topk_w, rule.address,
+                                             None if stream is None else _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_router_select_fwd")
+
+
+def moe_router_select_bwd(logits, topk_idx, topk_w, dtopk_w, dlogits, rule: RouterRule, accumulate: bool = False,
+                          stream=None) -> None:
+    """dlogits [T, E] (fp32 or bf16; fp32 with accumulate, which adds to it) from the weights' gradient dtopk_w fp32 [T, k]."""
+    rc = (_MARSHAL or _marshal()).select_bwd(logits, topk_idx, topk_w, dtopk_w, dlogits, rule.address, accumulate,
+                                             None if stream is None else _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_router_select_bwd")
+
+
+def moe_router_bias_step(counts, bias, rate: float, stream=None) -> None:
+    """bias fp32 [E] += rate * sign(mean - n), n the sums of counts int32 [B, E] over B."""
+    rc = (_MARSHAL or _marshal()).bias_step(counts, bias, rate, None if stream is None else _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_router_bias_step")
 
 
 def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:

@@ -71,6 +71,7 @@ struct Ctx {
     const float* topk_w;  // routing weights [T*k] (caller's tensor)
     long long wait_limit = 0;   // pipeline wait limit in cycles (0: the default)
     uint32_t test_flags = 0;    // MOE_TEST_* (moe_set_wait_limit)
+    bool no_pick = false;       // MOE_FLAG_NO_PICK
 };
 
 // routing: counts, offsets, padded offsets, m-tile prefix, expert order, perm / inv / pos / row_slot
@@ -82,7 +83,7 @@ struct RoutingBufs {
     int *hist, *base, *cnt, *off, *pad_off, *mtile, *order, *perm, *inv, *pos, *row_slot;
 };
 cudaError_t launch_routing_kernels(cudaStream_t st, const int32_t* topk_idx, int S, int E, const RoutingBufs& r,
-                                   int* status);
+                                   int* status, bool no_pick = false);
 // dst[r] = src[row_slot[r] / k] for every padded row r (zeros on padding rows); up to two pairs
 cudaError_t launch_gather(const Ctx& c, const void* src0, void* dst0, const void* src1, void* dst1);
 // out[t] = sum_j part[pos[t*k+j]] (fixed j order); optionally dtopk_w[s] = sum_n dtw[pos[s], n]
@@ -106,6 +107,36 @@ cudaError_t launch_balance_fwd(cudaStream_t st, const float* logits, const int* 
 cudaError_t launch_balance_bwd(cudaStream_t st, const float* logits, const int* topk_idx, const float* topk_w,
                                const float* dtopk_w, const uint8_t* mask, const int* seg_offsets, const int* counts,
                                const int* tokens, const float* dloss, int T, int E, int k, int B, float* dlogits);
+
+// routing by scores (select.cu); T = 0 launches nothing
+struct SelectArgs {
+    const void* logits;     // fp32 or bf16 [T, E]
+    const float* bias;      // [E] or null
+    const uint8_t* mask;    // [T] or null
+    bool bf16, sigmoid, renorm;
+    int T, E, k, G, kept, rank;
+    float scale;
+    int* idx;
+    float* w;
+    // by the launch: experts of a group, log2 of its lanes, the mask of a key's index, c's share that it takes
+    int gs, lpg_log2;
+    uint32_t low;
+    float quantum;
+};
+cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms);
+struct SelectGradArgs {
+    const void* logits;
+    const int* idx;
+    const float* w;
+    const float* dw;
+    bool bf16, sigmoid, renorm, out_bf16, accumulate;
+    int T, E, k;
+    float inv_scale;
+    void* dlogits;          // fp32 or bf16 [T, E]
+    int tile;               // by the launch: tokens of a tile
+};
+cudaError_t launch_select_bwd(cudaStream_t st, SelectGradArgs a, int num_sms);
+cudaError_t launch_select_bias(cudaStream_t st, const int* counts, int B, int E, float* bias, float rate);
 
 // Newton-Schulz orthogonalisation of N matrices [R, C] (orthogonal.cu); coeffs: 3 * steps host floats
 size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C);

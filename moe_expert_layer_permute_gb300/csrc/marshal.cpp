@@ -4,6 +4,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -118,10 +119,91 @@ PyObject* orthogonalise(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return PyLong_FromLong(rc);
 }
 
+// The arguments of calls that may be on any device: tensors of one of them, whose current stream is taken where none is
+// given, and which is the current device during the call.  `at` is where the stream stands.
+struct On {
+    c10::cuda::OptionalCUDAGuard guard;
+    void* stream = nullptr;
+};
+bool read_on(Args* a, On* on, PyObject* const* args, Py_ssize_t n, int tensors, Py_ssize_t want) {
+    if (n != want) {
+        PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
+        return false;
+    }
+    try {
+        int device = -1;
+        for (int i = 0; i < tensors; ++i) {
+            if (!view(args[i], &a->held[i], &a->t[i])) return false;
+            if (args[i] == Py_None || !THPVariable_Unpack(args[i]).is_cuda()) continue;
+            const int d = THPVariable_Unpack(args[i]).get_device();
+            if (device >= 0 && d != device) {
+                PyErr_SetString(PyExc_ValueError, "tensors of several devices");
+                return false;
+            }
+            device = d;
+        }
+        if (device >= 0) on->guard.set_index((c10::DeviceIndex)device);
+        PyObject* stream = args[want - 1];
+        on->stream = stream == Py_None ? (void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream() : PyLong_AsVoidPtr(stream);
+        return !PyErr_Occurred();
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return false;
+    }
+}
+
+// logits, bias, mask, topk_idx, topk_w, rule, stream
+PyObject* select_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    Args a;
+    On on;
+    if (!read_on(&a, &on, args, n, 5, 7)) return nullptr;
+    const auto* rule = static_cast<const moe_router_rule*>(PyLong_AsVoidPtr(args[5]));
+    if (PyErr_Occurred()) return nullptr;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = moe_router_select_fwd(a.t[0], a.t[1], a.t[2], a.t[3], a.t[4], rule, on.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
+
+// logits, topk_idx, topk_w, dtopk_w, dlogits, rule, accumulate, stream
+PyObject* select_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    Args a;
+    On on;
+    if (!read_on(&a, &on, args, n, 5, 8)) return nullptr;
+    const auto* rule = static_cast<const moe_router_rule*>(PyLong_AsVoidPtr(args[5]));
+    if (PyErr_Occurred()) return nullptr;
+    const int accumulate = PyObject_IsTrue(args[6]);
+    if (accumulate < 0) return nullptr;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = moe_router_select_bwd(a.t[0], a.t[1], a.t[2], a.t[3], a.t[4], rule, accumulate, on.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
+
+// counts, bias, rate, stream
+PyObject* bias_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    Args a;
+    On on;
+    if (!read_on(&a, &on, args, n, 2, 4)) return nullptr;
+    const double rate = PyFloat_AsDouble(args[2]);
+    if (PyErr_Occurred()) return nullptr;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = moe_router_bias_step(a.t[0], a.t[1], (float)rate, on.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
+
+#define MOE_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"balance_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(balance_fwd)), METH_FASTCALL, nullptr},
     {"balance_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(balance_bwd)), METH_FASTCALL, nullptr},
     {"orthogonalise", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(orthogonalise)), METH_FASTCALL, nullptr},
+    MOE_METHOD(select_fwd),
+    MOE_METHOD(select_bwd),
+    MOE_METHOD(bias_step),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -265,6 +265,7 @@ static Ctx make_ctx(cudaStream_t st, moe_scratch* s, const Layout* L, int nsm, c
     Ctx c{st, base, L, reinterpret_cast<int*>(base + L->ctrl), nsm, reinterpret_cast<const float*>(topk_w)};
     c.wait_limit = (long long)s->state[2];
     c.test_flags = (uint32_t)s->state[3];
+    c.no_pick = (s->desc.flags & MOE_FLAG_NO_PICK) != 0;
     return c;
 }
 
@@ -598,6 +599,98 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
         seg_offsets ? reinterpret_cast<const int*>(seg_offsets->data) : nullptr, reinterpret_cast<const int*>(counts->data),
         reinterpret_cast<const int*>(tokens->data), reinterpret_cast<const float*>(dloss->data), (int)T, (int)E, (int)k,
         (int)B, reinterpret_cast<float*>(dlogits->data)));
+    return MOE_OK;
+}
+
+// a tensor of fp32 or bf16 values; which one in *bf16
+static int check_float(const moe_tensor* t, int ndim, int64_t s0, int64_t s1, bool* bf16) {
+    if (!t) return MOE_ERR_NULL;
+    *bf16 = t->dtype == MOE_DT_BF16;
+    return check_tensor(t, *bf16 ? MOE_DT_BF16 : MOE_DT_F32, ndim, s0, s1, 0);
+}
+
+static int check_rule(const moe_router_rule* r, int64_t E, int64_t k) {
+    if (!r) return MOE_ERR_NULL;
+    if ((r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || r->groups < 1 || r->groups > 32 ||
+        r->group_rank < 1 || r->group_rank > 2 || !(r->scale > 0.f && r->scale <= 1e6f))
+        return MOE_ERR_UNSUPPORTED;
+    if (E % r->groups != 0 || r->topk_groups < 1 || r->topk_groups > r->groups || k > E / r->groups * r->topk_groups)
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int moe_router_select_fwd(const moe_tensor* logits, const moe_tensor* bias, const moe_tensor* mask, moe_tensor* topk_idx,
+                          moe_tensor* topk_w, const moe_router_rule* rule, void* stream) {
+    int64_t T, E, k;
+    int rc = router_shape(logits, topk_idx, &T, &E, &k);
+    if (rc) return rc;
+    if ((rc = check_rule(rule, E, k))) return rc;
+    SelectArgs a{};
+    if ((rc = check_float(logits, 2, T, E, &a.bf16))) return rc;
+    if (bias && (rc = check_tensor(bias, MOE_DT_F32, 1, E, 0, 0))) return rc;
+    if (mask && (rc = check_tensor(mask, MOE_DT_U8, 1, T, 0, 0))) return rc;
+    if ((rc = check_tensor(topk_idx, MOE_DT_I32, 2, T, k, 0))) return rc;
+    if ((rc = check_tensor(topk_w, MOE_DT_F32, 2, T, k, 0))) return rc;
+    const int nsm = num_sms_current();
+    if (nsm <= 0) return MOE_ERR_CUDA;
+    a.logits = logits->data;
+    a.bias = bias ? reinterpret_cast<const float*>(bias->data) : nullptr;
+    a.mask = mask ? reinterpret_cast<const uint8_t*>(mask->data) : nullptr;
+    a.sigmoid = rule->score == MOE_SCORE_SIGMOID;
+    a.renorm = rule->renormalise != 0;
+    a.T = (int)T, a.E = (int)E, a.k = (int)k;
+    a.G = rule->groups, a.kept = rule->topk_groups, a.rank = rule->group_rank;
+    if (a.kept == a.G) a.G = a.kept = 1;   // every group stays
+    if (a.rank > a.E / a.G) a.rank = 1;
+    a.scale = rule->scale;
+    a.idx = reinterpret_cast<int*>(topk_idx->data);
+    a.w = reinterpret_cast<float*>(topk_w->data);
+    MOE_TRY_CUDA(launch_select_fwd(reinterpret_cast<cudaStream_t>(stream), a, nsm));
+    return MOE_OK;
+}
+
+int moe_router_select_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const moe_tensor* topk_w,
+                          const moe_tensor* dtopk_w, moe_tensor* dlogits, const moe_router_rule* rule, int32_t accumulate,
+                          void* stream) {
+    int64_t T, E, k;
+    int rc = router_shape(logits, topk_idx, &T, &E, &k);
+    if (rc) return rc;
+    if ((rc = check_rule(rule, E, k))) return rc;
+    SelectGradArgs a{};
+    if ((rc = check_float(logits, 2, T, E, &a.bf16))) return rc;
+    if ((rc = check_tensor(topk_idx, MOE_DT_I32, 2, T, k, 0))) return rc;
+    if ((rc = check_tensor(topk_w, MOE_DT_F32, 2, T, k, 0))) return rc;
+    if ((rc = check_tensor(dtopk_w, MOE_DT_F32, 2, T, k, 0))) return rc;
+    if ((rc = check_float(dlogits, 2, T, E, &a.out_bf16))) return rc;
+    if (accumulate && a.out_bf16) return MOE_ERR_UNSUPPORTED;
+    const int nsm = num_sms_current();
+    if (nsm <= 0) return MOE_ERR_CUDA;
+    a.logits = logits->data;
+    a.idx = reinterpret_cast<const int*>(topk_idx->data);
+    a.w = reinterpret_cast<const float*>(topk_w->data);
+    a.dw = reinterpret_cast<const float*>(dtopk_w->data);
+    a.sigmoid = rule->score == MOE_SCORE_SIGMOID;
+    a.renorm = rule->renormalise != 0;
+    a.accumulate = accumulate != 0;
+    a.T = (int)T, a.E = (int)E, a.k = (int)k;
+    a.inv_scale = 1.f / rule->scale;
+    a.dlogits = dlogits->data;
+    MOE_TRY_CUDA(launch_select_bwd(reinterpret_cast<cudaStream_t>(stream), a, nsm));
+    return MOE_OK;
+}
+
+int moe_router_bias_step(const moe_tensor* counts, moe_tensor* bias, float rate, void* stream) {
+    if (!counts || !bias) return MOE_ERR_NULL;
+    if (counts->ndim != 2 || counts->shape[0] < 0 || counts->shape[0] > INT32_MAX) return MOE_ERR_SHAPE;
+    const int64_t B = counts->shape[0], E = counts->shape[1];
+    if (E < 1 || E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+    int rc;
+    if ((rc = check_tensor(counts, MOE_DT_I32, 2, B, E, 0))) return rc;
+    if ((rc = check_tensor(bias, MOE_DT_F32, 1, E, 0, 0))) return rc;
+    if (!(rate >= 0.f && rate <= 1e6f)) return MOE_ERR_UNSUPPORTED;
+    if (B == 0) return MOE_OK;
+    MOE_TRY_CUDA(launch_select_bias(reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const int*>(counts->data), (int)B,
+                                    (int)E, reinterpret_cast<float*>(bias->data), rate));
     return MOE_OK;
 }
 

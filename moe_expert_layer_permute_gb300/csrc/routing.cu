@@ -15,7 +15,8 @@
 //                 base[b][e] + (slots of e earlier in the chunk), ranking ties inside a warp with
 //                 __match_any_sync and across the block's warps with per-warp counts.
 // Expert ids outside [0, E) are never used as an index: they are counted nowhere, recorded as
-// MOE_DEV_BAD_EXPERT in the status word (when there is one), their slots get inv = pos = -1, and
+// MOE_DEV_BAD_EXPERT in the status word (when there is one; not -1 where the caller says that it stands for
+// no pick), their slots get inv = pos = -1, and
 // the sorted positions they leave free, [offsets[E], T*k), hold perm = -1.
 // The padded-layout outputs (pad_off, mtile, order, pos, row_slot) and the status word are
 // optional: the allocation-free entry point (route_static.cu) runs the same kernels without them.
@@ -30,7 +31,7 @@ constexpr int kRouteThreads = 256;   // route_hist
 constexpr int kPlaceThreads = 512;   // route_place: a 2048-slot chunk in four rounds
 
 __global__ void __launch_bounds__(kRouteThreads) route_hist_kernel(const int32_t* __restrict__ idx, int S, int E,
-                                                                    int* __restrict__ hist, int* status) {
+                                                                    int* __restrict__ hist, int* status, bool no_pick) {
     grid_dep_wait();
     extern __shared__ int sh_cnt[];
     for (int e = threadIdx.x; e < E; e += blockDim.x) sh_cnt[e] = 0;
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_hist_kernel(const int32_t
         const int e = idx[s];
         if ((unsigned)e < (unsigned)E)
             atomicAdd(&sh_cnt[e], 1);
-        else
+        else if (!(no_pick && e == -1))
             set_status(status, MOE_DEV_BAD_EXPERT);
     }
     __syncthreads();
@@ -179,12 +180,13 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(
 }
 
 cudaError_t launch_routing_kernels(cudaStream_t st, const int32_t* topk_idx, int S, int E, const RoutingBufs& r,
-                                   int* status) {
+                                   int* status, bool no_pick) {
     const int nb = (S + kRouteChunk - 1) / kRouteChunk;
     cudaError_t err = cudaSuccess;
     if (nb > 0) {
         trace_begin(st, kTraceRouteHist);
-        err = launch_pdl(route_hist_kernel, nb, kRouteThreads, E * sizeof(int), st, topk_idx, S, E, r.hist, status);
+        err = launch_pdl(route_hist_kernel, nb, kRouteThreads, E * sizeof(int), st, topk_idx, S, E, r.hist, status,
+                         no_pick);
         trace_end(st, kTraceRouteHist);
     }
     if (err != cudaSuccess) return err;
@@ -215,7 +217,7 @@ cudaError_t launch_routing(const Ctx& c, const int32_t* topk_idx) {
     auto at = [&](size_t off) { return reinterpret_cast<int*>(c.base + off); };
     const RoutingBufs r{at(L.hist), at(L.base), at(L.cnt), at(L.off), at(L.pad_off), at(L.mtile),
                         at(L.order),  at(L.perm), at(L.inv), at(L.pos), at(L.row_slot)};
-    return launch_routing_kernels(c.st, topk_idx, (int)L.S, (int)L.E, r, c.status);
+    return launch_routing_kernels(c.st, topk_idx, (int)L.S, (int)L.E, r, c.status, c.no_pick);
 }
 
 }  // namespace moe
