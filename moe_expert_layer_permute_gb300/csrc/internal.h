@@ -122,6 +122,8 @@ struct SelectArgs {
     int gs, lpg_log2;
     uint32_t low;
     float quantum;
+    bool few;               // tokens: latency counts
+    int batch;              // tokens that a warp takes at a time
 };
 cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms);
 struct SelectGradArgs {

@@ -19,6 +19,7 @@
 // index takes from c (7 bits at 128 experts) is part of the error above; it is small where the numbers are, so c is taken
 // relative to the largest bias and then to the row's largest c.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -32,23 +33,29 @@ __device__ __forceinline__ float sel_value(const SelectArgs& a, long long i) {
     return a.bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.logits) + i))
                   : __ldg(static_cast<const float*>(a.logits) + i);
 }
-__device__ __forceinline__ void sel_value4(const SelectArgs& a, long long i, float* x) {
-    if (a.bf16) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.logits) + i));
+// four of them, 16-byte (bf16: 8-byte) aligned
+template <bool BF>
+__device__ __forceinline__ void sel_load4(const void* p, float* x) {
+    if constexpr (BF) {
+        const uint2 v = __ldg(static_cast<const uint2*>(p));
         x[0] = __uint_as_float(v.x << 16);
         x[1] = __uint_as_float(v.x & 0xffff0000u);
         x[2] = __uint_as_float(v.y << 16);
         x[3] = __uint_as_float(v.y & 0xffff0000u);
     } else {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + i));
+        const float4 v = __ldg(static_cast<const float4*>(p));
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     }
 }
-// A float's order as an unsigned number: -0 is 0, NaN above everything; 0 is below every number
+template <bool BF>
+__device__ __forceinline__ float sel_load(const void* p) {
+    if constexpr (BF) return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p)));
+    else return __ldg(static_cast<const float*>(p));
+}
+// A float's order as an unsigned number: -0 is 0, NaN above everything, -inf 0x007fffff
 __device__ __forceinline__ uint32_t sel_key(float v) {
-    const uint32_t u = __float_as_uint(v + 0.f);   // (-0 + 0 is +0)
-    const uint32_t k = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
-    return v == v ? k : 0xffffffffu;
+    const uint32_t u = __float_as_uint(v + 0.f);   // (-0 + 0 is +0, a sum of any NaN the one NaN 0x7fffffff)
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float sel_unkey(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
@@ -61,16 +68,17 @@ __device__ __forceinline__ double sel_unkey64(uint64_t k) {
     return __longlong_as_double((long long)((k >> 63) ? k ^ 0x8000000000000000ull : ~k));
 }
 __device__ __forceinline__ float sel_exp(float x) { return exp2_approx(x * 1.442695041f); }
-__device__ __forceinline__ float sel_sigmoid(float x) { return __fdividef(1.f, 1.f + sel_exp(-x)); }
-// (__fdividef is 0 for a divisor over 2^126, of infinity too: the sigmoid of -88 and less)
+__device__ __forceinline__ float sel_sigmoid(float x) { return rcp_approx(1.f + sel_exp(-x)); }   // (0 for an infinite power)
 
-// How far an fp32 c = s + b may be from the exact one where s <= `most`: the exponential's argument is rounded (by
-// 2^-24 of it, which is at most -ln s + ln E), the power, the quotient and the softmax's sum to some 2^-22, the sum to half
-// of c's last bit.
-__device__ __forceinline__ float sel_error(float c, float most) {
+// How far an fp32 score may be from the exact one where it is at most `most`.  The power is off by 2^-22 relative, its
+// argument z (times log2 e) by 2^-24 of it, a quotient by 2^-23.
+//   sigmoid: s (1 - s) (2^-22 + 2^-23 |z|) + 2^-23 s, at most 3e-7, and for a small s, -z up to 88, 1.1e-5 s
+//   softmax: s (2^-22 + 2^-23 (-ln s)) and the sum's error, some 2^-21 with its exponentials'; s (-ln s) is at most 0.37
+__device__ __forceinline__ float sel_error(bool sigmoid, float most) {
     const float s = fminf(fmaxf(most, 1e-37f), 1.f);
-    return s * (1.5e-6f - 1.5e-7f * __logf(s)) + 1.2e-7f * fabsf(c);
+    return sigmoid ? fminf(3e-7f, 1.1e-5f * s) : 9e-7f * s + fminf(4.5e-8f, 1.1e-5f * s);
 }
+constexpr float kSelSum = 1.2e-7f;   // of a sum's size: a rounding of it, and one of its bias less the largest
 
 template <int W>
 __device__ __forceinline__ float sel_max(float v) {
@@ -102,22 +110,68 @@ __device__ __forceinline__ float sel_segment_max(float v, int n) {
 }
 
 // ---- one token again, exactly, by a whole warp ---------------------------------------------------------------
-// A pick as the forward keeps it: 0 for none, else any bits over `low` bits that hold low - e.
-__device__ __forceinline__ uint32_t sel_pick(int e, uint32_t low) { return 0x80000000u | (low - (uint32_t)e); }
+// A pick as the forward keeps it: 0 for none, else bits of a key, the last of which hold low - e.
+__device__ __forceinline__ uint32_t sel_pick(int e, uint32_t low) { return 0xff000000u | (low - (uint32_t)e); }
 
 struct SelRoom {              // a warp's shared memory
     uint64_t sorted[32];
     int candidate[32];
 };
+struct SelToken {             // what the forward found out about a token
+    float top;                // its largest c, less the largest bias
+    float max, inv;           // of the softmax: the largest logit and 1 / sum
+    uint32_t groups;          // bits of those that stay; 0: not known
+};
 
-// n <= 32: the candidates hold every expert that can be among the first k; the fp32 sums in full decide where they are
-// far enough apart, else sums in 64 bits (a softmax's over its fp32 sum, whose error stands in both terms and so counts
-// with their difference alone).  Where that is not enough either, or n is larger, all experts are gone through in 64
-// bits, their groups too: k rounds of the largest that is left.
-__device__ __noinline__ void select_again(const SelectArgs& a, long long t, int n, float row_max, float inv_sum, float span,
-                                          float top_bias, uint32_t low, SelRoom* room, uint32_t* picks) {
+// How far two distances from `top`, d and a smaller one, may come nearer: scores of at most `most`, what the index takes,
+// and the roundings of sums, of biases and of the distances themselves.
+__device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float d, float most) {
+    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (a.quantum + kSelSum) * d;
+}
+
+// open: bit j where picks j and j + 1 are too near each other.  The candidates are those from the first such pick on, as
+// far as their order is open (picks before and after them stand), and where the last pick is among them every expert
+// that may be; the fp32 sums in full decide where they are far enough apart, else sums in 64 bits (a softmax's over
+// its fp32 sum, whose error stands in both terms and so counts with their difference alone).  Where that is not enough
+// either, or there are more than 32, or nothing is known (0), all experts are gone through in 64 bits, their groups too:
+// k rounds of the largest that is left.
+__device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint32_t open, const SelToken& token, float span,
+                                          float top_bias, uint32_t low, uint32_t none, SelRoom* room, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
     const unsigned all = 0xffffffffu;
+    const bool scores = a.bias || a.G > 1;
+    const float row_max = token.max, inv_sum = token.inv;
+    int from = 0, n = 33;
+    if (open) {
+        from = __ffs(open) - 1;
+        n = min(33 - __clz(open), a.k) - from;
+        if (lane < n) room->candidate[lane] = (int)(low - (picks[from + lane] & low));
+        if ((open >> (a.k - 1)) & 1u) {
+            const uint32_t next = picks[a.k];
+            const int mine = lane < a.k ? (int)(low - (picks[lane] & low)) : -1;
+            // (every score is at most 1; a softmax's at most 1 / its sum)
+            const float d = __uint_as_float(~next & ~low);
+            const float far = d + 2.f * sel_margin(a, token.top, d, a.sigmoid ? 1.f : inv_sum);
+            for (int i = 0; i < a.E && n <= 32; i += 32) {
+                const int e = i + lane;
+                bool in = false;
+                if (e < a.E && (a.G == 1 || ((token.groups >> (e / a.gs)) & 1u))) {
+                    const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) - top_bias : 0.f;
+                    if (scores)
+                        in = x != -INFINITY && token.top - ((a.sigmoid ? sel_sigmoid(x) : sel_exp(x - row_max) * inv_sum) + b) <= far;
+                    else
+                        in = (sel_key(x) & ~low) >= (next & ~low);
+                }
+                for (uint32_t votes = __ballot_sync(all, in); votes; votes &= votes - 1) {
+                    const int it = i + __ffs(votes) - 1;
+                    if (__any_sync(all, mine == it)) continue;
+                    if (lane == 0 && n < 32) room->candidate[n] = it;
+                    ++n;
+                }
+            }
+        }
+        __syncwarp();
+    }
     if (n <= 32) {
         const int e = lane < n ? room->candidate[lane] : 0;
         const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
@@ -125,7 +179,7 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, int 
             float s = 0.f;
             double s64 = 0.0;
             uint64_t key;
-            if (!a.bias) {
+            if (!scores) {
                 key = (uint64_t)sel_key(x) << 32;
             } else if (pass == 0) {
                 s = a.sigmoid ? sel_sigmoid(x) : sel_exp(x - row_max) * inv_sum;
@@ -148,15 +202,15 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, int 
             }
             __syncwarp();
             bool near = false;
-            if (a.bias && !(a.sigmoid && pass == 1)) {
+            if (scores && !(a.sigmoid && pass == 1)) {
                 const int after = lane < n && rank + 1 < n ? room->candidate[rank + 1] : lane;
                 const double so = __shfl_sync(all, s64, after);
                 const float xo = __shfl_sync(all, x, after), bo = __shfl_sync(all, b, after);
-                if (after != lane && rank < a.k && !(x == xo && b == bo)) {   // (equal ones are in the order of their index)
+                if (after != lane && from + rank < a.k && !(x == xo && b == bo)) {   // (equal ones are in the order of their index)
                     const uint64_t next = room->sorted[rank + 1];
                     if (pass == 0) {
                         const float c = sel_unkey((uint32_t)(key >> 32)), d = sel_unkey((uint32_t)(next >> 32));
-                        near = !(c - d > sel_error(c, s + span) + sel_error(d, s + span));
+                        near = !(c - d > 2.f * sel_error(a.sigmoid, s + span) + kSelSum * (fabsf(c) + fabsf(d)));
                     } else {
                         const double c = sel_unkey64(key), d = sel_unkey64(next);
                         near = !(c - d > 2e-6 * fabs(s64 - so) + 1e-15 * (fabs(c) + fabs(b)));
@@ -164,8 +218,7 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, int 
                 }
             }
             if (!__any_sync(all, near)) {
-                if (lane < n && rank < a.k) picks[rank] = sel_pick(e, low);
-                for (int r = n + lane; r < a.k; r += 32) picks[r] = 0;
+                if (lane < n && from + rank < a.k) picks[from + rank] = sel_pick(e, low);
                 __syncwarp();
                 return;
             }
@@ -176,7 +229,6 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, int 
     uint64_t key[32];
     const int rows = (a.E + 31) >> 5;
     double top = -INFINITY, sum = 0.0;
-    const bool scores = a.bias || a.G > 1;
     if (!a.sigmoid && scores) {
         bool nan = false;
         for (int i = 0; i < rows; ++i)
@@ -258,30 +310,85 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, int 
     __syncwarp();
 }
 
+// Groups of one token that are too near each other at the border: which of the contenders stay, `slots` of them, as a mask of
+// groups; from the n candidates, which hold every expert that can be among a contender's `rank` largest, their sums in 64
+// bits.  0 where a softmax's sum, which has 32, leaves it open.
+__device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t, int n, int slots, float row_max, float inv_sum,
+                                               const SelRoom* room) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    const int e = lane < n ? room->candidate[lane] : 0, g = lane < n ? e / a.gs : -1 - lane;
+    const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)row_max) * (double)inv_sum;
+    const double c = s + (double)b;
+    const uint64_t key = sel_key64(c);
+    int place = 0;   // in its group
+    for (int i = 0; i < n; ++i) {
+        const uint64_t other = __shfl_sync(all, key, i);
+        const int oe = __shfl_sync(all, e, i), og = __shfl_sync(all, g, i);
+        place += og == g && (other > key || (other == key && oe < e));
+    }
+    double sum = 0.0, score = 0.0;
+    for (int i = 0; i < n; ++i) {
+        const double oc = __shfl_sync(all, c, i), os = __shfl_sync(all, s, i);
+        const int og = __shfl_sync(all, g, i), op = __shfl_sync(all, place, i);
+        if (og == g && op < a.rank) {
+            sum += oc;
+            score += os;
+        }
+    }
+    const bool first = lane < n && place == 0;
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double os = __shfl_sync(all, sum, i);
+        const int og = __shfl_sync(all, g, i);
+        const bool of = __shfl_sync(all, (int)first, i);
+        rank += of && (os > sum || (os == sum && og < g));
+    }
+    bool near = false;
+    if (!a.sigmoid)
+        for (int i = 0; i < n; ++i) {
+            const double os = __shfl_sync(all, sum, i), oc = __shfl_sync(all, score, i);
+            const bool stays = __shfl_sync(all, (int)(first && rank < slots), i);
+            near |= first && rank >= slots && stays && !(os - sum > 2e-6 * fabs(oc - score) + 1e-15 * (fabs(os) + 1.0));
+        }
+    const uint32_t mask = __reduce_or_sync(all, first && rank < slots ? 1u << g : 0u);
+    return __any_sync(all, near) ? 0u : mask;
+}
+
 // ---- forward ---------------------------------------------------------------------------------------------------
+// keys that a lane keeps in order: the k picks of a token fall on its W lanes, and a lane that has given all it kept looks
+// through its V keys again, which the whole warp waits for
+template <int W>
+constexpr int sel_kept() { return W == 32 ? 2 : W == 16 ? 3 : 4; }
+
 template <int W, int V, bool VEC>
 __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1) select_fwd_kernel(const SelectArgs a) {
     grid_dep_wait();
     constexpr int NT = 32 / W;   // tokens of a warp
-    extern __shared__ uint32_t sel_picks[];
+    extern __shared__ __align__(16) float sel_shared[];
     __shared__ SelRoom rooms[kSelWarps];
-    __shared__ float2 stats[kSelWarps][NT];   // a token's row maximum and 1 / sum
-    __shared__ float tops[kSelWarps][NT];     // and its largest c
+    __shared__ SelToken tokens[kSelWarps][32];
+    __shared__ float ends[2 * kSelWarps];
     const unsigned all = 0xffffffffu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane % W;
     const int lpg = 1 << a.lpg_log2, group = gl >> a.lpg_log2, lp = gl & (lpg - 1);
     const uint32_t low = a.low;
     const bool scores = a.bias || a.G > 1;                 // c is not the logit
     const bool row = !a.sigmoid && (scores || !a.renorm);  // the softmax's sum is needed
-    uint32_t* picks = sel_picks + warp * NT * (a.k + 1);
+    const uint32_t none = scores ? 0x80800000u : 0x00800000u;   // keys below it are no expert's
+    float* biases = sel_shared;                            // less the largest
+    uint32_t* picks = reinterpret_cast<uint32_t*>(sel_shared + (a.bias ? (a.E + 3) / 4 * 4 : 0)) + warp * a.batch * (a.k + 1);
     int kp = 1;                                            // lanes of a token where lanes take one pick each
     while (kp < a.k) kp *= 2;
+    const int per = 32 / kp;
 
     float span = 0.f, top_bias = 0.f;                      // of the finite biases
     if (a.bias) {
         float hi = -INFINITY, lo = INFINITY;
-        for (int e = lane; e < a.E; e += 32) {
+        for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) {
             const float b = __ldg(a.bias + e);
+            biases[e] = b;
             if (fabsf(b) < INFINITY) {
                 hi = fmaxf(hi, b);
                 lo = fminf(lo, b);
@@ -289,63 +396,130 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1)
         }
         hi = sel_max<32>(hi);
         lo = -sel_max<32>(-lo);
+        if (lane == 0) {
+            ends[warp] = hi;
+            ends[kSelWarps + warp] = lo;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) {
+            hi = fmaxf(hi, ends[w]);
+            lo = fminf(lo, ends[kSelWarps + w]);
+        }
         if (hi >= lo) {
             span = hi - lo;
             top_bias = hi;
         }
+        for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) biases[e] -= top_bias;
+        __syncthreads();
     }
-    const long long step = (long long)gridDim.x * kSelWarps * NT;
-    for (long long first = ((long long)blockIdx.x * kSelWarps + warp) * NT; first < a.T; first += step) {
-        const long long t = first + lane / W;
+    auto place = [&](int i) { return VEC ? 4 * (lp + lpg * (i >> 2)) + (i & 3) : lp + lpg * i; };
+    const int e0 = group * a.gs;
+    const int held = group < a.G ? a.gs : 0;               // places below it hold experts
+    const uint32_t code0 = low - (uint32_t)e0;
+    // A warp takes `batch` tokens, NT at a time, and then all of their picks at once.
+    const long long step = (long long)gridDim.x * kSelWarps * a.batch;
+    for (long long first = ((long long)blockIdx.x * kSelWarps + warp) * a.batch; first < a.T; first += step) {
+    for (int part = 0; part < a.batch; part += NT) {
+        const int at_token = part + lane / W;
+        const long long t = first + at_token;
         const bool live = t < a.T && !(a.mask && !__ldg(a.mask + t));
+        const int read = live ? held : 0;
         float x[V];
-        auto place = [&](int i) { return VEC ? 4 * (lp + lpg * (i >> 2)) + (i & 3) : lp + lpg * i; };
-        const int e0 = group * a.gs;
-        const int room_left = live && group < a.G ? a.gs : 0;   // places below it hold experts
+        auto load = [&](auto bf) {   // (a copy of the loop for each type, so that none is chosen for each value)
+            constexpr bool BF = decltype(bf)::value;
+            const char* from = static_cast<const char*>(a.logits) + (t * a.E + e0 + place(0)) * (BF ? 2 : 4);
+            const int stride = lpg * (BF ? 2 : 4);         // bytes between a lane's places (four times it if VEC)
+            if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = -INFINITY;
-        if constexpr (VEC) {
+                for (int i = 0; i < V; i += 4) {
+                    x[i] = x[i + 1] = x[i + 2] = x[i + 3] = -INFINITY;
+                    if (place(i) < read) sel_load4<BF>(from + i * stride, x + i);
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; i += 4)
-                if (place(i) < room_left) sel_value4(a, t * a.E + e0 + place(i), x + i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (place(i) < room_left) x[i] = sel_value(a, t * a.E + e0 + place(i));
-        }
+                for (int i = 0; i < V; ++i) x[i] = place(i) < read ? sel_load<BF>(from + i * stride) : -INFINITY;
+            }
+        };
+        if (a.bf16) load(std::true_type{}); else load(std::false_type{});
         float m = 0.f, inv = 1.f;
         if (row) {
             m = x[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
             m = sel_max<W>(m);
-            const float base = m == -INFINITY ? 0.f : m;
+            if (m == -INFINITY) m = 0.f;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += sel_exp(x[i] - base);   // (a NaN stays one)
+            for (int i = 0; i < V; ++i) sum += sel_exp(x[i] - m);   // (a NaN stays one)
             inv = 1.f / sel_sum<W>(sum);
-            m = base;
-            if (gl == 0) stats[warp][lane / W] = make_float2(m, inv);
         }
-        bool again = false;   // the groups at the border are too near
+        bool again = false;   // all of it in 64 bits
+        uint32_t groups = ~0u;
+        float top = 0.f;
         uint32_t key[V];
         if (scores) {
-            float m1 = -INFINITY, m2 = -INFINITY;
-            bool nan = false;
+            // c, less the largest bias; -inf where there is no expert or none that may be picked
+            float most_c = -INFINITY, least_x = INFINITY;
+            bool odd = false;     // NaN or +inf
+            auto sums = [&](auto sigmoid, auto biased) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool there = x[i] != -INFINITY;
-                float c = a.sigmoid ? sel_sigmoid(x[i]) : sel_exp(x[i] - m) * inv;
-                if (a.bias && place(i) < room_left) c += __ldg(a.bias + e0 + place(i)) - top_bias;
-                if (!there) c = -INFINITY;
-                nan |= c != c;
-                m2 = fmaxf(m2, fminf(m1, c));
-                m1 = fmaxf(m1, c);
-                key[i] = __float_as_uint(c);
+                for (int i = 0; i < V; i += VEC ? 4 : 1) {
+                    float b[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (place(i) < held) {
+                        if constexpr (!decltype(biased)::value) {
+                            b[0] = b[1] = b[2] = b[3] = 0.f;
+                        } else if constexpr (VEC) {
+                            const float4 v = *reinterpret_cast<const float4*>(biases + e0 + place(i));
+                            b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
+                        } else {
+                            b[0] = biases[e0 + place(i)];
+                        }
+#pragma unroll
+                        for (int q = 0; q < (VEC ? 4 : 1); ++q) least_x = fminf(least_x, x[i + q]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < (VEC ? 4 : 1); ++q) {
+                        float c = b[q];
+                        if constexpr (decltype(sigmoid)::value) c += sel_sigmoid(x[i + q]);
+                        else c += sel_exp(x[i + q] - m) * inv;
+                        odd |= !(c < INFINITY);
+                        most_c = fmaxf(most_c, c);
+                        key[i + q] = __float_as_uint(c);
+                    }
+                }
+            };
+            if (a.sigmoid) {
+                if (a.bias) sums(std::true_type{}, std::true_type{}); else sums(std::true_type{}, std::false_type{});
+            } else {
+                if (a.bias) sums(std::false_type{}, std::true_type{}); else sums(std::false_type{}, std::false_type{});
             }
-            float top = m1;   // the row's largest, its groups apart
+            if (__any_sync(all, live && least_x == -INFINITY)) {   // excluded by their logits
+                most_c = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float c = __uint_as_float(key[i]);
+                    if (place(i) < read && sel_value(a, t * a.E + e0 + place(i)) == -INFINITY) c = -INFINITY;
+                    most_c = fmaxf(most_c, c);
+                    key[i] = __float_as_uint(c);
+                }
+            }
+            top = sel_max<W>(most_c);
+            if (!(fabsf(top) < INFINITY)) top = 0.f;
+            if (__any_sync(all, live && odd)) {   // keys cannot tell them
+                again = live && odd;
+#pragma unroll
+                for (int o = W / 2; o; o >>= 1) again |= (bool)__shfl_xor_sync(all, (int)again, o);
+            }
             bool stays = true;
             if (a.G > 1) {
+                float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float c = __uint_as_float(key[i]);
+                    m2 = fmaxf(m2, fminf(m1, c));
+                    m1 = fmaxf(m1, c);
+                }
                 for (int o = 1; o < lpg; o <<= 1) {
                     const float o1 = __shfl_xor_sync(all, m1, o), o2 = __shfl_xor_sync(all, m2, o);
                     m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
@@ -360,151 +534,151 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1)
                     rank += other > vk || (other == vk && g < group);
                 }
                 stays = group < a.G && rank < a.kept && vk != 0u;
-                // the least that stays and the largest that does not (keys: 0 there is an excluded group)
-                uint32_t least = stays ? vk : 0xffffffffu, most = stays || group >= a.G ? 0u : vk;
-                least = ~sel_max<W>(~least);
-                most = sel_max<W>(most);
-                if (most != 0u) {
-                    const float lv = sel_unkey(least), mv = sel_unkey(most);
-                    const float err = 2.f * (sel_error(lv, fabsf(lv) + 2.f * span) + sel_error(mv, fabsf(lv) + 2.f * span));
-                    again = !(lv - mv > err);
-                }
-                again |= nan;   // fmaxf has passed over it
+                // the least that stays and the largest that does not (0: only excluded ones)
+                const uint32_t least = ~sel_max<W>(stays ? ~vk : 0u), most = sel_max<W>(stays || group >= a.G ? 0u : vk);
+                const float lv = sel_unkey(least), mv = sel_unkey(most);
+                // (each score is at most top + span, each c at most top, so that a sum's terms are at most it and 2 top)
+                const float err = 4.f * sel_error(a.sigmoid, fabsf(top) + span) +
+                                  2.f * kSelSum * (fabsf(lv) + fabsf(mv) + 4.f * fabsf(top) + (a.rank == 2 ? fabsf(top_bias) : 0.f));
+                uint32_t border = __ballot_sync(all, live && most != 0u && !(lv - mv > err) && !again);
+                while (border) {
+                    const int owner = __ffs(border) - 1, base = owner & ~(W - 1);
+                    border &= W == 32 ? 0u : ~(((1u << (W & 31)) - 1u) << base);
+                    const float its = __shfl_sync(all, lv, owner), e2 = 2.f * __shfl_sync(all, err, owner);
+                    const bool mine = (lane & ~(W - 1)) == base && group < a.G && vk != 0u;
+                    const bool contends = mine && fabsf(value - its) <= e2;
+                    const int sure = __popc(__ballot_sync(all, mine && lp == 0 && value > its + e2));
+                    const float from = (a.rank == 2 && m2 != -INFINITY ? m2 : m1) - e2;
+                    int n = 0;
 #pragma unroll
-                for (int o = W / 2; o; o >>= 1) again |= __shfl_xor_sync(all, again, o);
+                    for (int i = 0; i < V; ++i) {
+                        const float c = __uint_as_float(key[i]);
+                        const bool in = contends && c >= from && c > -INFINITY;
+                        const uint32_t votes = __ballot_sync(all, in);
+                        const int at = n + __popc(votes & ((1u << lane) - 1u));
+                        if (in && at < 32) rooms[warp].candidate[at] = e0 + place(i);
+                        n += __popc(votes);
+                    }
+                    __syncwarp();
+                    const float om = __shfl_sync(all, m, owner), oi = __shfl_sync(all, inv, owner);
+                    const uint32_t mask = n <= 32 ? select_groups(a, first + part + owner / W, n, a.kept - sure, om, oi, &rooms[warp]) : 0u;
+                    __syncwarp();
+                    if ((lane & ~(W - 1)) == base && mask == 0u) again = true;
+                    if (contends) stays = (mask >> group) & 1u;
+                }
+                groups = stays ? 1u << group : 0u;
+#pragma unroll
+                for (int o = W / 2; o; o >>= 1) groups |= __shfl_xor_sync(all, groups, o);
             }
-            top = sel_max<W>(top);
-            if (!(fabsf(top) < INFINITY)) top = 0.f;
+            // keys by the distance from the largest: small ones are finer
+            const float of = stays && live ? top : INFINITY;
+            const uint32_t keep = ~low;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float c = __uint_as_float(key[i]);
-                key[i] = !stays || c == -INFINITY ? 0u : (sel_key(c - top) & ~low) | (low - (uint32_t)(e0 + place(i)));
+                const uint32_t d = __float_as_uint(of - __uint_as_float(key[i]));
+                key[i] = (~d & keep) | ((code0 - (uint32_t)place(i)) & low);
             }
-            if (gl == 0) tops[warp][lane / W] = top;
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = x[i] == -INFINITY ? 0u : (sel_key(x[i]) & ~low) | (low - (uint32_t)(e0 + place(i)));
+                key[i] = (sel_key(x[i]) & ~low) | ((code0 - (uint32_t)place(i)) & low);
         }
-        // picks, and the one after them
+        // the picks and the one after them
         {
-            uint32_t best = 0;
+            constexpr int K = sel_kept<W>();
+            uint32_t n[K];
 #pragma unroll
-            for (int i = 0; i < V; ++i) best = max(best, key[i]);
-            uint32_t* mine = picks + (lane / W) * (a.k + 1);
-            for (int r = 0; r <= a.k; ++r) {
-                best = sel_max<W>(best);
+            for (int j = 0; j < K; ++j) n[j] = 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                uint32_t v = key[i];
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    const uint32_t was = n[j];
+                    n[j] = max(was, v);
+                    v = min(was, v);
+                }
+            }
+            if (gl == 0) tokens[warp][at_token] = {top, m, inv, again ? 0u : live ? groups : ~0u};
+            uint32_t* mine = picks + at_token * (a.k + 1);
+            for (int r = 0;; ++r) {
+                const uint32_t best = sel_max<W>(n[0]);
                 if (gl == 0) mine[r] = best;
-                uint32_t below = 0u - best;   // (that of 0, which is below every key)
+                if (r == a.k) break;
+                const bool won = n[0] == best;
 #pragma unroll
-                for (int i = 0; i < V; ++i) below = max(below, key[i] - best);
-                best = best ? best + below : 0u;   // (0: none is left)
+                for (int j = 0; j + 1 < K; ++j) n[j] = won ? n[j + 1] : n[j];
+                n[K - 1] = won ? 0u : n[K - 1];
+                if (__any_sync(all, n[0] == 0u)) {
+                    uint32_t below = 0u - best;   // (that of 0, which is below every key)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) below = max(below, key[i] - best);
+                    if (n[0] == 0u && best) n[0] = best + below;
+                }
             }
         }
+    }
         __syncwarp();
-        // neighbours that are too near each other
-        uint32_t redo = __ballot_sync(all, again && gl == 0);   // bit of the token's first lane
-        if (a.bias || !a.bf16) {
-            const int per = 32 / kp;
-            for (int q = 0; q < NT; q += per) {
-                const int tk = q + lane / kp, j = lane & (kp - 1);
-                const bool on = tk < NT && first + tk < a.T && j < a.k;
-                const uint32_t k0 = on ? picks[tk * (a.k + 1) + j] : 0u, k1 = on ? picks[tk * (a.k + 1) + j + 1] : 0u;
-                bool near = false;
-                if (!a.bias) {
-                    near = k0 && k1 && ((k0 ^ k1) & ~low) == 0u;
-                    if (near && j + 1 < a.k) {   // equal ones inside are in the order of their index (at the end
-                                                 // another, larger one may follow)
-                        const long long at = (first + tk) * a.E;
-                        near = sel_value(a, at + (low - (k0 & low))) != sel_value(a, at + (low - (k1 & low)));
-                    }
-                } else {
-                    float xj = 0.f, bj = 0.f, c0 = 0.f, c1 = 0.f;
-                    if (k0) {
-                        const int e = (int)(low - (k0 & low));
-                        xj = sel_value(a, (first + tk) * a.E + e);
-                        bj = __ldg(a.bias + e);
-                    }
+        // A lane to a pick.  Neighbours that are too near each other first, then weights, relative to the largest of the
+        // picks, so that small scores keep their digits.
+        for (int q = 0; q < a.batch; q += per) {
+            const int tk = q + lane / kp, j = lane & (kp - 1);
+            const bool on = tk < a.batch && first + tk < a.T && j < a.k;
+            const uint32_t* its = picks + tk * (a.k + 1) + j;
+            uint32_t k0 = on ? its[0] : 0u, k1 = on ? its[1] : 0u;
+            const SelToken token = tokens[warp][tk & 31];
+            if (k0 < none) k0 = 0u;
+            int e = k0 ? (int)(low - (k0 & low)) : -1;
+            float xj = k0 ? sel_value(a, (first + tk) * a.E + e) : -INFINITY;
+            bool near = false;
+            if (scores) {
+                const float d0 = __uint_as_float(~k0 & ~low), d1 = __uint_as_float(~k1 & ~low);   // distances from the largest
+                const float most = a.sigmoid ? 1.f : sel_exp(xj - token.max) * token.inv + span;
+                near = k0 && k1 >= none && !(d1 - d0 > sel_margin(a, token.top, d1, most));
+                // (equal logits and biases inside are in the order of their index)
+                if (__any_sync(all, near && j + 1 < a.k)) {
+                    const float bj = a.bias && k0 ? biases[e] : 0.f;
                     const float xn = __shfl_down_sync(all, xj, 1), bn = __shfl_down_sync(all, bj, 1);
-                    if (k0 && k1) {
-                        c0 = sel_unkey(k0 & ~low);
-                        c1 = sel_unkey(k1 & ~low);
-                        const float2 st = stats[warp][tk];
-                        const float s = (a.sigmoid ? sel_sigmoid(xj) : sel_exp(xj - st.x) * st.y) + span;
-                        const float of = tops[warp][tk];
-                        const float err = sel_error(c0 + of, s) + sel_error(c1 + of, s) + (a.quantum + 2.4e-7f) * fmaxf(fabsf(c1), 1e-37f);
-                        near = !(c0 - c1 > err) && !(j + 1 < a.k && xj == xn && bj == bn);
-                    }
+                    if (j + 1 < a.k && xj == xn && bj == bn) near = false;
                 }
-                // (the ballot's bits back to tokens: any lane of a segment)
-                const uint32_t votes = __ballot_sync(all, near);
-                for (int p = 0; p < per && q + p < NT; ++p) {
-                    const uint32_t segment = kp == 32 ? votes : (votes >> (p * kp)) & ((1u << kp) - 1u);
-                    if (segment) redo |= 1u << ((q + p) * W);
-                }
+            } else if (!a.bf16) {
+                near = k0 && k1 >= none && ((k0 ^ k1) & ~low) == 0u;
+                // (equal ones inside too; at the end another, larger one may follow)
+                const float xn = __shfl_down_sync(all, xj, 1);
+                if (j + 1 < a.k && xj == xn) near = false;
             }
-        }
-        const uint32_t grouped = __ballot_sync(all, again);
-        while (redo) {
-            const int owner = __ffs(redo) - 1, tk = owner / W;
-            redo &= redo - 1;
-            uint32_t* its = picks + tk * (a.k + 1);
-            int n = 33;
-            if (!((grouped >> owner) & 1u)) {
-                // every expert that may be among the first k
-                uint32_t from = its[a.k];
-                if (from == 0u) {
-                    from = 1u;
-                } else if (a.bias) {
-                    const float c = sel_unkey(from & ~low);
-                    // (every score is at most 1; a softmax's at most 1 / its sum)
-                    const float err = 4.f * sel_error(c + tops[warp][tk], a.sigmoid ? 1.f : stats[warp][tk].y) +
-                                      2.f * (a.quantum + 2.4e-7f) * fmaxf(fabsf(c), 1e-37f);
-                    from = c - err > -INFINITY ? sel_key(c - err) & ~low : 1u;   // (a NaN: all)
-                } else {
-                    from &= ~low;
-                }
-                n = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const bool in = lane / W == tk && key[i] && key[i] >= from;
-                    const uint32_t votes = __ballot_sync(all, in);
-                    const int at = n + __popc(votes & ((1u << lane) - 1u));
-                    if (in && at < 32) rooms[warp].candidate[at] = (int)(low - (key[i] & low));
-                    n += __popc(votes);
+            const bool unknown = on && token.groups == 0u;
+            if (__any_sync(all, near || unknown)) {
+                const uint32_t votes = __ballot_sync(all, near), lost = __ballot_sync(all, unknown);
+                for (int p = 0; p < per; ++p) {
+                    const uint32_t segment = kp == 32 ? ~0u : (1u << kp) - 1u;
+                    const uint32_t open = (votes >> (p * kp)) & segment, whole = (lost >> (p * kp)) & segment;
+                    if (open || whole)
+                        select_again(a, first + q + p, whole ? 0u : open, tokens[warp][q + p], span, top_bias, low, none, &rooms[warp],
+                                     picks + (q + p) * (a.k + 1));
                 }
                 __syncwarp();
+                k0 = on ? its[0] : 0u;
+                if (k0 < none) k0 = 0u;
+                e = k0 ? (int)(low - (k0 & low)) : -1;
+                xj = k0 ? sel_value(a, (first + tk) * a.E + e) : -INFINITY;
             }
-            const float2 st = row ? stats[warp][tk] : make_float2(0.f, 1.f);
-            select_again(a, first + tk, n, st.x, st.y, span, top_bias, low, &rooms[warp], its);
-        }
-        __syncwarp();
-        // weights, a lane to a pick; relative to the largest of the picks, so that small scores keep their digits
-        {
-            const int per = 32 / kp;
-            for (int q = 0; q < NT; q += per) {
-                const int tk = q + lane / kp, j = lane & (kp - 1);
-                const bool on = tk < NT && first + tk < a.T && j < a.k;
-                const uint32_t k0 = on ? picks[tk * (a.k + 1) + j] : 0u;
-                const int e = k0 ? (int)(low - (k0 & low)) : -1;
-                const float xj = k0 ? sel_value(a, (first + tk) * a.E + e) : -INFINITY;
-                float u = 0.f;
-                if (a.renorm) {
-                    const float z = a.sigmoid ? fminf(xj, 0.f) : xj;
-                    const float base = sel_segment_max(z, kp);
-                    if (k0) u = expf(z - base);
-                    if (k0 && row && isnan(stats[warp][tk].y)) u = NAN;   // a NaN beside the picks
-                    if (a.sigmoid && k0) u = xj == xj ? u / (1.f + expf(-fabsf(xj))) : xj;   // (fminf drops a NaN)
-                    const float total = sel_segment_sum(u, kp);
-                    if (k0) u = u / total;
-                } else if (k0) {
-                    u = a.sigmoid ? 1.f / (1.f + expf(-xj)) : expf(xj - stats[warp][tk].x) * stats[warp][tk].y;
-                }
-                if (on) {
-                    const long long at = (first + tk) * a.k + j;
-                    a.idx[at] = e;
-                    a.w[at] = u * a.scale;
-                }
+            float u = 0.f;
+            if (a.renorm) {
+                const float z = a.sigmoid ? fminf(xj, 0.f) : xj;
+                const float base = sel_segment_max(z, kp);
+                if (k0) u = sel_exp(z - base);
+                if (k0 && row && isnan(token.inv)) u = NAN;   // a NaN beside the picks
+                if (a.sigmoid && k0) u = xj == xj ? __fdividef(u, 1.f + sel_exp(-fabsf(xj))) : xj;   // (fminf drops a NaN)
+                const float total = sel_segment_sum(u, kp);
+                if (k0) u = __fdividef(u, total);
+            } else if (k0) {
+                u = a.sigmoid ? sel_sigmoid(xj) : sel_exp(xj - token.max) * token.inv;
+            }
+            if (on) {
+                const long long at = (first + tk) * a.k + j;
+                a.idx[at] = e;
+                a.w[at] = u * a.scale;
             }
         }
         __syncwarp();
@@ -643,7 +817,10 @@ __global__ void __launch_bounds__(256, V == 16 ? 4 : 2) select_bwd_dense_kernel(
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
-                if (any && place(i) < a.E) sel_value4(row, t * a.E + place(i), x + i);
+                if (any && place(i) < a.E) {
+                    if (a.bf16) sel_load4<true>(static_cast<const __nv_bfloat16*>(a.logits) + t * a.E + place(i), x + i);
+                    else sel_load4<false>(static_cast<const float*>(a.logits) + t * a.E + place(i), x + i);
+                }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -745,10 +922,13 @@ static int log2_of(int p) {
 }
 
 template <int W, int V, bool VEC>
-static cudaError_t select_c(cudaStream_t st, const SelectArgs& a, int num_sms) {
+static cudaError_t select_c(cudaStream_t st, SelectArgs a, int num_sms) {
     constexpr int NT = 32 / W;
-    const size_t smem = (size_t)kSelWarps * NT * (a.k + 1) * 4;   // at most 17 KB
-    const unsigned grid = sel_grid(a.T, kSelWarps * NT, V <= 16 ? 4 : V == 32 ? 2 : 1, num_sms);
+    // where a batch has many tokens a warp takes as many as fill its lanes with picks
+    const int per = 32 / pow2_at_least(a.k);
+    a.batch = a.few ? NT : std::max(NT, per);
+    const size_t smem = ((size_t)kSelWarps * a.batch * (a.k + 1) + (a.bias ? (a.E + 3) / 4 * 4 : 0)) * 4;   // at most 21 KB
+    const unsigned grid = sel_grid(a.T, kSelWarps * a.batch, V <= 16 ? 4 : V == 32 ? 2 : 1, num_sms);
     return launch_pdl(select_fwd_kernel<W, V, VEC>, grid, 32 * kSelWarps, smem, st, a);
 }
 template <int V, bool VEC>
@@ -784,9 +964,9 @@ cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms) {
     // values a lane: 4 or 8 and a whole warp where there is less than a warp of tokens to fill an SM's schedulers with,
     // 16 otherwise; more where groups do not fit 32 lanes
     int V = 0, W = 32, lanes = 32;
-    const bool few = a.T <= 8 * num_sms;
+    a.few = a.T <= 8 * num_sms;
     for (int v : {4, 8, 16, 32, 64}) {
-        if (v < 16 && !few) continue;
+        if (v < 16 && !a.few) continue;
         lanes = pow2_at_least((a.gs + v - 1) / v);
         if ((long long)a.G * lanes > 32) continue;
         V = v;
