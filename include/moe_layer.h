@@ -64,7 +64,7 @@ extern "C" {
  * types row; the English copy of that table drops the row).  Forward only, like DeepGEMM's kernel:
  * moe_bwd returns MOE_ERR_UNSUPPORTED for it. */
 typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_FP8_BWD = 2, MOE_FP8_FP4 = 3 } moe_precision;
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_I32 = 2, MOE_DT_U8 = 3 } moe_dtype;
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_I32 = 2, MOE_DT_U8 = 3, MOE_DT_E4M3 = 4 } moe_dtype;
 
 /* A view of a caller-owned buffer: `data` is a device pointer for the layer calls. */
 typedef struct {
@@ -321,6 +321,49 @@ int moe_balance_bwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
 size_t moe_orthogonalise_workspace_bytes(int64_t N, int64_t R, int64_t C);   /* 0: outside the limits */
 int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const float* coeffs, float eps,
                       moe_scratch* workspace, void* stream);
+
+/* ---- training the weights: AdamW over many tensors, norm of their gradients ------------------------ */
+/* What does not go through moe_orthogonalise (a router, its bias, norms; or all of it).  For every tensor of a list, with
+ * g' = grad_scale g and t = step:
+ *   m' = beta1 m + (1 - beta1) g',   v' = beta2 v + (1 - beta2) g'^2
+ *   p' = p - lr (m' / (1 - beta1^t) / (sqrt(v' / (1 - beta2^t)) + eps) + weight_decay p),   copy = bf16(p')
+ * in place of p (fp32), m and v.  moe_adamw_step takes `count` tensors (<= 65536) in one launch for each 384: arrays of
+ * views params, grads, m, v and, or NULL, copies; element i of each has as many values (any shape, contiguous; empty
+ * ones are passed over).  grads fp32 or bf16, each its own.  A parameter may stand in the list once
+ * (MOE_ERR_UNSUPPORTED); that tensors do not overlap otherwise is the caller's to see to.
+ *   States in 32 bits: m, v fp32.  m_scales and v_scales are not read.
+ *   States in 8 bits: m and v uint8 or E4M3 (all tensors of a call alike), v holding codes of r = sqrt(v); m_scales and
+ * v_scales fp32 [ceil(n / 256)] views, 4-byte aligned: value i of m is code[i] m_scales[i / 256].  Zeros are the state to
+ * start from.  The step decodes, steps in fp32 and encodes again: scale = max|x| / 448 over the 256 values, x / scale
+ * rounded up with the probability of its distance to the code below (`seed` chooses the numbers: give another for each
+ * step; results repeat with it).  Codes of r are at least 1 (2^-9), so a value that has had no gradient beside others
+ * that have holds a small v.  Blocks with nothing over 1e-35 become zeros; a NaN or an infinity in m' or v' makes its
+ * block NaN.
+ *   lr, step, grad_scale: numbers on the device (fp32, int32, fp32, one element each, 4-byte aligned) or NULL, then lr and
+ * step of the struct and 1.  A graph that is replayed wants them there; the step's number is then added to the seed.
+ * A grad_scale that is not finite leaves everything as it is.
+ *   lr in [0, 1e6], betas in [0, 1), eps in [1e-20, 1], weight_decay in [0, 1e6]; step >= 1.
+ *
+ * moe_grad_norm: out fp32 [2] (4-byte aligned) = (norm, factor) of all values of `count` gradients, fp32 or bf16: the square root of
+ * the sum of their squares, and min(1, max_norm / norm), 1 if max_norm is 0; a factor of NaN where the norm is not finite in fp32
+ * (no step, if it is grad_scale).  Squares and sums of 64 are fp32 (values over 1e18 or under 1e-22 are beyond it), the rest
+ * 64 bits, in an order that depends on the sizes alone.  `workspace`: a zeroed moe_scratch handle of at least
+ * moe_grad_norm_workspace_bytes(elements, count) bytes, 256-byte aligned, which the caller has set to zero once;
+ * MOE_ERR_STATE for one that moe_orthogonalise has used. */
+#define MOE_ADAMW_BLOCK 256
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t  step;
+    uint64_t seed;
+    const moe_tensor* lr_on_device;
+    const moe_tensor* step_on_device;
+    const moe_tensor* grad_scale;
+} moe_adamw_options;
+int moe_adamw_step(int64_t count, const moe_tensor* params, const moe_tensor* grads, const moe_tensor* m, const moe_tensor* v,
+                   const moe_tensor* m_scales, const moe_tensor* v_scales, const moe_tensor* copies,
+                   const moe_adamw_options* options, void* stream);
+size_t moe_grad_norm_workspace_bytes(int64_t elements, int64_t count);   /* 0: outside the limits */
+int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float max_norm, moe_scratch* workspace, void* stream);
 
 /* ---- routing without caller-provided scratch ---------------------------------------------- */
 /* The pages have no counterpart to this entry point; it exists for callers that cannot allocate

@@ -19,7 +19,7 @@ from . import build as _build
 
 # ---- C structures ---------------------------------------------------------------------------
 MOE_BF16, MOE_MXFP8, MOE_FP8_BWD, MOE_FP8_FP4 = 0, 1, 2, 3
-MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8 = 0, 1, 2, 3
+MOE_DT_BF16, MOE_DT_F32, MOE_DT_I32, MOE_DT_U8, MOE_DT_E4M3 = 0, 1, 2, 3, 4
 MOE_FLAG_SAVE_GU, MOE_FLAG_REUSE_FWD, MOE_FLAG_REUSE_WEIGHTS, MOE_FLAG_FUSED_COMBINE = 0x1, 0x2, 0x4, 0x8
 MOE_FLAG_NO_PICK = 0x10
 (MOE_VIEW_COUNTS, MOE_VIEW_OFFSETS, MOE_VIEW_PERM, MOE_VIEW_INV, MOE_VIEW_PAD_OFFSETS, MOE_VIEW_XPERM,
@@ -40,7 +40,7 @@ EXPORTS = ("moe_scratch_bytes", "moe_fwd", "moe_bwd", "moe_read_device_status", 
            "moe_scratch_view", "moe_trace_enable", "moe_trace_reset", "moe_trace_read", "moe_route_static",
            "moe_router_fwd", "moe_router_bwd", "moe_set_wait_limit", "moe_balance_workspace_bytes", "moe_balance_fwd",
            "moe_balance_bwd", "moe_orthogonalise_workspace_bytes", "moe_orthogonalise", "moe_router_select_fwd",
-           "moe_router_select_bwd", "moe_router_bias_step")
+           "moe_router_select_bwd", "moe_router_bias_step", "moe_adamw_step", "moe_grad_norm_workspace_bytes", "moe_grad_norm")
 
 
 class MoeTensor(ctypes.Structure):
@@ -61,6 +61,12 @@ class MoeScratch(ctypes.Structure):
 class MoeRouterRule(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
                 ("group_rank", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeAdamwOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", ctypes.c_int64), ("seed", ctypes.c_uint64)] + \
+        [(n, ctypes.POINTER(MoeTensor)) for n in ("lr_on_device", "step_on_device", "grad_scale")]
 
 
 _P = ctypes.POINTER
@@ -115,6 +121,12 @@ def _load() -> ctypes.CDLL:
     lib.moe_router_select_bwd.restype = ctypes.c_int
     lib.moe_router_bias_step.argtypes = [_P(MoeTensor)] * 2 + [ctypes.c_float, ctypes.c_void_p]
     lib.moe_router_bias_step.restype = ctypes.c_int
+    lib.moe_adamw_step.argtypes = [ctypes.c_int64] + [_P(MoeTensor)] * 7 + [_P(MoeAdamwOptions), ctypes.c_void_p]
+    lib.moe_adamw_step.restype = ctypes.c_int
+    lib.moe_grad_norm_workspace_bytes.argtypes = [ctypes.c_int64] * 2
+    lib.moe_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_grad_norm.argtypes = [ctypes.c_int64] + [_P(MoeTensor)] * 2 + [ctypes.c_float, _P(MoeScratch), ctypes.c_void_p]
+    lib.moe_grad_norm.restype = ctypes.c_int
     return lib
 
 
@@ -351,7 +363,7 @@ def moe_router_bias_step(counts, bias, rate: float, stream=None) -> None:
     """bias fp32 [E] += rate * sign(mean - n), n the sums of counts int32 [B, E] over B."""
     rc = (_MARSHAL or _marshal()).bias_step(counts, bias, rate, None if stream is None else _stream_ptr(stream))
     if rc:
-        raise MoeError(rc, "moe_router_bias_step")
+        raise MoeError(rc, "moe_router_bias_step", "moe_adamw_step", "moe_grad_norm_workspace_bytes", "moe_grad_norm")
 
 
 def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
@@ -406,3 +418,49 @@ def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, e
     rc = (_MARSHAL or _marshal()).orthogonalise(G, O, workspace.address, None if stream is None else _stream_ptr(stream), steps, eps, *co)
     if rc:
         raise MoeError(rc, "moe_orthogonalise")
+
+
+class TensorList:
+    """Tensors for moe_adamw_step and moe_grad_norm, which take any sequence of them; one of these is looked through once for as
+    many calls as there are (a call of 240 tensors' lists takes some 20 us less).  It holds its tensors."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.capsule = _marshal().make_list(self.tensors)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _list(tensors):
+    if tensors is None:
+        return None
+    return (tensors if isinstance(tensors, TensorList) else TensorList(tensors)).capsule
+
+
+def moe_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, m_scales=None,
+                   v_scales=None, copies=None, grad_scale=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over lists of tensors, in place: params fp32, grads fp32 or bf16, m and v fp32, or float8_e4m3fn (or
+    uint8) with m_scales and v_scales fp32 [ceil(n / 256)]; copies bf16, or None.  step and lr are numbers, or tensors
+    of one element on the device (int32, fp32); grad_scale fp32 [1] on the device, or None: a factor of the gradients, no
+    step where it is not finite.  seed: of the 8-bit states' rounding, another one for each step."""
+    step_at = step if isinstance(step, torch.Tensor) else None
+    lr_at = lr if isinstance(lr, torch.Tensor) else None
+    rc = (_MARSHAL or _marshal()).adamw_step(_list(params), _list(grads), _list(m), _list(v), _list(m_scales), _list(v_scales), _list(copies),
+                                             0.0 if lr_at is not None else lr, betas[0], betas[1], eps, weight_decay,
+                                             0 if step_at is not None else step, seed, lr_at, step_at, grad_scale,
+                                             None if stream is None else _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_adamw_step")
+
+
+def moe_grad_norm_workspace_bytes(elements: int, count: int) -> int:
+    return int(LIB.moe_grad_norm_workspace_bytes(elements, count))
+
+
+def moe_grad_norm(grads, out, workspace: Workspace, max_norm: float = 0.0, stream=None) -> None:
+    """out fp32 [2] = (norm of all gradients, the factor min(1, max_norm / norm) that brings it to max_norm; 1 with
+    max_norm 0).  out[1:] is a grad_scale for moe_adamw_step."""
+    rc = (_MARSHAL or _marshal()).grad_norm(_list(grads), out, max_norm, workspace.address, None if stream is None else _stream_ptr(stream))
+    if rc:
+        raise MoeError(rc, "moe_grad_norm")

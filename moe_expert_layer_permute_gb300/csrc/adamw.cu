@@ -1,0 +1,357 @@
+// adamw.cu - one AdamW step over many tensors at once, states in 32 bits or in 8, and the norm of many gradients.
+//
+//   g' = scale g;  m' = b1 m + (1 - b1) g';  v' = b2 v + (1 - b2) g'^2
+//   p' = p - lr (m' / (1 - b1^t) / (sqrt(v' / (1 - b2^t)) + eps) + decay p)
+//
+// In 8 bits m and r = sqrt(v) are E4M3 codes times one fp32 scale for each 256 values of a tensor, x = code scale with
+// scale = max|x| / 448.  Rounded to nearest such a state would stand still: with b2 = 0.999 a step moves v by a
+// thousandth, and half a code's step is 3 to 6 %.  So x goes up to the next code with the probability of its distance to
+// the one below, by 16 bits of a hash of the seed, the tensor's number and the value's: exact in the mean.  r's codes are
+// at least the smallest, so that no v that a gradient has touched becomes 0 beside an m that has not.
+//
+// Bound by memory: 28 bytes a value (fp32 gradients and states), 14 (bf16 gradients, 8-bit states), 2 more for the
+// bf16 copy.  A warp takes 256 neighbouring values at a time, 4 a lane in two groups, so that every access is a row of
+// whole sectors and a block of 8-bit states is one warp's: its largest value is one reduction, and no warp waits for
+// another.  The tensors' addresses come as the launch's arguments, up to 384 tensors of any sizes a launch (by a table in
+// memory each call would wait for a copy).
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+constexpr int kAdamWarps = 8;
+constexpr int kAdamUnit = 256;     // values of a warp at a time, and of a block of 8-bit states
+constexpr int kNormSteps = 16;     // units that a lane adds up in 32 bits
+
+template <int MOST>
+struct ListArgs {
+    ListTensor tensor[MOST];
+    int start[MOST + 1];           // units before each tensor
+    int count;
+};
+// the tensor of unit u, from `at` on (units ascend)
+template <int MOST>
+__device__ __forceinline__ int list_find(const ListArgs<MOST>& a, int at, int u) {
+    while (u >= a.start[at + 1]) ++at;
+    return at;
+}
+template <int MOST>
+__device__ __forceinline__ int list_search(const ListArgs<MOST>& a, int u) {
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (u >= a.start[mid]) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// four fp32 or bf16 values at place i; `left` of them are there
+__device__ __forceinline__ void list_load4(float* x, const void* p, bool bf16, long long i, int left) {
+    if (left >= 4) {
+        if (bf16) {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+            x[0] = __uint_as_float(v.x << 16);
+            x[1] = __uint_as_float(v.x & 0xffff0000u);
+            x[2] = __uint_as_float(v.y << 16);
+            x[3] = __uint_as_float(v.y & 0xffff0000u);
+        } else {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[q] = 0.f;
+            if (q < left) x[q] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i + q]) : static_cast<const float*>(p)[i + q];
+        }
+    }
+}
+__device__ __forceinline__ void list_store4(float* p, const float* x, long long i, int left) {
+    if (left >= 4) {
+        *reinterpret_cast<float4*>(p + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q < left) p[i + q] = x[q];
+    }
+}
+__device__ __forceinline__ uint32_t list_load_codes(const void* p, long long i, int left) {
+    const uint8_t* c = static_cast<const uint8_t*>(p) + i;
+    if (left >= 4) return *reinterpret_cast<const uint32_t*>(c);
+    uint32_t v = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (q < left) v |= (uint32_t)c[q] << (8 * q);
+    return v;
+}
+__device__ __forceinline__ void list_store_codes(void* p, uint32_t v, long long i, int left) {
+    uint8_t* c = static_cast<uint8_t*>(p) + i;
+    if (left >= 4) {
+        *reinterpret_cast<uint32_t*>(c) = v;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q < left) c[q] = (uint8_t)(v >> (8 * q));
+    }
+}
+// four E4M3 codes times a scale, one rounding each
+__device__ __forceinline__ void decode4(float* x, uint32_t codes, float scale) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * h)), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+        x[2 * h] = __fmul_rn(f.x, scale);
+        x[2 * h + 1] = __fmul_rn(f.y, scale);
+    }
+}
+// 32 random bits of a value's number: two rounds of xor-shift and multiplication over its place in a Weyl sequence
+__device__ __forceinline__ uint32_t adam_noise(uint32_t place, uint32_t key) {
+    uint32_t h = place * 0x9E3779B1u + key;
+    h = (h ^ (h >> 16)) * 0x7FEB352Du;
+    h = (h ^ (h >> 15)) * 0x846CA68Bu;
+    return h ^ (h >> 16);
+}
+// |x| up, at most 448 and a rounding, to a code: times 2^-120 its codes are the leading bits of the fp32 form (those below
+// 2^-6 the leading bits of numbers without an exponent), and a carry into them is the step up
+__device__ __forceinline__ uint32_t encode(float x, float up, uint32_t bits16, uint32_t least) {
+    const float y = __fmul_rn(__fmul_rn(fabsf(x), up), 7.52316384526264e-37f);   // 2^-120
+    return max(min((__float_as_uint(y) + (bits16 << 4) + 8u) >> 20, 126u), least);
+}
+// what the codes of a block are scaled by: its largest value's bits -> 448 / it (0: none, or not finite) and the scale
+__device__ __forceinline__ float block_scale(uint32_t most, float* scale) {
+    float s = __uint_as_float(most);
+    if (s < 1e-35f) s = 0.f;
+    *scale = __fmul_rn(s, 1.f / 448.f);
+    return s > 0.f ? __fmul_rn(__frcp_rn(s), 448.f) : 0.f;
+}
+
+template <int MOST, bool EIGHT>
+__global__ void __launch_bounds__(32 * kAdamWarps, 4) adamw_kernel(const __grid_constant__ ListArgs<MOST> list, const AdamArgs a) {
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31;
+    const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
+    if (!(fabsf(gs) < INFINITY)) return;   // no step
+    const float lr = a.lr_at ? __ldg(a.lr_at) : a.lr;
+    float fix1 = a.fix1, fix2 = a.fix2;
+    uint32_t seed = a.seed;
+    if (a.step_at) {
+        // 1 - b^t = -expm1(t ln b), t ln b to 2^-24 of itself, and so its result
+        const float t = (float)__ldg(a.step_at);
+        fix1 = 1.f / -expm1f(t * a.log_b1);
+        fix2 = rsqrtf(-expm1f(t * a.log_b2));
+        seed += (uint32_t)__ldg(a.step_at);
+    }
+    const int units = list.start[list.count], stride = gridDim.x * kAdamWarps;
+    int u = blockIdx.x * kAdamWarps + (threadIdx.x >> 5);
+    if (u >= units) return;
+    for (int at = list_search(list, u); u < units; u += stride) {
+        at = list_find(list, at, u);
+        const ListTensor& t = list.tensor[at];
+        const long long block = u - list.start[at], first = block * kAdamUnit + 4 * lane;
+        float p[8], g[8], m[8], v[8];
+        int left[2];
+        float ms = 0.f, vs = 0.f;
+        uint32_t mc[2], vc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long i = first + 128 * h;
+            left[h] = (int)max(min(t.n - i, 4ll), 0ll);
+            list_load4(g + 4 * h, t.g, t.g_bf16, i, left[h]);
+            list_load4(p + 4 * h, t.p, false, i, left[h]);
+            if constexpr (EIGHT) {
+                mc[h] = list_load_codes(t.m, i, left[h]);
+                vc[h] = list_load_codes(t.v, i, left[h]);
+            } else {
+                list_load4(m + 4 * h, t.m, false, i, left[h]);
+                list_load4(v + 4 * h, t.v, false, i, left[h]);
+            }
+        }
+        if constexpr (EIGHT) {
+            ms = t.m_scale[block];
+            vs = t.v_scale[block];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                decode4(m + 4 * h, mc[h], ms);
+                decode4(v + 4 * h, vc[h], vs);
+            }
+        }
+        uint32_t mm = 0, vm = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // (roundings as they stand in the formulas, no fused ones: the codes follow them)
+            const float x = a.grad_scale ? __fmul_rn(g[i], gs) : g[i];
+            if constexpr (EIGHT) v[i] = __fmul_rn(v[i], v[i]);
+            m[i] = __fadd_rn(__fmul_rn(m[i], a.b1), __fmul_rn(x, a.c1));
+            v[i] = __fadd_rn(__fmul_rn(v[i], a.b2), __fmul_rn(__fmul_rn(x, x), a.c2));
+            const float root = __fsqrt_rn(v[i]);
+            const float step = __fdividef(m[i] * fix1, fmaf(root, fix2, a.eps));
+            p[i] = fmaf(-lr, fmaf(a.decay, p[i], step), p[i]);
+            if constexpr (EIGHT) {
+                v[i] = root;
+                mm = max(mm, __float_as_uint(m[i]) & 0x7fffffffu);
+                vm = max(vm, __float_as_uint(root) & 0x7fffffffu);
+            }
+        }
+        if constexpr (EIGHT) {
+            mm = __reduce_max_sync(0xffffffffu, mm);
+            vm = __reduce_max_sync(0xffffffffu, vm);
+            const float mu = block_scale(mm, &ms), vu = block_scale(vm, &vs);
+            const uint32_t key = seed + (uint32_t)(t.ordinal + 1) * 0x85EBCA77u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t place = (uint32_t)(first + 128 * h);
+                uint32_t cm = 0, cv = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t noise = adam_noise(place + q, key);
+                    const float x = m[4 * h + q];
+                    cm |= (encode(x, mu, noise & 0xffffu, 0u) | ((__float_as_uint(x) >> 24) & 0x80u)) << (8 * q);
+                    cv |= encode(v[4 * h + q], vu, noise >> 16, 1u) << (8 * q);
+                }
+                list_store_codes(t.m, mu > 0.f ? cm : 0u, first + 128 * h, left[h]);
+                list_store_codes(t.v, vu > 0.f ? cv : 0u, first + 128 * h, left[h]);
+            }
+            if (lane == 0) {
+                t.m_scale[block] = ms;
+                t.v_scale[block] = vs;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long i = first + 128 * h;
+            list_store4(t.p, p + 4 * h, i, left[h]);
+            if constexpr (!EIGHT) {
+                list_store4(static_cast<float*>(t.m), m + 4 * h, i, left[h]);
+                list_store4(static_cast<float*>(t.v), v + 4 * h, i, left[h]);
+            }
+            if (t.copy) {
+                if (left[h] >= 4) {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p[4 * h], p[4 * h + 1]), hi = __floats2bfloat162_rn(p[4 * h + 2], p[4 * h + 3]);
+                    *reinterpret_cast<uint2*>(t.copy + i) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < left[h]) t.copy[i + q] = __float2bfloat16(p[4 * h + q]);
+                }
+            }
+        }
+    }
+}
+
+// Sum of squares: a lane adds up kNormSteps units in 32 bits, those sums and all others in 64.  A block's sum goes to
+// partial[its number in all launches]; the block that finishes last adds them in their order, so that the result does
+// not depend on who came when.
+template <int MOST>
+__global__ void __launch_bounds__(32 * kAdamWarps, 4) norm_kernel(const __grid_constant__ ListArgs<MOST> list, const NormArgs a) {
+    grid_dep_wait();
+    __shared__ double part[kAdamWarps];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = list.start[list.count], stride = gridDim.x * kAdamWarps;
+    int u = blockIdx.x * kAdamWarps + warp;
+    double sum = 0.0;
+    if (u < units) {
+        int at = list_search(list, u);
+        while (u < units) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < kNormSteps && u < units; ++k, u += stride) {
+                at = list_find(list, at, u);
+                const ListTensor& t = list.tensor[at];
+                const long long first = (long long)(u - list.start[at]) * kAdamUnit + 4 * lane;
+                float g[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    list_load4(g + 4 * h, t.g, t.g_bf16, first + 128 * h, (int)max(min(t.n - first - 128 * h, 4ll), 0ll));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s0 = fmaf(g[i], g[i], s0);
+                    s1 = fmaf(g[4 + i], g[4 + i], s1);
+                }
+            }
+            sum += (double)(s0 + s1);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kAdamWarps; ++w) sum += part[w];
+        a.partial[a.first_block + blockIdx.x] = sum;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1) == a.blocks - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    sum = 0.0;
+    for (int i = threadIdx.x; i < a.blocks; i += 32 * kAdamWarps) sum += __ldcg(a.partial + i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
+    if (lane == 0) part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.0;
+        for (int w = 0; w < kAdamWarps; ++w) sum += part[w];
+        const double norm = sqrt(sum);
+        a.out[0] = (float)norm;
+        // not a number where the norm is none or infinite, which a step takes as no step
+        const bool finite = norm <= 3.4028234663852886e38;
+        a.out[1] = !finite ? NAN : a.most > 0.f && norm > (double)a.most ? (float)((double)a.most / norm) : 1.f;
+        *a.ticket = 0;
+    }
+}
+
+// ---- launches --------------------------------------------------------------------------------------------------
+template <int MOST>
+static ListArgs<MOST> list_args(const ListTensor* t, int count) {
+    ListArgs<MOST> a;
+    a.count = count;
+    int at = 0;
+    for (int i = 0; i < count; ++i) {
+        a.tensor[i] = t[i];
+        a.start[i] = at;
+        at += (int)((t[i].n + kAdamUnit - 1) / kAdamUnit);
+    }
+    a.start[count] = at;
+    return a;
+}
+static int list_blocks(int units, int num_sms) {
+    return std::max(1, std::min((units + kAdamWarps - 1) / kAdamWarps, 4 * num_sms));
+}
+
+template <int MOST>
+static cudaError_t adamw_n(cudaStream_t st, const ListTensor* t, int count, bool eight, const AdamArgs& a, int num_sms) {
+    const ListArgs<MOST> list = list_args<MOST>(t, count);
+    const int blocks = list_blocks(list.start[count], num_sms);
+    return eight ? launch_pdl(adamw_kernel<MOST, true>, blocks, 32 * kAdamWarps, 0, st, list, a)
+                 : launch_pdl(adamw_kernel<MOST, false>, blocks, 32 * kAdamWarps, 0, st, list, a);
+}
+// (a launch with few tensors has fewer bytes of arguments)
+cudaError_t launch_adamw(cudaStream_t st, const ListTensor* t, int count, bool eight, const AdamArgs& a, int num_sms) {
+    if (count <= 8) return adamw_n<8>(st, t, count, eight, a, num_sms);
+    if (count <= 48) return adamw_n<48>(st, t, count, eight, a, num_sms);
+    return adamw_n<kListMost>(st, t, count, eight, a, num_sms);
+}
+
+int norm_blocks(const ListTensor* t, int count, int num_sms) {
+    long long units = 0;
+    for (int i = 0; i < count; ++i) units += (t[i].n + kAdamUnit - 1) / kAdamUnit;
+    return list_blocks((int)units, num_sms);
+}
+template <int MOST>
+static cudaError_t norm_n(cudaStream_t st, const ListTensor* t, int count, const NormArgs& a, int num_sms) {
+    const ListArgs<MOST> list = list_args<MOST>(t, count);
+    return launch_pdl(norm_kernel<MOST>, list_blocks(list.start[count], num_sms), 32 * kAdamWarps, 0, st, list, a);
+}
+cudaError_t launch_norm(cudaStream_t st, const ListTensor* t, int count, const NormArgs& a, int num_sms) {
+    if (count <= 8) return norm_n<8>(st, t, count, a, num_sms);
+    if (count <= 48) return norm_n<48>(st, t, count, a, num_sms);
+    return norm_n<kListMost>(st, t, count, a, num_sms);
+}
+
+}  // namespace moe

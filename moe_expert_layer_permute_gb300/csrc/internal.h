@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -139,6 +140,40 @@ struct SelectGradArgs {
 };
 cudaError_t launch_select_bwd(cudaStream_t st, SelectGradArgs a, int num_sms);
 cudaError_t launch_select_bias(cudaStream_t st, const int* counts, int B, int E, float* bias, float rate);
+
+// AdamW over a list of tensors, and the norm of a list of gradients (adamw.cu)
+constexpr int kListMost = 384;       // tensors of a launch
+struct ListTensor {
+    float* p;
+    const void* g;                   // fp32 or bf16
+    void* m;                         // fp32, or E4M3 codes
+    void* v;
+    float* m_scale;                  // with codes: one for each 256 values
+    float* v_scale;
+    __nv_bfloat16* copy;             // or null
+    long long n;
+    int ordinal;                     // its place in the caller's list
+    bool g_bf16;
+};
+struct AdamArgs {
+    float lr, b1, c1, b2, c2, eps, decay;   // c1 = 1 - b1, c2 = 1 - b2
+    float fix1, fix2;                // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    float log_b1, log_b2;            // used with a step on the device
+    uint32_t seed;
+    const float* lr_at;              // on the device, or null
+    const int* step_at;
+    const float* grad_scale;
+};
+struct NormArgs {
+    double* partial;                 // of every block of all launches
+    int* ticket;
+    int first_block, blocks;         // this launch's first, and all launches'
+    float most;                      // 0: no clipping
+    float* out;                      // norm, factor
+};
+cudaError_t launch_adamw(cudaStream_t st, const ListTensor* t, int count, bool eight, const AdamArgs& a, int num_sms);
+int norm_blocks(const ListTensor* t, int count, int num_sms);
+cudaError_t launch_norm(cudaStream_t st, const ListTensor* t, int count, const NormArgs& a, int num_sms);
 
 // Newton-Schulz orthogonalisation of N matrices [R, C] (orthogonal.cu); coeffs: 3 * steps host floats
 size_t orthogonalise_workspace(int64_t N, int64_t R, int64_t C);

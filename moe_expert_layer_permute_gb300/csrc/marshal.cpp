@@ -9,6 +9,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <memory>
+#include <vector>
 
 #include "../../include/moe_layer.h"
 
@@ -196,6 +198,194 @@ PyObject* bias_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return PyLong_FromLong(rc);
 }
 
+// ---- lists of tensors ----
+// Views of a list's tensors, made once for as many calls as there are; the tensors are held, and one whose memory has
+// changed since is looked at again by the call.
+struct List {
+    std::vector<at::Tensor> held;
+    std::vector<moe_tensor> views;
+    std::vector<const void*> at;   // where each was
+    int device = -1;               // -2: of several devices
+};
+// a contiguous tensor of any shape as its elements in a row
+moe_tensor flat(const at::Tensor& t) {
+    moe_tensor v{};
+    v.ndim = 1;
+    const bool strided = t.layout() == at::kStrided;
+    v.shape[0] = strided ? t.numel() : 0;
+    v.stride[0] = strided && t.is_contiguous() ? 1 : 2;
+    switch (t.scalar_type()) {
+        case at::kBFloat16: v.dtype = MOE_DT_BF16; break;
+        case at::kFloat: v.dtype = MOE_DT_F32; break;
+        case at::kInt: v.dtype = MOE_DT_I32; break;
+        case at::kByte: v.dtype = MOE_DT_U8; break;
+        case at::kFloat8_e4m3fn: v.dtype = MOE_DT_E4M3; break;
+        default: v.dtype = -1;
+    }
+    if (!strided) v.dtype = -1;
+    v.data = strided && t.is_cuda() && t.numel() ? t.mutable_data_ptr() : nullptr;
+    return v;
+}
+void look(List* l, size_t i) {
+    const at::Tensor& t = l->held[i];
+    l->views[i] = flat(t);
+    l->at[i] = t.layout() == at::kStrided ? t.const_data_ptr() : nullptr;
+}
+constexpr char kListName[] = "moe_tensor_list";
+List* list_of(PyObject* o) { return static_cast<List*>(PyCapsule_GetPointer(o, kListName)); }
+
+PyObject* make_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 1) {
+        PyErr_SetString(PyExc_TypeError, "expected a sequence of tensors");
+        return nullptr;
+    }
+    PyObject* seq = PySequence_Fast(args[0], "expected a sequence of tensors");
+    if (!seq) return nullptr;
+    PyObject* made = nullptr;
+    try {
+        auto l = std::make_unique<List>();
+        const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
+        l->held.reserve(count);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            PyObject* o = PySequence_Fast_GET_ITEM(seq, i);
+            if (!THPVariable_Check(o)) {
+                PyErr_SetString(PyExc_TypeError, "expected a sequence of tensors");
+                Py_DECREF(seq);
+                return nullptr;
+            }
+            const at::Tensor& t = THPVariable_Unpack(o);
+            l->held.push_back(t);
+            if (t.is_cuda()) l->device = l->device == -1 || l->device == t.get_device() ? (int)t.get_device() : -2;
+        }
+        l->views.resize(count);
+        l->at.resize(count);
+        for (Py_ssize_t i = 0; i < count; ++i) look(l.get(), i);
+        made = PyCapsule_New(l.get(), kListName, [](PyObject* c) { delete list_of(c); });
+        if (made) l.release();
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    }
+    Py_DECREF(seq);
+    return made;
+}
+
+// A call's lists: of one length and one device, whose current stream is taken where none is given.
+struct Lists {
+    List* list[7];
+    Py_ssize_t count = -1;
+    int device = -1;
+    bool add(int i, PyObject* o) {
+        list[i] = nullptr;
+        if (o == Py_None) return true;
+        List* l = list_of(o);
+        if (!l) return false;
+        if (count < 0) count = (Py_ssize_t)l->views.size();
+        if ((Py_ssize_t)l->views.size() != count) {
+            PyErr_SetString(PyExc_ValueError, "lists of different lengths");
+            return false;
+        }
+        for (size_t k = 0; k < l->held.size(); ++k)
+            if (l->held[k].layout() == at::kStrided && l->held[k].const_data_ptr() != l->at[k]) look(l, k);
+        list[i] = l;
+        return on(l->device);
+    }
+    bool on(int d) {
+        if (d == -1) return true;
+        if (d == -2 || (device >= 0 && d != device)) {
+            PyErr_SetString(PyExc_ValueError, "tensors of several devices");
+            return false;
+        }
+        device = d;
+        return true;
+    }
+    const moe_tensor* views(int i) const { return list[i] ? list[i]->views.data() : nullptr; }
+};
+// a number on the device, or None
+bool number(PyObject* o, moe_tensor* held, const moe_tensor** at, Lists* lists) {
+    *at = nullptr;
+    if (o == Py_None) return true;
+    if (!THPVariable_Check(o)) {
+        PyErr_SetString(PyExc_TypeError, "expected a tensor or None");
+        return false;
+    }
+    const at::Tensor& t = THPVariable_Unpack(o);
+    *held = flat(t);
+    *at = held;
+    return !t.is_cuda() || lists->on((int)t.get_device());
+}
+
+// params, grads, m, v, m_scales, v_scales, copies (lists), lr, beta1, beta2, eps, weight_decay, step, seed, lr, step and
+// grad_scale on the device, stream
+PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 18) {
+        PyErr_Format(PyExc_TypeError, "expected 18 arguments, got %zd", n);
+        return nullptr;
+    }
+    try {
+        Lists l;
+        for (int i = 0; i < 7; ++i)
+            if (!l.add(i, args[i])) return nullptr;
+        moe_adamw_options o{};
+        double* of[5] = {&o.lr, &o.beta1, &o.beta2, &o.eps, &o.weight_decay};
+        for (int i = 0; i < 5; ++i) {
+            *of[i] = PyFloat_AsDouble(args[7 + i]);
+            if (PyErr_Occurred()) return nullptr;
+        }
+        o.step = PyLong_AsLongLong(args[12]);
+        if (PyErr_Occurred()) return nullptr;
+        o.seed = PyLong_AsUnsignedLongLongMask(args[13]);
+        if (PyErr_Occurred()) return nullptr;
+        moe_tensor held[3];
+        if (!number(args[14], &held[0], &o.lr_on_device, &l) || !number(args[15], &held[1], &o.step_on_device, &l) ||
+            !number(args[16], &held[2], &o.grad_scale, &l))
+            return nullptr;
+        c10::cuda::OptionalCUDAGuard guard;
+        if (l.device >= 0) guard.set_index((c10::DeviceIndex)l.device);
+        void* stream = args[17] == Py_None ? (void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)l.device).stream() : PyLong_AsVoidPtr(args[17]);
+        if (PyErr_Occurred()) return nullptr;
+        int rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = moe_adamw_step(l.count < 0 ? 0 : l.count, l.views(0), l.views(1), l.views(2), l.views(3), l.views(4), l.views(5), l.views(6), &o,
+                            stream);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLong(rc);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// grads (a list), out, max_norm, workspace, stream
+PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 5) {
+        PyErr_Format(PyExc_TypeError, "expected 5 arguments, got %zd", n);
+        return nullptr;
+    }
+    try {
+        Lists l;
+        if (!l.add(0, args[0])) return nullptr;
+        moe_tensor held;
+        const moe_tensor* out;
+        if (!number(args[1], &held, &out, &l)) return nullptr;
+        const double most = PyFloat_AsDouble(args[2]);
+        if (PyErr_Occurred()) return nullptr;
+        auto* workspace = static_cast<moe_scratch*>(PyLong_AsVoidPtr(args[3]));
+        if (PyErr_Occurred()) return nullptr;
+        c10::cuda::OptionalCUDAGuard guard;
+        if (l.device >= 0) guard.set_index((c10::DeviceIndex)l.device);
+        void* stream = args[4] == Py_None ? (void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)l.device).stream() : PyLong_AsVoidPtr(args[4]);
+        if (PyErr_Occurred()) return nullptr;
+        int rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = moe_grad_norm(l.count < 0 ? 0 : l.count, l.views(0), const_cast<moe_tensor*>(out), (float)most, workspace, stream);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLong(rc);
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 #define MOE_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"balance_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(balance_fwd)), METH_FASTCALL, nullptr},
@@ -204,6 +394,9 @@ PyMethodDef methods[] = {
     MOE_METHOD(select_fwd),
     MOE_METHOD(select_bwd),
     MOE_METHOD(bias_step),
+    MOE_METHOD(make_list),
+    MOE_METHOD(adamw_step),
+    MOE_METHOD(grad_norm),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

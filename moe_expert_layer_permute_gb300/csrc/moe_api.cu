@@ -12,6 +12,9 @@
 // The single call per direction and the GPU-only scratch in place of intermediate tensors follow
 // MarkTechPost, "Prime Intellect Releases Prime Mega MoE", section "How does the fused kernel
 // work?"; the shape rules follow ic.work analysis, section "算子下沉时代的硬件死锁暗礁".
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -691,6 +694,207 @@ int moe_router_bias_step(const moe_tensor* counts, moe_tensor* bias, float rate,
     if (B == 0) return MOE_OK;
     MOE_TRY_CUDA(launch_select_bias(reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const int*>(counts->data), (int)B,
                                     (int)E, reinterpret_cast<float*>(bias->data), rate));
+    return MOE_OK;
+}
+
+// ---- lists of tensors ----
+// Elements of a contiguous tensor of any shape, or -1 where it is none; alignment is checked where there are elements.
+static int check_listed(const moe_tensor& t, int dtype, size_t align, int64_t* n) {
+    if (t.ndim < 1 || t.ndim > 3) return MOE_ERR_SHAPE;
+    int64_t count = 1;
+    for (int i = 0; i < t.ndim; ++i) {
+        if (t.shape[i] < 0 || (t.shape[i] > 0 && count > ((int64_t)1 << 40) / t.shape[i])) return MOE_ERR_SHAPE;
+        count *= t.shape[i];
+    }
+    if (t.dtype != dtype) return MOE_ERR_DTYPE;
+    *n = count;
+    if (count == 0) return MOE_OK;
+    int64_t expect = 1;
+    for (int i = t.ndim - 1; i >= 0; --i) {
+        if (t.shape[i] > 1 && t.stride[i] != expect) return MOE_ERR_LAYOUT;
+        expect *= t.shape[i];
+    }
+    if (!t.data) return MOE_ERR_NULL;
+    return reinterpret_cast<uintptr_t>(t.data) % align ? MOE_ERR_ALIGN : MOE_OK;
+}
+static int check_gradient(const moe_tensor& t, ListTensor* out, int64_t* n) {
+    out->g_bf16 = t.dtype == MOE_DT_BF16;
+    out->g = t.data;
+    return check_listed(t, out->g_bf16 ? MOE_DT_BF16 : MOE_DT_F32, 16, n);
+}
+// one number of 4 bytes on the device, or null
+static int check_number(const moe_tensor* t, int dtype, const void** out) {
+    *out = nullptr;
+    if (!t) return MOE_OK;
+    int64_t n = 0;
+    const int rc = check_listed(*t, dtype, 4, &n);
+    if (rc) return rc;
+    if (n != 1) return MOE_ERR_SHAPE;
+    *out = t->data;
+    return MOE_OK;
+}
+// Whether an address stands among the tensors twice (empty ones aside): a table of twice their number, by open addressing.
+static int check_distinct(const moe_tensor* t, int64_t count) {
+    uintptr_t small[1024];
+    size_t size = 16;
+    while (size < 2 * (size_t)count) size *= 2;
+    uintptr_t* table = size <= 1024 ? small : static_cast<uintptr_t*>(malloc(size * sizeof(uintptr_t)));
+    if (!table) return MOE_ERR_CUDA;
+    memset(table, 0, size * sizeof(uintptr_t));
+    int rc = MOE_OK;
+    for (int64_t i = 0; i < count && !rc; ++i) {
+        bool empty = false;
+        for (int d = 0; d < t[i].ndim && d < 3; ++d) empty |= t[i].shape[d] == 0;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t[i].data);
+        if (empty || !p) continue;
+        size_t at = (p >> 4) * 0x9E3779B97F4A7C15ull >> 20 & (size - 1);
+        while (table[at] && table[at] != p) at = (at + 1) & (size - 1);
+        if (table[at] == p) rc = MOE_ERR_UNSUPPORTED;
+        table[at] = p;
+    }
+    if (table != small) free(table);
+    return rc;
+}
+constexpr int64_t kListCount = 65536;   // tensors of a call
+
+int moe_adamw_step(int64_t count, const moe_tensor* params, const moe_tensor* grads, const moe_tensor* m, const moe_tensor* v,
+                   const moe_tensor* m_scales, const moe_tensor* v_scales, const moe_tensor* copies,
+                   const moe_adamw_options* options, void* stream) {
+    if (!options) return MOE_ERR_NULL;
+    if (count < 0) return MOE_ERR_SHAPE;
+    if (count > kListCount) return MOE_ERR_UNSUPPORTED;
+    if (count > 0 && (!params || !grads || !m || !v)) return MOE_ERR_NULL;
+    const moe_adamw_options& o = *options;
+    if (!(o.lr >= 0.0 && o.lr <= 1e6) || !(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) ||
+        !(o.eps >= 1e-20 && o.eps <= 1.0) || !(o.weight_decay >= 0.0 && o.weight_decay <= 1e6))
+        return MOE_ERR_UNSUPPORTED;
+    if (!o.step_on_device && o.step < 1) return MOE_ERR_SHAPE;
+    AdamArgs a{};
+    int rc;
+    const void *lr_at, *step_at, *grad_scale;
+    if ((rc = check_number(o.lr_on_device, MOE_DT_F32, &lr_at))) return rc;
+    if ((rc = check_number(o.step_on_device, MOE_DT_I32, &step_at))) return rc;
+    if ((rc = check_number(o.grad_scale, MOE_DT_F32, &grad_scale))) return rc;
+    a.lr_at = reinterpret_cast<const float*>(lr_at);
+    a.step_at = reinterpret_cast<const int*>(step_at);
+    a.grad_scale = reinterpret_cast<const float*>(grad_scale);
+    if (count == 0) return MOE_OK;
+    const bool eight = m[0].dtype == MOE_DT_E4M3 || m[0].dtype == MOE_DT_U8;
+    if (eight && (!m_scales || !v_scales)) return MOE_ERR_NULL;
+    auto state = [&](const moe_tensor& t, int64_t* n) {
+        return check_listed(t, eight ? t.dtype == MOE_DT_U8 ? MOE_DT_U8 : MOE_DT_E4M3 : MOE_DT_F32, 16, n);
+    };
+    auto fill = [&](int64_t i, ListTensor* t) {
+        int64_t n = 0, other = 0;
+        int e;
+        if ((e = check_listed(params[i], MOE_DT_F32, 16, &n))) return e;
+        if ((e = check_gradient(grads[i], t, &other))) return e;
+        if (other != n) return MOE_ERR_SHAPE;
+        if ((e = state(m[i], &other))) return e;
+        if (other != n) return MOE_ERR_SHAPE;
+        if ((e = state(v[i], &other))) return e;
+        if (other != n) return MOE_ERR_SHAPE;
+        if (eight) {
+            const int64_t blocks = (n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK;
+            if ((e = check_listed(m_scales[i], MOE_DT_F32, 4, &other))) return e;
+            if (other != blocks) return MOE_ERR_SHAPE;
+            if ((e = check_listed(v_scales[i], MOE_DT_F32, 4, &other))) return e;
+            if (other != blocks) return MOE_ERR_SHAPE;
+            t->m_scale = reinterpret_cast<float*>(m_scales[i].data);
+            t->v_scale = reinterpret_cast<float*>(v_scales[i].data);
+        }
+        t->copy = nullptr;
+        if (copies) {
+            if ((e = check_listed(copies[i], MOE_DT_BF16, 16, &other))) return e;
+            if (other != n) return MOE_ERR_SHAPE;
+            t->copy = reinterpret_cast<__nv_bfloat16*>(copies[i].data);
+        }
+        t->p = reinterpret_cast<float*>(params[i].data);
+        t->m = m[i].data;
+        t->v = v[i].data;
+        t->n = n;
+        t->ordinal = (int)i;
+        return MOE_OK;
+    };
+    ListTensor list[kListMost];
+    // everything is looked at before anything is launched
+    for (int64_t i = 0; i < count; ++i)
+        if ((rc = fill(i, &list[i % kListMost]))) return rc;
+    if ((rc = check_distinct(params, count))) return rc;
+    const int nsm = num_sms_current();
+    if (nsm <= 0) return MOE_ERR_CUDA;
+    a.lr = (float)o.lr;
+    a.b1 = (float)o.beta1, a.c1 = (float)(1.0 - o.beta1);
+    a.b2 = (float)o.beta2, a.c2 = (float)(1.0 - o.beta2);
+    a.eps = (float)o.eps, a.decay = (float)o.weight_decay;
+    if (!a.step_at) {
+        a.fix1 = (float)(1.0 / (1.0 - pow(o.beta1, (double)o.step)));
+        a.fix2 = (float)(1.0 / sqrt(1.0 - pow(o.beta2, (double)o.step)));
+    } else {
+        a.log_b1 = (float)log(o.beta1), a.log_b2 = (float)log(o.beta2);
+    }
+    a.seed = (uint32_t)(o.seed ^ (o.seed >> 32));
+    for (int64_t first = 0; first < count; first += kListMost) {
+        const int n = (int)std::min<int64_t>(kListMost, count - first);
+        if (count > kListMost)
+            for (int i = 0; i < n; ++i) fill(first + i, &list[i]);
+        MOE_TRY_CUDA(launch_adamw(reinterpret_cast<cudaStream_t>(stream), list, n, eight, a, nsm));
+    }
+    return MOE_OK;
+}
+
+// the status word's line, the ticket's, a partial sum for each block of each launch
+static size_t norm_workspace(int64_t elements, int64_t count) {
+    const int64_t launches = (count + kListMost - 1) / kListMost;
+    const int64_t units = elements / 256 + count;
+    // (at most four blocks an SM and launch, of a GPU of up to 1024 SMs, and not more than a block for each unit)
+    return 512 + 8 * (size_t)std::min<int64_t>(launches * 4096, units + launches);
+}
+size_t moe_grad_norm_workspace_bytes(int64_t elements, int64_t count) {
+    if (elements < 0 || elements > ((int64_t)1 << 40) || count < 0 || count > kListCount) return 0;
+    return norm_workspace(elements, count);
+}
+
+int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float max_norm, moe_scratch* workspace, void* stream) {
+    if (count < 0) return MOE_ERR_SHAPE;
+    if (count > kListCount) return MOE_ERR_UNSUPPORTED;
+    if ((count > 0 && !grads) || !out) return MOE_ERR_NULL;
+    if (!(max_norm >= 0.f && max_norm <= 3e38f)) return MOE_ERR_UNSUPPORTED;
+    int rc;
+    int64_t n = 0, elements = 0;
+    if ((rc = check_listed(*out, MOE_DT_F32, 4, &n))) return rc;
+    if (n != 2) return MOE_ERR_SHAPE;
+    ListTensor list[kListMost] = {};
+    for (int64_t i = 0; i < count; ++i) {
+        if ((rc = check_gradient(grads[i], &list[i % kListMost], &n))) return rc;
+        list[i % kListMost].n = n;
+        elements += n;
+    }
+    if ((rc = check_workspace(workspace, norm_workspace(elements, count)))) return rc;
+    if (workspace->state[0] == 1) return MOE_ERR_STATE;   // moe_orthogonalise has left data there
+    const int nsm = num_sms_current();
+    if (nsm <= 0) return MOE_ERR_CUDA;
+    workspace->state[0] = 2;   // holds sums: moe_balance_fwd refuses it
+    NormArgs a{};
+    a.ticket = reinterpret_cast<int*>(reinterpret_cast<char*>(workspace->data) + 256);
+    a.partial = reinterpret_cast<double*>(reinterpret_cast<char*>(workspace->data) + 512);
+    a.most = max_norm;
+    a.out = reinterpret_cast<float*>(out->data);
+    auto part = [&](int64_t first) {
+        const int some = (int)std::min<int64_t>(kListMost, std::max<int64_t>(count - first, 0));
+        if (count > kListMost)
+            for (int i = 0; i < some; ++i) {
+                check_gradient(grads[first + i], &list[i], &n);
+                list[i].n = n;
+            }
+        return some;
+    };
+    for (int64_t first = 0; first == 0 || first < count; first += kListMost) a.blocks += norm_blocks(list, part(first), nsm);
+    for (int64_t first = 0; first == 0 || first < count; first += kListMost) {
+        const int some = part(first);
+        MOE_TRY_CUDA(launch_norm(reinterpret_cast<cudaStream_t>(stream), list, some, a, nsm));
+        a.first_block += norm_blocks(list, some, nsm);
+    }
     return MOE_OK;
 }
 

@@ -27,7 +27,7 @@
 
 namespace moe {
 
-constexpr int kSelWarps = 8;
+constexpr int kSelWarps = 4;
 
 __device__ __forceinline__ float sel_value(const SelectArgs& a, long long i) {
     return a.bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.logits) + i))
@@ -113,6 +113,43 @@ __device__ __forceinline__ float sel_segment_max(float v, int n) {
 // A pick as the forward keeps it: 0 for none, else bits of a key, the last of which hold low - e.
 __device__ __forceinline__ uint32_t sel_pick(int e, uint32_t low) { return 0xff000000u | (low - (uint32_t)e); }
 
+// e^y in 64 bits, to some 2^-52, for y in [-708, 708] (beyond it the ends' values): 2^n times the power series of what is
+// left of y, at most ln 2 / 2, whose term 14 is under 2^-57.  The code that follows runs for a few tokens of a thousand
+// and mostly waits for its own instructions, so it is kept short and out of line, its loops rolled (with the library's
+// exponential and quotient and the loops unrolled 16,384 x 256 in 8 groups took 19.5 us).
+__device__ __noinline__ double sel_exp64(double y) {
+    if (y > 708.0) y = 708.0;
+    if (y < -708.0) y = -708.0;   // (a NaN stays)
+    const double n = rint(y * 1.4426950408889634);
+    const double r = fma(n, -2.3190468138462996e-17, fma(n, -0.6931471805599453, y));
+    double p = 1.0 / 6227020800.0, f = 1.0 / 479001600.0;
+    p = fma(p, r, f);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return p * __hiloint2double((__double2int_rn(n) + 1023) << 20, 0);
+}
+// The score of logit x; a softmax's with the row's largest logit and 1 / sum.
+__device__ __forceinline__ double sel_score64(const SelectArgs& a, float x, double row_max, double inv_sum) {
+    const double z = sel_exp64(a.sigmoid ? -(double)x : (double)x - row_max);
+    if (!a.sigmoid) return z * inv_sum;
+    // 1 / (1 + z): from fp32's, or its exponent alone, by Newton's steps, each of which doubles the digits
+    const double d = 1.0 + z;
+    double q = d < 1e30 ? (double)rcp_approx((float)d) : 1.0 / d;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) q = fma(q, fma(-d, q, 1.0), q);
+    return q;
+}
+
 struct SelRoom {              // a warp's shared memory
     uint64_t sorted[32];
     int candidate[32];
@@ -123,18 +160,122 @@ struct SelToken {             // what the forward found out about a token
     uint32_t groups;          // bits of those that stay; 0: not known
 };
 
-// How far two distances from `top`, d and a smaller one, may come nearer: scores of at most `most`, what the index takes,
-// and the roundings of sums, of biases and of the distances themselves.
-__device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float d, float most) {
-    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (a.quantum + kSelSum) * d;
+// How far two sums may come nearer to each other than they are in fp32: scores of at most `most`, roundings of sums, biases
+// and distances from `top`, of which d is the larger; `quantum` is what the index has taken from d, if anything.
+__device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float d, float most, float quantum) {
+    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d;
+}
+
+// Every expert in 64 bits, their groups too: k rounds of the largest that is left.
+__device__ __noinline__ void select_all(const SelectArgs& a, long long t, uint32_t low, uint32_t* picks) {
+    const int lane = threadIdx.x & 31;
+    const unsigned all = 0xffffffffu;
+    const bool scores = a.bias || a.G > 1;
+    // keys of expert lane + 32 i (0: excluded, or taken)
+    uint64_t key[32];
+    const int rows = (a.E + 31) >> 5;
+    double top = -INFINITY, sum = 0.0;
+    if (!a.sigmoid && scores) {
+        bool nan = false;
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i)
+            if (lane + 32 * i < a.E) {
+                const float x = sel_value(a, t * a.E + lane + 32 * i);
+                nan |= isnan(x);
+                top = fmax(top, (double)x);
+            }
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(all, top, o));
+        if (__any_sync(all, nan)) top = NAN;
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i)
+            if (lane + 32 * i < a.E) sum += sel_exp64((double)sel_value(a, t * a.E + lane + 32 * i) - top);
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
+    }
+    const double inv = 1.0 / sum;
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = 0;
+        if (e >= a.E) continue;
+        const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
+        if (x == -INFINITY || b == -INFINITY) continue;
+        double c = (double)x;
+        if (scores) c = sel_score64(a, x, top, inv) + (double)b;
+        key[i] = sel_key64(c);
+    }
+    if (a.G > 1) {
+        uint64_t value = 0;   // of group `lane`
+#pragma unroll 1
+        for (int g = 0; g < a.G; ++g) {
+            uint64_t m1 = 0, m2 = 0;
+#pragma unroll 1
+            for (int i = 0; i < rows; ++i) {
+                const int e = lane + 32 * i;
+                if (e < g * a.gs || e >= (g + 1) * a.gs) continue;
+                const uint64_t v = key[i];
+                m2 = max(m2, min(m1, v));
+                m1 = max(m1, v);
+            }
+#pragma unroll 1
+            for (int o = 16; o; o >>= 1) {
+                const uint64_t o1 = __shfl_xor_sync(all, m1, o), o2 = __shfl_xor_sync(all, m2, o);
+                m2 = max(max(m2, o2), min(m1, o1));
+                m1 = max(m1, o1);
+            }
+            if (a.rank == 2 && m2) m1 = sel_key64(sel_unkey64(m1) + sel_unkey64(m2));
+            if (lane == g) value = m1;
+        }
+        int rank = 0;
+#pragma unroll 1
+        for (int g = 0; g < a.G; ++g) {
+            const uint64_t other = __shfl_sync(all, value, g);
+            rank += other > value || (other == value && g < lane);
+        }
+        const uint32_t kept = __ballot_sync(all, lane < a.G && value && rank < a.kept);
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.E && !((kept >> (e / a.gs)) & 1u)) key[i] = 0;
+        }
+    }
+    if (!a.bias && a.G > 1)
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i)
+            if (key[i]) key[i] = sel_key64((double)sel_value(a, t * a.E + lane + 32 * i));
+#pragma unroll 1
+    for (int r = 0; r < a.k; ++r) {
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        uint64_t top_key = best;
+        int e = lane + 32 * at;
+#pragma unroll 1
+        for (int o = 16; o; o >>= 1) {
+            const uint64_t ok = __shfl_xor_sync(all, top_key, o);
+            const int oe = __shfl_xor_sync(all, e, o);
+            if (ok > top_key || (ok == top_key && oe < e)) {
+                top_key = ok;
+                e = oe;
+            }
+        }
+        if (top_key && (e & 31) == lane) key[e >> 5] = 0;
+        if (lane == 0) picks[r] = top_key ? sel_pick(e, low) : 0u;
+    }
+    __syncwarp();
 }
 
 // open: bit j where picks j and j + 1 are too near each other.  The candidates are those from the first such pick on, as
 // far as their order is open (picks before and after them stand), and where the last pick is among them every expert
 // that may be; the fp32 sums in full decide where they are far enough apart, else sums in 64 bits (a softmax's over
 // its fp32 sum, whose error stands in both terms and so counts with their difference alone).  Where that is not enough
-// either, or there are more than 32, or nothing is known (0), all experts are gone through in 64 bits, their groups too:
-// k rounds of the largest that is left.
+// either, or there are more than 32, or nothing is known (0), all experts are gone through.
 __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint32_t open, const SelToken& token, float span,
                                           float top_bias, uint32_t low, uint32_t none, SelRoom* room, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
@@ -151,7 +292,8 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint
             const int mine = lane < a.k ? (int)(low - (picks[lane] & low)) : -1;
             // (every score is at most 1; a softmax's at most 1 / its sum)
             const float d = __uint_as_float(~next & ~low);
-            const float far = d + 2.f * sel_margin(a, token.top, d, a.sigmoid ? 1.f : inv_sum);
+            const float far = d + 2.f * sel_margin(a, token.top, d, a.sigmoid ? 1.f : inv_sum, a.quantum);
+#pragma unroll 1
             for (int i = 0; i < a.E && n <= 32; i += 32) {
                 const int e = i + lane;
                 bool in = false;
@@ -162,6 +304,7 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint
                     else
                         in = (sel_key(x) & ~low) >= (next & ~low);
                 }
+#pragma unroll 1
                 for (uint32_t votes = __ballot_sync(all, in); votes; votes &= votes - 1) {
                     const int it = i + __ffs(votes) - 1;
                     if (__any_sync(all, mine == it)) continue;
@@ -175,6 +318,7 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint
     if (n <= 32) {
         const int e = lane < n ? room->candidate[lane] : 0;
         const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
+#pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
             float s = 0.f;
             double s64 = 0.0;
@@ -185,11 +329,12 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint
                 s = a.sigmoid ? sel_sigmoid(x) : sel_exp(x - row_max) * inv_sum;
                 key = (uint64_t)sel_key(s + (b - top_bias)) << 32;
             } else {
-                s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)row_max) * (double)inv_sum;
+                s64 = sel_score64(a, x, (double)row_max, (double)inv_sum);
                 key = sel_key64(s64 + (double)b);
             }
             if (lane >= n) key = 0;
             int rank = 0;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const uint64_t other = __shfl_sync(all, key, i);
                 const int oe = __shfl_sync(all, e, i);
@@ -225,89 +370,7 @@ __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint
             __syncwarp();
         }
     }
-    // every expert: keys of expert lane + 32 i (0: excluded, or taken)
-    uint64_t key[32];
-    const int rows = (a.E + 31) >> 5;
-    double top = -INFINITY, sum = 0.0;
-    if (!a.sigmoid && scores) {
-        bool nan = false;
-        for (int i = 0; i < rows; ++i)
-            if (lane + 32 * i < a.E) {
-                const float x = sel_value(a, t * a.E + lane + 32 * i);
-                nan |= isnan(x);
-                top = fmax(top, (double)x);
-            }
-        for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(all, top, o));
-        if (__any_sync(all, nan)) top = NAN;
-        for (int i = 0; i < rows; ++i)
-            if (lane + 32 * i < a.E) sum += exp((double)sel_value(a, t * a.E + lane + 32 * i) - top);
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
-    }
-    for (int i = 0; i < rows; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = 0;
-        if (e >= a.E) continue;
-        const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
-        if (x == -INFINITY || b == -INFINITY) continue;
-        double c = (double)x;
-        if (scores) c = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / sum) + (double)b;
-        key[i] = sel_key64(c);
-    }
-    if (a.G > 1) {
-        uint64_t value = 0;   // of group `lane`
-        for (int g = 0; g < a.G; ++g) {
-            uint64_t m1 = 0, m2 = 0;
-            for (int i = 0; i < rows; ++i) {
-                const int e = lane + 32 * i;
-                if (e < g * a.gs || e >= (g + 1) * a.gs) continue;
-                const uint64_t v = key[i];
-                m2 = max(m2, min(m1, v));
-                m1 = max(m1, v);
-            }
-            for (int o = 16; o; o >>= 1) {
-                const uint64_t o1 = __shfl_xor_sync(all, m1, o), o2 = __shfl_xor_sync(all, m2, o);
-                m2 = max(max(m2, o2), min(m1, o1));
-                m1 = max(m1, o1);
-            }
-            if (a.rank == 2 && m2) m1 = sel_key64(sel_unkey64(m1) + sel_unkey64(m2));
-            if (lane == g) value = m1;
-        }
-        int rank = 0;
-        for (int g = 0; g < a.G; ++g) {
-            const uint64_t other = __shfl_sync(all, value, g);
-            rank += other > value || (other == value && g < lane);
-        }
-        const uint32_t kept = __ballot_sync(all, lane < a.G && value && rank < a.kept);
-        for (int i = 0; i < rows; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E && !((kept >> (e / a.gs)) & 1u)) key[i] = 0;
-        }
-    }
-    if (!a.bias && a.G > 1)
-        for (int i = 0; i < rows; ++i)
-            if (key[i]) key[i] = sel_key64((double)sel_value(a, t * a.E + lane + 32 * i));
-    for (int r = 0; r < a.k; ++r) {
-        uint64_t best = 0;
-        int at = 0;
-        for (int i = 0; i < rows; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        uint64_t top_key = best;
-        int e = lane + 32 * at;
-        for (int o = 16; o; o >>= 1) {
-            const uint64_t ok = __shfl_xor_sync(all, top_key, o);
-            const int oe = __shfl_xor_sync(all, e, o);
-            if (ok > top_key || (ok == top_key && oe < e)) {
-                top_key = ok;
-                e = oe;
-            }
-        }
-        if (top_key && (e & 31) == lane) key[e >> 5] = 0;
-        if (lane == 0) picks[r] = top_key ? sel_pick(e, low) : 0u;
-    }
-    __syncwarp();
+    select_all(a, t, low, picks);
 }
 
 // Groups of one token that are too near each other at the border: which of the contenders stay, `slots` of them, as a mask of
@@ -319,16 +382,18 @@ __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t,
     const unsigned all = 0xffffffffu;
     const int e = lane < n ? room->candidate[lane] : 0, g = lane < n ? e / a.gs : -1 - lane;
     const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
-    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)row_max) * (double)inv_sum;
+    const double s = sel_score64(a, x, (double)row_max, (double)inv_sum);
     const double c = s + (double)b;
     const uint64_t key = sel_key64(c);
     int place = 0;   // in its group
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         const uint64_t other = __shfl_sync(all, key, i);
         const int oe = __shfl_sync(all, e, i), og = __shfl_sync(all, g, i);
         place += og == g && (other > key || (other == key && oe < e));
     }
     double sum = 0.0, score = 0.0;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         const double oc = __shfl_sync(all, c, i), os = __shfl_sync(all, s, i);
         const int og = __shfl_sync(all, g, i), op = __shfl_sync(all, place, i);
@@ -339,6 +404,7 @@ __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t,
     }
     const bool first = lane < n && place == 0;
     int rank = 0;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         const double os = __shfl_sync(all, sum, i);
         const int og = __shfl_sync(all, g, i);
@@ -347,6 +413,7 @@ __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t,
     }
     bool near = false;
     if (!a.sigmoid)
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const double os = __shfl_sync(all, sum, i), oc = __shfl_sync(all, score, i);
             const bool stays = __shfl_sync(all, (int)(first && rank < slots), i);
@@ -359,11 +426,11 @@ __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t,
 // ---- forward ---------------------------------------------------------------------------------------------------
 // keys that a lane keeps in order: the k picks of a token fall on its W lanes, and a lane that has given all it kept looks
 // through its V keys again, which the whole warp waits for
-template <int W>
-constexpr int sel_kept() { return W == 32 ? 2 : W == 16 ? 3 : 4; }
+template <int W, int V>
+constexpr int sel_kept() { return W == 32 && V <= 16 ? 2 : W >= 16 ? 3 : 4; }
 
 template <int W, int V, bool VEC>
-__global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1) select_fwd_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2) select_fwd_kernel(const SelectArgs a) {
     grid_dep_wait();
     constexpr int NT = 32 / W;   // tokens of a warp
     extern __shared__ __align__(16) float sel_shared[];
@@ -585,7 +652,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1)
         }
         // the picks and the one after them
         {
-            constexpr int K = sel_kept<W>();
+            constexpr int K = sel_kept<W, V>();
             uint32_t n[K];
 #pragma unroll
             for (int j = 0; j < K; ++j) n[j] = 0u;
@@ -632,15 +699,15 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 4 : V == 32 ? 2 : 1)
             float xj = k0 ? sel_value(a, (first + tk) * a.E + e) : -INFINITY;
             bool near = false;
             if (scores) {
-                const float d0 = __uint_as_float(~k0 & ~low), d1 = __uint_as_float(~k1 & ~low);   // distances from the largest
-                const float most = a.sigmoid ? 1.f : sel_exp(xj - token.max) * token.inv + span;
-                near = k0 && k1 >= none && !(d1 - d0 > sel_margin(a, token.top, d1, most));
-                // (equal logits and biases inside are in the order of their index)
-                if (__any_sync(all, near && j + 1 < a.k)) {
-                    const float bj = a.bias && k0 ? biases[e] : 0.f;
-                    const float xn = __shfl_down_sync(all, xj, 1), bn = __shfl_down_sync(all, bj, 1);
-                    if (j + 1 < a.k && xj == xn && bj == bn) near = false;
-                }
+                // The sums of neighbours inside in full; the last pick's and the one behind it, of which there is the key.
+                // (Equal logits and biases inside are in the order of their index.)
+                const float bj = a.bias && k0 ? biases[e] : 0.f, sj = a.sigmoid ? sel_sigmoid(xj) : sel_exp(xj - token.max) * token.inv;
+                const float d0 = token.top - (sj + bj), xn = __shfl_down_sync(all, xj, 1), bn = __shfl_down_sync(all, bj, 1);
+                const float dn = __shfl_down_sync(all, d0, 1);
+                const bool inside = j + 1 < a.k;
+                const float d1 = inside ? dn : __uint_as_float(~k1 & ~low);
+                near = k0 && k1 >= none && !(inside && xj == xn && bj == bn) &&
+                       !(d1 - d0 > sel_margin(a, token.top, d1, a.sigmoid ? 1.f : sj + span, inside ? 0.f : a.quantum));
             } else if (!a.bf16) {
                 near = k0 && k1 >= none && ((k0 ^ k1) & ~low) == 0u;
                 // (equal ones inside too; at the end another, larger one may follow)
@@ -928,7 +995,7 @@ static cudaError_t select_c(cudaStream_t st, SelectArgs a, int num_sms) {
     const int per = 32 / pow2_at_least(a.k);
     a.batch = a.few ? NT : std::max(NT, per);
     const size_t smem = ((size_t)kSelWarps * a.batch * (a.k + 1) + (a.bias ? (a.E + 3) / 4 * 4 : 0)) * 4;   // at most 21 KB
-    const unsigned grid = sel_grid(a.T, kSelWarps * a.batch, V <= 16 ? 4 : V == 32 ? 2 : 1, num_sms);
+    const unsigned grid = sel_grid(a.T, kSelWarps * a.batch, V <= 16 ? 8 : V == 32 ? 4 : 2, num_sms);
     return launch_pdl(select_fwd_kernel<W, V, VEC>, grid, 32 * kSelWarps, smem, st, a);
 }
 template <int V, bool VEC>
