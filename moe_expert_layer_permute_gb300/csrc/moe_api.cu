@@ -700,6 +700,10 @@ int moe_router_bias_step(const moe_tensor* counts, moe_tensor* bias, float rate,
 // ---- lists of tensors ----
 // Elements of a contiguous tensor of any shape, or -1 where it is none; alignment is checked where there are elements.
 static int check_listed(const moe_tensor& t, int dtype, size_t align, int64_t* n) {
+    if (t.ndim == 1 && t.dtype == dtype && t.shape[0] > 0 && t.shape[0] <= (int64_t)1 << 40 && (t.stride[0] == 1 || t.shape[0] == 1) && t.data) {
+        *n = t.shape[0];   // (most of a list, and a list is long)
+        return reinterpret_cast<uintptr_t>(t.data) % align ? MOE_ERR_ALIGN : MOE_OK;
+    }
     if (t.ndim < 1 || t.ndim > 3) return MOE_ERR_SHAPE;
     int64_t count = 1;
     for (int i = 0; i < t.ndim; ++i) {
@@ -864,7 +868,7 @@ int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float
     int64_t n = 0, elements = 0;
     if ((rc = check_listed(*out, MOE_DT_F32, 4, &n))) return rc;
     if (n != 2) return MOE_ERR_SHAPE;
-    ListTensor list[kListMost] = {};
+    ListTensor list[kListMost];
     for (int64_t i = 0; i < count; ++i) {
         if ((rc = check_gradient(grads[i], &list[i % kListMost], &n))) return rc;
         list[i % kListMost].n = n;

@@ -151,10 +151,12 @@ def test_rounding_is_exact_in_the_mean(cuda_lib):
 
 
 def test_8_bit_states_follow_32_bit_ones(cuda_lib):
-    """v grows and falls with its gradients, as it could not by rounding to nearest.  After 3000 steps of gradients of
-    level 1 and 2000 of 0.25, sqrt(v) is the 32-bit one's within the rounding's spread: a step changes r by a rounding of
-    standard deviation at most q / 2, q <= r / 8, and v forgets with 0.999, so its relative variance stays under
-    2 (1/8)^2 / 4 / (2 x 0.001) x ... per value; the mean over 4096 values has 1/64 of its deviation."""
+    """v grows and falls with its gradients, as it could not by rounding to nearest (3000 steps of level 1, 2000 of 0.25).
+    Rounding leaves r's mean as it is and adds its variance q^2 f (1 - f) <= q d to v, q <= r / 8 a code's step and d how
+    far r has come from a code: r came from one, and v's decay, the gradient and the block's scale move it against the codes
+    by about 0.0005 r each in the mean, so v gains at most 0.0002 v a step where its memory is 0.001: 1 / (1 - 0.2) = 1.25
+    times v, and with r's own spread under 1.5.  The mean over 4096 values has 1.6 % of a value's deviation, which is under
+    its size: below 1 it may be by 5 %."""
     n = 4096
     g = torch.Generator(device="cuda").manual_seed(2)
     p = [torch.zeros(n, device="cuda") for _ in range(2)]
@@ -169,10 +171,9 @@ def test_8_bit_states_follow_32_bit_ones(cuda_lib):
             cuda_lib.moe_adamw_step([p[0]], [grad], [m], [v], step, lr=1e-4)
             cuda_lib.moe_adamw_step([p[1]], [grad], [m8], [v8], step, lr=1e-4, m_scales=[ms], v_scales=[vs], seed=step)
         r8, r = decode(v8, vs), v.sqrt().double().cpu()
-        # a rounding adds up to q^2 / 4 <= r^2 / 256 to the mean of v each step: 0.004 x 0.999 / 0.001 would be too much if q
-        # were an eighth throughout; it is r / 16 on average, and what is left shows as a factor under 2.5 in v
         ratio = float((r8 ** 2).mean() / (r ** 2).mean())
-        assert 0.9 < ratio < 2.5
+        print('level', level, 'v in 8 bits over v in 32:', ratio)
+        assert 0.95 < ratio < 1.5
 
 
 def test_noise_repeats_and_depends_on_the_seed_alone(cuda_lib):
