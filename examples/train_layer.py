@@ -1,7 +1,8 @@
 """Trains one MoE layer with its router: the layer's forward and backward, the router's balance loss,
-z-loss and gradient, and orthogonalised (Muon) updates of every weight.
+z-loss and gradient, and orthogonalised (Muon) updates of every weight; or, with --routing bias, sigmoid scores in
+groups of experts that a bias balances, with Muon for the experts and clipped AdamW for the router.
 
-    python examples/train_layer.py --steps 100
+    python examples/train_layer.py --steps 100 [--routing bias]
 
 The data are synthetic: tokens of packed sequences of uneven length with padding, and targets from a fixed
 layer of the same shape.  Each step
@@ -9,6 +10,9 @@ layer of the same shape.  Each step
     dy     = y - target        -> moe_bwd -> moe_balance_bwd (joins the top-k weights' gradient) -> dWr = dlogits^T x
     W     <- W - lr scale O(M)    M a momentum of the gradients, O its orthogonalised form (moe_orthogonalise),
                                   gate and up projections as matrices of their own
+and with --routing bias
+    logits -> moe_router_select_fwd (padded tokens get no pick) -> moe_fwd -> moe_bwd -> moe_router_select_bwd
+    bias follows the layer's counts (moe_router_bias_step), Wr by moe_grad_norm and moe_adamw_step (8-bit states)
 """
 import argparse
 import os
@@ -38,7 +42,27 @@ class Muon:
         self.weight.copy_(self.master)
 
 
-def train(steps=100, T=1024, H=256, I=128, E=8, k=2, lr=0.01, balance=0.01, z=1e-3, seed=0, log=print):
+class AdamW:
+    """fp32 weights with AdamW states in 8 bits, their gradients clipped together."""
+
+    def __init__(self, moe, weights, lr, clip=1.0, block=256):
+        dev = weights[0].device
+        self.moe, self.lr, self.clip, self.step_number = moe, lr, clip, 0
+        self.grads = [torch.zeros_like(w) for w in weights]
+        self.lists = [moe.TensorList(t) for t in (
+            weights, self.grads, *([torch.zeros_like(w, dtype=torch.float8_e4m3fn) for w in weights] for _ in range(2)))]
+        self.scales = [moe.TensorList([torch.zeros(-(-w.numel() // block), device=dev) for w in weights]) for _ in range(2)]
+        self.norm = torch.empty(2, device=dev)
+        self.workspace = moe.Workspace(moe.moe_grad_norm_workspace_bytes(sum(w.numel() for w in weights), len(weights)))
+
+    def step(self):
+        self.step_number += 1
+        self.moe.moe_grad_norm(self.lists[1], self.norm, self.workspace, max_norm=self.clip)
+        self.moe.moe_adamw_step(*self.lists, self.step_number, lr=self.lr, m_scales=self.scales[0], v_scales=self.scales[1],
+                                grad_scale=self.norm[1:], seed=self.step_number)
+
+
+def train(steps=100, T=1024, H=256, I=128, E=8, k=2, lr=0.01, balance=0.01, z=1e-3, seed=0, routing="balance", log=print):
     from moe_expert_layer_permute_gb300 import binding as moe
     dev = "cuda"
     g = torch.Generator(device=dev).manual_seed(seed)
@@ -71,18 +95,33 @@ def train(steps=100, T=1024, H=256, I=128, E=8, k=2, lr=0.01, balance=0.01, z=1e
     dx, dW13, dW2 = torch.empty_like(x), torch.empty_like(W13, dtype=torch.float32), torch.empty_like(W2, dtype=torch.float32)
     dw, dlogits = torch.empty(T, k, device=dev), torch.empty(T, E, device=dev)
     experts = [Muon(moe, W13, (2 * E, I, H), lr), Muon(moe, W2, (E, H, I), lr)]
-    router = Muon(moe, Wr, (1, E, H), lr)
+    by_bias = routing == "bias"
+    if by_bias:
+        rule = moe.RouterRule(score="sigmoid", groups=E // 2, topk_groups=max(1, E // 4), group_rank=2)
+        bias = torch.zeros(E, device=dev)
+        expert_counts = scratch.view(moe.MOE_VIEW_COUNTS, torch.int32, (1, E))
+    router = AdamW(moe, [Wr], lr) if by_bias else Muon(moe, Wr, (1, E, H), lr)
+    no_pick = moe.MOE_FLAG_NO_PICK if by_bias else 0
     history = []
     for step in range(steps):
         logits = x.float() @ Wr.t()
-        moe.moe_router_fwd(logits, idx, w)
+        if by_bias:
+            moe.moe_router_select_fwd(logits, idx, w, rule, bias=bias, mask=mask)
+        else:
+            moe.moe_router_fwd(logits, idx, w)
         moe.moe_balance_fwd(logits, idx, counts, tokens, losses, workspace, mask=mask, seg_offsets=offsets)
-        moe.moe_fwd(x, idx, w, W13, W2, y, scratch, flags=moe.MOE_FLAG_SAVE_GU)
+        moe.moe_fwd(x, idx, w, W13, W2, y, scratch, flags=moe.MOE_FLAG_SAVE_GU | no_pick)
         error = (y.float() - target.float()) * mask[:, None]
         dy = (error / mask.sum()).to(bf)
-        moe.moe_bwd(dy, x, idx, w, W13, W2, dx, dW13, dW2, dw, scratch, flags=moe.MOE_FLAG_REUSE_FWD)
-        moe.moe_balance_bwd(logits, idx, w, dw, counts, tokens, dloss, dlogits, mask=mask, seg_offsets=offsets)
-        router.step(dlogits.t() @ x.float())
+        moe.moe_bwd(dy, x, idx, w, W13, W2, dx, dW13, dW2, dw, scratch, flags=moe.MOE_FLAG_REUSE_FWD | no_pick)
+        if by_bias:
+            moe.moe_router_select_bwd(logits, idx, w, dw, dlogits, rule)
+            moe.moe_router_bias_step(expert_counts, bias, 1e-2)
+            torch.matmul(dlogits.t(), x.float(), out=router.grads[0])
+            router.step()
+        else:
+            moe.moe_balance_bwd(logits, idx, w, dw, counts, tokens, dloss, dlogits, mask=mask, seg_offsets=offsets)
+            router.step(dlogits.t() @ x.float())
         for weight, grad in zip(experts, (dW13, dW2)):
             weight.step(grad)
         scratch.epoch += 1                                          # the weights changed in place
@@ -101,7 +140,8 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=100)
     ap.add_argument("--seed", type=int, default=0)
+    ap.add_argument("--routing", choices=("balance", "bias"), default="balance")
     args = ap.parse_args()
     from moe_expert_layer_permute_gb300 import build
     build.build()
-    train(steps=args.steps, seed=args.seed)
+    train(steps=args.steps, seed=args.seed, routing=args.routing)

@@ -363,7 +363,7 @@ def moe_router_bias_step(counts, bias, rate: float, stream=None) -> None:
     """bias fp32 [E] += rate * sign(mean - n), n the sums of counts int32 [B, E] over B."""
     rc = (_MARSHAL or _marshal()).bias_step(counts, bias, rate, None if stream is None else _stream_ptr(stream))
     if rc:
-        raise MoeError(rc, "moe_router_bias_step", "moe_adamw_step", "moe_grad_norm_workspace_bytes", "moe_grad_norm")
+        raise MoeError(rc, "moe_router_bias_step")
 
 
 def moe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
