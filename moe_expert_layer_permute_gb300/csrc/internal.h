@@ -125,6 +125,7 @@ struct SelectArgs {
     float quantum;
     bool few;               // tokens: latency counts
     int batch;              // tokens that a warp takes at a time
+    int room;               // and that it puts off
 };
 cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms);
 struct SelectGradArgs {

@@ -28,7 +28,7 @@ def choose64(logits, k, score="softmax", G=1, kept=1, rank=1, renorm=True, scale
     """Picks and weights of each token: stable sorts in 64 bits, so that equal ones keep the order of their index."""
     T, E = logits.shape
     x = logits.double().cpu()
-    s = scores64(x, score)
+    s = scores64(x.cuda(), score).cpu()   # (the GPU's 64-bit exponential: sums that are equal but for its last bit are in no other order)
     b = torch.zeros(E, dtype=torch.float64) if bias is None else bias.double().cpu()
     above = lambda v: torch.where(v.isnan(), math.inf, v)  # noqa: E731  (NaN ranks highest; no test has infinities beside it)
     out = (x == -math.inf) | (b == -math.inf)
@@ -147,11 +147,38 @@ def test_sums_within_fp32_of_each_other(cuda_lib):
             if score == "softmax":
                 bias = (target - torch.softmax(logits[0].double(), 0)).float()
             check(cuda_lib, logits.cuda(), k, bias=bias.cuda(), score=score, G=G, kept=kept, rank=2)
+    # one that is larger behind equal ones, by less than fp32 or a key can tell, with and without a bias
+    x = torch.full((100, 64), 0.5)
+    x[torch.arange(100), torch.randint(0, 64, (100,), generator=g)] += 2.0 ** -24 * 2
+    x[torch.arange(100), torch.randint(0, 64, (100,), generator=g)] += 2.0 ** -24 * 4
+    for bias in (None, torch.full((64,), 0.25).cuda()):
+        check(cuda_lib, x.cuda(), 6, bias=bias, score="sigmoid")
+        check(cuda_lib, x.repeat(13, 1).cuda(), 6, bias=bias)
     # logits a last bit apart, without a bias
     base = torch.full((200, 96), 1.5)
     base += torch.randint(0, 5, (200, 96), generator=g) * 2.0 ** -23
     check(cuda_lib, base.cuda(), 7)
     check(cuda_lib, -base.cuda(), 7, score="sigmoid", G=8, kept=3, rank=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("rank,biased", [(1, False), (2, False), (1, True), (2, True)])
+def test_groups_within_fp32_of_each_other(cuda_lib, score, rank, biased):
+    """Sums of groups that fp32 cannot tell apart at the border, in few and in many tokens, groups with one expert or none left."""
+    g = torch.Generator().manual_seed(15)
+    for T, E, G, kept, k in [(200, 64, 8, 3, 5), (1300, 128, 8, 4, 8), (1300, 96, 12, 5, 6), (60, 1000, 20, 7, 9), (1300, 256, 4, 1, 4)]:
+        base = torch.randn(T, 1, E // G, generator=g).expand(T, G, E // G).reshape(T, E).clone()     # every group the same, in another order
+        order = torch.stack([torch.randperm(E // G, generator=g) + i * (E // G) for i in range(G)]).flatten()
+        logits = base[:, order]
+        logits[1::3] += 2e-7 * torch.randn(logits[1::3].shape, generator=g)
+        logits[2::3] += 1e-3 * torch.randn(logits[2::3].shape, generator=g)
+        bias = None
+        if biased:
+            bias = 0.25 * torch.randint(0, 2, (E,), generator=g).float()
+            bias[:E // G] = -math.inf
+            bias[0] = 0.25                                                                # one left in the first group
+            bias[E // G:2 * (E // G)] = -math.inf
+        check(cuda_lib, logits.cuda(), k, bias=None if bias is None else bias.cuda(), score=score, G=G, kept=kept, rank=rank)
 
 
 def test_saturated_scores(cuda_lib):
@@ -160,6 +187,8 @@ def test_saturated_scores(cuda_lib):
     x = 40 + 30 * torch.rand(100, 64, generator=g)
     check(cuda_lib, x.cuda(), 5, score="sigmoid")
     check(cuda_lib, x.cuda(), 5, score="sigmoid", bias=torch.zeros(64).cuda())
+    check(cuda_lib, x.cuda(), 5, score="sigmoid", G=8, kept=3, rank=2)          # groups tie, their experts do not
+    check(cuda_lib, x.cuda(), 5, score="sigmoid", G=8, kept=3, rank=1, bias=(0.25 * torch.randint(0, 2, (64,), generator=g)).cuda())
     # small scores keep their digits where weights are relative
     check(cuda_lib, (-60 - 20 * torch.rand(100, 64, generator=g)).cuda(), 5, score="sigmoid")
     check(cuda_lib, (30 * torch.randn(100, 64, generator=g)).cuda(), 5, score="softmax", bias=torch.zeros(64).cuda())
