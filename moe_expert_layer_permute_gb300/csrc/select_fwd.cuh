@@ -134,7 +134,9 @@ struct SelToken {             // what the forward found out about a token
     float max, inv;           // of the softmax: the largest logit and 1 / sum
     uint32_t groups;          // bits of those that stay
     int doubt;                // 1: whether it is these; 2: of everything (a NaN, an infinity)
+    int behind;               // picks after the last that were looked for too: 1, or 1 + kSelBehind where the first is near
 };
+constexpr int kSelBehind = 3;
 
 struct SelOpen {              // one that is to be gone through again
     int t;
@@ -259,7 +261,7 @@ static __device__ __noinline__ void select_all(const SelectArgs& a, long long t,
 // stands in both of two terms and so counts with their difference alone; where that is not enough, or there are more
 // than 32, all experts are gone through.
 static __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint32_t open, const SelToken& token, float top_bias,
-                                                 uint32_t low, SelRoom* room, uint32_t* picks) {
+                                                 uint32_t low, uint32_t none, SelRoom* room, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
     const unsigned all = 0xffffffffu;
     const int from = __ffs(open) - 1;
@@ -267,10 +269,17 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
     if (lane < n) room->candidate[lane] = (int)(low - (picks[from + lane] & low));
     if ((open >> (a.k - 1)) & 1u) {
         const uint32_t next = picks[a.k];
-        const int mine = lane < a.k ? (int)(low - (picks[lane] & low)) : -1;
         // (every score is at most 1; a softmax's at most 1 / its sum)
         const float d = __uint_as_float(~next & ~low);
         const float far = d + 2.f * sel_margin(a, token.top, d, a.sigmoid ? 1.f : token.inv, a.quantum);
+        const uint32_t it = lane < token.behind ? picks[a.k + lane] : 0u;
+        const bool may = it >= none && (a.bias ? __uint_as_float(~it & ~low) <= far : ((it ^ next) & ~low) == 0u);
+        const int count = __popc(__ballot_sync(all, may));
+        if (count < token.behind) {   // the last that was looked for is far enough, or there is none
+            if (may && n + lane < 32) room->candidate[n + lane] = (int)(low - (it & low));
+            n += count;
+        } else {
+        const int mine = lane < a.k ? (int)(low - (picks[lane] & low)) : -1;
 #pragma unroll 4
         for (int i = 0; i < a.E; i += 32) {
             const int e = i + lane;
@@ -287,6 +296,7 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
                 if (lane == 0 && n < 32) room->candidate[n] = it;
                 ++n;
             }
+        }
         }
     }
     __syncwarp();
@@ -473,9 +483,10 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
     const bool row = !a.sigmoid && (scores || !a.renorm);  // the softmax's sum is needed
     const uint32_t none = a.bias ? 0x80800000u : 0x00800000u;   // keys below it are no expert's
     float* biases = sel_shared;                            // less the largest
-    uint32_t* picks = reinterpret_cast<uint32_t*>(sel_shared + (a.bias ? (a.E + 3) / 4 * 4 : 0)) + warp * (a.batch + a.room) * (a.k + 1);
-    uint32_t* open_picks = picks + a.batch * (a.k + 1);
-    float* values = reinterpret_cast<float*>(picks + (kSelWarps - warp) * (a.batch + a.room) * (a.k + 1)) + warp * (a.batch + a.room) * 2 * a.G;
+    const int stride_k = a.k + 1 + kSelBehind;             // a token's picks and those behind them
+    uint32_t* picks = reinterpret_cast<uint32_t*>(sel_shared + (a.bias ? (a.E + 3) / 4 * 4 : 0)) + warp * (a.batch + a.room) * stride_k;
+    uint32_t* open_picks = picks + a.batch * stride_k;
+    float* values = reinterpret_cast<float*>(picks + (kSelWarps - warp) * (a.batch + a.room) * stride_k) + warp * (a.batch + a.room) * 2 * a.G;
     float* open_values = values + a.batch * 2 * a.G;       // (not there without groups)
     int kp = 1;                                            // lanes of a token where lanes take one pick each
     while (kp < a.k) kp *= 2;
@@ -715,13 +726,28 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                     v = min(was, v);
                 }
             }
-            if (gl == 0) tokens[warp][at_token] = {top, m, inv, groups, again ? 2 : doubt ? 1 : 0};
-            uint32_t* mine = picks + at_token * (a.k + 1);
+            uint32_t* mine = picks + at_token * stride_k;
+            uint32_t before = 0u;
+            int end = a.k;
 #pragma unroll 4
             for (int r = 0;; ++r) {
                 const uint32_t best = sel_max<W>(n[0]);
                 if (gl == 0) mine[r] = best;
-                if (r == a.k) break;
+                if (r == end) {
+                    // where the first that is left is too near the last pick, a few more, so that it is known which may
+                    // change places with it
+                    if (end != a.k) break;
+                    bool edge = best >= none;
+                    if (a.bias) {
+                        const float d = __uint_as_float(~best & ~low);
+                        edge = edge && !(d - __uint_as_float(~before & ~low) > sel_margin(a, top, d, a.sigmoid ? 1.f : inv, 3.f * a.quantum));
+                    } else {
+                        edge = edge && ((best ^ before) & ~low) == 0u;
+                    }
+                    if (!__any_sync(all, edge && (a.bias || !a.bf16))) break;
+                    end = a.k + kSelBehind;
+                }
+                before = best;
                 const bool won = n[0] == best;
 #pragma unroll
                 for (int j = 0; j + 1 < K; ++j) n[j] = won ? n[j + 1] : n[j];
@@ -733,6 +759,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                     if (n[0] == 0u && best) n[0] = best + below;
                 }
             }
+            if (gl == 0) tokens[warp][at_token] = {top, m, inv, groups, again ? 2 : doubt ? 1 : 0, 1 + end - a.k};
         }
     }
         __syncwarp();
@@ -740,7 +767,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
         for (int q = 0; q < a.batch; q += per) {
             const int tk = q + lane / kp, j = lane & (kp - 1);
             const bool on = tk < a.batch && first + tk < a.T && j < a.k;
-            const uint32_t* its = picks + tk * (a.k + 1) + j;
+            const uint32_t* its = picks + tk * stride_k + j;
             uint32_t k0 = on ? its[0] : 0u;
             const uint32_t k1 = on ? its[1] : 0u;
             const SelToken token = tokens[warp][tk & 31];
@@ -777,7 +804,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                     if (lane == 0) opens[warp][waiting] = {(int)(first + q + p), open, tokens[warp][q + p]};
                     if (tokens[warp][q + p].doubt == 1)
                         for (int r = lane; r < 2 * a.G; r += 32) open_values[waiting * 2 * a.G + r] = values[(q + p) * 2 * a.G + r];
-                    for (int r = lane; r <= a.k; r += 32) open_picks[waiting * (a.k + 1) + r] = picks[(q + p) * (a.k + 1) + r];
+                    for (int r = lane; r < stride_k; r += 32) open_picks[waiting * stride_k + r] = picks[(q + p) * stride_k + r];
                     ++waiting;
                 }
             }
@@ -787,19 +814,20 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
     }
     for (int i = 0; i < waiting; ++i) {
         SelOpen open = opens[warp][i];
-        uint32_t* its = open_picks + i * (a.k + 1);
+        uint32_t* its = open_picks + i * stride_k;
         bool lost = open.token.doubt == 2;
         if (open.token.doubt == 1) {
             const uint32_t groups = select_groups(a, open.t, open_values + i * 2 * a.G, open.token, span, top_bias, &rooms[warp]);
             lost = groups == 0u;
             if (!lost && groups != open.token.groups) {
                 open.token.groups = groups;
+                open.token.behind = 1;
                 const int pairs = min(a.k, select_picks(a, open.t, open.token, groups, top_bias, low, none, its) - 1);
                 open.open = pairs <= 0 ? 0u : pairs >= 32 ? ~0u : (1u << pairs) - 1u;
             }
         }
         if (lost) select_all(a, open.t, low, its);
-        else if (open.open) select_again(a, open.t, open.open, open.token, top_bias, low, &rooms[warp], its);
+        else if (open.open) select_again(a, open.t, open.open, open.token, top_bias, low, none, &rooms[warp], its);
         const int j = lane & (kp - 1);
         uint32_t pick = j < a.k ? its[j] : 0u;
         if (pick < none) pick = 0u;
@@ -834,7 +862,7 @@ static cudaError_t select_c(cudaStream_t st, SelectArgs a, int num_sms) {
     a.batch = a.few ? NT : std::max(NT, per);
     while (a.batch > NT && a.batch * a.G > 256) a.batch /= 2;
     a.room = std::max(8, a.batch);
-    const size_t words = (size_t)kSelWarps * (a.batch + a.room) * (a.k + 1 + (a.G > 1 ? 2 * a.G : 0));
+    const size_t words = (size_t)kSelWarps * (a.batch + a.room) * (a.k + 1 + kSelBehind + (a.G > 1 ? 2 * a.G : 0));
     const size_t smem = (words + (a.bias ? (a.E + 3) / 4 * 4 : 0)) * 4;   // at most 33 KB
     const unsigned grid = sel_grid(a.T, kSelWarps * a.batch, V <= 16 ? 8 : V == 32 ? 4 : 2, num_sms);
     return launch_pdl(select_fwd_kernel<W, V, KIND>, grid, 32 * kSelWarps, smem, st, a);
