@@ -14,86 +14,108 @@ extern template cudaError_t select_kind<kSelFull>(cudaStream_t, const SelectArgs
 //   sigmoid                 dl_j = w_j (dw_j - D / scale) (1 - s_j), without the D where weights are not renormalised
 //   softmax, renormalised   dl_j = w_j (dw_j - D / scale)
 //   softmax, not            dl_e = -s_e D, and + w_j dw_j at the picks
-// The first two touch the picks alone: a block keeps tiles of zeros in shared memory, puts a tile's picks in, sends it
+// The first two touch the picks alone: a warp keeps two tiles of zeros in shared memory, puts a tile's picks in, sends it
 // off as one bulk copy (tokens' rows follow one another) and takes the picks out again, so that a row costs k stores
-// and no instruction for its zeros.
-struct SelItem {
-    int e;
-    float d;
+// and no instruction for its zeros.  A tile's time is that of two loads, one after the other, and memory is kept busy by
+// the tiles of twelve and more warps an SM (131,072 x 512, k = 8: a block to a tile, with its barriers, took 68 us).
+struct SelItem {              // pick j of a token, over kp lanes of it
+    int e;                    // -1: none
+    float w, dw, x;
 };
-// pick j of token t (j over kp lanes of the token); D over the segment
-__device__ __forceinline__ SelItem sel_grad(const SelectGradArgs& a, long long t, int j, bool on, int kp) {
-    int e = -1;
-    float w = 0.f, dw = 0.f, keep = 1.f;
+__device__ __forceinline__ SelItem sel_pick_of(const SelectGradArgs& a, long long t, int j, bool on) {
+    SelItem g{-1, 0.f, 0.f, 0.f};
     if (on) {
-        e = __ldg(a.idx + t * a.k + j);
-        if ((unsigned)e >= (unsigned)a.E) e = -1;
+        g.e = __ldg(a.idx + t * a.k + j);
+        g.w = __ldg(a.w + t * a.k + j);
+        g.dw = __ldg(a.dw + t * a.k + j);
     }
-    if (e >= 0) {
-        w = __ldg(a.w + t * a.k + j);
-        dw = __ldg(a.dw + t * a.k + j);
-        if (a.sigmoid) {
-            const float x = a.bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.logits) + t * a.E + e))
-                                   : __ldg(static_cast<const float*>(a.logits) + t * a.E + e);
-            keep = 1.f / (1.f + expf(x));
-        }
-    }
-    const float D = a.renorm ? sel_segment_sum(w * dw, kp) * a.inv_scale : 0.f;
-    return {e, w * (dw - D) * keep};
+    return g;
+}
+__device__ __forceinline__ void sel_logit_of(const SelectGradArgs& a, long long t, SelItem& g) {
+    if ((unsigned)g.e >= (unsigned)a.E) g.e = -1;
+    if (g.e >= 0 && a.sigmoid)
+        g.x = a.bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(a.logits) + t * a.E + g.e))
+                     : __ldg(static_cast<const float*>(a.logits) + t * a.E + g.e);
+}
+__device__ __forceinline__ float sel_grad(const SelectGradArgs& a, SelItem g, int kp) {
+    if (g.e < 0) g.w = g.dw = 0.f;   // (whatever stands beside no pick)
+    const float D = a.renorm ? sel_segment_sum(g.w * g.dw, kp) * a.inv_scale : 0.f;
+    const float keep = a.sigmoid ? 1.f / (1.f + expf(g.x)) : 1.f;
+    return g.w * (g.dw - D) * keep;
 }
 
+constexpr int kSparseWarps = 4;
+
 template <bool BF>
-__global__ void __launch_bounds__(256) select_bwd_sparse_kernel(const SelectGradArgs a) {
+__global__ void __launch_bounds__(32 * kSparseWarps) select_bwd_sparse_kernel(const SelectGradArgs a) {
     grid_dep_wait();
+    using V = std::conditional_t<BF, __nv_bfloat16, float>;
     extern __shared__ __align__(128) unsigned char sel_tiles[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int es = BF ? 2 : 4;
-    const uint32_t tile_bytes = (uint32_t)a.tile * a.E * es;     // a multiple of 16
-    for (uint32_t i = threadIdx.x * 16; i < 2 * tile_bytes; i += 256 * 16)
-        *reinterpret_cast<uint4*>(sel_tiles + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    const uint32_t tile_bytes = (uint32_t)a.tile * a.E * sizeof(V);     // a multiple of 16
+    V* const tiles = reinterpret_cast<V*>(sel_tiles + warp * 2 * tile_bytes);
+    int* const spots = reinterpret_cast<int*>(sel_tiles + kSparseWarps * 2 * tile_bytes) + warp * 2 * a.tile * a.k;   // of the picks
     int kp = 1;
     while (kp < a.k) kp *= 2;
-    const int per = 32 / kp;
-    int slot = 0, used = 0;
-    for (long long tile = blockIdx.x; tile * a.tile < a.T; tile += gridDim.x, slot ^= 1, ++used) {
+    const int per = 32 / kp, j = lane & (kp - 1), mine = lane / kp;
+    const bool once = a.tile <= per;   // a lane has one pick of a tile: those of the next two are under way meanwhile
+    const long long stride = (long long)gridDim.x * kSparseWarps;
+    long long tile = (long long)blockIdx.x * kSparseWarps + warp;
+    auto token = [&](long long of, int tk) { return of * a.tile + tk; };
+    auto there = [&](long long of, int tk) { return tk < a.tile && j < a.k && token(of, tk) < a.T; };
+    SelItem now{}, next{};
+    if (once) {
+        now = sel_pick_of(a, token(tile, mine), j, there(tile, mine));
+        next = sel_pick_of(a, token(tile + stride, mine), j, there(tile + stride, mine));
+        sel_logit_of(a, token(tile, mine), now);
+    }
+    for (int n = 0; tile * a.tile < a.T; tile += stride, ++n) {
         const long long t0 = tile * a.tile;
-        const int tokens = (int)min((long long)a.tile, a.T - t0);
-        unsigned char* buf = sel_tiles + slot * tile_bytes;
-        if (used >= 2) {   // the copy of two tiles ago has been read; its picks go
-            if (threadIdx.x == 0) bulk_wait_read<1>();
-            __syncthreads();
-            const long long old = (tile - 2 * (long long)gridDim.x) * a.tile;
-            for (int i = threadIdx.x; i < a.tile * a.k; i += 256) {
-                const int e = __ldg(a.idx + old * a.k + i);
-                if ((unsigned)e < (unsigned)a.E) {
-                    const int at = i / a.k * a.E + e;
-                    if constexpr (BF) reinterpret_cast<__nv_bfloat16*>(buf)[at] = __float2bfloat16(0.f);
-                    else reinterpret_cast<float*>(buf)[at] = 0.f;
-                }
-            }
-            __syncthreads();
+        const int tokens = (int)min((long long)a.tile, a.T - t0), slot = n & 1;
+        V* const buf = tiles + slot * a.tile * a.E;
+        int* const spot = spots + slot * a.tile * a.k;
+        if (n < 2) {
+            for (uint32_t i = lane * 16; i < tile_bytes; i += 32 * 16)
+                *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(buf) + i) = make_uint4(0, 0, 0, 0);
+        } else {   // the copy of two tiles ago has been read; its picks go
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            for (int i = lane; i < a.tile * a.k; i += 32)
+                if (spot[i] >= 0) buf[spot[i]] = V(0.f);
         }
-        for (int q = warp * per; q < tokens; q += 8 * per) {
-            const int tk = q + lane / kp, j = lane & (kp - 1);
-            const SelItem g = sel_grad(a, t0 + tk, j, tk < tokens && j < a.k, kp);
-            if (g.e >= 0) {
-                if constexpr (BF) reinterpret_cast<__nv_bfloat16*>(buf)[tk * a.E + g.e] = __float2bfloat16(g.d);
-                else reinterpret_cast<float*>(buf)[tk * a.E + g.e] = g.d;
+        __syncwarp();
+        auto place = [&](const SelItem& g, int tk) {
+            const float d = sel_grad(a, g, kp);
+            const int at = g.e >= 0 ? tk * a.E + g.e : -1;
+            if (at >= 0) buf[at] = V(d);
+            if (tk < a.tile && j < a.k) spot[tk * a.k + j] = at;
+        };
+        if (once) {
+            sel_logit_of(a, token(tile + stride, mine), next);
+            const SelItem after = sel_pick_of(a, token(tile + 2 * stride, mine), j, there(tile + 2 * stride, mine));
+            place(now, mine);
+            now = next;
+            next = after;
+        } else {
+            for (int q = 0; q < a.tile; q += per) {
+                const int tk = q + mine;
+                SelItem g = sel_pick_of(a, token(tile, tk), j, there(tile, tk));
+                sel_logit_of(a, token(tile, tk), g);
+                place(g, tk);
             }
         }
         fence_proxy_async_cta();
-        __syncthreads();
-        unsigned char* out = static_cast<unsigned char*>(a.dlogits) + t0 * a.E * es;
-        const uint32_t bytes = (uint32_t)tokens * a.E * es, whole = bytes & ~15u;
-        if (threadIdx.x == 0 && whole) {
-            bulk_store(out, buf, whole);
+        __syncwarp();
+        unsigned char* out = static_cast<unsigned char*>(a.dlogits) + t0 * a.E * (long long)sizeof(V);
+        const uint32_t bytes = (uint32_t)tokens * a.E * sizeof(V), whole = bytes & ~15u;
+        if (lane == 0) {
+            if (whole) bulk_store(out, buf, whole);
             bulk_commit();
         }
-        if (threadIdx.x * 2 < bytes - whole)   // the last tile's end
-            reinterpret_cast<uint16_t*>(out + whole)[threadIdx.x] = reinterpret_cast<const uint16_t*>(buf + whole)[threadIdx.x];
+        if (lane * 2 < bytes - whole)   // the last tile's end
+            reinterpret_cast<uint16_t*>(out + whole)[lane] = reinterpret_cast<const uint16_t*>(reinterpret_cast<unsigned char*>(buf) + whole)[lane];
     }
-    if (threadIdx.x == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
 }
 
 // dlogits += the gradient where only picks have one
@@ -104,8 +126,10 @@ __global__ void __launch_bounds__(256) select_bwd_add_kernel(const SelectGradArg
     const int lane = threadIdx.x & 31, per = 32 / kp;
     const long long t = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * per + lane / kp;
     const int j = lane & (kp - 1);
-    const SelItem g = sel_grad(a, t, j, t < a.T && j < a.k, kp);
-    if (g.e >= 0) static_cast<float*>(a.dlogits)[t * a.E + g.e] += g.d;
+    SelItem g = sel_pick_of(a, t, j, t < a.T && j < a.k);
+    sel_logit_of(a, t, g);
+    const float d = sel_grad(a, g, kp);
+    if (g.e >= 0) static_cast<float*>(a.dlogits)[t * a.E + g.e] += d;
 }
 
 template <int W, int V, bool VEC>
@@ -278,10 +302,13 @@ cudaError_t launch_select_bwd(cudaStream_t st, SelectGradArgs a, int num_sms) {
         const int per = 8 * (32 / pow2_at_least(a.k));
         return launch_pdl(select_bwd_add_kernel, (unsigned)((a.T + per - 1) / per), 256, 0, st, a);
     }
-    // tokens of a tile: a multiple of 8, so that a tile is one of 16 bytes; 8 KB or 8 tokens
+    // Tokens of a tile: 4 (bf16: 8), so that a tile is a multiple of 16 bytes; as many as give each lane a pick; where rows are so
+    // short that this is under 2 KB, more, while each SM has eight tiles.
     const int es = a.out_bf16 ? 2 : 4;
-    a.tile = std::max(8, std::min(64, 8192 / (a.E * es) / 8 * 8));
-    const size_t smem = 2 * (size_t)a.tile * a.E * es;   // at most 64 KB
+    a.tile = std::max(a.out_bf16 ? 8 : 4, 32 / pow2_at_least(a.k));
+    while (a.tile > (a.out_bf16 ? 8 : 4) && a.tile * a.E * es > 8192) a.tile /= 2;
+    while (a.tile * a.E * es < 2048 && a.tile < 64 && (long long)a.T >= 16LL * a.tile * num_sms) a.tile *= 2;
+    const size_t smem = (size_t)kSparseWarps * 2 * a.tile * (a.E * es + 4 * a.k);   // at most 136 KB
     auto kern = a.out_bf16 ? select_bwd_sparse_kernel<true> : select_bwd_sparse_kernel<false>;
     static PerDevice<int> allowed[2];
     int dev = 0, done = 0;
@@ -289,10 +316,11 @@ cudaError_t launch_select_bwd(cudaStream_t st, SelectGradArgs a, int num_sms) {
     if (e != cudaSuccess) return e;
     e = allowed[a.out_bf16].get(dev, &done, [&](int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 140 * 1024);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, sel_grid(a.T, a.tile, smem > 32768 ? 3 : 6, num_sms), 256, smem, st, a);
+    const int blocks_sm = (int)std::max<size_t>(1, std::min<size_t>(8, 200 * 1024 / smem));
+    return launch_pdl(kern, sel_grid(a.T, a.tile * kSparseWarps, blocks_sm, num_sms), 32 * kSparseWarps, smem, st, a);
 }
 
 cudaError_t launch_select_bias(cudaStream_t st, const int* counts, int B, int E, float* bias, float rate) {
