@@ -59,17 +59,18 @@ __global__ void __launch_bounds__(32 * kSparseWarps) select_bwd_sparse_kernel(co
     while (kp < a.k) kp *= 2;
     const int per = 32 / kp, j = lane & (kp - 1), mine = lane / kp;
     const bool once = a.tile <= per;   // a lane has one pick of a tile: those of the next two are under way meanwhile
-    const long long stride = (long long)gridDim.x * kSparseWarps;
-    long long tile = (long long)blockIdx.x * kSparseWarps + warp;
+    // from the last tile to the first: the logits that a forward has read last may still be in L2
+    const long long stride = -(long long)gridDim.x * kSparseWarps;
+    long long tile = (a.T - 1) / a.tile - ((long long)blockIdx.x * kSparseWarps + warp);
     auto token = [&](long long of, int tk) { return of * a.tile + tk; };
-    auto there = [&](long long of, int tk) { return tk < a.tile && j < a.k && token(of, tk) < a.T; };
+    auto there = [&](long long of, int tk) { return of >= 0 && tk < a.tile && j < a.k && token(of, tk) < a.T; };
     SelItem now{}, next{};
     if (once) {
         now = sel_pick_of(a, token(tile, mine), j, there(tile, mine));
         next = sel_pick_of(a, token(tile + stride, mine), j, there(tile + stride, mine));
         sel_logit_of(a, token(tile, mine), now);
     }
-    for (int n = 0; tile * a.tile < a.T; tile += stride, ++n) {
+    for (int n = 0; tile >= 0; tile += stride, ++n) {
         const long long t0 = tile * a.tile;
         const int tokens = (int)min((long long)a.tile, a.T - t0), slot = n & 1;
         V* const buf = tiles + slot * a.tile * a.E;
