@@ -87,6 +87,11 @@ __device__ __forceinline__ float sel_max3(float a, float b, float c) {   // one 
 }
 template <int W>
 __device__ __forceinline__ float sel_max(float v) {
+    if constexpr (W == 32) {
+        float r;
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    }
 #pragma unroll
     for (int o = W / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
@@ -457,8 +462,12 @@ static __device__ __noinline__ int select_picks(const SelectArgs& a, long long t
 }
 
 // ---- forward ---------------------------------------------------------------------------------------------------
-// keys that a lane keeps in order: the k picks of a token fall on its W lanes, and a lane that has given all it kept looks
-// through its V keys again, which the whole warp waits for
+// Keys that a lane keeps in order.  The k picks of a token fall on its W lanes; a lane that has given all it kept looks
+// through its V keys again, which the whole warp waits for.  Of a token on a whole warp hardly a lane gives more than
+// three of up to 12 picks (7 % of tokens at k = 8), so there the rounds do without looking, a maximum and a step down in the
+// lane that held it, and are gone through again where that was wrong (131,072 x 512: 113 -> 110 us; with fewer lanes a
+// token more would have to be kept, and 16,384 x 128 takes 8.1 us instead of 6.9).
+constexpr int kSelOnce = 12, kSelOnceKept = 3;
 template <int W, int V>
 constexpr int sel_kept() { return W == 32 && V <= 16 ? 2 : W >= 16 ? 3 : 4; }
 
@@ -697,7 +706,8 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const uint32_t d = __float_as_uint(of - __uint_as_float(key[i]));
-                    key[i] = (~d & keep) | ((code0 - (uint32_t)place(i)) & low);
+                    const uint32_t code = code0 - (uint32_t)place(i);
+                    key[i] = FULL ? (~d & keep) | code : (~d & keep) | (code & low);
                 }
             } else {
                 if (a.bf16) load(std::true_type{}); else load(std::false_type{});   // (the scores took their place)
@@ -712,53 +722,65 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
         }
         // the picks and the one after them
         {
-            constexpr int K = sel_kept<W, V>();
-            uint32_t n[K];
-#pragma unroll
-            for (int j = 0; j < K; ++j) n[j] = 0u;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                uint32_t v = key[i];
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    const uint32_t was = n[j];
-                    n[j] = max(was, v);
-                    v = min(was, v);
-                }
-            }
             uint32_t* mine = picks + at_token * stride_k;
-            uint32_t before = 0u;
             int end = a.k;
-#pragma unroll 4
-            for (int r = 0;; ++r) {
-                const uint32_t best = sel_max<W>(n[0]);
-                if (gl == 0) mine[r] = best;
-                if (r == end) {
-                    // where the first that is left is too near the last pick, a few more, so that it is known which may
-                    // change places with it
-                    if (end != a.k) break;
-                    bool edge = best >= none;
-                    if (a.bias) {
-                        const float d = __uint_as_float(~best & ~low);
-                        edge = edge && !(d - __uint_as_float(~before & ~low) > sel_margin(a, top, d, a.sigmoid ? 1.f : inv, 3.f * a.quantum));
-                    } else {
-                        edge = edge && ((best ^ before) & ~low) == 0u;
+            auto rounds = [&](auto kept, auto look) {
+                constexpr int K = decltype(kept)::value;
+                constexpr bool LOOK = decltype(look)::value;
+                uint32_t n[K];
+#pragma unroll
+                for (int j = 0; j < K; ++j) n[j] = 0u;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    uint32_t v = key[i];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) {
+                        const uint32_t was = n[j];
+                        n[j] = max(was, v);
+                        if (j + 1 < K) v = min(was, v);
                     }
-                    if (!__any_sync(all, edge && (a.bias || !a.bf16))) break;
-                    end = a.k + kSelBehind;
                 }
-                before = best;
-                const bool won = n[0] == best;
+                const bool more = n[K - 1] != 0u;   // than it keeps, perhaps
+                uint32_t before = 0u;
+                end = a.k;
+#pragma unroll 4
+                for (int r = 0;; ++r) {
+                    const uint32_t best = sel_max<W>(n[0]);
+                    if (gl == 0) mine[r] = best;
+                    if (r == end) {
+                        // where the first that is left is too near the last pick, a few more, so that it is known which
+                        // may change places with it
+                        if (end != a.k) break;
+                        bool edge = best >= none;
+                        if (a.bias) {
+                            const float d = __uint_as_float(~best & ~low);
+                            edge = edge && !(d - __uint_as_float(~before & ~low) > sel_margin(a, top, d, a.sigmoid ? 1.f : inv, 3.f * a.quantum));
+                        } else {
+                            edge = edge && ((best ^ before) & ~low) == 0u;
+                        }
+                        if (!__any_sync(all, edge && (a.bias || !a.bf16))) break;
+                        end = a.k + kSelBehind;
+                    }
+                    before = best;
+                    const bool won = n[0] == best;
 #pragma unroll
-                for (int j = 0; j + 1 < K; ++j) n[j] = won ? n[j + 1] : n[j];
-                n[K - 1] = won ? 0u : n[K - 1];
-                if (__any_sync(all, n[0] == 0u)) {
-                    uint32_t below = 0u - best;   // (that of 0, which is below every key)
+                    for (int j = 0; j + 1 < K; ++j) n[j] = won ? n[j + 1] : n[j];
+                    n[K - 1] = won ? 0u : n[K - 1];
+                    if constexpr (LOOK) {
+                        if (__any_sync(all, n[0] == 0u)) {
+                            uint32_t below = 0u - best;   // (that of 0, which is below every key)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) below = max(below, key[i] - best);
-                    if (n[0] == 0u && best) n[0] = best + below;
+                            for (int i = 0; i < V; ++i) below = max(below, key[i] - best);
+                            if (n[0] == 0u && best) n[0] = best + below;
+                        }
+                    }
                 }
-            }
+                return !LOOK && __any_sync(all, more && n[0] == 0u);
+            };
+            bool again_looking = true;
+            if constexpr (W == 32 && V >= 16)   // (where tokens are few the code's own way to the SM counts)
+                again_looking = a.k > kSelOnce || rounds(std::integral_constant<int, kSelOnceKept>{}, std::false_type{});
+            if (again_looking) rounds(std::integral_constant<int, sel_kept<W, V>()>{}, std::true_type{});
             if (gl == 0) tokens[warp][at_token] = {top, m, inv, groups, again ? 2 : doubt ? 1 : 0, 1 + end - a.k};
         }
     }
