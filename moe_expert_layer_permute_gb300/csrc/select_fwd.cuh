@@ -796,19 +796,22 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             if (k0 < none) k0 = 0u;
             const int e = (int)(low - (k0 & low));
             const float xj = k0 ? sel_value(a, (first + tk) * a.E + e) : -INFINITY;
-            bool near = false, equal = false;
+            bool near = false, equal = false, chain = false;
             if (a.bias) {
                 // The sums of neighbours inside in full; the last pick's and the one behind it, of which there is the key.
                 // (Equal logits and biases inside are in the order of their index.)
                 const float bj = a.bias && k0 ? biases[e] : 0.f, sj = a.sigmoid ? sel_sigmoid(xj) : sel_exp(xj - token.max) * token.inv;
                 const float d0 = token.top - (sj + bj), xn = __shfl_down_sync(all, xj, 1), bn = __shfl_down_sync(all, bj, 1);
                 const float dn = __shfl_down_sync(all, d0, 1);
-                const bool inside = j + 1 < a.k;
-                const float d1 = inside ? dn : __uint_as_float(~k1 & ~low);
-                near = k0 && k1 >= none && !(d1 - d0 > sel_margin(a, token.top, d1, a.sigmoid ? 1.f : sj + span, inside ? 0.f : a.quantum));
+                const bool inside = j + 1 < a.k, both = k0 && k1 >= none;
+                const float t0 = __uint_as_float(~k0 & ~low), t1 = __uint_as_float(~k1 & ~low), d1 = inside ? dn : t1;
+                const float most = a.sigmoid ? 1.f : sj + span;
+                near = both && !(d1 - d0 > sel_margin(a, token.top, d1, most, inside ? 0.f : a.quantum));
                 equal = inside && xj == xn && bj == bn;
+                // (what is out of order may belong behind others whose keys are as near)
+                chain = both && !(t1 - t0 > sel_margin(a, token.top, t1, most, 2.f * a.quantum));
             } else if (!a.bf16) {
-                near = k0 && k1 >= none && ((k0 ^ k1) & ~low) == 0u;
+                near = chain = k0 && k1 >= none && ((k0 ^ k1) & ~low) == 0u;
                 // (equal ones inside too; at the end another, larger one may follow)
                 const float xn = __shfl_down_sync(all, xj, 1);
                 equal = j + 1 < a.k && xj == xn;
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             const bool unknown = on && token.doubt != 0;
             bool waits = false;
             if (__any_sync(all, (near && !equal) || unknown)) {
-                const uint32_t unequal = __ballot_sync(all, near && !equal), votes = __ballot_sync(all, near), lost = __ballot_sync(all, unknown);
+                const uint32_t unequal = __ballot_sync(all, near && !equal), votes = __ballot_sync(all, near || chain), lost = __ballot_sync(all, unknown);
                 for (int p = 0; p < per; ++p) {
                     const uint32_t segment = kp == 32 ? ~0u : (1u << kp) - 1u;
                     // (equal neighbours alone are in order, but what follows them may belong before both)

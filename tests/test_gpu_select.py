@@ -290,6 +290,22 @@ def test_accumulate_joins_the_balance_loss(cuda_lib):
         assert ((both.double() - there.double() - d.double()).abs() <= 2 ** -23 * (there.abs() + d.abs() + both.abs())).all()
 
 
+@pytest.mark.parametrize("E,G,kept,k", [(500, 1, 1, 30), (999, 3, 2, 31), (256, 8, 4, 8), (64, 1, 1, 17), (1024, 1, 1, 12), (512, 1, 1, 9)])
+@pytest.mark.parametrize("score,biased", list(itertools.product(["softmax", "sigmoid"], [False, True])))
+def test_dense_sums(cuda_lib, E, G, kept, k, score, biased):
+    """Scores so close together that most tokens have several within what a key holds, in no order of their index."""
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    for T, width in ((3000, 0.02), (3000, 0.002), (900, 0.01)):
+        logits = 1 + width * torch.randn(T, E, generator=g, device="cuda")
+        bias = None
+        if biased:   # against the scores' own spread
+            bias = width * (0.2 if score == "sigmoid" else 1.0 / E) * torch.randn(E, generator=g, device="cuda")
+        idx, w = run(cuda_lib, logits, k, bias=bias, score=score, G=G, kept=kept, rank=2)
+        ri, rw = choose64(logits, k, bias=bias, score=score, G=G, kept=kept, rank=2)
+        assert torch.equal(idx.cpu().long(), ri)
+        assert ((w.cpu().double() - rw).abs() <= W_REL * rw).all()
+
+
 def test_long_batches_and_many_blocks(cuda_lib):
     """More tokens than one wave of blocks, against the plain order in 64 bits on the GPU."""
     g = torch.Generator(device="cuda").manual_seed(11)
