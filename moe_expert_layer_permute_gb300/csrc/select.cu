@@ -39,7 +39,16 @@ __device__ __forceinline__ void sel_logit_of(const SelectGradArgs& a, long long 
 }
 __device__ __forceinline__ float sel_grad(const SelectGradArgs& a, SelItem g, int kp) {
     if (g.e < 0) g.w = g.dw = 0.f;   // (whatever stands beside no pick)
-    const float D = a.renorm ? sel_segment_sum(g.w * g.dw, kp) * a.inv_scale : 0.f;
+    float D = 0.f;
+    if (a.renorm) {
+        // less the heaviest pick's dw throughout, which the weights' sum of `scale` leaves as it was: a token of which one
+        // pick has nearly all the weight keeps the digits of what is left
+        const int first = (threadIdx.x & 31) & ~(kp - 1);
+        const uint32_t heaviest = __ballot_sync(0xffffffffu, g.w == sel_segment_max(g.w, kp)) >> first;
+        const float dw0 = __shfl_sync(0xffffffffu, g.dw, first + (heaviest ? __ffs(heaviest) - 1 : 0) % kp);
+        if (g.e >= 0) g.dw -= dw0;
+        D = sel_segment_sum(g.w * g.dw, kp) * a.inv_scale;
+    }
     const float keep = a.sigmoid ? 1.f / (1.f + expf(g.x)) : 1.f;
     return g.w * (g.dw - D) * keep;
 }

@@ -136,6 +136,7 @@ struct SelRoom {              // a warp's shared memory
 };
 struct SelToken {             // what the forward found out about a token
     float top;                // its largest c, less the largest bias
+    float last;               // what 64 bits may round from a sum with that bias back in
     float max, inv;           // of the softmax: the largest logit and 1 / sum
     uint32_t groups;          // bits of those that stay
     int doubt;                // 1: whether it is these; 2: of everything (a NaN, an infinity)
@@ -150,9 +151,10 @@ struct SelOpen {              // one that is to be gone through again
 };
 
 // How far two sums may come nearer to each other than they are in fp32: scores of at most `most`, roundings of sums, biases
-// and distances from `top`, of which d is the larger; `quantum` is what the index has taken from d, if anything.
-__device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float d, float most, float quantum) {
-    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d;
+// and distances from `top`, of which d is the larger; `last` is what sums in 64 bits, which are what counts, lose; `quantum`
+// is what the index has taken from d, if anything.
+__device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float last, float d, float most, float quantum) {
+    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d + last;
 }
 
 // Every expert in 64 bits, their groups too: k rounds of the largest that is left.
@@ -276,7 +278,7 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
         const uint32_t next = picks[a.k];
         // (every score is at most 1; a softmax's at most 1 / its sum)
         const float d = __uint_as_float(~next & ~low);
-        const float far = d + 2.f * sel_margin(a, token.top, d, a.sigmoid ? 1.f : token.inv, a.quantum);
+        const float far = d + 2.f * sel_margin(a, token.top, token.last, d, a.sigmoid ? 1.f : token.inv, a.quantum);
         const uint32_t it = lane < token.behind ? picks[a.k + lane] : 0u;
         const bool may = it >= none && (a.bias ? __uint_as_float(~it & ~low) <= far : ((it ^ next) & ~low) == 0u);
         const int count = __popc(__ballot_sync(all, may));
@@ -336,7 +338,7 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
 // sum in size, with a score of at most |top| + span.
 __device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float span, float top_bias, float v, float w) {
     return 4.f * sel_error(a.sigmoid, fabsf(top) + span) +
-           2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (a.rank == 2 ? fabsf(top_bias) : 0.f));
+           2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (a.rank == 2 ? fabsf(top_bias) : 0.f)) + 4e-15f * fabsf(top_bias);
 }
 
 // A token whose groups at the border are too near each other: which stay, from the sums in 64 bits of those alone that may.
@@ -357,7 +359,8 @@ static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long 
     const bool stays = rank < a.kept && vk != 0u;
     const float lv = sel_unkey(~__reduce_max_sync(all, stays ? ~vk : 0u)), mv = sel_unkey(__reduce_max_sync(all, stays ? 0u : vk));
     const float e2 = 2.f * sel_group_margin(a, token.top, span, top_bias, lv, mv);
-    const uint32_t sure = __ballot_sync(all, vk != 0u && value > lv + e2), open = __ballot_sync(all, vk != 0u && fabsf(value - lv) <= e2);
+    const float over = value - lv;   // (one difference for both, so that none falls between them)
+    const uint32_t sure = __ballot_sync(all, vk != 0u && over > e2), open = __ballot_sync(all, vk != 0u && !(over > e2) && over >= -e2);
     int n = 0;
 #pragma unroll 1
     for (uint32_t rest = open; rest; rest &= rest - 1) {
@@ -433,7 +436,7 @@ static __device__ __noinline__ int select_picks(const SelectArgs& a, long long t
                                                 uint32_t none, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
     const unsigned all = 0xffffffffu;
-    uint32_t last = 0xffffffffu;
+    uint32_t last = 0u;
     int count = 0;
 #pragma unroll 1
     for (int r = 0; r <= a.k; ++r) {
@@ -450,7 +453,7 @@ static __device__ __noinline__ int select_picks(const SelectArgs& a, long long t
                 key = sel_key(x);
             }
             key = (key & ~low) | (low - (uint32_t)e);
-            if (key < last) best = max(best, key);
+            if (r == 0 || key < last) best = max(best, key);   // (expert 0 as the largest has every bit set)
         }
         last = __reduce_max_sync(all, best);
         if (lane == 0) picks[r] = last;
@@ -533,6 +536,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
         for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) biases[e] -= top_bias;
         odd_bias = __syncthreads_or(odd_bias);
     }
+    const float last = 1e-15f * fabsf(top_bias);
     auto place = [&](int i) { return VEC ? 4 * (lp + lpg * (i >> 2)) + (i & 3) : lp + lpg * i; };
     const int e0 = group * a.gs;
     const int held = group < a.G ? a.gs : 0;               // places below it hold experts
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                         bool edge = best >= none;
                         if (a.bias) {
                             const float d = __uint_as_float(~best & ~low);
-                            edge = edge && !(d - __uint_as_float(~before & ~low) > sel_margin(a, top, d, a.sigmoid ? 1.f : inv, 3.f * a.quantum));
+                            edge = edge && !(d - __uint_as_float(~before & ~low) > sel_margin(a, top, last, d, a.sigmoid ? 1.f : inv, 3.f * a.quantum));
                         } else {
                             edge = edge && ((best ^ before) & ~low) == 0u;
                         }
@@ -781,7 +785,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             if constexpr (W == 32 && V >= 16)   // (where tokens are few the code's own way to the SM counts)
                 again_looking = a.k > kSelOnce || rounds(std::integral_constant<int, kSelOnceKept>{}, std::false_type{});
             if (again_looking) rounds(std::integral_constant<int, sel_kept<W, V>()>{}, std::true_type{});
-            if (gl == 0) tokens[warp][at_token] = {top, m, inv, groups, again ? 2 : doubt ? 1 : 0, 1 + end - a.k};
+            if (gl == 0) tokens[warp][at_token] = {top, last, m, inv, groups, again ? 2 : doubt ? 1 : 0, 1 + end - a.k};
         }
     }
         __syncwarp();
@@ -806,10 +810,10 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 const bool inside = j + 1 < a.k, both = k0 && k1 >= none;
                 const float t0 = __uint_as_float(~k0 & ~low), t1 = __uint_as_float(~k1 & ~low), d1 = inside ? dn : t1;
                 const float most = a.sigmoid ? 1.f : sj + span;
-                near = both && !(d1 - d0 > sel_margin(a, token.top, d1, most, inside ? 0.f : a.quantum));
+                near = both && !(d1 - d0 > sel_margin(a, token.top, last, d1, most, inside ? 0.f : a.quantum));
                 equal = inside && xj == xn && bj == bn;
                 // (what is out of order may belong behind others whose keys are as near)
-                chain = both && !(t1 - t0 > sel_margin(a, token.top, t1, most, 2.f * a.quantum));
+                chain = both && !(t1 - t0 > sel_margin(a, token.top, last, t1, most, 2.f * a.quantum));
             } else if (!a.bf16) {
                 near = chain = k0 && k1 >= none && ((k0 ^ k1) & ~low) == 0u;
                 // (equal ones inside too; at the end another, larger one may follow)

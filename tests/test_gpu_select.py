@@ -181,6 +181,16 @@ def test_groups_within_fp32_of_each_other(cuda_lib, score, rank, biased):
         check(cuda_lib, logits.cuda(), k, bias=None if bias is None else bias.cuda(), score=score, G=G, kept=kept, rank=rank)
 
 
+def test_sums_that_a_large_bias_makes_equal(cuda_lib):
+    """s + b in 64 bits loses what s has under 2^-50 of b: such sums are equal, and the lower index comes first, groups too."""
+    g = torch.Generator().manual_seed(16)
+    for T, E, G, kept, k in [(300, 6, 6, 2, 1), (300, 32, 32, 7, 7), (1500, 12, 4, 2, 5), (1500, 64, 1, 1, 6), (100, 13, 13, 4, 4)]:
+        logits = -30 + 0.003 * torch.randn(T, E, generator=g)
+        logits[::3, E // 2] = 40.0
+        for b in (7.25, 0.0):
+            check(cuda_lib, logits.cuda(), k, bias=torch.full((E,), b).cuda(), score="sigmoid", G=G, kept=kept, rank=2, renorm=False)
+
+
 def test_saturated_scores(cuda_lib):
     """Logits so large that scores are 1 in 64 bits: ordered by the logits without a bias, equal with one."""
     g = torch.Generator().manual_seed(6)
@@ -290,12 +300,12 @@ def test_accumulate_joins_the_balance_loss(cuda_lib):
         assert ((both.double() - there.double() - d.double()).abs() <= 2 ** -23 * (there.abs() + d.abs() + both.abs())).all()
 
 
-@pytest.mark.parametrize("E,G,kept,k", [(500, 1, 1, 30), (999, 3, 2, 31), (256, 8, 4, 8), (64, 1, 1, 17), (1024, 1, 1, 12), (512, 1, 1, 9)])
+@pytest.mark.parametrize("E,G,kept,k", [(500, 1, 1, 30), (999, 3, 2, 31), (256, 8, 4, 8), (201, 3, 2, 2), (13, 13, 11, 10), (40, 8, 2, 8), (64, 1, 1, 17), (1024, 1, 1, 12), (512, 1, 1, 9)])
 @pytest.mark.parametrize("score,biased", list(itertools.product(["softmax", "sigmoid"], [False, True])))
 def test_dense_sums(cuda_lib, E, G, kept, k, score, biased):
     """Scores so close together that most tokens have several within what a key holds, in no order of their index."""
     g = torch.Generator(device="cuda").manual_seed(E + k)
-    for T, width in ((3000, 0.02), (3000, 0.002), (900, 0.01)):
+    for T, width in ((3000, 0.02), (3000, 0.002), (900, 0.01), (20000, 0.003)):
         logits = 1 + width * torch.randn(T, E, generator=g, device="cuda")
         bias = None
         if biased:   # against the scores' own spread
