@@ -18,6 +18,10 @@
 // p + max_i(key_i - p) modulo 2^32, two instructions a value (three and a half with a mark and a search).  What the
 // index takes from c (7 bits at 128 experts) is part of the error above; it is small where the numbers are, so c is taken
 // relative to the largest bias and then to the row's largest c.
+//
+// Bound by instruction issue: 131,072 x 512 (sigmoid, bias, k = 8) takes 110 us, 740 instructions a token at three quarters
+// of the issue slots, where its logits take 42 us to read; 16,384 x 256 in 8 groups 18.7 us, of which about 5 are the tail
+// that a token gone through again leaves (3 us each, most of it waiting for code and 64-bit arithmetic).
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -336,9 +340,10 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
 
 // How far two groups' sums may come nearer to each other than they are in fp32: of two terms each, each at most 2 |top| and the
 // sum in size, with a score of at most |top| + span.
-__device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float span, float top_bias, float v, float w) {
+// partial: a group of one expert has the largest bias taken off its sum once more, which rounds.
+__device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float span, float top_bias, bool partial, float v, float w) {
     return 4.f * sel_error(a.sigmoid, fabsf(top) + span) +
-           2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (a.rank == 2 ? fabsf(top_bias) : 0.f)) + 4e-15f * fabsf(top_bias);
+           2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (partial ? fabsf(top_bias) : 0.f)) + 4e-15f * fabsf(top_bias);
 }
 
 // A token whose groups at the border are too near each other: which stay, from the sums in 64 bits of those alone that may.
@@ -358,7 +363,7 @@ static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long 
     }
     const bool stays = rank < a.kept && vk != 0u;
     const float lv = sel_unkey(~__reduce_max_sync(all, stays ? ~vk : 0u)), mv = sel_unkey(__reduce_max_sync(all, stays ? 0u : vk));
-    const float e2 = 2.f * sel_group_margin(a, token.top, span, top_bias, lv, mv);
+    const float e2 = 2.f * sel_group_margin(a, token.top, span, top_bias, a.rank == 2, lv, mv);
     const float over = value - lv;   // (one difference for both, so that none falls between them)
     const uint32_t sure = __ballot_sync(all, vk != 0u && over > e2), open = __ballot_sync(all, vk != 0u && !(over > e2) && over >= -e2);
     int n = 0;
@@ -693,7 +698,8 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 // the least that stays and the largest that does not (0: only excluded ones)
                 const uint32_t least = ~sel_max<W>(stays ? ~vk : 0u), most = sel_max<W>(stays || group >= a.G ? 0u : vk);
                 const float lv = sel_unkey(least), mv = sel_unkey(most);
-                const float err = sel_group_margin(a, top, span, top_bias, lv, mv);
+                const bool partial = a.rank == 2 && __any_sync(all, m1 != -INFINITY && m2 == -INFINITY);
+                const float err = sel_group_margin(a, top, span, top_bias, partial, lv, mv);
                 doubt = live && most != 0u && !(lv - mv > err);
                 if (__any_sync(all, doubt) && lp == 0 && group < a.G) {   // (for select_groups)
                     values[at_token * 2 * a.G + group] = value;
