@@ -266,7 +266,7 @@ int moe_router_bias_step(const moe_tensor* counts, moe_tensor* bias, float rate,
  *   moe_balance_workspace_bytes(T, E, B) bytes, 256-byte aligned, which the caller has set to zero once
  *   (every call leaves zeros, so calls of any sizes may follow; seg_offsets that descend may not, and the
  *   buffer has to be zeroed again); its desc is not read.  MOE_ERR_STATE for one that moe_orthogonalise
- *   has used.
+ *   or moe_grad_norm has used.
  * moe_balance_bwd: dlogits fp32 [T, E] (overwritten) of sum_s dloss[s] . loss[s], counts taken as
  *   constants, plus, with topk_w and dtopk_w (both or neither), what moe_router_bwd gives for them, in
  *   the same pass:

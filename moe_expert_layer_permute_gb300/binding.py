@@ -2,7 +2,7 @@
 
 Argument marshalling only: torch tensors become `moe_tensor` views (device pointer, dtype,
 shape, strides), the current torch CUDA stream becomes the `stream` argument, and every step of
-the layer runs in the CUDA library.  The balance loss and the orthogonalisation marshal in C++
+the layer runs in the CUDA library.  The balance loss, the orthogonalisation, the routing by scores and AdamW marshal in C++
 (`csrc/marshal.cpp`), since their smallest calls take a few microseconds.  The library is loaded on
 import, the compiled marshalling by the first call that wants it; if they have not been built, that raises
 (there is no fallback).
@@ -231,9 +231,9 @@ class Scratch:
 
 
 class Workspace:
-    """A caller-owned device buffer and its C handle for moe_balance_fwd and moe_orthogonalise (their
+    """A caller-owned device buffer and its C handle for moe_balance_fwd, moe_orthogonalise and moe_grad_norm (their
     *_workspace_bytes); moe_read_device_status takes it as it takes a Scratch.  One that moe_orthogonalise
-    has used is no longer zero, and moe_balance_fwd refuses it."""
+    has used is no longer zero, and moe_balance_fwd and moe_grad_norm refuse it; moe_balance_fwd refuses one of moe_grad_norm too."""
 
     def __init__(self, nbytes: int, device="cuda"):
         if nbytes <= 0:

@@ -3,8 +3,8 @@
 Each translation unit under `csrc/` is compiled in parallel, then linked into one shared library
 with the CUDA runtime linked statically (the library needs no libcuda at load time: the driver
 entry point for tensor-map encoding is looked up at run time).  Beside it `_marshal.so`, a Python
-module that turns torch tensors into the library's arguments for the balance loss and the
-orthogonalisation, from `csrc/marshal.cpp` with the host compiler and Python's and torch's headers; where
+module that turns torch tensors into the library's arguments for the balance loss, the orthogonalisation, the routing by
+scores and AdamW, from `csrc/marshal.cpp` with the host compiler and Python's and torch's headers; where
 those are missing the library is built all the same, with a warning, and only those calls cannot be made.
 A stamp of the sources and flags skips each rebuild when nothing changed.
 """
@@ -129,7 +129,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if obj := marshal.result():
                 _link_marshal(obj)
         except (RuntimeError, OSError, ImportError) as e:
-            warnings.warn(f"the balance loss and the orthogonalisation cannot be called, marshalling was not built: {e}")
+            warnings.warn(f"the balance loss, the orthogonalisation, the routing by scores and AdamW cannot be called, marshalling was not built: {e}")
     return LIB
 
 
