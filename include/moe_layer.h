@@ -217,7 +217,7 @@ int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const m
  * fewer than k experts are left, the other picks are -1 with weight 0.  The bias carries no gradient.
  *
  * moe_router_select_fwd: logits fp32 or bf16 [T, E] -> topk_idx int32 [T, k], topk_w fp32 [T, k] (overwritten).
- *   bias: fp32 [E] or NULL.  mask: uint8 [T] or NULL; a token whose mask is 0 (padding) is not read: it gets picks
+ *   bias: fp32 [E] or NULL.  mask: uint8 [T] or NULL; a token whose mask is 0 (padding) may hold anything: it gets picks
  *   of -1 and weights of 0.  A layer that is to take such picks wants MOE_FLAG_NO_PICK, else it records them.
  * moe_router_select_bwd: dlogits [T, E], fp32 or bf16 (overwritten; with `accumulate`, fp32 only, added to, so that the
  *   balance loss's gradient, from moe_balance_bwd without topk_w, may stand there already) of

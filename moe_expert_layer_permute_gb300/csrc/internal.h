@@ -126,6 +126,7 @@ struct SelectArgs {
     bool few;               // tokens: latency counts
     int batch;              // tokens that a warp takes at a time
     int room;               // and that it puts off
+    float sum_error;        // of a softmax's sum and its exponentials, relative
 };
 cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms);
 struct SelectGradArgs {

@@ -77,10 +77,11 @@ __device__ __forceinline__ float sel_sigmoid(float x) { return rcp_approx(1.f + 
 // How far an fp32 score may be from the exact one where it is at most `most`.  The power is off by 2^-22 relative, its
 // argument z (times log2 e) by 2^-24 of it, a quotient by 2^-23.
 //   sigmoid: s (1 - s) (2^-22 + 2^-23 |z|) + 2^-23 s, at most 3e-7, and for a small s, -z up to 88, 1.1e-5 s
-//   softmax: s (2^-22 + 2^-23 (-ln s)) and the sum's error, some 2^-21 with its exponentials'; s (-ln s) is at most 0.37
-__device__ __forceinline__ float sel_error(bool sigmoid, float most) {
+//   softmax: s (2^-22 + 2^-23 (-ln s)) and the sum's error, 2^-24 for each of V / 4 additions one after the other and some 2^-21
+//            with the tree's and the exponentials'; s (-ln s) is at most 0.37
+__device__ __forceinline__ float sel_error(const SelectArgs& a, float most) {
     const float s = fminf(fmaxf(most, 1e-37f), 1.f);
-    return sigmoid ? fminf(3e-7f, 1.1e-5f * s) : 9e-7f * s + fminf(4.5e-8f, 1.1e-5f * s);
+    return a.sigmoid ? fminf(3e-7f, 1.1e-5f * s) : a.sum_error * s + fminf(4.5e-8f, 1.1e-5f * s);
 }
 constexpr float kSelSum = 1.2e-7f;   // of a sum's size: a rounding of it, and one of its bias less the largest
 
@@ -93,7 +94,7 @@ template <int W>
 __device__ __forceinline__ float sel_max(float v) {
     if constexpr (W == 32) {
         float r;
-        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
         return r;
     }
 #pragma unroll
@@ -158,7 +159,7 @@ struct SelOpen {              // one that is to be gone through again
 // and distances from `top`, of which d is the larger; `last` is what sums in 64 bits, which are what counts, lose; `quantum`
 // is what the index has taken from d, if anything.
 __device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, float last, float d, float most, float quantum) {
-    return 2.f * sel_error(a.sigmoid, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d + last;
+    return 2.f * sel_error(a, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d + last;
 }
 
 // Every expert in 64 bits, their groups too: k rounds of the largest that is left.
@@ -326,7 +327,7 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
             if (a.bias && !a.sigmoid) {
                 const double oc = __shfl_sync(all, c, i), os = __shfl_sync(all, s, i);
                 const float ox = __shfl_sync(all, x, i), ob = __shfl_sync(all, b, i);
-                near |= lane < n && i != lane && !(x == ox && b == ob) && !(fabs(c - oc) > 2e-6 * fabs(s - os) + 1e-15 * (fabs(c) + fabs(b)));
+                near |= lane < n && i != lane && !(x == ox && b == ob) && !(fabs(c - oc) > 2.0 * a.sum_error * fabs(s - os) + 1e-15 * (fabs(c) + fabs(b)));
             }
         }
         if (!__any_sync(all, near)) {
@@ -342,7 +343,7 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
 // sum in size, with a score of at most |top| + span.
 // partial: a group of one expert has the largest bias taken off its sum once more, which rounds.
 __device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float span, float top_bias, bool partial, float v, float w) {
-    return 4.f * sel_error(a.sigmoid, fabsf(top) + span) +
+    return 4.f * sel_error(a, fabsf(top) + span) +
            2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (partial ? fabsf(top_bias) : 0.f)) + 4e-15f * fabsf(top_bias);
 }
 
@@ -428,7 +429,7 @@ static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long 
         for (int i = 0; i < n; ++i) {
             const double os = __shfl_sync(all, sum, i), oc = __shfl_sync(all, score, i);
             const bool in = __shfl_sync(all, (int)(first && order < slots), i);
-            near |= first && order >= slots && in && !(os - sum > 2e-6 * fabs(oc - score) + 1e-15 * (fabs(os) + 1.0));
+            near |= first && order >= slots && in && !(os - sum > 2.0 * a.sum_error * fabs(oc - score) + 1e-15 * (fabs(os) + 1.0));
         }
         if (__any_sync(all, near)) return 0u;
     }
@@ -605,10 +606,10 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             for (int i = 1; i + 1 < V; i += 2) m = sel_max3(m, x[i], x[i + 1]);
             m = sel_max<W>(fmaxf(m, x[V - 1]));
             if (m == -INFINITY) m = 0.f;
-            float sum = 0.f;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};   // (four shorter sums round less than one)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += sel_exp(x[i] - m);   // (a NaN stays one)
-            inv = 1.f / sel_sum<W>(sum);
+            for (int i = 0; i < V; ++i) part[i & 3] += sel_exp(x[i] - m);   // (a NaN stays one)
+            inv = 1.f / sel_sum<W>((part[0] + part[1]) + (part[2] + part[3]));
         }
         bool again = false, doubt = false;   // of everything, of the groups
         uint32_t groups = ~0u;
@@ -897,6 +898,7 @@ static cudaError_t select_c(cudaStream_t st, SelectArgs a, int num_sms) {
     a.batch = a.few ? NT : std::max(NT, per);
     while (a.batch > NT && a.batch * a.G > 256) a.batch /= 2;
     a.room = std::max(8, a.batch);
+    a.sum_error = 9e-7f + 1.5e-8f * V;
     const size_t words = (size_t)kSelWarps * (a.batch + a.room) * (a.k + 1 + kSelBehind + (a.G > 1 ? 2 * a.G : 0));
     const size_t smem = (words + (a.bias ? (a.E + 3) / 4 * 4 : 0)) * 4;   // at most 33 KB
     const unsigned grid = sel_grid(a.T, kSelWarps * a.batch, V <= 16 ? 8 : V == 32 ? 4 : 2, num_sms);
