@@ -271,10 +271,10 @@ cudaError_t launch_select_fwd(cudaStream_t st, SelectArgs a, int num_sms) {
     const int bits = log2_of(a.E);
     a.low = (1u << bits) - 1u;
     a.quantum = (float)(1 << bits) * 1.1920929e-7f;   // what the last bits hold, relative to c
-    // values a lane: 4 or 8 and a whole warp where there is less than a warp of tokens to fill an SM's schedulers with,
-    // 16 otherwise; more where groups do not fit 32 lanes
+    // Values a lane: 4 or 8 and a whole warp where there are few tokens (2400 x 128 3.7 us, 4.3 with 16 values and 8 lanes; 2400 x
+    // 256 in 8 groups 8.5 and 9.6; from 4800 on it is the other way round), 16 otherwise; more where groups do not fit 32 lanes.
     int V = 0, W = 32, lanes = 32;
-    a.few = a.T <= 8 * num_sms;
+    a.few = a.T <= 16 * num_sms;
     for (int v : {4, 8, 16, 32, 64}) {
         if (v < 16 && !a.few) continue;
         lanes = pow2_at_least((a.gs + v - 1) / v);

@@ -893,10 +893,11 @@ inline int log2_of(int p) {
 template <int W, int V, int KIND>
 static cudaError_t select_c(cudaStream_t st, SelectArgs a, int num_sms) {
     constexpr int NT = 32 / W;
-    // where a batch has many tokens a warp takes as many as fill its lanes with picks
+    // Where there are many tokens a warp takes as many as fill its lanes with picks; not where that leaves an SM fewer than 16
+    // warps (k = 8, four tokens against one or two: 4800 x 512 15.2 and 12.2 us, 9600 x 512 the same, 16,384 x 512 20.1 and 23.9).
     const int per = 32 / pow2_at_least(a.k);
     a.batch = a.few ? NT : std::max(NT, per);
-    while (a.batch > NT && a.batch * a.G > 256) a.batch /= 2;
+    while (a.batch > NT && (a.batch * a.G > 256 || a.T < (long long)a.batch * 16 * num_sms)) a.batch /= 2;
     a.room = std::max(8, a.batch);
     a.sum_error = 9e-7f + 1.5e-8f * V;
     const size_t words = (size_t)kSelWarps * (a.batch + a.room) * (a.k + 1 + kSelBehind + (a.G > 1 ? 2 * a.G : 0));

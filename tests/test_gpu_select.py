@@ -97,7 +97,7 @@ def check(moe, logits, k, bias=None, mask=None, seed=0, out=None, **rule):
     return idx, w, d
 
 
-SHAPES = [(1, 1, 1, 1, 1), (3, 2, 1, 1, 1), (7, 8, 2, 1, 1), (33, 16, 16, 1, 1), (70, 24, 5, 3, 2), (64, 256, 8, 8, 4), (50, 100, 7, 1, 1),
+SHAPES = [(2500, 128, 8, 1, 1), (2600, 256, 8, 8, 4), (5000, 512, 8, 1, 1), (10_000, 64, 4, 4, 2), (1, 1, 1, 1, 1), (3, 2, 1, 1, 1), (7, 8, 2, 1, 1), (33, 16, 16, 1, 1), (70, 24, 5, 3, 2), (64, 256, 8, 8, 4), (50, 100, 7, 1, 1),
           (40, 1000, 32, 20, 9), (20, 1024, 32, 32, 8), (31, 999, 31, 3, 2), (29, 1023, 9, 31, 17), (45, 60, 13, 12, 5), (130, 127, 6, 1, 1),
           (66, 384, 8, 1, 1), (1230, 48, 6, 4, 2), (1220, 512, 8, 1, 1), (1220, 700, 3, 7, 3), (1290, 20, 3, 5, 4), (1220, 1020, 5, 17, 4),
           (1300, 128, 8, 1, 1), (1300, 256, 8, 8, 4), (1250, 31, 4, 31, 9)]
