@@ -512,6 +512,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
 
     float span = 0.f, top_bias = 0.f;                      // of the finite biases
     bool odd_bias = false;                                 // one is NaN or +inf
+    bool rounded = false;                                  // one is not what it was, so that unlike ones may be equal
     if (a.bias) {
         float hi = -INFINITY, lo = INFINITY;
         for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) {
@@ -539,8 +540,14 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             span = hi - lo;
             top_bias = hi;
         }
-        for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) biases[e] -= top_bias;
+        bool rounds = false;
+        for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) {
+            const float b = biases[e], d = b - top_bias;
+            biases[e] = d;
+            rounds |= d + top_bias != b;
+        }
         odd_bias = __syncthreads_or(odd_bias);
+        rounded = __syncthreads_or(rounds);
     }
     const float last = 1e-15f * fabsf(top_bias);
     auto place = [&](int i) { return VEC ? 4 * (lp + lpg * (i >> 2)) + (i & 3) : lp + lpg * i; };
@@ -818,7 +825,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 const float t0 = __uint_as_float(~k0 & ~low), t1 = __uint_as_float(~k1 & ~low), d1 = inside ? dn : t1;
                 const float most = a.sigmoid ? 1.f : sj + span;
                 near = both && !(d1 - d0 > sel_margin(a, token.top, last, d1, most, inside ? 0.f : a.quantum));
-                equal = inside && xj == xn && bj == bn;
+                equal = inside && xj == xn && bj == bn && !rounded;
                 // (what is out of order may belong behind others whose keys are as near)
                 chain = both && !(t1 - t0 > sel_margin(a, token.top, last, t1, most, 2.f * a.quantum));
             } else if (!a.bf16) {

@@ -191,6 +191,26 @@ def test_sums_that_a_large_bias_makes_equal(cuda_lib):
             check(cuda_lib, logits.cuda(), k, bias=torch.full((E,), b).cuda(), score="sigmoid", G=G, kept=kept, rank=2, renorm=False)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,G,kept,dtype", [(40, 100, 1, 1, torch.float32), (3000, 387, 1, 1, torch.bfloat16), (60, 96, 3, 2, torch.float32)])
+def test_biases_that_are_equal_less_the_largest(cuda_lib, score, T, E, G, kept, dtype):
+    # equal logits, biases one step of 32 bits apart, the larger at the higher index; 0.5 above them both, they are the same number
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, E, generator=g)
+    bias = torch.rand(E, generator=g) * 1e-2
+    b = torch.tensor(-1.5e-5)
+    for e in (5, 9, 14, 30):
+        x[:, e] = 4.0
+        bias[e] = b
+        b = torch.nextafter(b, torch.tensor(0.0))
+    bias[E - 1] = 0.5
+    x[:, E - 1] = -30.0 if score == "sigmoid" else -3.0
+    assert len({float(bias[e]) for e in (5, 9, 14, 30)}) == 4 and len({float(bias[e] - bias[E - 1]) for e in (5, 9, 14, 30)}) == 1
+    idx, _, _ = check(cuda_lib, x.to(dtype).cuda(), 8, bias=bias.cuda(), score=score, G=G, kept=kept)
+    order = [e for e in idx[0].tolist() if e in (5, 9, 14, 30)]
+    assert G > 1 or order == [30, 14, 9, 5]
+
+
 def test_saturated_scores(cuda_lib):
     """Logits so large that scores are 1 in 64 bits: ordered by the logits without a bias, equal with one."""
     g = torch.Generator().manual_seed(6)
