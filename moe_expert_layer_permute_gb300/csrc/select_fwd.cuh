@@ -340,12 +340,14 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
 }
 
 // How far two groups' sums may come nearer to each other than they are in fp32: of two terms each, each at most 2 |top| and the
-// sum in size, with a score of at most |top| + span.
+// sum in size, with a score of at most `most`.
 // partial: a group of one expert has the largest bias taken off its sum once more, which rounds.
-__device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float span, float top_bias, bool partial, float v, float w) {
-    return 4.f * sel_error(a, fabsf(top) + span) +
+__device__ __forceinline__ float sel_group_margin(const SelectArgs& a, float top, float most, float top_bias, bool partial, float v, float w) {
+    return 4.f * sel_error(a, most) +
            2.f * kSelSum * (fabsf(v) + fabsf(w) + 4.f * fabsf(top) + (partial ? fabsf(top_bias) : 0.f)) + 4e-15f * fabsf(top_bias);
 }
+// No softmax's score is above 1 / its sum, however far biases have spread.
+__device__ __forceinline__ float sel_most(const SelectArgs& a, float most, float inv) { return a.sigmoid ? most : fminf(most, inv); }
 
 // A token whose groups at the border are too near each other: which stay, from the sums in 64 bits of those alone that may.
 // values: G sums as the forward has them (less the bias), then the least term of each (-inf: an excluded group).  0
@@ -364,7 +366,7 @@ static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long 
     }
     const bool stays = rank < a.kept && vk != 0u;
     const float lv = sel_unkey(~__reduce_max_sync(all, stays ? ~vk : 0u)), mv = sel_unkey(__reduce_max_sync(all, stays ? 0u : vk));
-    const float e2 = 2.f * sel_group_margin(a, token.top, span, top_bias, a.rank == 2, lv, mv);
+    const float e2 = 2.f * sel_group_margin(a, token.top, sel_most(a, fabsf(token.top) + span, token.inv), top_bias, a.rank == 2, lv, mv);
     const float over = value - lv;   // (one difference for both, so that none falls between them)
     const uint32_t sure = __ballot_sync(all, vk != 0u && over > e2), open = __ballot_sync(all, vk != 0u && !(over > e2) && over >= -e2);
     int n = 0;
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 const uint32_t least = ~sel_max<W>(stays ? ~vk : 0u), most = sel_max<W>(stays || group >= a.G ? 0u : vk);
                 const float lv = sel_unkey(least), mv = sel_unkey(most);
                 const bool partial = a.rank == 2 && __any_sync(all, m1 != -INFINITY && m2 == -INFINITY);
-                const float err = sel_group_margin(a, top, span, top_bias, partial, lv, mv);
+                const float err = sel_group_margin(a, top, sel_most(a, fabsf(top) + span, inv), top_bias, partial, lv, mv);
                 doubt = live && most != 0u && !(lv - mv > err);
                 if (__any_sync(all, doubt) && lp == 0 && group < a.G) {   // (for select_groups)
                     values[at_token * 2 * a.G + group] = value;
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 const float dn = __shfl_down_sync(all, d0, 1);
                 const bool inside = j + 1 < a.k, both = k0 && k1 >= none;
                 const float t0 = __uint_as_float(~k0 & ~low), t1 = __uint_as_float(~k1 & ~low), d1 = inside ? dn : t1;
-                const float most = a.sigmoid ? 1.f : sj + span;
+                const float most = sel_most(a, a.sigmoid ? 1.f : sj + span, token.inv);
                 near = both && !(d1 - d0 > sel_margin(a, token.top, last, d1, most, inside ? 0.f : a.quantum));
                 equal = inside && xj == xn && bj == bn && !rounded;
                 // (what is out of order may belong behind others whose keys are as near)
