@@ -162,6 +162,16 @@ __device__ __forceinline__ float sel_margin(const SelectArgs& a, float top, floa
     return 2.f * sel_error(a, most) + 2.f * kSelSum * (fabsf(top) + d) + (quantum + kSelSum) * d + last;
 }
 
+// The sum of a softmax's exponentials in 64 bits.
+static __device__ __noinline__ double select_sum(const SelectArgs& a, long long t, double row_max) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) sum += sel_score64(false, sel_value(a, t * a.E + e), row_max, 1.0);
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
 // Every expert in 64 bits, their groups too: k rounds of the largest that is left.
 static __device__ __noinline__ void select_all(const SelectArgs& a, long long t, uint32_t low, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
@@ -183,11 +193,7 @@ static __device__ __noinline__ void select_all(const SelectArgs& a, long long t,
 #pragma unroll 1
         for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(all, top, o));
         if (__any_sync(all, nan)) top = NAN;
-#pragma unroll 1
-        for (int i = 0; i < rows; ++i)
-            if (lane + 32 * i < a.E) sum += sel_score64(false, sel_value(a, t * a.E + lane + 32 * i), top, 1.0);
-#pragma unroll 1
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(all, sum, o);
+        sum = select_sum(a, t, top);
     }
     const double inv = 1.0 / sum;
 #pragma unroll 1
@@ -270,8 +276,9 @@ static __device__ __noinline__ void select_all(const SelectArgs& a, long long t,
 // open: bit j where picks j and j + 1 are too near each other.  The candidates are those from the first such pick on, as
 // far as their order is open (picks before and after them stand), and where the last pick is among them every expert
 // that may be; their sums in 64 bits (without a bias their logits) decide.  A softmax's have its fp32 sum, whose error
-// stands in both of two terms and so counts with their difference alone; where that is not enough, or there are more
-// than 32, all experts are gone through.
+// stands in both of two terms and so counts with their difference alone; where that is not enough, its sum is made in 64 bits
+// (4097 x 999, k = 31: one such token of a batch made its forward 170 us instead of 79, by going through all experts).  Where
+// there are more than 32, all experts are gone through.
 static __device__ __noinline__ void select_again(const SelectArgs& a, long long t, uint32_t open, const SelToken& token, float top_bias,
                                                  uint32_t low, uint32_t none, SelRoom* room, uint32_t* picks) {
     const int lane = threadIdx.x & 31;
@@ -315,25 +322,30 @@ static __device__ __noinline__ void select_again(const SelectArgs& a, long long 
     if (n <= 32) {
         const int e = lane < n ? room->candidate[lane] : 0;
         const float x = sel_value(a, t * a.E + e), b = a.bias ? __ldg(a.bias + e) : 0.f;
-        const double s = a.bias ? sel_score64(a.sigmoid, x, (double)token.max, (double)token.inv) : 0.0, c = a.bias ? s + (double)b : (double)x;
-        const uint64_t key = sel_key64(c);
-        int rank = 0;
-        bool near = false;
+        double inv = (double)token.inv;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            const uint64_t other = __shfl_sync(all, key, i);
-            const int oe = __shfl_sync(all, e, i);
-            rank += other > key || (other == key && oe < e);
-            if (a.bias && !a.sigmoid) {
-                const double oc = __shfl_sync(all, c, i), os = __shfl_sync(all, s, i);
-                const float ox = __shfl_sync(all, x, i), ob = __shfl_sync(all, b, i);
-                near |= lane < n && i != lane && !(x == ox && b == ob) && !(fabs(c - oc) > 2.0 * a.sum_error * fabs(s - os) + 1e-15 * (fabs(c) + fabs(b)));
+        for (bool exact = !a.bias || a.sigmoid;; exact = true) {
+            const double s = a.bias ? sel_score64(a.sigmoid, x, (double)token.max, inv) : 0.0, c = a.bias ? s + (double)b : (double)x;
+            const uint64_t key = sel_key64(c);
+            int rank = 0;
+            bool near = false;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                const uint64_t other = __shfl_sync(all, key, i);
+                const int oe = __shfl_sync(all, e, i);
+                rank += other > key || (other == key && oe < e);
+                if (!exact) {
+                    const double oc = __shfl_sync(all, c, i), os = __shfl_sync(all, s, i);
+                    const float ox = __shfl_sync(all, x, i), ob = __shfl_sync(all, b, i);
+                    near |= lane < n && i != lane && !(x == ox && b == ob) && !(fabs(c - oc) > 2.0 * a.sum_error * fabs(s - os) + 1e-15 * (fabs(c) + fabs(b)));
+                }
             }
-        }
-        if (!__any_sync(all, near)) {
-            if (lane < n && from + rank < a.k) picks[from + rank] = sel_pick(e, low);
-            __syncwarp();
-            return;
+            if (exact || !__any_sync(all, near)) {
+                if (lane < n && from + rank < a.k) picks[from + rank] = sel_pick(e, low);
+                __syncwarp();
+                return;
+            }
+            inv = 1.0 / select_sum(a, t, (double)token.max);
         }
     }
     select_all(a, t, low, picks);
