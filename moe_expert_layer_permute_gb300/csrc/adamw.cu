@@ -23,8 +23,8 @@
 
 namespace moe {
 
-constexpr int kAdamWarps = 8;
-constexpr int kAdamUnit = 256;     // values of a warp at a time, and of a block of 8-bit states
+constexpr int kAdamWarps = kListWarps;
+constexpr int kAdamUnit = kListUnit;   // and values of a block of 8-bit states
 // Blocks an SM.  In 8 bits a value is some 75 instructions and 14 to 18 bytes, so that issue slots and memory are both near
 // their ends (70 % and 85 %) and more warps cover more of the wait: with 4 blocks (64 registers a thread) 604 M values take
 // 6 % longer than with 5, with 6 (spills) 3 %.
@@ -401,12 +401,10 @@ cudaError_t launch_adamw(cudaStream_t st, const ListTensor* t, int count, bool e
     return adamw_n<kListMost>(st, t, count, eight, a, num_sms);
 }
 
-// Four units a warp at least: blocks come to one ticket at the end, a few nanoseconds each (1.2 M values in 586 blocks
-// took 8.6 us).
 int norm_blocks(const ListTensor* t, int count, int num_sms) {
     long long units = 0;
-    for (int i = 0; i < count; ++i) units += (t[i].n + kAdamUnit - 1) / kAdamUnit;
-    return (int)std::max<long long>(1, std::min<long long>((units + 4 * kAdamWarps - 1) / (4 * kAdamWarps), 4 * num_sms));
+    for (int i = 0; i < count; ++i) units += list_units(t[i].n);
+    return norm_blocks_of(units, num_sms);
 }
 template <int MOST>
 static cudaError_t norm_n(cudaStream_t st, const ListTensor* t, int count, const NormArgs& a, int num_sms) {

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/moe_layer.h"
+#include "norm_plan.h"
 
 namespace moe {
 
@@ -144,7 +145,6 @@ cudaError_t launch_select_bwd(cudaStream_t st, SelectGradArgs a, int num_sms);
 cudaError_t launch_select_bias(cudaStream_t st, const int* counts, int B, int E, float* bias, float rate);
 
 // AdamW over a list of tensors, and the norm of a list of gradients (adamw.cu)
-constexpr int kListMost = 384;       // tensors of a launch
 struct ListTensor {
     float* p;
     const void* g;                   // fp32 or bf16

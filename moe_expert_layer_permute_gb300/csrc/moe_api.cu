@@ -847,16 +847,9 @@ int moe_adamw_step(int64_t count, const moe_tensor* params, const moe_tensor* gr
     return MOE_OK;
 }
 
-// the status word's line, the ticket's, a partial sum for each block of each launch
-static size_t norm_workspace(int64_t elements, int64_t count) {
-    const int64_t launches = (count + kListMost - 1) / kListMost;
-    const int64_t units = elements / 256 + count;
-    // (at most four blocks an SM and launch, of a GPU of up to 1024 SMs, and not more than a block for each unit)
-    return 512 + 8 * (size_t)std::min<int64_t>(launches * 4096, units + launches);
-}
 size_t moe_grad_norm_workspace_bytes(int64_t elements, int64_t count) {
     if (elements < 0 || elements > ((int64_t)1 << 40) || count < 0 || count > kListCount) return 0;
-    return norm_workspace(elements, count);
+    return norm_room(elements, count);
 }
 
 int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float max_norm, moe_scratch* workspace, void* stream) {
@@ -874,10 +867,10 @@ int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float
         list[i % kListMost].n = n;
         elements += n;
     }
-    if ((rc = check_workspace(workspace, norm_workspace(elements, count)))) return rc;
+    if ((rc = check_workspace(workspace, norm_room(elements, count)))) return rc;
     if (workspace->state[0] == 1) return MOE_ERR_STATE;   // moe_orthogonalise has left data there
     const int nsm = num_sms_current();
-    if (nsm <= 0) return MOE_ERR_CUDA;
+    if (nsm <= 0 || nsm > kNormMostSms) return MOE_ERR_CUDA;
     workspace->state[0] = 2;   // holds sums: moe_balance_fwd refuses it
     NormArgs a{};
     a.ticket = reinterpret_cast<int*>(reinterpret_cast<char*>(workspace->data) + 256);
