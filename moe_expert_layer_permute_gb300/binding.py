@@ -421,8 +421,10 @@ def moe_orthogonalise(G, O, workspace: Workspace, steps: int = 5, coeffs=None, e
 
 
 class TensorList:
-    """Tensors for moe_adamw_step and moe_grad_norm, which take any sequence of them; one of these is looked through once for as
-    many calls as there are (a call of 240 tensors' lists takes some 20 us less).  It holds its tensors."""
+    """Tensors for moe_adamw_step and moe_grad_norm, which take any sequence of them; of one of these the views are made once for as
+    many calls as there are (a call of 240 tensors' lists takes some 20 us less).  It holds its tensors: what is done to them in
+    place, `.data` set to other memory or sizes included, counts from the next call on, but a `.grad` that was set to None and made
+    anew is another tensor and wants another list."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <memory>
+#include <utility>
 #include <vector>
 
 #include "../../include/moe_layer.h"
@@ -199,12 +200,26 @@ PyObject* bias_step(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // ---- lists of tensors ----
-// Views of a list's tensors, made once for as many calls as there are; the tensors are held, and one whose memory has
-// changed since is looked at again by the call.
+// Views of a list's tensors, made once for as many calls as there are.  The tensors are held, and each call looks whether
+// they are still what the views say: a tensor may get another size, order, type or device, with or without
+// another address.  Then new views are made; a call under way in another thread keeps those that it has.
+struct Seen {                      // of a tensor: what its view and the list's device follow from
+    const void* at;
+    int64_t count;
+    caffe2::TypeMeta type;
+    bool contiguous;
+    c10::Device device;
+    explicit Seen(const c10::TensorImpl& t)
+        : at(t.data()), count(t.numel()), type(t.dtype()), contiguous(t.is_contiguous()), device(t.device()) {}
+    bool holds(const c10::TensorImpl& t) const {
+        return t.numel() == count && t.data() == at && t.is_contiguous() == contiguous && t.dtype() == type && t.device() == device;
+    }
+};
+using Views = std::shared_ptr<const std::vector<moe_tensor>>;
 struct List {
     std::vector<at::Tensor> held;
-    std::vector<moe_tensor> views;
-    std::vector<const void*> at;   // where each was
+    std::vector<std::pair<const c10::TensorImpl*, Seen>> seen;   // of the strided ones (others are refused, and stay what they are)
+    Views views;
     int device = -1;               // -2: of several devices
 };
 // a contiguous tensor of any shape as its elements in a row
@@ -226,10 +241,20 @@ moe_tensor flat(const at::Tensor& t) {
     v.data = strided && t.is_cuda() && t.numel() ? t.mutable_data_ptr() : nullptr;
     return v;
 }
-void look(List* l, size_t i) {
-    const at::Tensor& t = l->held[i];
-    l->views[i] = flat(t);
-    l->at[i] = t.layout() == at::kStrided ? t.const_data_ptr() : nullptr;
+void look(List* l) {
+    auto views = std::make_shared<std::vector<moe_tensor>>();
+    decltype(l->seen) seen;
+    views->reserve(l->held.size());
+    seen.reserve(l->held.size());
+    int device = -1;
+    for (const at::Tensor& t : l->held) {
+        views->push_back(flat(t));
+        if (t.layout() == at::kStrided) seen.emplace_back(t.unsafeGetTensorImpl(), Seen(*t.unsafeGetTensorImpl()));
+        if (t.is_cuda()) device = device == -1 || device == t.get_device() ? (int)t.get_device() : -2;
+    }
+    l->seen.swap(seen);   // (all of it or nothing: whatever throws does so before)
+    l->views = std::move(views);
+    l->device = device;
 }
 constexpr char kListName[] = "moe_tensor_list";
 List* list_of(PyObject* o) { return static_cast<List*>(PyCapsule_GetPointer(o, kListName)); }
@@ -253,13 +278,9 @@ PyObject* make_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
                 Py_DECREF(seq);
                 return nullptr;
             }
-            const at::Tensor& t = THPVariable_Unpack(o);
-            l->held.push_back(t);
-            if (t.is_cuda()) l->device = l->device == -1 || l->device == t.get_device() ? (int)t.get_device() : -2;
+            l->held.push_back(THPVariable_Unpack(o));
         }
-        l->views.resize(count);
-        l->at.resize(count);
-        for (Py_ssize_t i = 0; i < count; ++i) look(l.get(), i);
+        look(l.get());
         made = PyCapsule_New(l.get(), kListName, [](PyObject* c) { delete list_of(c); });
         if (made) l.release();
     } catch (const std::exception& e) {
@@ -271,22 +292,24 @@ PyObject* make_list(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // A call's lists: of one length and one device, whose current stream is taken where none is given.
 struct Lists {
-    List* list[7];
+    Views of[7];
     Py_ssize_t count = -1;
     int device = -1;
     bool add(int i, PyObject* o) {
-        list[i] = nullptr;
         if (o == Py_None) return true;
         List* l = list_of(o);
         if (!l) return false;
-        if (count < 0) count = (Py_ssize_t)l->views.size();
-        if ((Py_ssize_t)l->views.size() != count) {
+        if (count < 0) count = (Py_ssize_t)l->held.size();
+        if ((Py_ssize_t)l->held.size() != count) {
             PyErr_SetString(PyExc_ValueError, "lists of different lengths");
             return false;
         }
-        for (size_t k = 0; k < l->held.size(); ++k)
-            if (l->held[k].layout() == at::kStrided && l->held[k].const_data_ptr() != l->at[k]) look(l, k);
-        list[i] = l;
+        for (const auto& [t, as] : l->seen)
+            if (!as.holds(*t)) {
+                look(l);
+                break;
+            }
+        of[i] = l->views;
         return on(l->device);
     }
     bool on(int d) {
@@ -298,7 +321,7 @@ struct Lists {
         device = d;
         return true;
     }
-    const moe_tensor* views(int i) const { return list[i] ? list[i]->views.data() : nullptr; }
+    const moe_tensor* views(int i) const { return of[i] ? of[i]->data() : nullptr; }
 };
 // a number on the device, or None
 bool number(PyObject* o, moe_tensor* held, const moe_tensor** at, Lists* lists) {
