@@ -363,7 +363,7 @@ __device__ __forceinline__ float sel_most(const SelectArgs& a, float most, float
 
 // A token whose groups at the border are too near each other: which stay, from the sums in 64 bits of those alone that may.
 // values: G sums as the forward has them (less the bias), then the least term of each (-inf: an excluded group).  0
-// where that leaves it open (more than 32 experts may be terms; a softmax's sum has 32 bits).
+// where that leaves it open (more than 32 experts may be terms; a softmax's sum has 32 bits; a sum is beyond 32 bits).
 static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long long t, const float* values, const SelToken& token, float span,
                                                       float top_bias, SelRoom* room) {
     const int lane = threadIdx.x & 31;
@@ -379,6 +379,8 @@ static __device__ __noinline__ uint32_t select_groups(const SelectArgs& a, long 
     const bool stays = rank < a.kept && vk != 0u;
     const float lv = sel_unkey(~__reduce_max_sync(all, stays ? ~vk : 0u)), mv = sel_unkey(__reduce_max_sync(all, stays ? 0u : vk));
     const float e2 = 2.f * sel_group_margin(a, token.top, sel_most(a, fabsf(token.top) + span, token.inv), top_bias, a.rank == 2, lv, mv);
+    // (two biases near the least number that there is add up to -inf, and no difference of those tells which is larger)
+    if (!(e2 < INFINITY)) return 0u;
     const float over = value - lv;   // (one difference for both, so that none falls between them)
     const uint32_t sure = __ballot_sync(all, vk != 0u && over > e2), open = __ballot_sync(all, vk != 0u && !(over > e2) && over >= -e2);
     int n = 0;
