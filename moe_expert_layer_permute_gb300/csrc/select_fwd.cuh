@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
     const int per = 32 / kp;
 
     float span = 0.f, top_bias = 0.f;                      // of the finite biases
-    bool odd_bias = false;                                 // one is NaN or +inf
+    bool odd_bias = false;                                 // one is NaN or +inf, or finite and, less the largest, -inf
     bool rounded = false;                                  // one is not what it was, so that unlike ones may be equal
     if (a.bias) {
         float hi = -INFINITY, lo = INFINITY;
@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
             const float b = biases[e], d = b - top_bias;
             biases[e] = d;
             rounds |= d + top_bias != b;
+            odd_bias |= fabsf(b) < INFINITY && d == -INFINITY;
         }
         odd_bias = __syncthreads_or(odd_bias);
         rounded = __syncthreads_or(rounds);
@@ -679,13 +680,17 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 if (a.bias) sums(std::false_type{}, std::true_type{}); else sums(std::false_type{}, std::false_type{});
             }
             if (odd_bias || __any_sync(all, live && special)) {
-                // experts that are excluded by their logits; sums that are NaN or +inf, which keys cannot tell
+                // experts that are excluded by their logits; sums that are NaN or +inf, which keys cannot tell, or -inf without
+                // being excluded
                 bool odd = false;
                 most_c = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float c = __uint_as_float(key[i]);
-                    if (place(i) < read && sel_value(a, t * a.E + e0 + place(i)) == -INFINITY) c = -INFINITY;
+                    if (place(i) < read) {
+                        if (sel_value(a, t * a.E + e0 + place(i)) == -INFINITY) c = -INFINITY;
+                        else if (c == -INFINITY) odd |= __ldg(a.bias + e0 + place(i)) != -INFINITY;   // (without biases no sum is)
+                    }
                     odd |= !(c < INFINITY);
                     most_c = fmaxf(most_c, c);
                     key[i] = __float_as_uint(c);
