@@ -336,7 +336,7 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
  * v_scales fp32 [ceil(n / 256)] views, 4-byte aligned: value i of m is code[i] m_scales[i / 256].  Zeros are the state to
  * start from.  The step decodes, steps in fp32 and encodes again: scale = max|x| / 448 over the 256 values, x / scale
  * rounded up with the probability of its distance to the code below (`seed` chooses the numbers: give another for each
- * step; results repeat with it).  Codes of r are at least 1 (2^-9), so a value that has had no gradient beside others
+ * step, its number for one, since a state that meets the same numbers each time stays where it is; results repeat with it).  Codes of r are at least 1 (2^-9), so a value that has had no gradient beside others
  * that have holds a small v.  Blocks with nothing over 1e-35 become zeros; a NaN or an infinity in m' or v' makes its
  * block NaN.
  *   lr, step, grad_scale: numbers on the device (fp32, int32, fp32, one element each, 4-byte aligned) or NULL, then lr and

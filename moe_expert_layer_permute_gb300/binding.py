@@ -441,13 +441,17 @@ def _list(tensors):
 
 
 def moe_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, m_scales=None,
-                   v_scales=None, copies=None, grad_scale=None, seed: int = 0, stream=None) -> None:
+                   v_scales=None, copies=None, grad_scale=None, seed: int | None = None, stream=None) -> None:
     """One AdamW step over lists of tensors, in place: params fp32, grads fp32 or bf16, m and v fp32, or float8_e4m3fn (or
     uint8) with m_scales and v_scales fp32 [ceil(n / 256)]; copies bf16, or None.  step and lr are numbers, or tensors
     of one element on the device (int32, fp32); grad_scale fp32 [1] on the device, or None: a factor of the gradients, no
-    step where it is not finite.  seed: of the 8-bit states' rounding, another one for each step."""
+    step where it is not finite.  seed: of the 8-bit states' rounding, the step's number if None; it has to be
+    another one for each step (a step on the device is added to it), since a state that meets the same bits each time stays where
+    it is."""
     step_at = step if isinstance(step, torch.Tensor) else None
     lr_at = lr if isinstance(lr, torch.Tensor) else None
+    if seed is None:
+        seed = 0 if step_at is not None else step
     rc = (_MARSHAL or _marshal()).adamw_step(_list(params), _list(grads), _list(m), _list(v), _list(m_scales), _list(v_scales), _list(copies),
                                              0.0 if lr_at is not None else lr, betas[0], betas[1], eps, weight_decay,
                                              0 if step_at is not None else step, seed, lr_at, step_at, grad_scale,
