@@ -341,7 +341,7 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
  * block NaN.
  *   lr, step, grad_scale: numbers on the device (fp32, int32, fp32, one element each, 4-byte aligned) or NULL, then lr and
  * step of the struct and 1.  A graph that is replayed wants them there; the step's number is then added to the seed.
- * A grad_scale that is not finite leaves everything as it is.
+ * A grad_scale that is not finite, or a step on the device below 1, leaves everything as it is.
  *   lr in [0, 1e6], betas in [0, 1), eps in [1e-20, 1], weight_decay in [0, 1e6]; step >= 1.
  *
  * moe_grad_norm: out fp32 [2] (4-byte aligned) = (norm, factor) of all values of `count` gradients, fp32 or bf16: the square root of

@@ -445,9 +445,9 @@ def moe_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1
     """One AdamW step over lists of tensors, in place: params fp32, grads fp32 or bf16, m and v fp32, or float8_e4m3fn (or
     uint8) with m_scales and v_scales fp32 [ceil(n / 256)]; copies bf16, or None.  step and lr are numbers, or tensors
     of one element on the device (int32, fp32); grad_scale fp32 [1] on the device, or None: a factor of the gradients, no
-    step where it is not finite.  seed: of the 8-bit states' rounding, the step's number if None; it has to be
-    another one for each step (a step on the device is added to it), since a state that meets the same bits each time stays where
-    it is."""
+    step where it is not finite, nor at a step on the device below 1.  seed: of the 8-bit states' rounding, the step's
+    number if None; it has to be another one for each step (a step on the device is added to it), since a state that meets the
+    same bits each time stays where it is."""
     step_at = step if isinstance(step, torch.Tensor) else None
     lr_at = lr if isinstance(lr, torch.Tensor) else None
     if seed is None:

@@ -183,10 +183,12 @@ __global__ void __launch_bounds__(32 * kAdamWarps, adam_blocks_sm<EIGHT>()) adam
     uint32_t seed = a.seed;
     if (a.step_at) {
         // 1 - b^t = -expm1(t ln b), t ln b to 2^-24 of itself, and so its result
-        const float t = (float)__ldg(a.step_at);
+        const int number = __ldg(a.step_at);
+        if (number < 1) return;   // no step either: nothing corrects a mean of no gradients
+        const float t = (float)number;
         fix1 = 1.f / -expm1f(t * a.log_b1);
         fix2 = rsqrtf(-expm1f(t * a.log_b2));
-        seed += (uint32_t)__ldg(a.step_at);
+        seed += (uint32_t)number;
     }
     const int units = list.start[list.count], stride = gridDim.x * kAdamWarps;
     int u = blockIdx.x * kAdamWarps + (threadIdx.x >> 5);

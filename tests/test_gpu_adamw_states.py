@@ -46,3 +46,22 @@ def test_without_a_seed_a_step_is_the_same_from_the_host_and_the_device(cuda_lib
         codes.append([x.view(torch.uint8) for x in (m8, v8)])
     assert all(torch.equal(a, b) for a, b in zip(codes[0], codes[1]))
     assert not any(torch.equal(a, b) for a, b in zip(codes[0], codes[2]))
+
+
+@pytest.mark.parametrize("state", [32, 8])
+@pytest.mark.parametrize("number", [0, -1, -2 ** 31])
+def test_no_step_below_the_first(cuda_lib, state, number):
+    """A step's number on the device cannot be refused by the call: it leaves everything as it is."""
+    n = 1000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    t = {k: torch.randn(n, generator=g, device="cuda") for k in ("p", "g")}
+    m, v, ms, vs = _zeros(n)
+    if state == 32:
+        m, v = torch.rand(n, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    t.update(m=m, v=v, ms=ms, vs=vs, copy=torch.full((n,), 3.0, dtype=torch.bfloat16, device="cuda"))
+    before = {k: x.clone() for k, x in t.items()}
+    step = torch.tensor([number], dtype=torch.int32, device="cuda")
+    cuda_lib.moe_adamw_step([t["p"]], [t["g"]], [m], [v], step, m_scales=[ms] if state == 8 else None, v_scales=[vs] if state == 8 else None,
+                            copies=[t["copy"]])
+    for k in t:
+        assert torch.equal(before[k].view(torch.uint8), t[k].view(torch.uint8))
