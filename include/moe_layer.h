@@ -349,7 +349,8 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
  * (no step, if it is grad_scale).  Squares and sums of 64 are fp32 (values over 1e18 or under 1e-22 are beyond it), the rest
  * 64 bits, in an order that depends on the sizes alone.  `workspace`: a zeroed moe_scratch handle of at least
  * moe_grad_norm_workspace_bytes(elements, count) bytes, 256-byte aligned, which the caller has set to zero once;
- * MOE_ERR_STATE for one that moe_orthogonalise has used. */
+ * MOE_ERR_STATE for one that moe_orthogonalise has used, and after a call of which a launch failed (until the buffer and the handle
+ * are set to zero again). */
 #define MOE_ADAMW_BLOCK 256
 typedef struct {
     double lr, beta1, beta2, eps, weight_decay;

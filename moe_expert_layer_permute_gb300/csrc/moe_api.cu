@@ -567,7 +567,7 @@ int moe_balance_fwd(const moe_tensor* logits, const moe_tensor* topk_idx, const 
     if ((rc = check_tensor(tokens, MOE_DT_I32, 1, B, 0, 0))) return rc;
     if ((rc = check_tensor(loss, MOE_DT_F32, 2, B, 2, 0))) return rc;
     if ((rc = check_workspace(workspace, balance_workspace(T, E, B)))) return rc;
-    if (workspace->state[0] != 0) return MOE_ERR_STATE;   // not zero any more
+    if (workspace->state[0] != kWorkspaceZero) return MOE_ERR_STATE;
     MOE_TRY_CUDA(launch_balance_fwd(
         reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const float*>(logits->data),
         reinterpret_cast<const int*>(topk_idx->data), mask ? reinterpret_cast<const uint8_t*>(mask->data) : nullptr,
@@ -868,10 +868,9 @@ int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float
         elements += n;
     }
     if ((rc = check_workspace(workspace, norm_room(elements, count)))) return rc;
-    if (workspace->state[0] == 1) return MOE_ERR_STATE;   // moe_orthogonalise has left data there
+    if (workspace->state[0] == kWorkspaceData) return MOE_ERR_STATE;   // moe_orthogonalise's, or of a norm that failed
     const int nsm = num_sms_current();
     if (nsm <= 0 || nsm > kNormMostSms) return MOE_ERR_CUDA;
-    workspace->state[0] = 2;   // holds sums: moe_balance_fwd refuses it
     NormArgs a{};
     a.ticket = reinterpret_cast<int*>(reinterpret_cast<char*>(workspace->data) + 256);
     a.partial = reinterpret_cast<double*>(reinterpret_cast<char*>(workspace->data) + 512);
@@ -887,11 +886,12 @@ int moe_grad_norm(int64_t count, const moe_tensor* grads, moe_tensor* out, float
         return some;
     };
     for (int64_t first = 0; first == 0 || first < count; first += kListMost) a.blocks += norm_blocks(list, part(first), nsm);
-    for (int64_t first = 0; first == 0 || first < count; first += kListMost) {
+    MOE_TRY_CUDA(norm_launches(count, &workspace->state[0], [&](int64_t first) {
         const int some = part(first);
-        MOE_TRY_CUDA(launch_norm(reinterpret_cast<cudaStream_t>(stream), list, some, a, nsm));
+        const cudaError_t e = launch_norm(reinterpret_cast<cudaStream_t>(stream), list, some, a, nsm);
         a.first_block += norm_blocks(list, some, nsm);
-    }
+        return e;
+    }));
     return MOE_OK;
 }
 
@@ -923,7 +923,7 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
         if (!(co[i] >= -16.f && co[i] <= 16.f)) return MOE_ERR_UNSUPPORTED;
     }
     if (N == 0) return MOE_OK;
-    workspace->state[0] = 1;   // holds data: moe_balance_fwd refuses it
+    workspace->state[0] = kWorkspaceData;   // moe_balance_fwd and moe_grad_norm refuse it
     const int nsm = num_sms_current();
     if (nsm <= 0) return MOE_ERR_CUDA;
     MOE_TRY_CUDA(launch_orthogonalise(reinterpret_cast<cudaStream_t>(stream), G->data, f32, N, R, C, O->data, steps, co, eps,

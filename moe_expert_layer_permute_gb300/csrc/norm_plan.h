@@ -27,4 +27,19 @@ inline size_t norm_room(int64_t elements, int64_t count) {
     return 512 + 8 * (size_t)std::min<int64_t>(launches * 4 * kNormMostSms, elements / kListUnit + count + launches);
 }
 
+// What state[0] of a workspace's handle says about the buffer.
+enum : uint64_t { kWorkspaceZero = 0, kWorkspaceData = 1, kWorkspaceSums = 2 };
+
+// A norm's launches, of the tensors from `first` on, until one fails (not 0).  The sums' ticket is zero again after the
+// last of them only, so until then, and after a failure, the buffer counts as one that holds data: it is to be set
+// to zero again, its handle with it.
+template <typename Launch>
+auto norm_launches(int64_t count, uint64_t* state, Launch launch) -> decltype(launch(count)) {
+    *state = kWorkspaceData;
+    for (int64_t first = 0; first == 0 || first < count; first += kListMost)
+        if (const auto failed = launch(first)) return failed;
+    *state = kWorkspaceSums;   // which moe_balance_fwd refuses
+    return decltype(launch(count))(0);
+}
+
 }  // namespace moe

@@ -61,3 +61,35 @@ def test_a_norm_of_nothing_is_refused_a_workspace_without_room_for_its_sum():
     assert bd.moe_grad_norm_workspace_bytes(0, 0) > 512
     ws.bytes = 512
     assert bd.LIB.moe_grad_norm(0, None, ctypes.byref(out), 1.0, ctypes.byref(ws), None) == bd.ERR["MOE_ERR_SCRATCH"]
+
+
+LAUNCHES = r"""
+#include <cassert>
+#include <vector>
+#include "norm_plan.h"
+int main() {
+    using namespace moe;
+    for (long long count : {0ll, 1ll, 384ll, 385ll, 2000ll}) {
+        const int all = (int)std::max(1ll, (count + kListMost - 1) / kListMost);
+        for (int fails = 0; fails <= all; ++fails) {        // the launch that fails (the last of them: none)
+            uint64_t state = kWorkspaceZero;
+            std::vector<long long> at;
+            const int e = norm_launches(count, &state, [&](int64_t first) {
+                assert(state == kWorkspaceData);            // nothing else takes it meanwhile
+                at.push_back(first);
+                return (int)at.size() - 1 == fails ? 7 : 0;
+            });
+            for (int i = 0; i < (int)at.size(); ++i) assert(at[i] == (long long)i * kListMost);
+            assert((int)at.size() == (fails < all ? fails + 1 : all));
+            assert(e == (fails < all ? 7 : 0) && state == (fails < all ? kWorkspaceData : kWorkspaceSums));
+        }
+    }
+}
+"""
+
+
+def test_a_norm_that_failed_between_its_launches_leaves_a_workspace_that_is_refused(tmp_path):
+    _run(tmp_path, LAUNCHES)
+    with open(os.path.join(CSRC, "moe_api.cu")) as f:
+        body = f.read().split("int moe_grad_norm(")[1].split("\n}\n")[0]
+    assert "norm_launches(count, &workspace->state[0]" in body and body.count("workspace->state[0]") == 2   # by this alone
