@@ -337,6 +337,8 @@ class RouterRule:
     def __init__(self, score="softmax", groups=1, topk_groups=1, group_rank=1, renormalise=True, scale=1.0):
         if score not in self.SCORES:
             raise MoeError(ERR["MOE_ERR_UNSUPPORTED"], "RouterRule")
+        if any(abs(n) > 2 ** 31 - 1 for n in (groups, topk_groups, group_rank)):   # (a field takes a number modulo 2^32)
+            raise MoeError(ERR["MOE_ERR_UNSUPPORTED"], "RouterRule")
         self.handle = MoeRouterRule(self.SCORES[score], groups, topk_groups, group_rank, 1 if renormalise else 0, scale)
         self.address = ctypes.addressof(self.handle)
 
