@@ -469,6 +469,9 @@ def moe_grad_norm_workspace_bytes(elements: int, count: int) -> int:
 def moe_grad_norm(grads, out, workspace: Workspace, max_norm: float = 0.0, stream=None) -> None:
     """out fp32 [2] = (norm of all gradients, the factor min(1, max_norm / norm) that brings it to max_norm; 1 with
     max_norm 0).  out[1:] is a grad_scale for moe_adamw_step."""
+    room = getattr(workspace, "buffer", None)
+    if room is not None and isinstance(out, torch.Tensor) and room.device != out.device:   # (out and grads are compared by the call)
+        raise ValueError("tensors of several devices")
     rc = (_MARSHAL or _marshal()).grad_norm(_list(grads), out, max_norm, workspace.address, None if stream is None else _stream_ptr(stream))
     if rc:
         raise MoeError(rc, "moe_grad_norm")

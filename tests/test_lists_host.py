@@ -62,3 +62,12 @@ def test_one_of_many(bd):  # noqa: F811
         change()
         with pytest.raises(bd.MoeError, match=code):
             _step(bd, lists)
+
+
+def test_a_norm_whose_workspace_is_on_another_device(bd):  # noqa: F811
+    """The call runs on the gradients' device, which would write to another one's memory."""
+    ws = bd.Workspace(1024, device="cpu")
+    with pytest.raises(ValueError, match="devices"):
+        bd.moe_grad_norm([], torch.empty(2, device="meta"), ws, stream=0)
+    with pytest.raises(bd.MoeError, match="NULL"):               # here nothing is on a GPU
+        bd.moe_grad_norm([], torch.empty(2), ws, stream=0)
