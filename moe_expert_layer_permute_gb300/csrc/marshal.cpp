@@ -9,6 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <limits>
 #include <memory>
 #include <utility>
 #include <vector>
@@ -392,6 +393,8 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (!number(args[1], &held, &out, &l)) return nullptr;
         const double most = PyFloat_AsDouble(args[2]);
         if (PyErr_Occurred()) return nullptr;
+        // (0 would be no clipping)
+        const float max_norm = most > 0.0 && (float)most == 0.f ? std::numeric_limits<float>::denorm_min() : (float)most;
         auto* workspace = static_cast<moe_scratch*>(PyLong_AsVoidPtr(args[3]));
         if (PyErr_Occurred()) return nullptr;
         c10::cuda::OptionalCUDAGuard guard;
@@ -400,7 +403,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         if (PyErr_Occurred()) return nullptr;
         int rc;
         Py_BEGIN_ALLOW_THREADS;
-        rc = moe_grad_norm(l.count < 0 ? 0 : l.count, l.views(0), const_cast<moe_tensor*>(out), (float)most, workspace, stream);
+        rc = moe_grad_norm(l.count < 0 ? 0 : l.count, l.views(0), const_cast<moe_tensor*>(out), max_norm, workspace, stream);
         Py_END_ALLOW_THREADS;
         return PyLong_FromLong(rc);
     } catch (const std::exception& e) {

@@ -78,3 +78,15 @@ def test_tensors_that_come_to_the_gpu(cuda_lib):
     _step(cuda_lib, {k: [x] for k, x in want.items()}, 32)
     for k in ("p", "m", "v", "copy"):
         assert torch.equal(t[k], want[k])
+
+
+@pytest.mark.parametrize("most", [1e-30, 1e-44, 1e-50, 1e-300])
+def test_a_norm_clipped_to_next_to_nothing(cuda_lib, most):
+    """A max_norm below the numbers of fp32 still clips; only 0 does not.  The factor is most / 4, off by a rounding of the
+    quotient and of max_norm: 2^-23 of it, or two of the smallest steps, 2^-148."""
+    grads = [torch.ones(16, device="cuda")]
+    ws, out = cuda_lib.Workspace(cuda_lib.moe_grad_norm_workspace_bytes(16, 1)), torch.empty(2, device="cuda")
+    cuda_lib.moe_grad_norm(grads, out, ws, max_norm=most)
+    assert float(out[0]) == 4 and abs(float(out[1]) - most / 4) <= 2.0 ** -23 * most / 4 + 2.0 ** -148
+    cuda_lib.moe_grad_norm(grads, out, ws, max_norm=0.0)
+    assert out.tolist() == [4.0, 1.0]
