@@ -126,7 +126,8 @@ __device__ __forceinline__ void decode4(float* x, uint32_t codes, float scale) {
         x[2 * h + 1] = __fmul_rn(f.y, scale);
     }
 }
-// 32 random bits of a value's number: two rounds of xor-shift and multiplication over its place in a Weyl sequence
+// 32 random bits of a value's number: C. Wellons's published mixing of 32 bits (2018; xor-shifts of 16, 15 and 16, and two
+// multipliers of the least bias that a search found) over its place in a Weyl sequence of the golden ratio
 __device__ __forceinline__ uint32_t adam_noise(uint32_t place, uint32_t key) {
     uint32_t h = place * 0x9E3779B1u + key;
     h = (h ^ (h >> 16)) * 0x7FEB352Du;
@@ -150,20 +151,6 @@ __device__ __forceinline__ float max_abs(float most, float x) {
     asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(most), "f"(x));
     return r;
 }
-// sqrt(x) rounded to nearest, so that a code is the same wherever it is computed: from 1 / sqrt(x) by a step of Newton's whose
-// remainder x - s^2 is exact (a fused product).  For 0 and from 1e-30 to 1e30, where it agrees with the library's for
-// every number; what is added makes no difference there but for 0.
-constexpr float kRootLeast = 1e-30f, kRootMost = 1e30f;
-__device__ __forceinline__ float sqrt_exact(float x) {
-    float q;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(x + 2e-38f));
-    const float s = x * q;
-    return fmaf(fmaf(-s, s, x), 0.5f * q, s);
-}
-__device__ __forceinline__ bool root_outside(float x) {   // apart from those over kRootMost, infinity and NaN
-    return __float_as_uint(x) - 1u < __float_as_uint(kRootLeast) - 1u;
-}
-
 // what the codes of a block are scaled by: its largest value's bits -> 448 / it (0: none, or not finite) and the scale
 __device__ __forceinline__ float block_scale(uint32_t most, float* scale) {
     float s = __uint_as_float(most);
@@ -225,24 +212,19 @@ __global__ void __launch_bounds__(32 * kAdamWarps, adam_blocks_sm<EIGHT>()) adam
             }
         }
         // Roundings as they stand in the formulas, none of them fused: one more or less in a million moves a code, and that
-        // code's value the next step by a tenth.
+        // code's value the next step by a tenth.  The root is the library's, rounded to nearest (a Newton step on an approximate
+        // one and the library's beyond its range took 1707 us instead of 1708 for 604 M values in 8 bits, 3170 instead of 3182 in 32).
         [[maybe_unused]] float most_m = 0.f, root[8];
         float most_v = 0.f;
-        bool odd = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float x = __fmul_rn(g[i], gs);
             if constexpr (EIGHT) v[i] = __fmul_rn(v[i], v[i]);
             m[i] = __fadd_rn(__fmul_rn(m[i], a.b1), __fmul_rn(x, a.c1));
             v[i] = __fadd_rn(__fmul_rn(v[i], a.b2), __fmul_rn(__fmul_rn(x, x), a.c2));
-            root[i] = sqrt_exact(v[i]);
-            odd |= root_outside(v[i]);
+            root[i] = __fsqrt_rn(v[i]);
             most_v = max_abs(most_v, v[i]);
             if constexpr (EIGHT) most_m = max_abs(most_m, m[i]);
-        }
-        if (odd || !(most_v < kRootMost)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) root[i] = __fsqrt_rn(v[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
