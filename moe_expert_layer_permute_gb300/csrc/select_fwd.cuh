@@ -558,10 +558,14 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
         }
         bool rounds = false;
         for (int e = threadIdx.x; e < a.E; e += 32 * kSelWarps) {
-            const float b = biases[e], d = b - top_bias;
+            const float b = biases[e];
+            float d = b - top_bias;
+            if (d == -INFINITY && b != -INFINITY) {   // which excludes nobody: sums that keys cannot tell
+                d = NAN;
+                odd_bias = true;
+            }
             biases[e] = d;
             rounds |= d + top_bias != b;
-            odd_bias |= fabsf(b) < INFINITY && d == -INFINITY;
         }
         odd_bias = __syncthreads_or(odd_bias);
         rounded = __syncthreads_or(rounds);
@@ -680,17 +684,13 @@ __global__ void __launch_bounds__(32 * kSelWarps, V <= 16 ? 8 : V == 32 ? 4 : 2)
                 if (a.bias) sums(std::false_type{}, std::true_type{}); else sums(std::false_type{}, std::false_type{});
             }
             if (odd_bias || __any_sync(all, live && special)) {
-                // experts that are excluded by their logits; sums that are NaN or +inf, which keys cannot tell, or -inf without
-                // being excluded
+                // experts that are excluded by their logits; sums that are NaN or +inf, which keys cannot tell
                 bool odd = false;
                 most_c = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float c = __uint_as_float(key[i]);
-                    if (place(i) < read) {
-                        if (sel_value(a, t * a.E + e0 + place(i)) == -INFINITY) c = -INFINITY;
-                        else if (c == -INFINITY) odd |= __ldg(a.bias + e0 + place(i)) != -INFINITY;   // (without biases no sum is)
-                    }
+                    if (place(i) < read && sel_value(a, t * a.E + e0 + place(i)) == -INFINITY) c = -INFINITY;
                     odd |= !(c < INFINITY);
                     most_c = fmaxf(most_c, c);
                     key[i] = __float_as_uint(c);
