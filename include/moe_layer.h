@@ -329,16 +329,18 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
  *   p' = p - lr (m' / (1 - beta1^t) / (sqrt(v' / (1 - beta2^t)) + eps) + weight_decay p),   copy = bf16(p')
  * in place of p (fp32), m and v.  moe_adamw_step takes `count` tensors (<= 65536) in one launch for each 384: arrays of
  * views params, grads, m, v and, or NULL, copies; element i of each has as many values (any shape, contiguous; empty
- * ones are passed over).  grads fp32 or bf16, each its own.  A parameter may stand in the list once
- * (MOE_ERR_UNSUPPORTED); that tensors do not overlap otherwise is the caller's to see to.
+ * ones are passed over) and begins at 16 bytes, codes too: in a buffer that holds many, leave gaps (MOE_ERR_ALIGN).  grads
+ * fp32 or bf16, each its own.  A parameter may stand in the list once (MOE_ERR_UNSUPPORTED); that tensors do not overlap
+ * otherwise is the caller's to see to.
  *   States in 32 bits: m, v fp32.  m_scales and v_scales are not read.
  *   States in 8 bits: m and v uint8 or E4M3 (all tensors of a call alike), v holding codes of r = sqrt(v); m_scales and
  * v_scales fp32 [ceil(n / 256)] views, 4-byte aligned: value i of m is code[i] m_scales[i / 256].  Zeros are the state to
  * start from.  The step decodes, steps in fp32 and encodes again: scale = max|x| / 448 over the 256 values, x / scale
  * rounded up with the probability of its distance to the code below (`seed` chooses the numbers: give another for each
- * step, its number for one, since a state that meets the same numbers each time stays where it is; results repeat with it).  Codes of r are at least 1 (2^-9), so a value that has had no gradient beside others
- * that have holds a small v.  Blocks with nothing over 1e-35 become zeros; a NaN or an infinity in m' or v' makes its
- * block NaN.
+ * step, its number for one, since a state that meets the same numbers each time stays where it is; results repeat with it).
+ * Codes of r are at least 1 (2^-9), so a value that has had no gradient beside others that have holds a small v.  At steady
+ * state the root of v is some 17 % off (rms) and m 8 % of its rms, v's mean 5 % too large.  Blocks with nothing over 1e-35
+ * become zeros; a NaN or an infinity in m' or v' makes its block NaN.
  *   lr, step, grad_scale: numbers on the device (fp32, int32, fp32, one element each, 4-byte aligned) or NULL, then lr and
  * step of the struct and 1.  A graph that is replayed wants them there; the step's number is then added to the seed.
  * A grad_scale that is not finite, or a step on the device below 1, leaves everything as it is.
@@ -349,8 +351,8 @@ int moe_orthogonalise(const moe_tensor* G, moe_tensor* O, int32_t steps, const f
  * (no step, if it is grad_scale).  Squares and sums of 64 are fp32 (values over 1e18 or under 1e-22 are beyond it), the rest
  * 64 bits, in an order that depends on the sizes alone.  `workspace`: a zeroed moe_scratch handle of at least
  * moe_grad_norm_workspace_bytes(elements, count) bytes, 256-byte aligned, which the caller has set to zero once;
- * MOE_ERR_STATE for one that moe_orthogonalise has used, and after a call of which a launch failed (until the buffer and the handle
- * are set to zero again). */
+ * MOE_ERR_STATE for one that moe_orthogonalise has used, and after a call of which a launch failed (until the buffer and the
+ * handle are set to zero again). */
 #define MOE_ADAMW_BLOCK 256
 typedef struct {
     double lr, beta1, beta2, eps, weight_decay;

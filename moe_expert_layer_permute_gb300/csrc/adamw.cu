@@ -8,6 +8,9 @@
 // thousandth, and half a code's step is 3 to 6 %.  So x goes up to the next code with the probability of its distance to
 // the one below, by 16 bits of a hash of the seed, the tensor's number and the value's: exact in the mean.  r's codes are
 // at least the smallest, so that no v that a gradient has touched becomes 0 beside an m that has not.
+// What that leaves: at steady state v is 1.05 times the 32-bit state's in the mean, its root 17 % off (rms, of itself) and m 8 %
+// (of its rms), at any level of the gradients (4096 values, 3000 steps at each of three levels); with the same bits at every step
+// v is 2.3 times too large and its root 70 % off.
 //
 // Bound by memory: 28 bytes a value (fp32 gradients and states), 14 (bf16 gradients, 8-bit states), 2 more for the
 // bf16 copy.  604 M values with the copy: fp32 2.8 ms (6.5 TB/s, 0.97 of a copy's rate), 8 bits 1.70 ms (5.7 TB/s, 0.85).  A warp takes 256 neighbouring values at a time, 4 a lane in two groups, so that every access is a row of

@@ -19,7 +19,37 @@
 // index takes from c (7 bits at 128 experts) is part of the error above; it is small where the numbers are, so c is taken
 // relative to the largest bias and then to the row's largest c.
 //
-// Bound by instruction issue: 131,072 x 512 (sigmoid, bias, k = 8) takes 110 us, 740 instructions a token at three quarters
+// What fp32 may be off by, and where each counts.  t is the largest finite bias, b - t a bias as it is kept, c a sum of it and a
+// score, d = top - c its distance from the row's largest, u = 2^-24:
+//
+//   a score                  sel_error(its size), below                          each of two sums that are compared
+//   b - t                    u |b - t| <= u (|c| + s); u s is within sel_error's   kSelSum |c| = 2 u |c|, with the next
+//                            slack (sigmoid 3e-7 of at most 1.6e-7, softmax
+//                            9e-7 s of 7.2e-7 s)
+//   c                        u |c|, |c| <= |top| + d                              (above)
+//   d                        u d                                                 kSelSum d
+//   the index in d's bits    quantum d = 2^bits 2^-23 d, bits = log2 of E           where keys alone are compared
+//   64 bits, b not less t    2 x 2^-53 |t| and what it takes from c               last = 1e-15 |t| (groups, two terms each: 4e-15 |t|)
+//
+//   two sums (sel_margin)         2 sel_error + 2 kSelSum (|top| + d) + (q + kSelSum) d + last, d the larger distance; q is
+//       0 between picks, whose sums are made again in full; quantum where one is in full and one a key (the last pick and the
+//       one behind it); 2 quantum for two keys (which neighbours hang together); 3 quantum where more picks are looked for,
+//       so that none is missed that the finer tests then ask for.  An expert further than twice a margin behind the first
+//       that was left out (select_again) cannot come before a pick.
+//   scores of at most             1 (sigmoid), 1 / the row's sum (softmax), and of two neighbours s_j + span: s_(j+1) is at most
+//       s_j + b_j - b_(j+1), span the finite biases' largest difference; of a group's terms |top| + span
+//   two groups (sel_group_margin) 4 sel_error + 2 kSelSum (|v| + |w| + 4 |top| + |t| where one expert stands for two) + 4e-15 |t|;
+//       a group's two terms and their sum v round by u (2 |m1| + 2 |m2| + |v|) <= u (3 |v| + 4 |top|) at most, as m1 <= top and
+//       |m1| + |m2| = |v| or, of unlike signs, |m2| <= |v| + |top|
+//   64 bits over a softmax's fp32 sum  2 sum_error |s - s'| (its error stands in both) + 1e-15 (|c| + |b|)
+//   beyond fp32                   a bias that is -inf only less t, a group's sum that is -inf, a NaN, +inf: all in 64 bits (select_all)
+//
+// A change to a key's bits, to a sum's order or to sel_score64 changes these.
+//
+// Every call of the warp (__shfl_sync, __ballot_sync, __any_sync, the reductions) is made by all 32 lanes: none stands behind &&,
+// || or ?: of a lane's own value, where lanes that have their answer would not take part, which is undefined.
+//
+// Bound by instruction issue: 131,072 x 512 (sigmoid, bias, k = 8) takes 110 us, 741 instructions a token at three quarters
 // of the issue slots, where its logits take 42 us to read; 16,384 x 256 in 8 groups 18.7 us, of which about 5 are the tail
 // that a token gone through again leaves (3 us each, most of it waiting for code and 64-bit arithmetic).
 #pragma once
