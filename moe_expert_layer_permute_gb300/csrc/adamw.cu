@@ -13,7 +13,7 @@
 // v is 2.3 times too large and its root 70 % off.
 //
 // Bound by memory: 28 bytes a value (fp32 gradients and states), 14 (bf16 gradients, 8-bit states), 2 more for the
-// bf16 copy.  604 M values with the copy: fp32 2.8 ms (6.5 TB/s, 0.97 of a copy's rate), 8 bits 1.70 ms (5.7 TB/s, 0.85).  A warp takes 256 neighbouring values at a time, 4 a lane in two groups, so that every access is a row of
+// bf16 copy.  604 M values with the copy: fp32 2.8 ms (6.5 TB/s, 0.97 of a copy's rate), 8 bits 1.71 ms (5.7 TB/s, 0.85).  A warp takes 256 neighbouring values at a time, 4 a lane in two groups, so that every access is a row of
 // whole sectors and a block of 8-bit states is one warp's: its largest value is one reduction, and no warp waits for
 // another.  The tensors' addresses come as the launch's arguments, up to 384 tensors of any sizes a launch (by a table in
 // memory each call would wait for a copy).
@@ -28,8 +28,8 @@ namespace moe {
 
 constexpr int kAdamWarps = kListWarps;
 constexpr int kAdamUnit = kListUnit;   // and values of a block of 8-bit states
-// Blocks an SM.  In 8 bits a value is some 75 instructions and 14 to 18 bytes, so that issue slots and memory are both near
-// their ends (70 % and 85 %) and more warps cover more of the wait: with 4 blocks (64 registers a thread) 604 M values take
+// Blocks an SM.  In 8 bits a value is some 85 instructions and 14 to 18 bytes, so that issue slots and memory are both near
+// their ends (74 % and 85 %) and more warps cover more of the wait: with 4 blocks (64 registers a thread) 604 M values take
 // 6 % longer than with 5, with 6 (spills) 3 %.
 template <bool EIGHT>
 constexpr int adam_blocks_sm() { return EIGHT ? 5 : 4; }

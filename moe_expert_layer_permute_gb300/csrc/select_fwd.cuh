@@ -49,7 +49,7 @@
 // Every call of the warp (__shfl_sync, __ballot_sync, __any_sync, the reductions) is made by all 32 lanes: none stands behind &&,
 // || or ?: of a lane's own value, where lanes that have their answer would not take part, which is undefined.
 //
-// Bound by instruction issue: 131,072 x 512 (sigmoid, bias, k = 8) takes 110 us, 741 instructions a token at three quarters
+// Bound by instruction issue: 131,072 x 512 (sigmoid, bias, k = 8) takes 110 us, 756 instructions a token at three quarters
 // of the issue slots, where its logits take 42 us to read; 16,384 x 256 in 8 groups 18.7 us, of which about 5 are the tail
 // that a token gone through again leaves (3 us each, most of it waiting for code and 64-bit arithmetic).
 #pragma once
