@@ -213,7 +213,8 @@ int moe_router_bwd(const moe_tensor* topk_idx, const moe_tensor* topk_w, const m
  *   topk_idx[t]: the k largest c of the groups that stay, in descending order
  *   topk_w[t,j] = scale s[t, topk_idx[t,j]], divided by the sum of the k picks' s if `renormalise` is not 0
  * c and the groups' values are compared in 64 bits; without a bias experts are compared by their logits, whose order is
- * that of their scores.  Equal ones go to the lower index (-0.0 equal to +0.0), NaN ranks above every number.  Where
+ * that of their scores.  Equal ones go to the lower index (-0.0 equal to +0.0), NaN ranks above every number.  (64 bits
+ * round too: of a softmax, whose sum they round, values within some 1e-15 of each other may be in either order.)  Where
  * fewer than k experts are left, the other picks are -1 with weight 0.  The bias carries no gradient.
  *
  * moe_router_select_fwd: logits fp32 or bf16 [T, E] -> topk_idx int32 [T, k], topk_w fp32 [T, k] (overwritten).

@@ -109,8 +109,10 @@ __device__ __forceinline__ float sel_sigmoid(float x) { return rcp_approx(1.f + 
 //   sigmoid: s (1 - s) (2^-22 + 2^-23 |z|) + 2^-23 s, at most 3e-7, and for a small s, -z up to 88, 1.1e-5 s
 //   softmax: s (2^-22 + 2^-23 (-ln s)) and the sum's error, 2^-24 for each of V / 4 additions one after the other and some 2^-21
 //            with the tree's and the exponentials'; s (-ln s) is at most 0.37
+// Scores under 2^-126 = 1.18e-38 are 0 (the quotient's least number; a power over 2^128 is infinite), and among numbers under
+// that a key's index takes 2^bits 2^-149 whatever their size: no score counts as smaller than 1.2e-33, 1.1e-5 of which is more.
 __device__ __forceinline__ float sel_error(const SelectArgs& a, float most) {
-    const float s = fminf(fmaxf(most, 1e-37f), 1.f);
+    const float s = fminf(fmaxf(most, 1.2e-33f), 1.f);
     return a.sigmoid ? fminf(3e-7f, 1.1e-5f * s) : a.sum_error * s + fminf(4.5e-8f, 1.1e-5f * s);
 }
 constexpr float kSelSum = 1.2e-7f;   // of a sum's size: a rounding of it, and one of its bias less the largest

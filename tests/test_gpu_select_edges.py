@@ -99,3 +99,16 @@ def test_gradients_of_masked_and_short_rows(cuda_lib, T, E, k, G, kept, score, r
         # which r may stand unrounded (a fused product): 2^-24 (2 |r| + |d| + |there + r| + |both|), at most the following.  (Where
         # one pick has all of a row's score r and q cancel, and d says nothing of their size.)
         assert ((both.double() - there.double() - d.double()).abs() <= 2 ** -23 * (there.abs() + d.abs() + both.abs()) + 2 ** -22 * size.cuda()).all()
+
+
+@pytest.mark.parametrize("T,E,G,kept,k", [(300, 16, 4, 2, 6), (2600, 16, 4, 3, 3), (2600, 128, 1, 1, 8), (60, 1000, 20, 7, 9), (2600, 256, 8, 4, 8), (40, 64, 1, 1, 8)])
+@pytest.mark.parametrize("score,rank", list(itertools.product(["softmax", "sigmoid"], [1, 2])))
+@pytest.mark.parametrize("biases", [None, (0.0,), (0.0, 1e-40, -1e-40), (0.0, 3e-39, 1e-38)])
+def test_scores_below_the_numbers_of_fp32(cuda_lib, T, E, G, kept, k, score, rank, biases):
+    """Scores under 1e-38 are 0 in the forward's 32 bits; groups and sums with biases as small are told apart all the same."""
+    g = torch.Generator().manual_seed(E + k + T)
+    logits = -84 - 20 * torch.rand(T, E, generator=g)
+    if score == "softmax":   # beside one that has nearly all of the sum
+        logits[:, E // 3] = 1.0
+    bias = None if biases is None else torch.tensor(biases)[torch.randint(0, len(biases), (E,), generator=g)].cuda()
+    check(cuda_lib, logits.cuda(), k, bias=bias, score=score, G=G, kept=kept, rank=rank)
